@@ -9,7 +9,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_async_debug.so" if DEBUG_BOUNDS else "lib
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_CAPACITY, MOE_ERR_DUPLICATE, MOE_ERR_STALE, \
     MOE_ERR_TIMEOUT, MOE_ERR_CUDA, MOE_ERR_UNSUPPORTED, MOE_ERR_BOUNDS = range(9)
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
 MOE_POLICY_MTFS, MOE_POLICY_THRESHOLD, MOE_POLICY_RANKS = 0, 1, 2
 MOE_EXPERT_SWIGLU, MOE_EXPERT_IDENTITY = 0, 1
 
@@ -23,7 +23,10 @@ EXPORTS = ("moe_async_create", "moe_async_route", "moe_async_enqueue", "moe_asyn
            "moe_async_get_trace", "moe_async_snapshot", "moe_async_destroy",
            "moe_async_status_string", "moe_async_host_writable", "moe_async_profile", "moe_async_profile_read",
            "moe_async_stream_setup", "moe_async_stream_run", "moe_async_stream_trace", "moe_async_stream_stats",
-           "moe_async_cancel", "moe_async_debug_append_record")
+           "moe_async_cancel", "moe_async_debug_append_record",
+           "moe_async_sort_experts", "moe_async_sort_rows", "moe_async_merge_rows", "moe_async_merge_rows_backward",
+           "moe_async_route_backward", "moe_async_add_rms_norm", "moe_async_add_rms_norm_backward",
+           "moe_async_add_rms_norm_backward_workspace", "moe_async_linear")
 
 KERNEL_KINDS = ("enqueue", "schedule", "ffn1", "ffn2", "collect", "tick")
 
@@ -62,6 +65,16 @@ class StreamStats(ctypes.Structure):
                [("peak_queue", ctypes.c_int32 * 16), ("occupancy_sum", ctypes.c_int64 * 16)]
 
 
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "out_dtype", "act", "rows", "fan_in", "fan_out", "groups")] + \
+               [(n, ctypes.c_void_p) for n in ("d_x", "d_w", "d_bias", "d_x_scale", "d_w_scale", "d_mul", "d_residual",
+                                               "d_offsets", "d_y")] + \
+               [(n, ctypes.c_int64) for n in ("x_stride", "w_stride", "mul_stride", "residual_stride", "y_stride")]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status, what=""):
         self.status = status
@@ -81,6 +94,7 @@ def load():
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, U32P, I32P, F32P = ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p
     VPP = ctypes.POINTER(ctypes.c_void_p)
+    I64, F32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "moe_async_create": [ctypes.POINTER(Config), VPP, VPP, VPP, VPP, VPP, VPP, P, ctypes.POINTER(P)],
         "moe_async_route": [F32P, I32, I32, I32, I32P, F32P, P],
@@ -107,11 +121,21 @@ def load():
         "moe_async_stream_stats": [P, P, ctypes.POINTER(StreamStats)],
         "moe_async_stream_run": [P, I32, I32, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32), P],
         "moe_async_stream_trace": [P, P, ctypes.POINTER(ctypes.c_int32), I32, ctypes.POINTER(ctypes.c_int32)],
+        "moe_async_sort_experts": [I32P, I32, I32, I32, I32P, I32P, I32P, P],
+        "moe_async_sort_rows": [I32, P, I64, I32P, I32, I32, I32, P, I64, I64, P],
+        "moe_async_merge_rows": [I32, P, I64, I64, I32P, F32P, I32, I32, I32, P, I64, P, I64, P],
+        "moe_async_merge_rows_backward": [I32, P, I64, P, I64, I64, I32P, F32P, I32, I32, I32, P, I64, F32P, P],
+        "moe_async_route_backward": [I32P, F32P, F32P, I32, I32, I32, F32P, P],
+        "moe_async_add_rms_norm": [I32, P, I64, P, I64, F32P, F32, I32, I32, P, I64, P, I64, F32P, P],
+        "moe_async_add_rms_norm_backward": [I32, P, I64, P, I64, F32P, F32, I32, I32, P, I64, P, I64, F32P, P, I64, P],
+        "moe_async_add_rms_norm_backward_workspace": [I32, I32],
+        "moe_async_linear": [ctypes.POINTER(LinearArgs), P],
     }
+    restype = {"moe_async_status_string": ctypes.c_char_p, "moe_async_add_rms_norm_backward_workspace": I64}
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
-        f.restype = ctypes.c_char_p if name == "moe_async_status_string" else ctypes.c_int
+        f.restype = restype.get(name, ctypes.c_int)
     _lib = lib
     return lib
 

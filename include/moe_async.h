@@ -63,7 +63,8 @@ typedef enum {
                                state was out of range; the access was skipped           */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+/* MOE_E4M3: operands of moe_async_linear and the 8-bit output of moe_async_add_rms_norm only */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2 } moe_dtype;
 
 typedef enum {
   MOE_POLICY_MTFS = 0,       /* most tokens first: deepest buckets first (StreamEP, section 4) */
@@ -401,6 +402,119 @@ moe_status moe_async_forward_noalloc(int32_t T, int32_t E, int32_t K, int32_t H,
                                      int32_t dtype, const void* d_x, const int32_t* d_expert,
                                      const float* d_w, const void* d_w1, const void* d_w3,
                                      const void* d_w2, void* d_y, void* stream);
+
+/* ---------------------------------------------------------------- stateless operators
+ * The synchronous form of the path for callers that hold a whole routed batch: norm, products,
+ * tokens sorted by expert and merged back, and the gradients a training step needs.  No handle,
+ * no allocation, nothing kept between calls; any number of calls may run at once on streams of
+ * their own, and every call can be captured into a graph.
+ *   - Row operands are [rows, width] with a row stride in elements (>= width); columns are
+ *     adjacent.  Rows whose base and stride are multiples of 16 bytes, and whose width is a
+ *     whole number of 16-byte units, move in such units; others element by element.
+ *   - Parameter vectors (gain, bias, scales, routing weights) are fp32.
+ *   - Sums are fp32 in an order fixed by the sizes and the alignment (no atomics): equal calls
+ *     give equal bits.
+ *   - An output may share memory with an input only where stated. */
+
+/* Sorted order of the pairs of a routed batch: by expert, pairs of one expert in pair order
+ * (pair i = t * K + k).
+ *   d_expert  : [T, K] int32; an id outside [0, E) belongs to no expert here (another rank's,
+ *               or a padded token's): its pair gets no row
+ *   d_offsets : [E + 1] int32 out: rows of expert e are offsets[e] .. offsets[e + 1]
+ *   d_pos     : [T, K] int32 out: the pair's row, -1 without one
+ *   d_pair    : [T * K] int32 out: the pair of each row; behind offsets[E], the pairs without
+ *               a row in pair order
+ * E <= 1024, K <= 32, T * K < 2^31 - 1024.  Asynchronous. */
+moe_status moe_async_sort_experts(const int32_t* d_expert, int32_t T, int32_t K, int32_t E, int32_t* d_offsets,
+                                  int32_t* d_pos, int32_t* d_pair, void* stream);
+
+/* rows[pos[t, k]] = x[t] for every pair whose pos lies in [0, n_rows); other rows are left as
+ * they were.  Each row is named by at most one pair.  dtype: MOE_F32 or MOE_BF16. */
+moe_status moe_async_sort_rows(int32_t dtype, const void* d_x, int64_t x_stride, const int32_t* d_pos, int32_t T,
+                               int32_t K, int32_t H, void* d_rows, int64_t rows_stride, int64_t n_rows, void* stream);
+
+/* y[t] = sum_k w[t, k] rows[pos[t, k]] + residual[t]: products and sums rounded in fp32 in
+ * ascending k, the residual last, as moe_async_collect merges.  Pairs whose pos lies outside
+ * [0, n_rows) add nothing and their weights are not looked at: a token without any gets its
+ * residual, or zeros.  d_w NULL: plain sums (the gradient of moe_async_sort_rows).  d_residual
+ * may be NULL, or y itself. */
+moe_status moe_async_merge_rows(int32_t dtype, const void* d_rows, int64_t rows_stride, int64_t n_rows,
+                                const int32_t* d_pos, const float* d_w, int32_t T, int32_t K, int32_t H,
+                                const void* d_residual, int64_t residual_stride, void* d_y, int64_t y_stride,
+                                void* stream);
+
+/* Gradients of moe_async_merge_rows: grad_rows[pos[t, k]] = w[t, k] grad[t] (other rows are left
+ * as they were) and grad_w[t, k] = <rows[pos[t, k]], grad[t]> (0 for a pair without a row); the
+ * residual's gradient is `grad` itself. */
+moe_status moe_async_merge_rows_backward(int32_t dtype, const void* d_grad, int64_t grad_stride, const void* d_rows,
+                                         int64_t rows_stride, int64_t n_rows, const int32_t* d_pos, const float* d_w,
+                                         int32_t T, int32_t K, int32_t H, void* d_grad_rows, int64_t grad_rows_stride,
+                                         float* d_grad_w, void* stream);
+
+/* Gradient of moe_async_route's weights: grad_logits[t, idx[t, k]] = w_k (grad_w_k - sum_j w_j
+ * grad_w_j), 0 at the experts not chosen; all of [T, E] is written.  d_idx and d_w are what
+ * moe_async_route returned. */
+moe_status moe_async_route_backward(const int32_t* d_idx, const float* d_w, const float* d_grad_w, int32_t T, int32_t E,
+                                    int32_t K, float* d_grad_logits, void* stream);
+
+/* h = x + residual, rounded to dtype; y = h / sqrt(mean(h^2) + eps) * gain per row.
+ *   d_residual : [T, H] or NULL (then h = x, and d_h must be NULL)
+ *   d_gain     : [H] fp32 or NULL (all ones)
+ *   d_h        : [T, H] out, the sum; may be NULL, d_x or d_residual
+ *   d_scale    : NULL: y is [T, H] in dtype.  Else [T] fp32 out and y is [T, H] e4m3:
+ *                scale = max(max|y| / 448, 2^-126), stored value y / scale, round to nearest
+ * A NaN makes its row NaN, an infinity (or a sum of squares beyond fp32) makes finite columns 0
+ * and itself NaN; in e4m3 either makes the whole row and its scale NaN.  dtype: MOE_F32 or
+ * MOE_BF16. */
+moe_status moe_async_add_rms_norm(int32_t dtype, const void* d_x, int64_t x_stride, const void* d_residual,
+                                  int64_t residual_stride, const float* d_gain, float eps, int32_t T, int32_t H,
+                                  void* d_h, int64_t h_stride, void* d_y, int64_t y_stride, float* d_scale,
+                                  void* stream);
+
+/* Gradients of moe_async_add_rms_norm's y at h (its output h, or x): with u = grad * gain and
+ * n = h / sqrt(mean(h^2) + eps), grad_x = (u - n mean(u n)) / sqrt(mean(h^2) + eps) + grad_h,
+ * the gradient of x and of the residual alike, and grad_gain[c] = sum_t grad[t, c] n[t, c].
+ *   d_grad_h    : [T, H] gradient that arrives at h itself, or NULL; may be d_grad_x
+ *   d_grad_gain : [H] fp32 out or NULL; it needs a workspace (16-byte aligned) of at least
+ *                 moe_async_add_rms_norm_backward_workspace(T, H) bytes, the caller's until the
+ *                 call has run; calls that may run at once need one each.  Smaller:
+ *                 MOE_ERR_CAPACITY */
+int64_t moe_async_add_rms_norm_backward_workspace(int32_t T, int32_t H);
+moe_status moe_async_add_rms_norm_backward(int32_t dtype, const void* d_grad, int64_t grad_stride, const void* d_h,
+                                           int64_t h_stride, const float* d_gain, float eps, int32_t T, int32_t H,
+                                           const void* d_grad_h, int64_t grad_h_stride, void* d_grad_x,
+                                           int64_t grad_x_stride, float* d_grad_gain, void* d_workspace,
+                                           int64_t workspace_bytes, void* stream);
+
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 /* with erf */, MOE_ACT_RELU = 3 } moe_act;
+
+/* y[t, n] = act(sx[t] sw[n] sum_k x[t, k] w[n, k] + bias[n]) * mul[t, n] + residual[t, n]
+ *   dtype     : MOE_BF16, or MOE_E4M3 with d_x_scale [rows] and d_w_scale [fan_out] fp32 (NULL
+ *               for MOE_BF16); MOE_F32 operands return MOE_ERR_UNSUPPORTED
+ *   d_x       : [rows, fan_in]    d_w : [fan_out, fan_in]    fp32 accumulation
+ *   d_y       : [rows, fan_out] in out_dtype (MOE_BF16 or MOE_F32), rounded once
+ *   d_bias    : [fan_out] fp32 or NULL
+ *   d_mul, d_residual : [rows, fan_out] in out_dtype or NULL; either may be y itself
+ *   groups = 0: dense.  groups = G > 0: one weight matrix per expert on sorted rows: d_w is
+ *   [G, fan_out, fan_in] (each matrix fan_out * w_stride elements), d_bias and d_w_scale are
+ *   [G, fan_out], and rows d_offsets[g] .. d_offsets[g + 1] (device, int32, ascending, clipped to
+ *   [0, rows]) meet matrix g; rows of no group are left as they were.
+ * fan_in, the bases and the strides of x and w are multiples of 16 bytes, else
+ * MOE_ERR_UNSUPPORTED; fan_out and the other strides are free.  Asynchronous. */
+typedef struct {
+  int32_t dtype, out_dtype, act, rows, fan_in, fan_out, groups;
+  const void* d_x;
+  const void* d_w;
+  const float* d_bias;
+  const float* d_x_scale;
+  const float* d_w_scale;
+  const void* d_mul;
+  const void* d_residual;
+  const int32_t* d_offsets;
+  void* d_y;
+  int64_t x_stride, w_stride, mul_stride, residual_stride, y_stride;
+} moe_async_linear_args;
+moe_status moe_async_linear(const moe_async_linear_args* args, void* stream);
 
 /* Bounds-checked build (libmoe_async_debug.so, compiled with MOE_DEBUG_BOUNDS): every bucket,
  * slot and k index the kernels read back from device state is checked before use, and an
