@@ -15,66 +15,71 @@ Every function runs on the device of its first tensor, on that device's current 
 (``MOE_ERR_INVALID``) for tensors that do not fit together.  Gradients are functions of their
 own (``*_backward``).  Matrices are [rows, width] with adjacent columns and any row stride.
 """
-import ctypes
+import struct
 
 import torch
 
 from . import _native as N
 
 _DT = {torch.float32: N.MOE_F32, torch.bfloat16: N.MOE_BF16, torch.float8_e4m3fn: N.MOE_E4M3}
-_ROWS = (torch.float32, torch.bfloat16)
+_F32, _BF16, _E4M3, _I32 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.int32
+_ROWS = (_F32, _BF16)
+_LINEAR_ARGS = struct.Struct("7i9P5q")           # moe_async_linear_args
+
+# A small call is bound by its host side (a decode step's norm runs 4 us on the GPU), so the
+# checks below read each property once and build no message before one is needed.
 
 
-def _need(ok, what):
-    if not ok:
-        raise N.MoEError(N.MOE_ERR_INVALID, what)
+def _bad(what, t=None):
+    if isinstance(t, torch.Tensor):
+        what += f"; got {tuple(t.shape)} of {t.dtype} on {t.device}, strides {t.stride()}"
+    raise N.MoEError(N.MOE_ERR_INVALID, what)
 
 
-def _matrix(t, name, like, shape, dtype):
-    """A [rows, width] operand on the device of `like`: adjacent columns, any row stride."""
-    _need(t.device == like.device and t.dtype == dtype and tuple(t.shape) == shape
-          and (shape[1] == 1 or t.stride(1) == 1) and (shape[0] <= 1 or t.stride(0) >= shape[1]),
-          f"{name}: expected {shape} of {dtype} on {like.device} with adjacent columns, got {tuple(t.shape)} of "
-          f"{t.dtype} on {t.device}, strides {t.stride()}")
+def _leading(t, name, dtypes):
+    """The matrix that names the call's device: (device, rows, width, row stride)."""
+    if t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda:
+        _bad(f"{name}: expected a CUDA matrix of {dtypes}", t)
+    rows, width = t.shape
+    return t.get_device(), rows, width, _rows(t, name, t.get_device(), t.dtype, rows, width)
 
 
-def _vector(t, name, like, shape, dtype):
-    _need(t.device == like.device and t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(),
-          f"{name}: expected contiguous {shape} of {dtype} on {like.device}, got {tuple(t.shape)} of {t.dtype} on "
-          f"{t.device}")
+def _rows(t, name, dev, dtype, rows, width):
+    """Row stride of a [rows, width] matrix with adjacent columns."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, width):
+        _bad(f"{name}: expected ({rows}, {width}) of {dtype} on cuda:{dev}", t)
+    if rows <= 1:
+        if width > 1 and t.stride(1) != 1:
+            _bad(f"{name}: expected adjacent columns", t)
+        return width
+    ld, step = t.stride()
+    if (step != 1 and width > 1) or ld < width:
+        _bad(f"{name}: expected adjacent columns and rows that do not overlap", t)
+    return ld
 
 
-def _first(t, name, dtypes):
-    _need(t.is_cuda and t.dim() == 2 and t.dtype in dtypes, f"{name}: expected a CUDA matrix of {dtypes}, got "
-          f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+def _whole(t, name, dev, dtype, shape):
+    """A contiguous tensor."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _bad(f"{name}: expected contiguous {tuple(shape)} of {dtype} on cuda:{dev}", t)
 
 
-def _ld(t):
-    """Row stride in elements (a single row has none: its width)."""
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+def _pairs(pos, dev, T=None):
+    """K of pos [T, K]."""
+    if pos.dim() != 2:
+        _bad("pos: expected [T, K]", pos)
+    _whole(pos, "pos", dev, _I32, pos.shape if T is None else (T, pos.shape[1]))
+    return pos.shape[1]
 
 
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-class _On:
-    """The call's device made current, and its stream."""
-    __slots__ = ("dev", "prev", "stream")
-
-    def __init__(self, t, stream):
-        self.dev, self.stream = t.device.index, stream
-
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.dev)
-        s = torch.cuda.current_stream() if self.stream is None else self.stream
-        return s.cuda_stream
-
-    def __exit__(self, *_):
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.prev)
+def _call(fn, what, dev, stream, *args):
+    """fn(*args, stream) with the call's device current."""
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _call(fn, what, dev, stream, *args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        raise N.MoEError(status, what)
 
 
 def sort_experts(expert, num_experts, stream=None):
@@ -83,33 +88,32 @@ def sort_experts(expert, num_experts, stream=None):
     expert int32 [T, K] (ids outside [0, num_experts) get no row) -> (offsets int32 [E + 1]: the
     rows of expert e are offsets[e]:offsets[e + 1]; pos int32 [T, K]: the row of each pair, -1
     without one; pair int32 [T * K]: the pair t * K + k of each row, pairs without one last)."""
-    _first(expert, "expert", (torch.int32,))
-    _need(expert.is_contiguous(), "expert: expected contiguous")
-    T, K = expert.shape
-    with _On(expert, stream) as s:
-        offsets = torch.empty(num_experts + 1 if num_experts > 0 else 1, dtype=torch.int32, device=expert.device)
-        pos, pair = torch.empty_like(expert), torch.empty(T * K, dtype=torch.int32, device=expert.device)
-        N.check(N.load().moe_async_sort_experts(_p(expert), T, K, num_experts, _p(offsets), _p(pos), _p(pair), s),
-                "sort_experts")
+    dev, T, K, _ = _leading(expert, "expert", (_I32,))
+    if not expert.is_contiguous():
+        _bad("expert: expected contiguous", expert)
+    if num_experts < 1:
+        _bad(f"num_experts: expected at least 1, got {num_experts}")
+    d = expert.device
+    offsets = torch.empty(num_experts + 1, dtype=_I32, device=d)
+    pos, pair = torch.empty_like(expert), torch.empty(T * K, dtype=_I32, device=d)
+    _call(N.load().moe_async_sort_experts, "sort_experts", dev, stream, expert.data_ptr(), T, K, num_experts,
+          offsets.data_ptr(), pos.data_ptr(), pair.data_ptr())
     return offsets, pos, pair
 
 
 def sort_rows(x, pos, out=None, stream=None):
     """rows[pos[t, k]] = x[t]: x [T, H] fp32 or bf16, pos int32 [T, K] -> rows [T * K, H] (or
     `out` [R, H]); rows that no pair names are left as they were."""
-    _first(x, "x", _ROWS)
-    T, H = x.shape
-    _matrix(x, "x", x, (T, H), x.dtype)
-    _need(pos.dim() == 2, "pos: expected [T, K]")
-    K = pos.shape[1]
-    _vector(pos, "pos", x, (T, K), torch.int32)
-    with _On(x, stream) as s:
-        if out is None:
-            out = torch.empty((T * K, H), dtype=x.dtype, device=x.device)
-        else:
-            _matrix(out, "out", x, (out.shape[0], H), x.dtype)
-        N.check(N.load().moe_async_sort_rows(_DT[x.dtype], _p(x), _ld(x), _p(pos), T, K, H, _p(out), _ld(out),
-                                             out.shape[0], s), "sort_rows")
+    dev, T, H, ldx = _leading(x, "x", _ROWS)
+    K = _pairs(pos, dev, T)
+    if out is None:
+        R, ldo = T * K, H
+        out = torch.empty((R, H), dtype=x.dtype, device=x.device)
+    else:
+        R = out.shape[0]
+        ldo = _rows(out, "out", dev, x.dtype, R, H)
+    _call(N.load().moe_async_sort_rows, "sort_rows", dev, stream, _DT[x.dtype], x.data_ptr(), ldx, pos.data_ptr(), T, K,
+          H, out.data_ptr(), ldo, R)
     return out
 
 
@@ -117,24 +121,21 @@ def merge_rows(rows, pos, w=None, residual=None, out=None, stream=None):
     """y[t] = sum_k w[t, k] rows[pos[t, k]] + residual[t] in fp32, ascending k, rounded once:
     rows [R, H], pos int32 [T, K], w fp32 [T, K] (None: plain sums), residual [T, H] or None ->
     y [T, H].  A pair without a row (pos outside [0, R)) adds nothing.  `out` may be `residual`."""
-    _first(rows, "rows", _ROWS)
-    R, H = rows.shape
-    _matrix(rows, "rows", rows, (R, H), rows.dtype)
-    _need(pos.dim() == 2, "pos: expected [T, K]")
-    T, K = pos.shape
-    _vector(pos, "pos", rows, (T, K), torch.int32)
+    dev, R, H, ldr = _leading(rows, "rows", _ROWS)
+    dt = rows.dtype
+    K = _pairs(pos, dev)
+    T = pos.shape[0]
     if w is not None:
-        _vector(w, "w", rows, (T, K), torch.float32)
-    if residual is not None:
-        _matrix(residual, "residual", rows, (T, H), rows.dtype)
-    with _On(rows, stream) as s:
-        if out is None:
-            out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
-        else:
-            _matrix(out, "out", rows, (T, H), rows.dtype)
-        N.check(N.load().moe_async_merge_rows(_DT[rows.dtype], _p(rows), _ld(rows), R, _p(pos), _p(w), T, K, H,
-                                              _p(residual), H if residual is None else _ld(residual), _p(out),
-                                              _ld(out), s), "merge_rows")
+        _whole(w, "w", dev, _F32, (T, K))
+    ldres = H if residual is None else _rows(residual, "residual", dev, dt, T, H)
+    if out is None:
+        ldo = H
+        out = torch.empty((T, H), dtype=dt, device=rows.device)
+    else:
+        ldo = _rows(out, "out", dev, dt, T, H)
+    _call(N.load().moe_async_merge_rows, "merge_rows", dev, stream, _DT[dt], rows.data_ptr(), ldr, R, pos.data_ptr(),
+          None if w is None else w.data_ptr(), T, K, H, None if residual is None else residual.data_ptr(), ldres,
+          out.data_ptr(), ldo)
     return out
 
 
@@ -147,67 +148,61 @@ def merge_rows_backward(grad, rows, pos, w, out=None, stream=None):
     """Gradients of merge_rows: (grad_rows, grad_w) with grad_rows[pos[t, k]] = w[t, k] grad[t]
     ([R, H] or `out`; rows that no pair names are left as they were) and grad_w[t, k] =
     <rows[pos[t, k]], grad[t]> (fp32, 0 for a pair without a row).  The residual's is `grad`."""
-    _first(rows, "rows", _ROWS)
-    R, H = rows.shape
-    _matrix(rows, "rows", rows, (R, H), rows.dtype)
-    _need(pos.dim() == 2, "pos: expected [T, K]")
-    T, K = pos.shape
-    _vector(pos, "pos", rows, (T, K), torch.int32)
-    _vector(w, "w", rows, (T, K), torch.float32)
-    _matrix(grad, "grad", rows, (T, H), rows.dtype)
-    with _On(rows, stream) as s:
-        if out is None:
-            out = torch.empty((R, H), dtype=rows.dtype, device=rows.device)
-        else:
-            _matrix(out, "out", rows, (R, H), rows.dtype)
-        grad_w = torch.empty_like(w)
-        N.check(N.load().moe_async_merge_rows_backward(_DT[rows.dtype], _p(grad), _ld(grad), _p(rows), _ld(rows), R,
-                                                       _p(pos), _p(w), T, K, H, _p(out), _ld(out), _p(grad_w), s),
-                "merge_rows_backward")
+    dev, R, H, ldr = _leading(rows, "rows", _ROWS)
+    dt = rows.dtype
+    K = _pairs(pos, dev)
+    T = pos.shape[0]
+    _whole(w, "w", dev, _F32, (T, K))
+    ldg = _rows(grad, "grad", dev, dt, T, H)
+    if out is None:
+        ldo = H
+        out = torch.empty((R, H), dtype=dt, device=rows.device)
+    else:
+        ldo = _rows(out, "out", dev, dt, R, H)
+    grad_w = torch.empty_like(w)
+    _call(N.load().moe_async_merge_rows_backward, "merge_rows_backward", dev, stream, _DT[dt], grad.data_ptr(), ldg,
+          rows.data_ptr(), ldr, R, pos.data_ptr(), w.data_ptr(), T, K, H, out.data_ptr(), ldo, grad_w.data_ptr())
     return out, grad_w
 
 
 def route_backward(idx, w, grad_w, num_experts, stream=None):
     """Gradient of route's weights: idx int32 and w fp32 [T, K] as route returned them, grad_w
     fp32 [T, K] -> grad_logits fp32 [T, num_experts]."""
-    _first(w, "w", (torch.float32,))
-    T, K = w.shape
-    _vector(w, "w", w, (T, K), torch.float32)
-    _vector(idx, "idx", w, (T, K), torch.int32)
-    _vector(grad_w, "grad_w", w, (T, K), torch.float32)
-    _need(num_experts >= 1, "num_experts: expected at least 1")
-    with _On(w, stream) as s:
-        out = torch.empty((T, num_experts), dtype=torch.float32, device=w.device)
-        N.check(N.load().moe_async_route_backward(_p(idx), _p(w), _p(grad_w), T, num_experts, K, _p(out), s),
-                "route_backward")
+    dev, T, K, _ = _leading(w, "w", (_F32,))
+    _whole(w, "w", dev, _F32, (T, K))
+    _whole(idx, "idx", dev, _I32, (T, K))
+    _whole(grad_w, "grad_w", dev, _F32, (T, K))
+    if num_experts < 1:
+        _bad(f"num_experts: expected at least 1, got {num_experts}")
+    out = torch.empty((T, num_experts), dtype=_F32, device=w.device)
+    _call(N.load().moe_async_route_backward, "route_backward", dev, stream, idx.data_ptr(), w.data_ptr(),
+          grad_w.data_ptr(), T, num_experts, K, out.data_ptr())
     return out
 
 
 def _norm(x, residual, gain, eps, e4m3, out, out_h, stream):
-    _first(x, "x", _ROWS)
-    T, H = x.shape
-    _matrix(x, "x", x, (T, H), x.dtype)
-    if residual is not None:
-        _matrix(residual, "residual", x, (T, H), x.dtype)
+    dev, T, H, ldx = _leading(x, "x", _ROWS)
+    dt, d = x.dtype, x.device
     if gain is not None:
-        _vector(gain, "gain", x, (H,), torch.float32)
-    _need(residual is not None or out_h is None, "out_h: there is no sum without a residual")
-    dt = torch.float8_e4m3fn if e4m3 else x.dtype
-    with _On(x, stream) as s:
-        h = x
-        if residual is not None:
-            h = torch.empty((T, H), dtype=x.dtype, device=x.device) if out_h is None else out_h
-            if out_h is not None:
-                _matrix(out_h, "out_h", x, (T, H), x.dtype)
-        if out is None:
-            out = torch.empty((T, H), dtype=dt, device=x.device)
+        _whole(gain, "gain", dev, _F32, (H,))
+    h, ldr, ldh = x, H, H
+    if residual is not None:
+        ldr = _rows(residual, "residual", dev, dt, T, H)
+        if out_h is None:
+            h = torch.empty((T, H), dtype=dt, device=d)
         else:
-            _matrix(out, "out", x, (T, H), dt)
-        scale = torch.empty(T, dtype=torch.float32, device=x.device) if e4m3 else None
-        N.check(N.load().moe_async_add_rms_norm(_DT[x.dtype], _p(x), _ld(x), _p(residual),
-                                                H if residual is None else _ld(residual), _p(gain), eps, T, H,
-                                                None if residual is None else _p(h), _ld(h), _p(out), _ld(out),
-                                                _p(scale), s), "add_rms_norm")
+            h, ldh = out_h, _rows(out_h, "out_h", dev, dt, T, H)
+    elif out_h is not None:
+        _bad("out_h: there is no sum without a residual")
+    if out is None:
+        ldo = H
+        out = torch.empty((T, H), dtype=_E4M3 if e4m3 else dt, device=d)
+    else:
+        ldo = _rows(out, "out", dev, _E4M3 if e4m3 else dt, T, H)
+    scale = torch.empty(T, dtype=_F32, device=d) if e4m3 else None
+    _call(N.load().moe_async_add_rms_norm, "add_rms_norm", dev, stream, _DT[dt], x.data_ptr(), ldx,
+          None if residual is None else residual.data_ptr(), ldr, None if gain is None else gain.data_ptr(), eps, T, H,
+          None if residual is None else h.data_ptr(), ldh, out.data_ptr(), ldo, scale.data_ptr() if e4m3 else None)
     return out, scale, h
 
 
@@ -229,32 +224,29 @@ def add_rms_norm_backward(grad, h, gain=None, eps=1e-6, grad_h=None, out=None, s
     """Gradients of add_rms_norm at its h: (grad_x, grad_gain) from grad, the gradient of y, and
     grad_h, the gradient that arrives at h itself (or None).  grad_x is the gradient of x and of
     the residual alike; grad_gain is fp32 [H], None without a gain.  `out` may be `grad_h`."""
-    _first(h, "h", _ROWS)
-    T, H = h.shape
-    _matrix(h, "h", h, (T, H), h.dtype)
-    _matrix(grad, "grad", h, (T, H), h.dtype)
-    if grad_h is not None:
-        _matrix(grad_h, "grad_h", h, (T, H), h.dtype)
-    if gain is not None:
-        _vector(gain, "gain", h, (H,), torch.float32)
+    dev, T, H, ldh = _leading(h, "h", _ROWS)
+    dt, d = h.dtype, h.device
+    ldg = _rows(grad, "grad", dev, dt, T, H)
+    ldgh = H if grad_h is None else _rows(grad_h, "grad_h", dev, dt, T, H)
+    if out is None:
+        ldo = H
+        out = torch.empty((T, H), dtype=dt, device=d)
+    else:
+        ldo = _rows(out, "out", dev, dt, T, H)
     lib = N.load()
-    with _On(h, stream) as s:
-        if out is None:
-            out = torch.empty((T, H), dtype=h.dtype, device=h.device)
-        else:
-            _matrix(out, "out", h, (T, H), h.dtype)
-        grad_gain = ws = None
-        size = 0
-        if gain is not None:
-            grad_gain = torch.empty_like(gain)
-            size = lib.moe_async_add_rms_norm_backward_workspace(T, H)
-            ws = torch.empty(size, dtype=torch.uint8, device=h.device)
-            if stream is not None:
-                ws.record_stream(stream)
-        N.check(lib.moe_async_add_rms_norm_backward(_DT[h.dtype], _p(grad), _ld(grad), _p(h), _ld(h), _p(gain), eps, T,
-                                                    H, _p(grad_h), H if grad_h is None else _ld(grad_h), _p(out),
-                                                    _ld(out), _p(grad_gain), _p(ws), size, s),
-                "add_rms_norm_backward")
+    grad_gain = ws = None
+    size = 0
+    if gain is not None:
+        _whole(gain, "gain", dev, _F32, (H,))
+        grad_gain = torch.empty_like(gain)
+        size = lib.moe_async_add_rms_norm_backward_workspace(T, H)
+        ws = torch.empty(size, dtype=torch.uint8, device=d)
+        if stream is not None:
+            ws.record_stream(stream)             # freed below, while the call may still run there
+    _call(lib.moe_async_add_rms_norm_backward, "add_rms_norm_backward", dev, stream, _DT[dt], grad.data_ptr(), ldg,
+          h.data_ptr(), ldh, None if gain is None else gain.data_ptr(), eps, T, H,
+          None if grad_h is None else grad_h.data_ptr(), ldgh, out.data_ptr(), ldo,
+          None if gain is None else grad_gain.data_ptr(), None if ws is None else ws.data_ptr(), size)
     return out, grad_gain
 
 
@@ -269,43 +261,54 @@ def linear(x, weight, bias=None, act="none", mul=None, residual=None, offsets=No
     With offsets (int32 [G + 1], as sort_experts gives them) weight is [G, N, F], bias and w_scale
     are [G, N], and rows offsets[g]:offsets[g + 1] of x meet weight[g]; other rows of `out` are
     left as they were."""
-    _first(x, "x", (torch.bfloat16, torch.float8_e4m3fn))
-    T, F = x.shape
-    _matrix(x, "x", x, (T, F), x.dtype)
-    G = 0
+    dev, T, F, ldx = _leading(x, "x", (_BF16, _E4M3))
+    dt = x.dtype
+    G, po = 0, 0
     if offsets is None:
-        _need(weight.dim() == 2, f"weight: expected [N, {F}], got {tuple(weight.shape)}")
-        n, per = weight.shape[0], (weight.shape[0],)
-        _matrix(weight, "weight", x, (n, F), x.dtype)
-        ldw = _ld(weight)
+        if weight.dim() != 2:
+            _bad(f"weight: expected [N, {F}]", weight)
+        n = weight.shape[0]
+        per = (n,)
+        ldw = _rows(weight, "weight", dev, dt, n, F)
     else:
-        _need(weight.dim() == 3, f"weight: expected [G, N, {F}], got {tuple(weight.shape)}")
-        G, n = weight.shape[:2]
-        per = (G, n)
-        _vector(weight, "weight", x, (G, n, F), x.dtype)
-        _vector(offsets, "offsets", x, (G + 1,), torch.int32)
-        ldw = F
-    _need(act in N.ACTS, f"act: expected one of {tuple(N.ACTS)}, got {act!r}")
-    out_dtype = out_dtype if out_dtype is not None else out.dtype if out is not None else torch.bfloat16
-    _need(out_dtype in _ROWS, f"out_dtype: expected fp32 or bf16, got {out_dtype}")
+        if weight.dim() != 3:
+            _bad(f"weight: expected [G, N, {F}]", weight)
+        per = weight.shape[:2]
+        G, n = per
+        if G < 1:
+            _bad("weight: expected at least one group", weight)
+        _whole(weight, "weight", dev, dt, (G, n, F))
+        _whole(offsets, "offsets", dev, _I32, (G + 1,))
+        ldw, po = F, offsets.data_ptr()
+    code = N.ACTS.get(act)
+    if code is None:
+        _bad(f"act: expected one of {tuple(N.ACTS)}, got {act!r}")
+    if out_dtype is None:
+        out_dtype = _BF16 if out is None else out.dtype
+    if out_dtype not in _ROWS:
+        _bad(f"out_dtype: expected fp32 or bf16, got {out_dtype}")
+    psx = psw = pb = pm = pr = 0
+    ldm = ldr = ldo = n
+    if dt is _E4M3:
+        if x_scale is None or w_scale is None:
+            _bad("x_scale, w_scale: both are needed with e4m3")
+        _whole(x_scale, "x_scale", dev, _F32, (T,))
+        _whole(w_scale, "w_scale", dev, _F32, per)
+        psx, psw = x_scale.data_ptr(), w_scale.data_ptr()
+    elif x_scale is not None or w_scale is not None:
+        _bad("x_scale, w_scale: bf16 operands have none")
     if bias is not None:
-        _vector(bias, "bias", x, per, torch.float32)
-    e4m3 = x.dtype is torch.float8_e4m3fn
-    _need((x_scale is not None) == e4m3 and (w_scale is not None) == e4m3, "x_scale, w_scale: both with e4m3, none with bf16")
-    if e4m3:
-        _vector(x_scale, "x_scale", x, (T,), torch.float32)
-        _vector(w_scale, "w_scale", x, per, torch.float32)
+        _whole(bias, "bias", dev, _F32, per)
+        pb = bias.data_ptr()
     if mul is not None:
-        _matrix(mul, "mul", x, (T, n), out_dtype)
+        ldm, pm = _rows(mul, "mul", dev, out_dtype, T, n), mul.data_ptr()
     if residual is not None:
-        _matrix(residual, "residual", x, (T, n), out_dtype)
-    with _On(x, stream) as s:
-        if out is None:
-            out = torch.empty((T, n), dtype=out_dtype, device=x.device)
-        else:
-            _matrix(out, "out", x, (T, n), out_dtype)
-        args = N.LinearArgs(_DT[x.dtype], _DT[out_dtype], N.ACTS[act], T, F, n, G, _p(x), _p(weight), _p(bias),
-                            _p(x_scale), _p(w_scale), _p(mul), _p(residual), _p(offsets), _p(out), _ld(x), ldw,
-                            n if mul is None else _ld(mul), n if residual is None else _ld(residual), _ld(out))
-        N.check(N.load().moe_async_linear(ctypes.byref(args), s), "linear")
+        ldr, pr = _rows(residual, "residual", dev, out_dtype, T, n), residual.data_ptr()
+    if out is None:
+        out = torch.empty((T, n), dtype=out_dtype, device=x.device)
+    else:
+        ldo = _rows(out, "out", dev, out_dtype, T, n)
+    _call(N.load().moe_async_linear, "linear", dev, stream,
+          _LINEAR_ARGS.pack(_DT[dt], _DT[out_dtype], code, T, F, n, G, x.data_ptr(), weight.data_ptr(), pb, psx, psw, pm,
+                            pr, po, out.data_ptr(), ldx, ldw, ldm, ldr, ldo))
     return out
