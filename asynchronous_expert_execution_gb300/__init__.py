@@ -11,5 +11,5 @@ abstract's streamFFN).  The compute lives in ``libmoe_async.so`` (C ABI in
 from ._native import MoEError, load  # noqa: F401
 from .api import MoEAsync, Policy, host_writable, route  # noqa: F401
 from .ops import (add_rms_norm, add_rms_norm_backward, add_rms_norm_e4m3, linear, merge_rows,  # noqa: F401
-                  merge_rows_backward, route_backward, sort_experts, sort_rows, sort_rows_backward)
+                  merge_rows_backward, ops_sync, route_backward, sort_experts, sort_rows, sort_rows_backward)
 from .replay import LayerReplay  # noqa: F401

@@ -25,9 +25,9 @@ VARIANTS = {"release": (LIB, []), "debug": (LIB_DEBUG, ["-DMOE_DEBUG_BOUNDS=1"])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE]
-# The tcgen05 kernel must not spill: it holds an SM's whole register file, and a build of a
+# The tcgen05 kernels must not spill: one holds an SM's whole register file, and a build of a
 # variant that spilled faulted on the GPU.  ptxas turns a spill into a build error.
-FILE_FLAGS = {"moe_ffn_tc.cu": ["-Xptxas", "--warn-on-spills,--warning-as-error"]}
+FILE_FLAGS = {f: ["-Xptxas", "--warn-on-spills,--warning-as-error"] for f in ("moe_ffn_tc.cu", "moe_linear.cu")}
 
 
 def _nvcc():

@@ -4,16 +4,42 @@
 //
 // x [T, F] and w [N, F] (or [G, N, F]: rows offsets[g] .. offsets[g + 1] of x meet w[g]) in bf16 or
 // e4m3, products summed in fp32, y in bf16 or fp32, rounded once.
+//
+// Weights are the MMA's 128 (or, over two SMs, 256) rows and tokens its columns, so one token and
+// thousands run on the same tiles: D[feature, token], both operands K-major as they lie in
+// memory, tiles of 128 bytes of K by TMA, accumulators in TMEM.  A thread of the epilogue owns a
+// feature (TMEM lane): bias and scale are one register, and a warp's stores cover 32 adjacent
+// features of a token.
+//
+// Two kernels, chosen by linear_launch:
+//   pair   persistent, tiles of 256 features x up to 256 tokens over two SMs (cta_group::2): each
+//          SM stages half of both operands, which halves the shared-memory traffic per product.
+//   split  one tile of 128 features x up to 128 tokens per cluster of up to 8 CTAs, K split over
+//          them; partials meet through distributed shared memory in rank order (no workspace,
+//          no atomics).  For few tiles: a lone SM streams weights far below the HBM rate.
+//
+// Every wait is bounded (2 s): a wait that runs out stops all roles, latches MOE_ERR_TIMEOUT in
+// the operators' error word, and the CTA still frees its TMEM.
 #include <cuda_fp8.h>
+#include <cudaTypedefs.h>
 #include <algorithm>
 #include "moe_ops.cuh"
+#include "moe_ptx.cuh"
 
 namespace moe {
 namespace {
 
+using namespace ptx;
+
+__device__ unsigned int g_ops_error;
+
+constexpr int kBM = 128;                           // weight rows per CTA
+constexpr int kBKBytes = 128;                      // K of a k-block (one swizzle atom)
+constexpr int kABlock = kBM * kBKBytes;            // 16 KB
+constexpr int kThreads = 256;                      // warps: TMA, MMA, TMEM, spare, 4 x epilogue
+constexpr unsigned long long kLimitNs = 2000000000ull;
+
 struct LinearParams {
-  const void* x;
-  const void* w;
   const float* bias;
   const float* sx;
   const float* sw;
@@ -21,9 +47,24 @@ struct LinearParams {
   const void* res;
   void* y;
   const int32_t* offsets;
-  int64_t ldx, ldw, ldmul, ldres, ldy;
-  int T, N, F, G, act;
+  int64_t ldmul, ldres, ldy;
+  int T, N, F, G, act, nk;
 };
+
+// Bounded wait; false once it ran out or another role gave up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try(bar, parity)) return true;
+  const unsigned long long t0 = now_ns();
+  while (true) {
+    if (mbar_try(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (now_ns() - t0 > kLimitNs) {
+      *abort_flag = 1;
+      atomicCAS(&g_ops_error, 0u, (unsigned)MOE_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
 
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
@@ -34,61 +75,471 @@ __device__ __forceinline__ float activate(float v, int act) {
   }
 }
 
-__device__ __forceinline__ float operand(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
-__device__ __forceinline__ float operand(const __nv_fp8_e4m3* p, int64_t i) { return float(p[i]); }
-
-constexpr int kTile = 32;
-
-// 32 x 32 outputs a block, one a thread, operands staged in shared memory as fp32.
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(1024) linear_kernel(LinearParams p) {
-  __shared__ float xs[kTile][kTile + 1], ws[kTile][kTile + 1];
-  ops_begin();
-  int g = 0, r0 = blockIdx.y * kTile, r1 = p.T;
-  if (p.offsets) {
-    int tile = blockIdx.y;
-    for (; g < p.G; ++g) {
-      const int a = min(p.T, max(0, p.offsets[g])), b = min(p.T, max(a, p.offsets[g + 1]));
-      const int n = (b - a + kTile - 1) / kTile;
-      if (tile < n) {
-        r0 = a + tile * kTile;
-        r1 = b;
-        break;
-      }
-      tile -= n;
-    }
-    if (g == p.G) return;
-  }
-  const TI* x = static_cast<const TI*>(p.x);
-  const TI* w = static_cast<const TI*>(p.w) + (size_t)g * p.N * p.ldw;
-  const int n0 = blockIdx.x * kTile, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  float acc = 0.f;
-  for (int k0 = 0; k0 < p.F; k0 += kTile) {
-    const int k = k0 + tx;
-    xs[ty][tx] = r0 + ty < r1 && k < p.F ? operand(x, (r0 + ty) * p.ldx + k) : 0.f;
-    ws[ty][tx] = n0 + ty < p.N && k < p.F ? operand(w, (int64_t)(n0 + ty) * p.ldw + k) : 0.f;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kTile; ++j) acc = fmaf(xs[ty][j], ws[tx][j], acc);
-    __syncthreads();
-  }
-  const long long r = r0 + ty;
-  const int n = n0 + tx;
-  if (r >= r1 || n >= p.N) return;
-  if (p.sx) acc = acc * p.sx[r] * p.sw[(size_t)g * p.N + n];
-  if (p.bias) acc += p.bias[(size_t)g * p.N + n];
-  acc = activate(acc, p.act);
-  if (p.mul) acc *= to_f(static_cast<const TO*>(p.mul)[r * p.ldmul + n]);
-  if (p.res) acc += to_f(static_cast<const TO*>(p.res)[r * p.ldres + n]);
-  static_cast<TO*>(p.y)[r * p.ldy + n] = from_f<TO>(acc);
+// Rows [a, b) of group g, clipped to the rows there are.
+struct Span {
+  int a, n;
+};
+__device__ __forceinline__ Span group_rows(const LinearParams& p, int g) {
+  if (!p.offsets) return {0, p.T};
+  const int a = min(p.T, max(0, __ldg(p.offsets + g))), b = min(p.T, max(a, __ldg(p.offsets + g + 1)));
+  return {a, b - a};
 }
 
-template <typename TI>
-moe_status linear_launch(const LinearParams& p, int32_t out_dtype, void* s) {
-  const int tiles = p.T / kTile + (p.offsets ? p.G : 1);         // at least one per row tile of every group
-  const dim3 grid((p.N + kTile - 1) / kTile, tiles);
-  return out_dtype == MOE_BF16 ? launch_op(linear_kernel<TI, __nv_bfloat16>, grid, 1024, 0, 1, s, p)
-                               : launch_op(linear_kernel<TI, float>, grid, 1024, 0, 1, s, p);
+// The epilogue of one thread: feature f of columns (tokens) [0, nj) at row r0, accumulators in v.
+template <typename TO>
+struct Finish {
+  const LinearParams& p;
+  long long r0;
+  int f;
+  bool live;
+  float sw, bias;
+  __device__ Finish(const LinearParams& q, int g, long long row0, int feature)
+      : p(q), r0(row0), f(feature), live(feature < q.N), sw(1.f), bias(0.f) {
+    if (live && q.sw) sw = __ldg(q.sw + (size_t)g * q.N + f);
+    if (live && q.bias) bias = __ldg(q.bias + (size_t)g * q.N + f);
+  }
+  template <int C>
+  __device__ __forceinline__ void operator()(const float (&v)[C], int j0, int nj) const {
+    if (!live) return;
+    const TO* mul = static_cast<const TO*>(p.mul);
+    const TO* res = static_cast<const TO*>(p.res);
+    TO* y = static_cast<TO*>(p.y);
+    float m[C], e[C], s[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const long long r = r0 + j0 + j;
+      const bool on = j0 + j < nj;
+      s[j] = p.sx && on ? __ldg(p.sx + r) * sw : 1.f;
+      m[j] = mul && on ? to_f(mul[r * p.ldmul + f]) : 1.f;
+      e[j] = res && on ? to_f(res[r * p.ldres + f]) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      if (j0 + j < nj) {
+        float a = v[j];
+        if (p.sx) a *= s[j];
+        a = activate(a + bias, p.act);
+        if (mul) a *= m[j];
+        if (res) a += e[j];
+        y[(r0 + j0 + j) * p.ldy + f] = from_f<TO>(a);
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ split kernel
+
+struct SplitParams {
+  CUtensorMap w, x;                 // x: boxes of bn rows
+  LinearParams l;
+  int bn, stages, splits, nft;      // tokens a tile, ring depth, CTAs a cluster, feature tiles
+};
+
+struct SplitTail {                  // behind the stages
+  static constexpr int kMaxStages = 12;
+  uint64_t full[kMaxStages], empty[kMaxStages], done;
+  uint32_t tmem;
+  int abort_flag;
+  int g, row0, nj, fti;             // this cluster's tile; nj = 0: none
+};
+
+template <bool E4M3, typename TO>
+__global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_constant__ SplitParams p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = kABlock + p.bn * kBKBytes;
+  SplitTail* s = reinterpret_cast<SplitTail*>(smem + p.stages * stage_bytes);
+  volatile int* abort_flag = &s->abort_flag;
+  const LinearParams& l = p.l;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.splits > 1 ? (int)cluster_rank() : 0;
+  const int tile = blockIdx.x / p.splits;
+  const uint32_t cols = max(32, p.bn);
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&p.w);
+    prefetch_map(&p.x);
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&s->full[i], 1);
+      mbar_init(&s->empty[i], 1);
+    }
+    mbar_init(&s->done, 1);
+    s->abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 2) tmem_alloc<1>(&s->tmem, cols);
+  ops_begin();
+  if (warp == 3) {                                   // token tile tile / nft of the groups' tiles
+    const int want = tile / p.nft;
+    int seen = 0, g = -1, row0 = 0, nj = 0;
+    for (int g0 = 0; g0 < l.G && g < 0; g0 += 32) {
+      const Span sp = g0 + lane < l.G ? group_rows(l, g0 + lane) : Span{0, 0};
+      const int nt = (sp.n + p.bn - 1) / p.bn;
+      int incl = nt;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, seen + incl > want);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        const int t = want - seen - __shfl_sync(0xffffffffu, incl - nt, src);
+        const int n = __shfl_sync(0xffffffffu, sp.n, src);
+        g = g0 + src;
+        row0 = __shfl_sync(0xffffffffu, sp.a, src) + t * p.bn;
+        nj = min(p.bn, n - t * p.bn);
+      }
+      seen += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      s->g = g;
+      s->row0 = row0;
+      s->nj = nj;
+      s->fti = tile % p.nft;
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = s->tmem;
+  const int nj = s->nj, g = s->g, row0 = s->row0, fti = s->fti;
+  const int kb0 = (int)((long long)l.nk * rank / p.splits), kb1 = (int)((long long)l.nk * (rank + 1) / p.splits);
+  constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
+
+  if (nj > 0 && warp == 0 && lane == 0) {
+    for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+      const int st = it % p.stages;
+      if (!wait(&s->empty[st], ((it / p.stages) & 1) ^ 1, abort_flag)) break;
+      const uint32_t a = smem_u32(smem + st * stage_bytes);
+      mbar_expect(&s->full[st], stage_bytes);
+      tma_3d<1>(a, &p.w, smem_u32(&s->full[st]), kb * kElems, fti * kBM, g);
+      tma_2d<1>(a + kABlock, &p.x, smem_u32(&s->full[st]), kb * kElems, row0);
+    }
+  } else if (nj > 0 && warp == 1 && lane == 0) {
+    const uint32_t idesc = mma_desc<E4M3>(kBM, p.bn);
+    bool ok = true;
+    for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+      const int st = it % p.stages;
+      if (!(ok = wait(&s->full[st], (it / p.stages) & 1, abort_flag))) break;
+      tc_after();
+      const uint32_t a = smem_u32(smem + st * stage_bytes);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma<1, E4M3>(tmem, operand_desc(a + 32 * k), operand_desc(a + kABlock + 32 * k), idesc, kb > kb0 || k > 0);
+      commit<1>(&s->empty[st]);
+    }
+    if (ok) commit<1>(&s->done);
+  }
+  const int q = warp & 3, row = 32 * q + lane;       // TMEM lane of an epilogue thread
+  const Finish<TO> finish(l, max(g, 0), row0, fti * kBM + row);
+  if (nj > 0 && warp >= 4) {
+    const bool ok = wait(&s->done, 0, abort_flag);
+    __syncwarp();
+    tc_after();
+    if (ok) {
+      const uint32_t t = tmem + ((uint32_t)(32 * q) << 16);
+      float* part = reinterpret_cast<float*>(smem);  // [column][row]: the ring is idle by now
+      for (int c = 0; c < nj; c += 16) {
+        float v[16];
+        tmem_ld16(t + c, v);
+        if (p.splits == 1) {
+          finish(v, c, nj);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[(c + j) * kBM + row] = v[j];
+        }
+      }
+    }
+  }
+  if (p.splits > 1) {                                // every rank sums and finishes its share of the columns
+    __syncwarp();
+    cluster_sync();
+    if (nj > 0 && warp >= 4) {
+      const int j0 = nj * rank / p.splits, j1 = nj * (rank + 1) / p.splits;
+      const uint32_t mine = smem_u32(smem) + row * 4;
+      for (int c = j0; c < j1; c += 4) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < p.splits; ++r) {
+          const uint32_t from = mapa(mine, r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c + j < j1) v[j] += ld_cluster_f32(from + (c + j) * kBM * 4);
+        }
+        finish(v, c, j1);
+      }
+    }
+    __syncwarp();
+    cluster_sync();                                  // a rank's partials stay until all have read them
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 2) tmem_dealloc<1>(tmem, cols);
+}
+
+// ------------------------------------------------------------------ pair kernel
+
+constexpr int kPairTokens = 256;
+constexpr int kPairStages = 3;
+constexpr int kPairStage = 72 * 1024;                // 2 k-blocks of a full tile, up to 4 of a narrow one
+constexpr int kPairKpsMax = 4;
+
+struct PairParams {
+  CUtensorMap w, x[4];              // x: boxes of 16, 32, 64, 128 rows
+  LinearParams l;
+  int nft;                          // feature tiles of 256
+};
+
+struct PairTail {
+  uint64_t full[kPairStages], empty[kPairStages], tfull[2], tempty[2];
+  uint32_t tmem;
+  int abort_flag;
+  int base[kMaxExperts + 1];        // first tile of each group
+};
+
+struct PairTile {
+  int g, row0, nj, fti, nmma, box, kps;
+};
+
+__device__ __forceinline__ PairTile pair_tile(const PairParams& p, const int* base, int t) {
+  const LinearParams& l = p.l;
+  int lo = 0, hi = l.G - 1;                          // last group whose first tile is <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (base[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  const Span sp = group_rows(l, lo);
+  const int ntt = (sp.n + kPairTokens - 1) / kPairTokens;
+  // eight token tiles meet one feature tile before the next: what runs at one time shares operands in L2
+  int local = t - base[lo];
+  const int band = local / (8 * p.nft);
+  local -= band * 8 * p.nft;
+  const int width = min(8, ntt - 8 * band);
+  PairTile tl;
+  tl.g = lo;
+  tl.fti = local / width;
+  const int j0 = (8 * band + local % width) * kPairTokens;
+  tl.row0 = sp.a + j0;
+  tl.nj = min(kPairTokens, sp.n - j0);
+  tl.nmma = (tl.nj + 31) & ~31;
+  const int half = tl.nmma / 2;                      // token rows each CTA stages: a box that holds them
+  tl.box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+  tl.kps = min(kPairKpsMax, kPairStage / (kABlock + (16 << tl.box) * kBKBytes));
+  return tl;
+}
+
+template <bool E4M3, typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ PairParams p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  PairTail* s = reinterpret_cast<PairTail*>(smem + kPairStages * kPairStage);
+  volatile int* abort_flag = &s->abort_flag;
+  const LinearParams& l = p.l;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  constexpr uint32_t kCols = 2 * kPairTokens;
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&p.w);
+    prefetch_map(&p.x[3]);
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&s->full[i], 1);                     // the leader's producer, for both CTAs' bytes
+      mbar_init(&s->empty[i], 1);                    // the MMA's commit, in both CTAs
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s->tfull[b], 1);
+      mbar_init(&s->tempty[b], 8);                   // the epilogue warps of both CTAs, at the leader
+    }
+    s->abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 2) tmem_alloc<2>(&s->tmem, kCols);
+  ops_begin();
+  if (warp == 3) {
+    int seen = 0;
+    for (int g0 = 0; g0 < l.G; g0 += 32) {
+      const int n = g0 + lane < l.G ? group_rows(l, g0 + lane).n : 0;
+      const int nt = (n + kPairTokens - 1) / kPairTokens * p.nft;
+      int incl = nt;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      if (g0 + lane < l.G) s->base[g0 + lane] = seen + incl - nt;
+      seen += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) s->base[l.G] = seen;
+  }
+  tc_before();
+  __syncthreads();
+  cluster_sync();
+  tc_after();
+  const uint32_t tmem = s->tmem;
+  const int n_tiles = s->base[l.G], pairs = gridDim.x / 2;
+  constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
+
+  if (warp == 0 && lane == 0) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x / 2; t < n_tiles && ok; t += pairs) {
+      const PairTile tl = pair_tile(p, s->base, t);
+      const int brows = 16 << tl.box, block = kABlock + brows * kBKBytes;
+      const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
+      for (int kb = 0; kb < l.nk; kb += tl.kps, ++it) {
+        const int st = it % kPairStages, nv = min(tl.kps, l.nk - kb);
+        if (!(ok = wait(&s->empty[st], ((it / kPairStages) & 1) ^ 1, abort_flag))) break;
+        const uint32_t a = smem_u32(smem + st * kPairStage);
+        const uint32_t bar = mapa(smem_u32(&s->full[st]), 0);
+        if (rank == 0) mbar_expect(&s->full[st], 2 * nv * block);
+        for (int j = 0; j < nv; ++j) {
+          tma_3d<2>(a + j * block, &p.w, bar, (kb + j) * kElems, wrow, tl.g);
+          tma_2d<2>(a + j * block + kABlock, &p.x[tl.box], bar, (kb + j) * kElems, xrow);
+        }
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    uint32_t it = 0, acc = 0;
+    bool ok = true;
+    for (int t = blockIdx.x / 2; t < n_tiles && ok; t += pairs, ++acc) {
+      const PairTile tl = pair_tile(p, s->base, t);
+      const int block = kABlock + (16 << tl.box) * kBKBytes;
+      const uint32_t idesc = mma_desc<E4M3>(2 * kBM, tl.nmma);
+      const int buf = acc & 1;
+      if (!(ok = wait(&s->tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag))) break;
+      tc_after();
+      const uint32_t d = tmem + buf * kPairTokens;
+      for (int kb = 0; kb < l.nk; kb += tl.kps, ++it) {
+        const int st = it % kPairStages, nv = min(tl.kps, l.nk - kb);
+        if (!(ok = wait(&s->full[st], (it / kPairStages) & 1, abort_flag))) break;
+        tc_after();
+        const uint32_t a0 = smem_u32(smem + st * kPairStage);
+        for (int j = 0; j < nv; ++j) {
+          const uint32_t a = a0 + j * block;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma<2, E4M3>(d, operand_desc(a + 32 * k), operand_desc(a + kABlock + 32 * k), idesc, kb + j > 0 || k > 0);
+        }
+        commit<2>(&s->empty[st]);
+      }
+      if (ok) commit<2>(&s->tfull[buf]);
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, row = 32 * q + lane;
+    uint32_t acc = 0;
+    for (int t = blockIdx.x / 2; t < n_tiles; t += pairs, ++acc) {
+      const PairTile tl = pair_tile(p, s->base, t);
+      const int buf = acc & 1;
+      const bool ok = wait(&s->tfull[buf], (acc >> 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_after();
+      const Finish<TO> finish(l, tl.g, tl.row0, tl.fti * 2 * kBM + rank * kBM + row);
+      const uint32_t d = tmem + ((uint32_t)(32 * q) << 16) + buf * kPairTokens;
+      for (int c = 0; c < tl.nj; c += 16) {
+        float v[16];
+        tmem_ld16(d + c, v);
+        finish(v, c, tl.nj);
+      }
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&s->tempty[buf]), 0));
+    }
+  }
+  __syncwarp();
+  tc_before();
+  __syncthreads();
+  cluster_sync();                                    // neither CTA's shared memory goes while the other may use it
+  tc_after();
+  if (warp == 2) tmem_dealloc<2>(tmem, kCols);
+}
+
+// ------------------------------------------------------------------ host side
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// [groups][rows][width] elements of `size` bytes, boxes of 128 bytes x box_rows, 128-byte swizzle,
+// zeros outside.
+bool encode(CUtensorMap* m, const void* base, int size, int width, int rows, int64_t ld, int groups, int box_rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)groups};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * size, (cuuint64_t)ld * size * rows};
+  const cuuint32_t box[3] = {(cuuint32_t)(kBKBytes / size), (cuuint32_t)box_rows, 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return fn(m, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups > 0 ? 3 : 2,
+            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+template <bool E4M3, typename TO>
+moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, int sms, void* s) {
+  constexpr int kSmem = kPairStages * kPairStage + (int)sizeof(PairTail) + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  constexpr int size = E4M3 ? 1 : 2;
+  PairParams p;
+  p.l = l;
+  p.nft = (l.N + 2 * kBM - 1) / (2 * kBM);
+  if (!encode(&p.w, a->d_w, size, l.F, l.N, a->w_stride, l.G, kBM)) return MOE_ERR_CUDA;
+  for (int i = 0; i < 4; ++i)
+    if (!encode(&p.x[i], a->d_x, size, l.F, l.T, a->x_stride, 0, 16 << i)) return MOE_ERR_CUDA;
+  if (cudaFuncSetAttribute(linear_pair_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return launch_op(linear_pair_kernel<E4M3, TO>, dim3(sms / 2 * 2), kThreads, kSmem, 1, s, p);
+}
+
+template <bool E4M3, typename TO>
+moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, int bn, int splits, int64_t tiles, void* s) {
+  constexpr int size = E4M3 ? 1 : 2;
+  SplitParams p;
+  p.l = l;
+  p.bn = bn;
+  p.splits = splits;
+  p.nft = (l.N + kBM - 1) / kBM;
+  // about 100 KB a CTA, so that two fit an SM
+  const int stage = kABlock + bn * kBKBytes;
+  p.stages = std::min(SplitTail::kMaxStages, 108 * 1024 / stage);
+  const int smem = p.stages * stage + (int)sizeof(SplitTail) + 1024;
+  if (!encode(&p.w, a->d_w, size, l.F, l.N, a->w_stride, l.G, kBM) ||
+      !encode(&p.x, a->d_x, size, l.F, l.T, a->x_stride, 0, bn))
+    return MOE_ERR_CUDA;
+  if (cudaFuncSetAttribute(linear_split_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return launch_op(linear_split_kernel<E4M3, TO>, dim3((unsigned)(tiles * splits)), kThreads, smem, splits, s, p);
+}
+
+template <bool E4M3, typename TO>
+moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, void* s) {
+  const int sms = sm_count();
+  if (sms < 2) return MOE_ERR_CUDA;
+  // The pair kernel wants most of the pairs at work; below that, smaller tiles on every SM, and
+  // where those are few too, K split over a cluster.  Groups count at most one ragged tile each.
+  const int64_t wide = (int64_t)((l.N + 255) / 256) * (l.offsets ? l.T / 256 + std::min(l.G, l.T) : (l.T + 255) / 256);
+  if (wide >= sms / 2 * 3 / 4) return launch_pair<E4M3, TO>(a, l, sms, s);
+  const int64_t per = l.offsets ? (l.T + l.G - 1) / l.G : l.T;
+  const int bn = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
+  const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * (l.offsets ? l.T / bn + std::min(l.G, l.T) : (l.T + bn - 1) / bn);
+  int splits = (int)std::max<int64_t>(1, std::min<int64_t>(8, sms / tiles));
+  splits = std::min(splits, std::max(1, l.nk / 2));
+  return launch_split<E4M3, TO>(a, l, bn, splits, tiles, s);
 }
 
 }  // namespace
@@ -97,7 +548,7 @@ moe_status linear_launch(const LinearParams& p, int32_t out_dtype, void* s) {
 extern "C" moe_status moe_async_linear(const moe_async_linear_args* a, void* stream) {
   using namespace moe;
   if (!a) return MOE_ERR_INVALID;
-  if (a->rows < 0 || a->fan_in < 1 || a->fan_out < 1 || a->groups < 0 || a->groups > kMaxExperts ||
+  if (a->rows < 0 || a->rows > INT32_MAX - 1024 || a->fan_in < 1 || a->fan_out < 1 || a->groups < 0 || a->groups > kMaxExperts ||
       a->act < MOE_ACT_NONE || a->act > MOE_ACT_RELU || (a->groups > 0) != (a->d_offsets != nullptr) ||
       (a->out_dtype != MOE_F32 && a->out_dtype != MOE_BF16))
     return MOE_ERR_INVALID;
@@ -110,11 +561,25 @@ extern "C" moe_status moe_async_linear(const moe_async_linear_args* a, void* str
       (a->d_x_scale != nullptr) != e4m3 || (a->d_w_scale != nullptr) != e4m3)
     return MOE_ERR_INVALID;
   // the operands move in 16-byte units
-  if (a->fan_in * size % 16 || !rows16(a->d_x, a->x_stride, size) || !rows16(a->d_w, a->w_stride, size))
+  if ((int64_t)a->fan_in * size % 16 || !rows16(a->d_x, a->x_stride, size) || !rows16(a->d_w, a->w_stride, size))
     return MOE_ERR_UNSUPPORTED;
-  LinearParams p{a->d_x,      a->d_w,      a->d_bias,   a->d_x_scale,  a->d_w_scale,       a->d_mul,    a->d_residual,
-                 a->d_y,      a->d_offsets, a->x_stride, a->w_stride,  a->mul_stride,      a->residual_stride,
-                 a->y_stride, a->rows,     a->fan_out,  a->fan_in,     std::max(1, a->groups), a->act};
-  return e4m3 ? linear_launch<__nv_fp8_e4m3>(p, a->out_dtype, stream)
-              : linear_launch<__nv_bfloat16>(p, a->out_dtype, stream);
+  const LinearParams l{a->d_bias,   a->d_x_scale,  a->d_w_scale,       a->d_mul,
+                       a->d_residual, a->d_y,      a->d_offsets,       a->mul_stride,
+                       a->residual_stride, a->y_stride, a->rows,       a->fan_out,
+                       a->fan_in,   std::max(1, a->groups), a->act,    (a->fan_in * size + kBKBytes - 1) / kBKBytes};
+  if (e4m3)
+    return a->out_dtype == MOE_BF16 ? linear_launch<true, __nv_bfloat16>(a, l, stream)
+                                    : linear_launch<true, float>(a, l, stream);
+  return a->out_dtype == MOE_BF16 ? linear_launch<false, __nv_bfloat16>(a, l, stream)
+                                  : linear_launch<false, float>(a, l, stream);
+}
+
+extern "C" moe_status moe_async_ops_status(void* stream) {
+  using namespace moe;
+  unsigned int e = 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaMemcpyFromSymbolAsync(&e, g_ops_error, sizeof(e), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return static_cast<moe_status>(e);
 }

@@ -312,3 +312,10 @@ def linear(x, weight, bias=None, act="none", mul=None, residual=None, offsets=No
           _LINEAR_ARGS.pack(_DT[dt], _DT[out_dtype], code, T, F, n, G, x.data_ptr(), weight.data_ptr(), pb, psx, psw, pm,
                             pr, po, out.data_ptr(), ldx, ldw, ldm, ldr, ldo))
     return out
+
+
+def ops_sync(device=None, stream=None):
+    """Wait for `stream` (default: the device's current one) and raise MoEError if a stateless
+    operator found an error on the device (a wait in linear that exceeded its bound)."""
+    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+    _call(N.load().moe_async_ops_status, "ops_sync", dev, stream)

@@ -516,6 +516,11 @@ typedef struct {
 } moe_async_linear_args;
 moe_status moe_async_linear(const moe_async_linear_args* args, void* stream);
 
+/* Synchronise `stream` and return the sticky error of the stateless operators on the current
+ * device: MOE_OK, or MOE_ERR_TIMEOUT once a device wait in moe_async_linear exceeded its 2 s
+ * bound (that call's output is then undefined). */
+moe_status moe_async_ops_status(void* stream);
+
 /* Bounds-checked build (libmoe_async_debug.so, compiled with MOE_DEBUG_BOUNDS): every bucket,
  * slot and k index the kernels read back from device state is checked before use, and an
  * index out of range latches MOE_ERR_BOUNDS (the access is skipped, the scheduler halts).  This

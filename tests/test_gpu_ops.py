@@ -589,6 +589,11 @@ def test_given_stream_is_used(moe):
     assert bool(((y.float() - 1).abs() < 1e-2).all()) and bool((gg > 0).all())
 
 
+def test_no_wait_ran_out(moe):
+    """After everything above: the operators' sticky device error is clear."""
+    moe.ops_sync()
+
+
 # ------------------------------------------------------------------ refusals (nothing is launched)
 
 def test_refusals(moe):
