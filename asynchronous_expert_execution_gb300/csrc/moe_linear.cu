@@ -7,9 +7,11 @@
 //
 // Weights are the MMA's 128 (or, over two SMs, 256) rows and tokens its columns, so one token and
 // thousands run on the same tiles: D[feature, token], both operands K-major as they lie in
-// memory, tiles of 128 bytes of K by TMA, accumulators in TMEM.  A thread of the epilogue owns a
-// feature (TMEM lane): bias and scale are one register, and a warp's stores cover 32 adjacent
-// features of a token.
+// memory, tiles of 128 bytes of K by TMA, accumulators in TMEM.  The epilogue passes through
+// shared memory as [token][feature]: a thread of a TMEM lane writes its feature's column there,
+// and reads back 8 adjacent features of one token, so rows move in 16-byte units (storing from
+// the lanes directly, 2 bytes a thread, cost 67,000 cycles a 128 x 256 tile, twice the products
+// of a 7168-deep e4m3 tile).
 //
 // Two kernels, chosen by linear_launch:
 //   pair   persistent, tiles of 256 features x up to 256 tokens over two SMs (cta_group::2): each
@@ -49,6 +51,7 @@ struct LinearParams {
   const int32_t* offsets;
   int64_t ldmul, ldres, ldy;
   int T, N, F, G, act, nk;
+  bool wide;                        // y, mul and residual: 16-byte units
 };
 
 // Bounded wait; false once it ran out or another role gave up.
@@ -66,13 +69,19 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case MOE_ACT_SILU: return v / (1.0f + expf(-v));
-    case MOE_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678f));
-    case MOE_ACT_RELU: return v < 0.f ? 0.f : v;     // NaN stays
-    default: return v;
-  }
+// The 128 threads of an epilogue group.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_all(bool pred, int id) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"((uint32_t)pred), "r"(id)
+      : "memory");
+  return out != 0;
 }
 
 // Rows [a, b) of group g, clipped to the rows there are.
@@ -85,44 +94,111 @@ __device__ __forceinline__ Span group_rows(const LinearParams& p, int g) {
   return {a, b - a};
 }
 
-// The epilogue of one thread: feature f of columns (tokens) [0, nj) at row r0, accumulators in v.
+// The epilogue of a tile of 128 features (from f0) in group g, token-major.  `wide`: rows of y,
+// mul and residual move in 16-byte units, a thread owns 8 adjacent features; else a lane owns
+// every 32nd feature, element by element.
 template <typename TO>
 struct Finish {
   const LinearParams& p;
-  long long r0;
-  int f;
-  bool live;
-  float sw, bias;
-  __device__ Finish(const LinearParams& q, int g, long long row0, int feature)
-      : p(q), r0(row0), f(feature), live(feature < q.N), sw(1.f), bias(0.f) {
-    if (live && q.sw) sw = __ldg(q.sw + (size_t)g * q.N + f);
-    if (live && q.bias) bias = __ldg(q.bias + (size_t)g * q.N + f);
+  int f0, n;                        // first feature, features of the tile that exist
+  bool wide;
+  float sw[8], bias[8];
+
+  static constexpr int kUnit = 8;
+  static constexpr int kUnitsPerToken = kBM / kUnit;
+
+  __device__ __forceinline__ int feature(int i) const {       // i-th feature of this thread, within the tile
+    return wide ? (threadIdx.x % kUnitsPerToken) * kUnit + i : (int)(threadIdx.x & 31) + 32 * i;
   }
-  template <int C>
-  __device__ __forceinline__ void operator()(const float (&v)[C], int j0, int nj) const {
-    if (!live) return;
-    const TO* mul = static_cast<const TO*>(p.mul);
-    const TO* res = static_cast<const TO*>(p.res);
-    TO* y = static_cast<TO*>(p.y);
-    float m[C], e[C], s[C];
+  __device__ Finish(const LinearParams& q, int g, int feature0) : p(q), f0(feature0), wide(q.wide) {
+    n = min(kBM, q.N - f0);
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const long long r = r0 + j0 + j;
-      const bool on = j0 + j < nj;
-      s[j] = p.sx && on ? __ldg(p.sx + r) * sw : 1.f;
-      m[j] = mul && on ? to_f(mul[r * p.ldmul + f]) : 1.f;
-      e[j] = res && on ? to_f(res[r * p.ldres + f]) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      const int f = feature(i);
+      const bool on = (wide || i < 4) && f < n;
+      sw[i] = q.sw && on ? __ldg(q.sw + (size_t)g * q.N + f0 + f) : 1.f;
+      bias[i] = q.bias && on ? __ldg(q.bias + (size_t)g * q.N + f0 + f) : 0.f;
+    }
+  }
+  // sums -> act(scaled sum + bias); sx: the token's scale
+  template <int C>
+  __device__ __forceinline__ void head(float (&v)[C], float sx) const {
+    if (p.sx) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] *= sx * sw[i];
     }
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      if (j0 + j < nj) {
-        float a = v[j];
-        if (p.sx) a *= s[j];
-        a = activate(a + bias, p.act);
-        if (mul) a *= m[j];
-        if (res) a += e[j];
-        y[(r0 + j0 + j) * p.ldy + f] = from_f<TO>(a);
+    for (int i = 0; i < C; ++i) v[i] += bias[i];
+    if (p.act == MOE_ACT_SILU) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = v[i] / (1.0f + expf(-v[i]));
+    } else if (p.act == MOE_ACT_GELU) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678f));
+    } else if (p.act == MOE_ACT_RELU) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays
+    }
+  }
+  // what the wide path reads of mul and residual for a token, ahead of use
+  struct Ahead {
+    uint4 m[sizeof(TO) / 2], e[sizeof(TO) / 2];
+    float sx;
+  };
+  __device__ __forceinline__ void ahead(Ahead& a, long long r, bool on) const {
+    const bool use = on && feature(0) < n;
+    const int64_t f = f0 + feature(0);
+    a.sx = p.sx && on ? __ldg(p.sx + r) : 1.f;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(TO) / 2; ++i) {
+      if (p.mul && use)
+        a.m[i] = *reinterpret_cast<const uint4*>(static_cast<const TO*>(p.mul) + r * p.ldmul + f + i * Vec<TO>::N);
+      if (p.res && use)
+        a.e[i] = *reinterpret_cast<const uint4*>(static_cast<const TO*>(p.res) + r * p.ldres + f + i * Vec<TO>::N);
+    }
+  }
+  __device__ __forceinline__ void unit(float (&v)[8], long long r, const Ahead& a) const {
+    constexpr int N = Vec<TO>::N;
+    if (feature(0) >= n) return;                     // wide: N is a whole number of units
+    head(v, a.sx);
+    TO* y = static_cast<TO*>(p.y) + r * p.ldy + f0 + feature(0);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(TO) / 2; ++i) {
+      float o[N], t[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = v[i * N + j];
+      if (p.mul) {
+        unpack16<TO>(a.m[i], t);
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] *= t[j];
       }
+      if (p.res) {
+        unpack16<TO>(a.e[i], t);
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] += t[j];
+      }
+      *reinterpret_cast<uint4*>(y + i * N) = pack16<TO>(o);
+    }
+  }
+  // one token by one warp, lane-strided features
+  __device__ __forceinline__ void token(float (&v)[4], long long r) const {
+    const TO* mul = static_cast<const TO*>(p.mul) + r * p.ldmul + f0;
+    const TO* res = static_cast<const TO*>(p.res) + r * p.ldres + f0;
+    TO* y = static_cast<TO*>(p.y) + r * p.ldy + f0;
+    float m[4], e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int f = feature(i);
+      m[i] = p.mul && f < n ? to_f(mul[f]) : 1.f;
+      e[i] = p.res && f < n ? to_f(res[f]) : 0.f;
+    }
+    head(v, p.sx ? __ldg(p.sx + r) : 1.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int f = feature(i);
+      if (p.mul) v[i] *= m[i];
+      if (p.res) v[i] += e[i];
+      if (f < n) y[f] = from_f<TO>(v[i]);
     }
   }
 };
@@ -144,7 +220,7 @@ struct SplitTail {                  // behind the stages
 };
 
 template <bool E4M3, typename TO>
-__global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_constant__ SplitParams p) {
+__global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_constant__ SplitParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int stage_bytes = kABlock + p.bn * kBKBytes;
@@ -231,44 +307,59 @@ __global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_con
     }
     if (ok) commit<1>(&s->done);
   }
-  const int q = warp & 3, row = 32 * q + lane;       // TMEM lane of an epilogue thread
-  const Finish<TO> finish(l, max(g, 0), row0, fti * kBM + row);
+  float* part = reinterpret_cast<float*>(smem);      // [token][feature]: the ring is idle by then
   if (nj > 0 && warp >= 4) {
+    const int q = warp & 3, row = 32 * q + lane;     // TMEM lane: a feature
     const bool ok = wait(&s->done, 0, abort_flag);
     __syncwarp();
     tc_after();
     if (ok) {
       const uint32_t t = tmem + ((uint32_t)(32 * q) << 16);
-      float* part = reinterpret_cast<float*>(smem);  // [column][row]: the ring is idle by now
       for (int c = 0; c < nj; c += 16) {
         float v[16];
         tmem_ld16(t + c, v);
-        if (p.splits == 1) {
-          finish(v, c, nj);
-        } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) part[(c + j) * kBM + row] = v[j];
-        }
+        for (int j = 0; j < 16; ++j) part[(c + j) * kBM + row] = v[j];
       }
     }
   }
-  if (p.splits > 1) {                                // every rank sums and finishes its share of the columns
-    __syncwarp();
-    cluster_sync();
-    if (nj > 0 && warp >= 4) {
+  __syncwarp();
+  if (p.splits > 1) cluster_sync(); else __syncthreads();
+  if (nj > 0) {                                      // every rank sums and finishes its share of the tile
+    const Finish<TO> finish(l, g, fti * kBM);
+    if (l.wide) {
+      const int units = nj * Finish<TO>::kUnitsPerToken;
+      const int u0 = (int)((long long)units / 16 * rank / p.splits) * 16;
+      const int u1 = (int)((long long)units / 16 * (rank + 1) / p.splits) * 16;
+      for (int u = u0 + threadIdx.x; u < u1; u += kThreads) {
+        const int j = u / Finish<TO>::kUnitsPerToken;
+        typename Finish<TO>::Ahead a;
+        finish.ahead(a, row0 + j, true);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const uint32_t mine = smem_u32(part + j * kBM + finish.feature(0));
+        for (int r = 0; r < p.splits; ++r) {
+          const uint32_t from = mapa(mine, r);
+          const float4 x = ld_cluster_v4(from), y = ld_cluster_v4(from + 16);
+          v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+          v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+        }
+        finish.unit(v, row0 + j, a);
+      }
+    } else {
       const int j0 = nj * rank / p.splits, j1 = nj * (rank + 1) / p.splits;
-      const uint32_t mine = smem_u32(smem) + row * 4;
-      for (int c = j0; c < j1; c += 4) {
+      for (int j = j0 + warp; j < j1; j += kThreads / 32) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t mine = smem_u32(part + j * kBM + lane);
         for (int r = 0; r < p.splits; ++r) {
           const uint32_t from = mapa(mine, r);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (c + j < j1) v[j] += ld_cluster_f32(from + (c + j) * kBM * 4);
+          for (int i = 0; i < 4; ++i) v[i] += ld_cluster_f32(from + 128 * i);
         }
-        finish(v, c, j1);
+        finish.token(v, row0 + j);
       }
     }
+  }
+  if (p.splits > 1) {
     __syncwarp();
     cluster_sync();                                  // a rank's partials stay until all have read them
   }
@@ -282,8 +373,11 @@ __global__ void __launch_bounds__(kThreads) linear_split_kernel(const __grid_con
 
 constexpr int kPairTokens = 256;
 constexpr int kPairStages = 3;
-constexpr int kPairStage = 72 * 1024;                // 2 k-blocks of a full tile, up to 4 of a narrow one
-constexpr int kPairKpsMax = 4;
+constexpr int kPairStage = 64 * 1024;                // 2 k-blocks of a full tile, 3 of a narrow one
+constexpr int kPairKpsMax = 3;
+constexpr int kPairThreads = 384;                    // warps: TMA, MMA, TMEM, spare, 2 x 4 epilogue
+constexpr int kChunk = 16;                           // tokens an epilogue group takes at a time
+constexpr int kStaging = kChunk * kBM * 4;
 
 struct PairParams {
   CUtensorMap w, x[4];              // x: boxes of 16, 32, 64, 128 rows
@@ -330,11 +424,11 @@ __device__ __forceinline__ PairTile pair_tile(const PairParams& p, const int* ba
 }
 
 template <bool E4M3, typename TO>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  PairTail* s = reinterpret_cast<PairTail*>(smem + kPairStages * kPairStage);
+  PairTail* s = reinterpret_cast<PairTail*>(smem + kPairStages * kPairStage + 2 * kStaging);
   volatile int* abort_flag = &s->abort_flag;
   const LinearParams& l = p.l;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -350,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s->tfull[b], 1);
-      mbar_init(&s->tempty[b], 8);                   // the epilogue warps of both CTAs, at the leader
+      mbar_init(&s->tempty[b], 16);                  // the epilogue warps of both CTAs, at the leader
     }
     s->abort_flag = 0;
     mbar_init_fence();
@@ -427,20 +521,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok) commit<2>(&s->tfull[buf]);
     }
   } else if (warp >= 4) {
-    const int q = warp & 3, row = 32 * q + lane;
+    const int q = warp & 3, row = 32 * q + lane, grp = (warp >> 2) - 1, et = threadIdx.x & 127;
+    float* stage = reinterpret_cast<float*>(smem + kPairStages * kPairStage + grp * kStaging);   // [token][feature]
     uint32_t acc = 0;
     for (int t = blockIdx.x / 2; t < n_tiles; t += pairs, ++acc) {
       const PairTile tl = pair_tile(p, s->base, t);
       const int buf = acc & 1;
+      const Finish<TO> finish(l, tl.g, tl.fti * 2 * kBM + rank * kBM);
       const bool ok = wait(&s->tfull[buf], (acc >> 1) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!group_all(ok, 1 + grp)) break;
       tc_after();
-      const Finish<TO> finish(l, tl.g, tl.row0, tl.fti * 2 * kBM + rank * kBM + row);
       const uint32_t d = tmem + ((uint32_t)(32 * q) << 16) + buf * kPairTokens;
-      for (int c = 0; c < tl.nj; c += 16) {
+      for (int c = grp * kChunk; c < tl.nj; c += 2 * kChunk) {
+        constexpr int kUnits = kChunk * Finish<TO>::kUnitsPerToken / 128;
+        typename Finish<TO>::Ahead a[kUnits];
+        if (l.wide) {
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const int j = c + (et + 128 * i) / Finish<TO>::kUnitsPerToken;
+            finish.ahead(a[i], tl.row0 + j, j < tl.nj);
+          }
+        }
         float v[16];
         tmem_ld16(d + c, v);
-        finish(v, c, tl.nj);
+        group_sync(1 + grp);                         // the chunk before has been read
+#pragma unroll
+        for (int j = 0; j < 16; ++j) stage[j * kBM + row] = v[j];
+        group_sync(1 + grp);
+        if (l.wide) {
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const int j = (et + 128 * i) / Finish<TO>::kUnitsPerToken;
+            if (c + j < tl.nj) {
+              float u[8];
+              const float4* from = reinterpret_cast<const float4*>(stage + j * kBM + finish.feature(0));
+              const float4 x = from[0], y = from[1];
+              u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w, u[4] = y.x, u[5] = y.y, u[6] = y.z, u[7] = y.w;
+              finish.unit(u, tl.row0 + c + j, a[i]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kChunk / 4; ++i) {
+            const int j = q + 4 * i;
+            if (c + j < tl.nj) {
+              float u[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) u[k] = stage[j * kBM + lane + 32 * k];
+              finish.token(u, tl.row0 + c + j);
+            }
+          }
+        }
       }
       tc_before();
       __syncwarp();
@@ -492,7 +623,7 @@ int sm_count() {
 
 template <bool E4M3, typename TO>
 moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, int sms, void* s) {
-  constexpr int kSmem = kPairStages * kPairStage + (int)sizeof(PairTail) + 1024;
+  constexpr int kSmem = kPairStages * kPairStage + 2 * kStaging + (int)sizeof(PairTail) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   constexpr int size = E4M3 ? 1 : 2;
   PairParams p;
@@ -503,7 +634,7 @@ moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, in
     if (!encode(&p.x[i], a->d_x, size, l.F, l.T, a->x_stride, 0, 16 << i)) return MOE_ERR_CUDA;
   if (cudaFuncSetAttribute(linear_pair_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return MOE_ERR_CUDA;
-  return launch_op(linear_pair_kernel<E4M3, TO>, dim3(sms / 2 * 2), kThreads, kSmem, 1, s, p);
+  return launch_op(linear_pair_kernel<E4M3, TO>, dim3(sms / 2 * 2), kPairThreads, kSmem, 1, s, p);
 }
 
 template <bool E4M3, typename TO>
@@ -563,10 +694,13 @@ extern "C" moe_status moe_async_linear(const moe_async_linear_args* a, void* str
   // the operands move in 16-byte units
   if ((int64_t)a->fan_in * size % 16 || !rows16(a->d_x, a->x_stride, size) || !rows16(a->d_w, a->w_stride, size))
     return MOE_ERR_UNSUPPORTED;
+  const int os = dtype_size(a->out_dtype);
+  const bool wide = a->fan_out % 8 == 0 && rows16(a->d_y, a->y_stride, os) && rows16(a->d_mul, a->mul_stride, os) &&
+                    rows16(a->d_residual, a->residual_stride, os);
   const LinearParams l{a->d_bias,   a->d_x_scale,  a->d_w_scale,       a->d_mul,
                        a->d_residual, a->d_y,      a->d_offsets,       a->mul_stride,
                        a->residual_stride, a->y_stride, a->rows,       a->fan_out,
-                       a->fan_in,   std::max(1, a->groups), a->act,    (a->fan_in * size + kBKBytes - 1) / kBKBytes};
+                       a->fan_in,   std::max(1, a->groups), a->act,    (int)(((int64_t)a->fan_in * size + kBKBytes - 1) / kBKBytes), wide};
   if (e4m3)
     return a->out_dtype == MOE_BF16 ? linear_launch<true, __nv_bfloat16>(a, l, stream)
                                     : linear_launch<true, float>(a, l, stream);
