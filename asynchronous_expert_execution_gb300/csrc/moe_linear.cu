@@ -11,7 +11,8 @@
 // shared memory as [token][feature]: a thread of a TMEM lane writes its feature's column there,
 // and reads back 8 adjacent features of one token, so rows move in 16-byte units (storing from
 // the lanes directly, 2 bytes a thread, cost 67,000 cycles a 128 x 256 tile, twice the products
-// of a 7168-deep e4m3 tile).
+// of a 7168-deep e4m3 tile; turning a whole tile's features at once, with two barriers of 128
+// threads per 16 tokens, 17,000).
 //
 // Two kernels, chosen by linear_launch:
 //   pair   persistent, tiles of 256 features x up to 256 tokens over two SMs (cta_group::2): each
@@ -69,21 +70,6 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
 }
 
-// The 128 threads of an epilogue group.
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool group_all(bool pred, int id) {
-  uint32_t out;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(out)
-      : "r"((uint32_t)pred), "r"(id)
-      : "memory");
-  return out != 0;
-}
-
 // Rows [a, b) of group g, clipped to the rows there are.
 struct Span {
   int a, n;
@@ -94,112 +80,97 @@ __device__ __forceinline__ Span group_rows(const LinearParams& p, int g) {
   return {a, b - a};
 }
 
-// The epilogue of a tile of 128 features (from f0) in group g, token-major.  `wide`: rows of y,
-// mul and residual move in 16-byte units, a thread owns 8 adjacent features; else a lane owns
-// every 32nd feature, element by element.
-template <typename TO>
+// The end of the epilogue for one thread, which owns C features of every token it meets: first,
+// first + step, ...  C = 8, step = 1: rows of y, mul and residual move in 16-byte units; else
+// element by element.  Pointers are to a token's row at feature `first`.
+template <typename TO, int C>
 struct Finish {
+  static constexpr bool kWide = C == 8;
+  static constexpr int kVecs = kWide ? C / Vec<TO>::N : C;
+  using RV = RowVec<TO, kWide ? Vec<TO>::N : 1>;
+  using Raw = typename RV::Raw;
   const LinearParams& p;
-  int f0, n;                        // first feature, features of the tile that exist
-  bool wide;
-  float sw[8], bias[8];
+  int step, live;                   // live: how many of the C features exist (wide: all or none)
+  float sw[C], bias[C];
 
-  static constexpr int kUnit = 8;
-  static constexpr int kUnitsPerToken = kBM / kUnit;
-
-  __device__ __forceinline__ int feature(int i) const {       // i-th feature of this thread, within the tile
-    return wide ? (threadIdx.x % kUnitsPerToken) * kUnit + i : (int)(threadIdx.x & 31) + 32 * i;
-  }
-  __device__ Finish(const LinearParams& q, int g, int feature0) : p(q), f0(feature0), wide(q.wide) {
-    n = min(kBM, q.N - f0);
+  __device__ Finish(const LinearParams& q, int g, int first, int step_) : p(q), step(step_) {
+    live = first >= q.N ? 0 : min(C, (q.N - first + step_ - 1) / step_);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int f = feature(i);
-      const bool on = (wide || i < 4) && f < n;
-      sw[i] = q.sw && on ? __ldg(q.sw + (size_t)g * q.N + f0 + f) : 1.f;
-      bias[i] = q.bias && on ? __ldg(q.bias + (size_t)g * q.N + f0 + f) : 0.f;
+    for (int i = 0; i < C; ++i) {
+      sw[i] = q.sw && i < live ? __ldg(q.sw + (size_t)g * q.N + first + i * step) : 1.f;
+      bias[i] = q.bias && i < live ? __ldg(q.bias + (size_t)g * q.N + first + i * step) : 0.f;
     }
   }
-  // sums -> act(scaled sum + bias); sx: the token's scale
-  template <int C>
-  __device__ __forceinline__ void head(float (&v)[C], float sx) const {
+  // what a token's epilogue reads, ahead of use
+  struct Ahead {
+    Raw m[kVecs], e[kVecs];
+    float sx;
+  };
+  __device__ __forceinline__ bool on(int i) const { return kWide ? live > 0 : i < live; }
+  __device__ __forceinline__ int at(int i) const { return kWide ? i * Vec<TO>::N : i * step; }
+  __device__ __forceinline__ void ahead(Ahead& a, const float* sx, const TO* mul, const TO* res, bool token) const {
+    a.sx = p.sx && token ? __ldg(sx) : 1.f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      if (p.mul && token && on(i)) a.m[i] = RV::load_rw(mul + at(i));
+      if (p.res && token && on(i)) a.e[i] = RV::load_rw(res + at(i));
+    }
+  }
+  __device__ __forceinline__ void operator()(float (&v)[C], TO* y, const Ahead& a) const {
     if (p.sx) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] *= sx * sw[i];
+      for (int i = 0; i < C; ++i) v[i] *= a.sx * sw[i];
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] += bias[i];
-    if (p.act == MOE_ACT_SILU) {
+    if (p.act != MOE_ACT_NONE) {
+      if (p.act == MOE_ACT_SILU) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = v[i] / (1.0f + expf(-v[i]));
-    } else if (p.act == MOE_ACT_GELU) {
+        for (int i = 0; i < C; ++i) v[i] = v[i] / (1.0f + expf(-v[i]));
+      } else if (p.act == MOE_ACT_GELU) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678f));
-    } else if (p.act == MOE_ACT_RELU) {
+        for (int i = 0; i < C; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678f));
+      } else {
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays
+        for (int i = 0; i < C; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // relu; NaN stays
+      }
     }
-  }
-  // what the wide path reads of mul and residual for a token, ahead of use
-  struct Ahead {
-    uint4 m[sizeof(TO) / 2], e[sizeof(TO) / 2];
-    float sx;
-  };
-  __device__ __forceinline__ void ahead(Ahead& a, long long r, bool on) const {
-    const bool use = on && feature(0) < n;
-    const int64_t f = f0 + feature(0);
-    a.sx = p.sx && on ? __ldg(p.sx + r) : 1.f;
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(TO) / 2; ++i) {
-      if (p.mul && use)
-        a.m[i] = *reinterpret_cast<const uint4*>(static_cast<const TO*>(p.mul) + r * p.ldmul + f + i * Vec<TO>::N);
-      if (p.res && use)
-        a.e[i] = *reinterpret_cast<const uint4*>(static_cast<const TO*>(p.res) + r * p.ldres + f + i * Vec<TO>::N);
-    }
-  }
-  __device__ __forceinline__ void unit(float (&v)[8], long long r, const Ahead& a) const {
-    constexpr int N = Vec<TO>::N;
-    if (feature(0) >= n) return;                     // wide: N is a whole number of units
-    head(v, a.sx);
-    TO* y = static_cast<TO*>(p.y) + r * p.ldy + f0 + feature(0);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(TO) / 2; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
+      constexpr int N = C / kVecs;
       float o[N], t[N];
 #pragma unroll
       for (int j = 0; j < N; ++j) o[j] = v[i * N + j];
       if (p.mul) {
-        unpack16<TO>(a.m[i], t);
+        RV::unpack(a.m[i], t);
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] *= t[j];
       }
       if (p.res) {
-        unpack16<TO>(a.e[i], t);
+        RV::unpack(a.e[i], t);
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] += t[j];
       }
-      *reinterpret_cast<uint4*>(y + i * N) = pack16<TO>(o);
+      if (on(i)) RV::store(y + at(i), RV::pack(o));
     }
   }
-  // one token by one warp, lane-strided features
-  __device__ __forceinline__ void token(float (&v)[4], long long r) const {
-    const TO* mul = static_cast<const TO*>(p.mul) + r * p.ldmul + f0;
-    const TO* res = static_cast<const TO*>(p.res) + r * p.ldres + f0;
-    TO* y = static_cast<TO*>(p.y) + r * p.ldy + f0;
-    float m[4], e[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int f = feature(i);
-      m[i] = p.mul && f < n ? to_f(mul[f]) : 1.f;
-      e[i] = p.res && f < n ? to_f(res[f]) : 0.f;
-    }
-    head(v, p.sx ? __ldg(p.sx + r) : 1.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int f = feature(i);
-      if (p.mul) v[i] *= m[i];
-      if (p.res) v[i] += e[i];
-      if (f < n) y[f] = from_f<TO>(v[i]);
-    }
+};
+
+// A thread's place in the epilogue's operands: token row r, feature f; advances by tokens.
+template <typename TO>
+struct Place {
+  const float* sx;
+  const TO* mul;
+  const TO* res;
+  TO* y;
+  __device__ __forceinline__ Place(const LinearParams& p, long long r, int f)
+      : sx(p.sx + r), mul(static_cast<const TO*>(p.mul) + r * p.ldmul + f),
+        res(static_cast<const TO*>(p.res) + r * p.ldres + f), y(static_cast<TO*>(p.y) + r * p.ldy + f) {}
+  __device__ __forceinline__ void advance(const LinearParams& p, int tokens) {
+    sx += tokens;
+    mul += tokens * p.ldmul;
+    res += tokens * p.ldres;
+    y += tokens * p.ldy;
   }
 };
 
@@ -211,13 +182,45 @@ struct SplitParams {
   int bn, stages, splits, nft;      // tokens a tile, ring depth, CTAs a cluster, feature tiles
 };
 
+constexpr int kSplitSmem = 226 * 1024;              // of an SM: for one CTA or two
+
 struct SplitTail {                  // behind the stages
   static constexpr int kMaxStages = 12;
-  uint64_t full[kMaxStages], empty[kMaxStages], done;
+  uint64_t full[kMaxStages], empty[kMaxStages], done, got;
   uint32_t tmem;
   int abort_flag;
-  int g, row0, nj, fti;             // this cluster's tile; nj = 0: none
+  int g, row0, nj;                  // this cluster's tile; nj = 0: none
 };
+
+// Tokens j0 + tk, + tks, .. < j1 of a tile at features f, f + step, ..: the ranks' partials summed in rank
+// order.  This rank's own lie at own [token][128], rank r's share for it at got + r * share [token - j0][128].
+template <typename TO, int C>
+__device__ __forceinline__ void split_finish(const SplitParams& p, int g, int row0, int f0, const float* own, const float* got,
+                                             int rank, int j0, int j1, int f, int step, int tk, int tks) {
+  const Finish<TO, C> finish(p.l, g, f0 + f, step);
+  Place<TO> place(p.l, row0 + j0 + tk, f0 + f);
+  const int share = (j1 - j0) * kBM;
+  for (int j = tk; j < j1 - j0; j += tks) {
+    typename Finish<TO, C>::Ahead a;
+    finish.ahead(a, place.sx, place.mul, place.res, true);
+    float v[C];
+    for (int r = 0; r < p.splits; ++r) {
+      const float* from = (r == rank ? own + j0 * kBM : got + r * share) + j * kBM + f;
+      float t[C];
+      if constexpr (C == 8) {
+        const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 4);
+        t[0] = x.x, t[1] = x.y, t[2] = x.z, t[3] = x.w, t[4] = y.x, t[5] = y.y, t[6] = y.z, t[7] = y.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) t[i] = from[step * i];
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = r ? v[i] + t[i] : t[i];
+    }
+    finish(v, place.y, a);
+    place.advance(p.l, tks);
+  }
+}
 
 template <bool E4M3, typename TO>
 __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_constant__ SplitParams p) {
@@ -240,46 +243,59 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
       mbar_init(&s->empty[i], 1);
     }
     mbar_init(&s->done, 1);
+    mbar_init(&s->got, 1);
     s->abort_flag = 0;
     mbar_init_fence();
   }
   if (warp == 2) tmem_alloc<1>(&s->tmem, cols);
-  ops_begin();
-  if (warp == 3) {                                   // token tile tile / nft of the groups' tiles
-    const int want = tile / p.nft;
-    int seen = 0, g = -1, row0 = 0, nj = 0;
-    for (int g0 = 0; g0 < l.G && g < 0; g0 += 32) {
-      const Span sp = g0 + lane < l.G ? group_rows(l, g0 + lane) : Span{0, 0};
-      const int nt = (sp.n + p.bn - 1) / p.bn;
-      int incl = nt;
+  int g = 0, nj = 0, row0 = tile / p.nft * p.bn;
+  const int fti = tile % p.nft;
+  if (!l.offsets) {                                  // dense: the tile is known before the inputs are
+    nj = min(p.bn, l.T - row0);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    ops_begin();
+  } else {
+    ops_begin();
+    if (warp == 3) {                                 // token tile tile / nft of the groups' tiles
+      const int want = tile / p.nft;
+      int seen = 0;
+      g = -1;
+      for (int g0 = 0; g0 < l.G && g < 0; g0 += 32) {
+        const Span sp = g0 + lane < l.G ? group_rows(l, g0 + lane) : Span{0, 0};
+        const int nt = (sp.n + p.bn - 1) / p.bn;
+        int incl = nt;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
+        for (int off = 1; off < 32; off <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += o;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, seen + incl > want);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          const int t = want - seen - __shfl_sync(0xffffffffu, incl - nt, src);
+          const int n = __shfl_sync(0xffffffffu, sp.n, src);
+          g = g0 + src;
+          row0 = __shfl_sync(0xffffffffu, sp.a, src) + t * p.bn;
+          nj = min(p.bn, n - t * p.bn);
+        }
+        seen += __shfl_sync(0xffffffffu, incl, 31);
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, seen + incl > want);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        const int t = want - seen - __shfl_sync(0xffffffffu, incl - nt, src);
-        const int n = __shfl_sync(0xffffffffu, sp.n, src);
-        g = g0 + src;
-        row0 = __shfl_sync(0xffffffffu, sp.a, src) + t * p.bn;
-        nj = min(p.bn, n - t * p.bn);
+      if (lane == 0) {
+        s->g = g;
+        s->row0 = row0;
+        s->nj = nj;
       }
-      seen += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) {
-      s->g = g;
-      s->row0 = row0;
-      s->nj = nj;
-      s->fti = tile % p.nft;
-    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    g = s->g;
+    row0 = s->row0;
+    nj = s->nj;
   }
-  tc_before();
-  __syncthreads();
-  tc_after();
   const uint32_t tmem = s->tmem;
-  const int nj = s->nj, g = s->g, row0 = s->row0, fti = s->fti;
   const int kb0 = (int)((long long)l.nk * rank / p.splits), kb1 = (int)((long long)l.nk * (rank + 1) / p.splits);
   constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
 
@@ -307,7 +323,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
     }
     if (ok) commit<1>(&s->done);
   }
-  float* part = reinterpret_cast<float*>(smem);      // [token][feature]: the ring is idle by then
+  float* own = reinterpret_cast<float*>(smem);       // [token][feature]: the ring is idle by then
+  float* got = own + p.bn * kBM;                     // the other ranks' partials of this rank's share
+  const int j0 = nj * rank / p.splits, j1 = nj * (rank + 1) / p.splits;
   if (nj > 0 && warp >= 4) {
     const int q = warp & 3, row = 32 * q + lane;     // TMEM lane: a feature
     const bool ok = wait(&s->done, 0, abort_flag);
@@ -319,49 +337,36 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
         float v[16];
         tmem_ld16(t + c, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * kBM + row] = v[j];
+        for (int j = 0; j < 16; ++j) own[(c + j) * kBM + row] = v[j];
       }
     }
+    if (p.splits > 1) fence_async();
+    if (p.splits > 1 && threadIdx.x == 128) mbar_expect(&s->got, (p.splits - 1) * (j1 - j0) * kBM * 4);
   }
   __syncwarp();
-  if (p.splits > 1) cluster_sync(); else __syncthreads();
-  if (nj > 0) {                                      // every rank sums and finishes its share of the tile
-    const Finish<TO> finish(l, g, fti * kBM);
-    if (l.wide) {
-      const int units = nj * Finish<TO>::kUnitsPerToken;
-      const int u0 = (int)((long long)units / 16 * rank / p.splits) * 16;
-      const int u1 = (int)((long long)units / 16 * (rank + 1) / p.splits) * 16;
-      for (int u = u0 + threadIdx.x; u < u1; u += kThreads) {
-        const int j = u / Finish<TO>::kUnitsPerToken;
-        typename Finish<TO>::Ahead a;
-        finish.ahead(a, row0 + j, true);
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        const uint32_t mine = smem_u32(part + j * kBM + finish.feature(0));
-        for (int r = 0; r < p.splits; ++r) {
-          const uint32_t from = mapa(mine, r);
-          const float4 x = ld_cluster_v4(from), y = ld_cluster_v4(from + 16);
-          v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-          v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-        }
-        finish.unit(v, row0 + j, a);
-      }
-    } else {
-      const int j0 = nj * rank / p.splits, j1 = nj * (rank + 1) / p.splits;
-      for (int j = j0 + warp; j < j1; j += kThreads / 32) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t mine = smem_u32(part + j * kBM + lane);
-        for (int r = 0; r < p.splits; ++r) {
-          const uint32_t from = mapa(mine, r);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += ld_cluster_f32(from + 128 * i);
-        }
-        finish.token(v, row0 + j);
-      }
+  if (p.splits > 1) {
+    // every share goes to its rank by bulk copies (reading the ranks' memory by loads moved 1.9 TB/s
+    // over the GPU: 9 us for 8 partials of 128 x 128)
+    cluster_sync();                                  // all rings are idle, all partials written
+    if (nj > 0 && warp == 0 && lane < p.splits && lane != rank) {
+      const int i0 = nj * lane / p.splits, i1 = nj * (lane + 1) / p.splits, share = (i1 - i0) * kBM;
+      if (share > 0)
+        bulk_to_cluster(mapa(smem_u32(got + rank * share), lane), smem_u32(own + i0 * kBM), share * 4,
+                        mapa(smem_u32(&s->got), lane));
     }
+    if (nj > 0) wait(&s->got, 0, abort_flag);
+  } else {
+    __syncthreads();
+  }
+  if (nj > 0) {                                      // every rank sums and finishes its share of the tokens
+    if (l.wide)
+      split_finish<TO, 8>(p, g, row0, fti * kBM, own, got, rank, j0, j1, threadIdx.x % 16 * 8, 1, threadIdx.x / 16, kThreads / 16);
+    else
+      split_finish<TO, 4>(p, g, row0, fti * kBM, own, got, rank, j0, j1, lane, 32, warp, kThreads / 32);
   }
   if (p.splits > 1) {
     __syncwarp();
-    cluster_sync();                                  // a rank's partials stay until all have read them
+    cluster_sync();                                  // the copies out of a rank's memory have been received
   }
   tc_before();
   __syncthreads();
@@ -376,8 +381,9 @@ constexpr int kPairStages = 3;
 constexpr int kPairStage = 64 * 1024;                // 2 k-blocks of a full tile, 3 of a narrow one
 constexpr int kPairKpsMax = 3;
 constexpr int kPairThreads = 384;                    // warps: TMA, MMA, TMEM, spare, 2 x 4 epilogue
-constexpr int kChunk = 16;                           // tokens an epilogue group takes at a time
-constexpr int kStaging = kChunk * kBM * 4;
+constexpr int kChunk = 32;                           // tokens an epilogue warp turns at a time
+constexpr int kTurn = kChunk * 32;                   // floats: 32 tokens x 32 features
+constexpr int kStaging = 8 * kTurn * 4;
 
 struct PairParams {
   CUtensorMap w, x[4];              // x: boxes of 16, 32, 64, 128 rows
@@ -389,46 +395,52 @@ struct PairTail {
   uint64_t full[kPairStages], empty[kPairStages], tfull[2], tempty[2];
   uint32_t tmem;
   int abort_flag;
-  int base[kMaxExperts + 1];        // first tile of each group
 };
 
 struct PairTile {
   int g, row0, nj, fti, nmma, box, kps;
 };
 
-__device__ __forceinline__ PairTile pair_tile(const PairParams& p, const int* base, int t) {
-  const LinearParams& l = p.l;
-  int lo = 0, hi = l.G - 1;                          // last group whose first tile is <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (base[mid] <= t) lo = mid; else hi = mid - 1;
+// The tiles of a pair of CTAs, in order: t, t + pairs, ..  Every role walks the groups by itself.
+struct PairWalk {
+  int t, g, base;                   // next tile; its group or an earlier one, and that group's first tile
+  Span sp;
+  __device__ PairWalk(const PairParams& p) : t(blockIdx.x / 2), g(0), base(0), sp(group_rows(p.l, 0)) {}
+
+  __device__ __forceinline__ bool next(const PairParams& p, PairTile& tl) {
+    int ntt;
+    while (true) {
+      ntt = (sp.n + kPairTokens - 1) / kPairTokens;
+      if (t - base < ntt * p.nft) break;
+      base += ntt * p.nft;
+      if (++g >= p.l.G) return false;
+      sp = group_rows(p.l, g);
+    }
+    // eight token tiles meet one feature tile before the next: what runs at one time shares operands in L2
+    int local = t - base;
+    const int band = local / (8 * p.nft);
+    local -= band * 8 * p.nft;
+    const int width = min(8, ntt - 8 * band);
+    tl.g = g;
+    tl.fti = local / width;
+    const int j0 = (8 * band + local % width) * kPairTokens;
+    tl.row0 = sp.a + j0;
+    tl.nj = min(kPairTokens, sp.n - j0);
+    tl.nmma = (tl.nj + 31) & ~31;
+    const int half = tl.nmma / 2;                    // token rows each CTA stages: a box that holds them
+    tl.box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+    tl.kps = min(kPairKpsMax, kPairStage / (kABlock + (16 << tl.box) * kBKBytes));
+    t += gridDim.x / 2;
+    return true;
   }
-  const Span sp = group_rows(l, lo);
-  const int ntt = (sp.n + kPairTokens - 1) / kPairTokens;
-  // eight token tiles meet one feature tile before the next: what runs at one time shares operands in L2
-  int local = t - base[lo];
-  const int band = local / (8 * p.nft);
-  local -= band * 8 * p.nft;
-  const int width = min(8, ntt - 8 * band);
-  PairTile tl;
-  tl.g = lo;
-  tl.fti = local / width;
-  const int j0 = (8 * band + local % width) * kPairTokens;
-  tl.row0 = sp.a + j0;
-  tl.nj = min(kPairTokens, sp.n - j0);
-  tl.nmma = (tl.nj + 31) & ~31;
-  const int half = tl.nmma / 2;                      // token rows each CTA stages: a box that holds them
-  tl.box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-  tl.kps = min(kPairKpsMax, kPairStage / (kABlock + (16 << tl.box) * kBKBytes));
-  return tl;
-}
+};
 
 template <bool E4M3, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  PairTail* s = reinterpret_cast<PairTail*>(smem + kPairStages * kPairStage + 2 * kStaging);
+  PairTail* s = reinterpret_cast<PairTail*>(smem + kPairStages * kPairStage + kStaging);
   volatile int* abort_flag = &s->abort_flag;
   const LinearParams& l = p.l;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -451,35 +463,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
   if (warp == 2) tmem_alloc<2>(&s->tmem, kCols);
   ops_begin();
-  if (warp == 3) {
-    int seen = 0;
-    for (int g0 = 0; g0 < l.G; g0 += 32) {
-      const int n = g0 + lane < l.G ? group_rows(l, g0 + lane).n : 0;
-      const int nt = (n + kPairTokens - 1) / kPairTokens * p.nft;
-      int incl = nt;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
-      }
-      if (g0 + lane < l.G) s->base[g0 + lane] = seen + incl - nt;
-      seen += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) s->base[l.G] = seen;
-  }
   tc_before();
   __syncthreads();
   cluster_sync();
   tc_after();
   const uint32_t tmem = s->tmem;
-  const int n_tiles = s->base[l.G], pairs = gridDim.x / 2;
+  PairWalk walk(p);
+  PairTile tl;
   constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
 
   if (warp == 0 && lane == 0) {
     uint32_t it = 0;
     bool ok = true;
-    for (int t = blockIdx.x / 2; t < n_tiles && ok; t += pairs) {
-      const PairTile tl = pair_tile(p, s->base, t);
+    while (ok && walk.next(p, tl)) {
       const int brows = 16 << tl.box, block = kABlock + brows * kBKBytes;
       const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
       for (int kb = 0; kb < l.nk; kb += tl.kps, ++it) {
@@ -497,8 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1 && lane == 0 && rank == 0) {
     uint32_t it = 0, acc = 0;
     bool ok = true;
-    for (int t = blockIdx.x / 2; t < n_tiles && ok; t += pairs, ++acc) {
-      const PairTile tl = pair_tile(p, s->base, t);
+    for (; ok && walk.next(p, tl); ++acc) {
       const int block = kABlock + (16 << tl.box) * kBKBytes;
       const uint32_t idesc = mma_desc<E4M3>(2 * kBM, tl.nmma);
       const int buf = acc & 1;
@@ -521,56 +516,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (ok) commit<2>(&s->tfull[buf]);
     }
   } else if (warp >= 4) {
-    const int q = warp & 3, row = 32 * q + lane, grp = (warp >> 2) - 1, et = threadIdx.x & 127;
-    float* stage = reinterpret_cast<float*>(smem + kPairStages * kPairStage + grp * kStaging);   // [token][feature]
+    const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..; two warps share a quarter's columns
+    float* turn = reinterpret_cast<float*>(smem + kPairStages * kPairStage) + (warp - 4) * kTurn;
     uint32_t acc = 0;
-    for (int t = blockIdx.x / 2; t < n_tiles; t += pairs, ++acc) {
-      const PairTile tl = pair_tile(p, s->base, t);
-      const int buf = acc & 1;
-      const Finish<TO> finish(l, tl.g, tl.fti * 2 * kBM + rank * kBM);
-      const bool ok = wait(&s->tfull[buf], (acc >> 1) & 1, abort_flag);
-      if (!group_all(ok, 1 + grp)) break;
-      tc_after();
+    for (; walk.next(p, tl); ++acc) {
+      const int buf = acc & 1, f = tl.fti * 2 * kBM + rank * kBM + 32 * q;
       const uint32_t d = tmem + ((uint32_t)(32 * q) << 16) + buf * kPairTokens;
-      for (int c = grp * kChunk; c < tl.nj; c += 2 * kChunk) {
-        constexpr int kUnits = kChunk * Finish<TO>::kUnitsPerToken / 128;
-        typename Finish<TO>::Ahead a[kUnits];
-        if (l.wide) {
+      if (l.wide) {
+        // 32 features x 32 tokens turned in the warp's own shared memory: lane i then holds 8
+        // features (i % 4) of tokens i / 4 + 8 u.  16-byte chunks of a token's row lie at
+        // chunk ^ (token & 7): neither the writes nor the reads meet a bank twice.
+        const int f8 = lane % 4, tk = lane / 4;
+        const Finish<TO, 8> finish(l, tl.g, f + f8 * 8, 1);
+        Place<TO> place(l, tl.row0 + half * kChunk + tk, f + f8 * 8);
+        const bool ok = wait(&s->tfull[buf], (acc >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_after();
+        for (int c = half * kChunk; c < tl.nj; c += 2 * kChunk) {
+          constexpr int kAt = sizeof(TO) == 2 ? 4 : 2;         // units whose operands are in flight
+          float v[32];
+          tmem_ld32(d + c, v);
 #pragma unroll
-          for (int i = 0; i < kUnits; ++i) {
-            const int j = c + (et + 128 * i) / Finish<TO>::kUnitsPerToken;
-            finish.ahead(a[i], tl.row0 + j, j < tl.nj);
+          for (int j = 0; j < 32; ++j) turn[j * 32 + (lane ^ ((j & 7) << 2))] = v[j];
+          __syncwarp();
+#pragma unroll
+          for (int u0 = 0; u0 < 4; u0 += kAt) {
+            typename Finish<TO, 8>::Ahead a[kAt];
+            Place<TO> at = place;
+#pragma unroll
+            for (int u = 0; u < kAt; ++u) {
+              finish.ahead(a[u], at.sx, at.mul, at.res, c + tk + 8 * (u0 + u) < tl.nj);
+              at.advance(l, 8);
+            }
+#pragma unroll
+            for (int u = 0; u < kAt; ++u) {
+              const int j = tk + 8 * (u0 + u);
+              const float* row = turn + j * 32;
+              const float4 x = *reinterpret_cast<const float4*>(row + ((2 * f8) ^ tk) * 4);
+              const float4 y = *reinterpret_cast<const float4*>(row + ((2 * f8 + 1) ^ tk) * 4);
+              float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+              if (c + j < tl.nj) finish(w, place.y, a[u]);
+              place.advance(l, 8);
+            }
           }
+          place.advance(l, kChunk);
+          __syncwarp();
         }
-        float v[16];
-        tmem_ld16(d + c, v);
-        group_sync(1 + grp);                         // the chunk before has been read
+      } else {
+        const Finish<TO, 1> finish(l, tl.g, f + lane, 1);
+        Place<TO> place(l, tl.row0 + half * kChunk, f + lane);
+        const bool ok = wait(&s->tfull[buf], (acc >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_after();
+        for (int c = half * kChunk; c < tl.nj; c += 2 * kChunk) {
+#pragma unroll 1
+          for (int c1 = 0; c1 < kChunk; c1 += 16) {
+            float v[16];
+            tmem_ld16(d + c + c1, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) stage[j * kBM + row] = v[j];
-        group_sync(1 + grp);
-        if (l.wide) {
+            for (int c2 = 0; c2 < 16; c2 += 8) {
+              typename Finish<TO, 1>::Ahead a[8];
+              Place<TO> at = place;
 #pragma unroll
-          for (int i = 0; i < kUnits; ++i) {
-            const int j = (et + 128 * i) / Finish<TO>::kUnitsPerToken;
-            if (c + j < tl.nj) {
-              float u[8];
-              const float4* from = reinterpret_cast<const float4*>(stage + j * kBM + finish.feature(0));
-              const float4 x = from[0], y = from[1];
-              u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w, u[4] = y.x, u[5] = y.y, u[6] = y.z, u[7] = y.w;
-              finish.unit(u, tl.row0 + c + j, a[i]);
+              for (int j = 0; j < 8; ++j) {
+                finish.ahead(a[j], at.sx, at.mul, at.res, c + c1 + c2 + j < tl.nj);
+                at.advance(l, 1);
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float w[1] = {v[c2 + j]};
+                if (c + c1 + c2 + j < tl.nj) finish(w, place.y, a[j]);
+                place.advance(l, 1);
+              }
             }
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kChunk / 4; ++i) {
-            const int j = q + 4 * i;
-            if (c + j < tl.nj) {
-              float u[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) u[k] = stage[j * kBM + lane + 32 * k];
-              finish.token(u, tl.row0 + c + j);
-            }
-          }
+          place.advance(l, kChunk);
         }
       }
       tc_before();
@@ -623,7 +643,7 @@ int sm_count() {
 
 template <bool E4M3, typename TO>
 moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, int sms, void* s) {
-  constexpr int kSmem = kPairStages * kPairStage + 2 * kStaging + (int)sizeof(PairTail) + 1024;
+  constexpr int kSmem = kPairStages * kPairStage + kStaging + (int)sizeof(PairTail) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   constexpr int size = E4M3 ? 1 : 2;
   PairParams p;
@@ -645,14 +665,14 @@ moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, i
   p.bn = bn;
   p.splits = splits;
   p.nft = (l.N + kBM - 1) / kBM;
-  // about 100 KB a CTA, so that two fit an SM
-  const int stage = kABlock + bn * kBKBytes;
-  p.stages = std::min(SplitTail::kMaxStages, 108 * 1024 / stage);
-  const int smem = p.stages * stage + (int)sizeof(SplitTail) + 1024;
+  // tiles of up to 32 tokens: two CTAs an SM, whose rings fill the gaps of each other; wider: one deep ring
+  const int stage = kABlock + bn * kBKBytes, rest = (int)sizeof(SplitTail) + 1024;
+  p.stages = std::min(SplitTail::kMaxStages, (kSplitSmem / (bn <= 32 ? 2 : 1) - rest) / stage);
+  const int smem = p.stages * stage + rest;
   if (!encode(&p.w, a->d_w, size, l.F, l.N, a->w_stride, l.G, kBM) ||
       !encode(&p.x, a->d_x, size, l.F, l.T, a->x_stride, 0, bn))
     return MOE_ERR_CUDA;
-  if (cudaFuncSetAttribute(linear_split_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024) != cudaSuccess)
+  if (cudaFuncSetAttribute(linear_split_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem) != cudaSuccess)
     return MOE_ERR_CUDA;
   return launch_op(linear_split_kernel<E4M3, TO>, dim3((unsigned)(tiles * splits)), kThreads, smem, splits, s, p);
 }
@@ -668,7 +688,7 @@ moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, 
   const int64_t per = l.offsets ? (l.T + l.G - 1) / l.G : l.T;
   const int bn = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
   const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * (l.offsets ? l.T / bn + std::min(l.G, l.T) : (l.T + bn - 1) / bn);
-  int splits = (int)std::max<int64_t>(1, std::min<int64_t>(8, sms / tiles));
+  int splits = (int)std::max<int64_t>(1, std::min<int64_t>(8, (bn <= 32 ? 2 : 1) * sms / tiles));
   splits = std::min(splits, std::max(1, l.nk / 2));
   return launch_split<E4M3, TO>(a, l, bn, splits, tiles, s);
 }
