@@ -17,7 +17,7 @@
 // Two kernels, chosen by linear_launch:
 //   pair   persistent, tiles of 256 features x up to 256 tokens over two SMs (cta_group::2): each
 //          SM stages half of both operands, which halves the shared-memory traffic per product.
-//   split  one tile of 128 features x up to 128 tokens per cluster of up to 8 CTAs, K split over
+//   split  one tile of 128 features x up to 64 tokens per cluster of up to 8 CTAs, K split over
 //          them; partials meet through distributed shared memory in rank order (no workspace,
 //          no atomics).  For few tiles: a lone SM streams weights far below the HBM rate.
 //
@@ -80,6 +80,18 @@ __device__ __forceinline__ Span group_rows(const LinearParams& p, int g) {
   return {a, b - a};
 }
 
+// A thread's place in the epilogue's operands: token row r, feature f.
+template <typename TO>
+struct Place {
+  const float* sx;
+  const TO* mul;
+  const TO* res;
+  TO* y;
+  __device__ __forceinline__ Place(const LinearParams& p, long long r, int f)
+      : sx(p.sx + r), mul(static_cast<const TO*>(p.mul) + r * p.ldmul + f),
+        res(static_cast<const TO*>(p.res) + r * p.ldres + f), y(static_cast<TO*>(p.y) + r * p.ldy + f) {}
+};
+
 // The end of the epilogue for one thread, which owns C features of every token it meets: first,
 // first + step, ...  C = 8, step = 1: rows of y, mul and residual move in 16-byte units; else
 // element by element.  Pointers are to a token's row at feature `first`.
@@ -108,12 +120,13 @@ struct Finish {
   };
   __device__ __forceinline__ bool on(int i) const { return kWide ? live > 0 : i < live; }
   __device__ __forceinline__ int at(int i) const { return kWide ? i * Vec<TO>::N : i * step; }
-  __device__ __forceinline__ void ahead(Ahead& a, const float* sx, const TO* mul, const TO* res, bool token) const {
-    a.sx = p.sx && token ? __ldg(sx) : 1.f;
+  // `token`: whether the token t behind the place's exists
+  __device__ __forceinline__ void ahead(Ahead& a, const Place<TO>& place, int t, bool token) const {
+    a.sx = p.sx && token ? __ldg(place.sx + t) : 1.f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      if (p.mul && token && on(i)) a.m[i] = RV::load_rw(mul + at(i));
-      if (p.res && token && on(i)) a.e[i] = RV::load_rw(res + at(i));
+      if (p.mul && token && on(i)) a.m[i] = RV::load_rw(place.mul + t * p.ldmul + at(i));
+      if (p.res && token && on(i)) a.e[i] = RV::load_rw(place.res + t * p.ldres + at(i));
     }
   }
   __device__ __forceinline__ void operator()(float (&v)[C], TO* y, const Ahead& a) const {
@@ -126,7 +139,7 @@ struct Finish {
     if (p.act != MOE_ACT_NONE) {
       if (p.act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = v[i] / (1.0f + expf(-v[i]));
+        for (int i = 0; i < C; ++i) v[i] = __fdividef(v[i], 1.0f + __expf(-v[i]));   // off by at most 2^-20 |v|: a 7 us tile less than exact ones
       } else if (p.act == MOE_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < C; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678f));
@@ -156,24 +169,6 @@ struct Finish {
   }
 };
 
-// A thread's place in the epilogue's operands: token row r, feature f; advances by tokens.
-template <typename TO>
-struct Place {
-  const float* sx;
-  const TO* mul;
-  const TO* res;
-  TO* y;
-  __device__ __forceinline__ Place(const LinearParams& p, long long r, int f)
-      : sx(p.sx + r), mul(static_cast<const TO*>(p.mul) + r * p.ldmul + f),
-        res(static_cast<const TO*>(p.res) + r * p.ldres + f), y(static_cast<TO*>(p.y) + r * p.ldy + f) {}
-  __device__ __forceinline__ void advance(const LinearParams& p, int tokens) {
-    sx += tokens;
-    mul += tokens * p.ldmul;
-    res += tokens * p.ldres;
-    y += tokens * p.ldy;
-  }
-};
-
 // ------------------------------------------------------------------ split kernel
 
 struct SplitParams {
@@ -182,10 +177,11 @@ struct SplitParams {
   int bn, stages, splits, nft;      // tokens a tile, ring depth, CTAs a cluster, feature tiles
 };
 
-constexpr int kSplitSmem = 226 * 1024;              // of an SM: for one CTA or two
+constexpr int kSplitSmem = 226 * 1024;              // of an SM: for two CTAs
+constexpr int kSplitTokens = 64;                    // most tokens a tile
 
 struct SplitTail {                  // behind the stages
-  static constexpr int kMaxStages = 12;
+  static constexpr int kMaxStages = 6;
   uint64_t full[kMaxStages], empty[kMaxStages], done, got;
   uint32_t tmem;
   int abort_flag;
@@ -197,28 +193,35 @@ struct SplitTail {                  // behind the stages
 template <typename TO, int C>
 __device__ __forceinline__ void split_finish(const SplitParams& p, int g, int row0, int f0, const float* own, const float* got,
                                              int rank, int j0, int j1, int f, int step, int tk, int tks) {
+  constexpr int kAt = C < 8 ? 4 : sizeof(TO) == 2 ? 2 : 1;              // tokens whose mul and residual are in flight
   const Finish<TO, C> finish(p.l, g, f0 + f, step);
-  Place<TO> place(p.l, row0 + j0 + tk, f0 + f);
+  const Place<TO> place(p.l, row0 + j0, f0 + f);
   const int share = (j1 - j0) * kBM;
-  for (int j = tk; j < j1 - j0; j += tks) {
-    typename Finish<TO, C>::Ahead a;
-    finish.ahead(a, place.sx, place.mul, place.res, true);
-    float v[C];
-    for (int r = 0; r < p.splits; ++r) {
-      const float* from = (r == rank ? own + j0 * kBM : got + r * share) + j * kBM + f;
-      float t[C];
-      if constexpr (C == 8) {
-        const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 4);
-        t[0] = x.x, t[1] = x.y, t[2] = x.z, t[3] = x.w, t[4] = y.x, t[5] = y.y, t[6] = y.z, t[7] = y.w;
-      } else {
+  for (int jb = tk; jb < j1 - j0; jb += kAt * tks) {
+    typename Finish<TO, C>::Ahead a[kAt];
 #pragma unroll
-        for (int i = 0; i < C; ++i) t[i] = from[step * i];
+    for (int u = 0; u < kAt; ++u) finish.ahead(a[u], place, jb + u * tks, jb + u * tks < j1 - j0);
+#pragma unroll
+    for (int u = 0; u < kAt; ++u) {
+      const int j = jb + u * tks;
+      if (j < j1 - j0) {
+        float v[C];
+        for (int r = 0; r < p.splits; ++r) {
+          const float* from = (r == rank ? own + j0 * kBM : got + r * share) + j * kBM + f;
+          float t[C];
+          if constexpr (C == 8) {
+            const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 4);
+            t[0] = x.x, t[1] = x.y, t[2] = x.z, t[3] = x.w, t[4] = y.x, t[5] = y.y, t[6] = y.z, t[7] = y.w;
+          } else {
+#pragma unroll
+            for (int i = 0; i < C; ++i) t[i] = from[step * i];
+          }
+#pragma unroll
+          for (int i = 0; i < C; ++i) v[i] = r ? v[i] + t[i] : t[i];
+        }
+        finish(v, place.y + j * p.l.ldy, a[u]);
       }
-#pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = r ? v[i] + t[i] : t[i];
     }
-    finish(v, place.y, a);
-    place.advance(p.l, tks);
   }
 }
 
@@ -395,6 +398,7 @@ struct PairTail {
   uint64_t full[kPairStages], empty[kPairStages], tfull[2], tempty[2];
   uint32_t tmem;
   int abort_flag;
+  int finishing;                    // tiles whose epilogue has begun
 };
 
 struct PairTile {
@@ -459,6 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(&s->tempty[b], 16);                  // the epilogue warps of both CTAs, at the leader
     }
     s->abort_flag = 0;
+    s->finishing = 0;
     mbar_init_fence();
   }
   if (warp == 2) tmem_alloc<2>(&s->tmem, kCols);
@@ -515,82 +520,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       if (ok) commit<2>(&s->tfull[buf]);
     }
+  } else if (warp == 3 && (l.mul || l.res)) {
+    // mul and residual of a tile into L2 while the tile before is finished: the epilogue's 16 KB of
+    // reads in flight an SM then last L2's latency (4096 x 512 x 7168 with mul: 80 -> 62 us)
+    volatile int* finishing = &s->finishing;
+    for (int i = 0; walk.next(p, tl); ++i) {
+      const unsigned long long t0 = now_ns();
+      while (*finishing < i && !*abort_flag && now_ns() - t0 < kLimitNs) __nanosleep(200);
+      const int f = tl.fti * 2 * kBM + rank * kBM, n = min(kBM, l.N - f) * (int)sizeof(TO), lines = kBM * (int)sizeof(TO) / 128;
+      for (int j = lane / lines; j < tl.nj; j += 32 / lines) {
+        const int64_t r = tl.row0 + j;
+        if (lane % lines * 128 < n) {
+          if (l.mul) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.mul) + r * l.ldmul + f) + lane % lines * 128);
+          if (l.res) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.res) + r * l.ldres + f) + lane % lines * 128);
+        }
+      }
+    }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..; two warps share a quarter's columns
     float* turn = reinterpret_cast<float*>(smem + kPairStages * kPairStage) + (warp - 4) * kTurn;
     uint32_t acc = 0;
     for (; walk.next(p, tl); ++acc) {
+      if (threadIdx.x == 128) *reinterpret_cast<volatile int*>(&s->finishing) = acc + 1;
       const int buf = acc & 1, f = tl.fti * 2 * kBM + rank * kBM + 32 * q;
       const uint32_t d = tmem + ((uint32_t)(32 * q) << 16) + buf * kPairTokens;
       if (l.wide) {
         // 32 features x 32 tokens turned in the warp's own shared memory: lane i then holds 8
-        // features (i % 4) of tokens i / 4 + 8 u.  16-byte chunks of a token's row lie at
-        // chunk ^ (token & 7): neither the writes nor the reads meet a bank twice.
+        // features (i % 4) of tokens i / 4 + 8 u, u < 4.  16-byte chunks of a token's row lie at
+        // chunk ^ (token & 7): neither the writes nor the reads meet a bank twice.  mul and
+        // residual are asked for kAt units ahead, the first ones before the products are done.
+        constexpr int kAt = sizeof(TO) == 2 ? 4 : 2;
         const int f8 = lane % 4, tk = lane / 4;
         const Finish<TO, 8> finish(l, tl.g, f + f8 * 8, 1);
-        Place<TO> place(l, tl.row0 + half * kChunk + tk, f + f8 * 8);
+        const Place<TO> place(l, tl.row0 + half * kChunk + tk, f + f8 * 8);
+        const int mine = tl.nj - half * kChunk - tk;           // tokens from this lane's first to the tile's end
+        typename Finish<TO, 8>::Ahead a[kAt];
+#pragma unroll
+        for (int u = 0; u < kAt; ++u) finish.ahead(a[u], place, 8 * u, 8 * u < mine);
         const bool ok = wait(&s->tfull[buf], (acc >> 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_after();
-        for (int c = half * kChunk; c < tl.nj; c += 2 * kChunk) {
-          constexpr int kAt = sizeof(TO) == 2 ? 4 : 2;         // units whose operands are in flight
-          float v[32];
-          tmem_ld32(d + c, v);
+        for (int c = 0; c < kPairTokens && c + half * kChunk < tl.nj; c += 2 * kChunk) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) turn[j * 32 + (lane ^ ((j & 7) << 2))] = v[j];
+          for (int h = 0; h < 2; ++h) {
+            float v[16];
+            tmem_ld16(d + c + half * kChunk + 16 * h, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) turn[(16 * h + j) * 32 + (lane ^ ((j & 7) << 2))] = v[j];
+          }
           __syncwarp();
 #pragma unroll
-          for (int u0 = 0; u0 < 4; u0 += kAt) {
-            typename Finish<TO, 8>::Ahead a[kAt];
-            Place<TO> at = place;
-#pragma unroll
-            for (int u = 0; u < kAt; ++u) {
-              finish.ahead(a[u], at.sx, at.mul, at.res, c + tk + 8 * (u0 + u) < tl.nj);
-              at.advance(l, 8);
-            }
-#pragma unroll
-            for (int u = 0; u < kAt; ++u) {
-              const int j = tk + 8 * (u0 + u);
-              const float* row = turn + j * 32;
-              const float4 x = *reinterpret_cast<const float4*>(row + ((2 * f8) ^ tk) * 4);
-              const float4 y = *reinterpret_cast<const float4*>(row + ((2 * f8 + 1) ^ tk) * 4);
-              float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-              if (c + j < tl.nj) finish(w, place.y, a[u]);
-              place.advance(l, 8);
-            }
+          for (int u = 0; u < 4; ++u) {
+            const float* row = turn + (tk + 8 * u) * 32;
+            const float4 x = *reinterpret_cast<const float4*>(row + ((2 * f8) ^ tk) * 4);
+            const float4 y = *reinterpret_cast<const float4*>(row + ((2 * f8 + 1) ^ tk) * 4);
+            float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            if (c + 8 * u < mine) finish(w, place.y + (c + 8 * u) * l.ldy, a[u % kAt]);
+            const int nx = u + kAt < 4 ? c + 8 * (u + kAt) : c + 2 * kChunk + 8 * (u + kAt - 4);
+            finish.ahead(a[u % kAt], place, nx, nx < mine);
           }
-          place.advance(l, kChunk);
           __syncwarp();
         }
       } else {
+        // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens in flight
+        constexpr int kAt = 16;
         const Finish<TO, 1> finish(l, tl.g, f + lane, 1);
-        Place<TO> place(l, tl.row0 + half * kChunk, f + lane);
+        const Place<TO> place(l, tl.row0 + half * kChunk, f + lane);
+        const int mine = tl.nj - half * kChunk;
+        typename Finish<TO, 1>::Ahead a[kAt];
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, j, j < mine);
         const bool ok = wait(&s->tfull[buf], (acc >> 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_after();
-        for (int c = half * kChunk; c < tl.nj; c += 2 * kChunk) {
-#pragma unroll 1
-          for (int c1 = 0; c1 < kChunk; c1 += 16) {
-            float v[16];
-            tmem_ld16(d + c + c1, v);
+        for (int c = 0; c < kPairTokens && c < mine;) {
+          const int next = c + (c % kChunk ? 2 * kChunk - 16 : 16);
+          float v[16];
+          tmem_ld16(d + c + half * kChunk, v);
 #pragma unroll
-            for (int c2 = 0; c2 < 16; c2 += 8) {
-              typename Finish<TO, 1>::Ahead a[8];
-              Place<TO> at = place;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                finish.ahead(a[j], at.sx, at.mul, at.res, c + c1 + c2 + j < tl.nj);
-                at.advance(l, 1);
-              }
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                float w[1] = {v[c2 + j]};
-                if (c + c1 + c2 + j < tl.nj) finish(w, place.y, a[j]);
-                place.advance(l, 1);
-              }
-            }
+          for (int j = 0; j < 16; ++j) {
+            float w[1] = {v[j]};
+            if (c + j < mine) finish(w, place.y + (c + j) * l.ldy, a[j % kAt]);
+            const int nx = j + kAt < 16 ? c + j + kAt : next + j + kAt - 16;
+            finish.ahead(a[j % kAt], place, nx, nx < mine);
           }
-          place.advance(l, kChunk);
+          c = next;
         }
       }
       tc_before();
@@ -657,6 +671,14 @@ moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, in
   return launch_op(linear_pair_kernel<E4M3, TO>, dim3(sms / 2 * 2), kPairThreads, kSmem, 1, s, p);
 }
 
+// the ring of a split CTA holds its own partials and its share of up to 8 ranks' (which may round up by a token each)
+constexpr bool split_fits(int bn) {
+  const int stage = kABlock + bn * kBKBytes;
+  const int stages = (kSplitSmem / 2 - (int)sizeof(SplitTail) - 1024) / stage;
+  return stages <= SplitTail::kMaxStages && (bn + bn + 8) * kBM * 4 <= stages * stage;
+}
+static_assert(split_fits(16) && split_fits(32) && split_fits(kSplitTokens), "shared memory of the split kernel");
+
 template <bool E4M3, typename TO>
 moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, int bn, int splits, int64_t tiles, void* s) {
   constexpr int size = E4M3 ? 1 : 2;
@@ -665,14 +687,15 @@ moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, i
   p.bn = bn;
   p.splits = splits;
   p.nft = (l.N + kBM - 1) / kBM;
-  // tiles of up to 32 tokens: two CTAs an SM, whose rings fill the gaps of each other; wider: one deep ring
+  // two CTAs an SM: their rings fill each other's gaps (64 tokens on 7168 x 7168: 23.4 us against 27.1 for one
+  // CTA with twice the ring)
   const int stage = kABlock + bn * kBKBytes, rest = (int)sizeof(SplitTail) + 1024;
-  p.stages = std::min(SplitTail::kMaxStages, (kSplitSmem / (bn <= 32 ? 2 : 1) - rest) / stage);
+  p.stages = (kSplitSmem / 2 - rest) / stage;
   const int smem = p.stages * stage + rest;
   if (!encode(&p.w, a->d_w, size, l.F, l.N, a->w_stride, l.G, kBM) ||
       !encode(&p.x, a->d_x, size, l.F, l.T, a->x_stride, 0, bn))
     return MOE_ERR_CUDA;
-  if (cudaFuncSetAttribute(linear_split_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem) != cudaSuccess)
+  if (cudaFuncSetAttribute(linear_split_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem / 2) != cudaSuccess)
     return MOE_ERR_CUDA;
   return launch_op(linear_split_kernel<E4M3, TO>, dim3((unsigned)(tiles * splits)), kThreads, smem, splits, s, p);
 }
@@ -681,14 +704,17 @@ template <bool E4M3, typename TO>
 moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, void* s) {
   const int sms = sm_count();
   if (sms < 2) return MOE_ERR_CUDA;
-  // The pair kernel wants most of the pairs at work; below that, smaller tiles on every SM, and
-  // where those are few too, K split over a cluster.  Groups count at most one ragged tile each.
+  // A third of the pairs at work is enough for the pair kernel (measured, bf16, pair / split us: 28 wide
+  // tiles of 7168 deep 42.7 / 47.3, 56 of them 43.5 / 93, 24 of 2880 deep 21.6 / 21.8, 48 of them 21.9 /
+  // 44; but 8 of 7168 deep 40.8 / 18.0, 16 of 592 deep 19.7 / 8.7), if the tiles are more than half full
+  // (28 of 7168 deep: 128 tokens 37 / 29, one token 30.4 / 21.5).  Groups count at most one ragged tile each.
   const int64_t wide = (int64_t)((l.N + 255) / 256) * (l.offsets ? l.T / 256 + std::min(l.G, l.T) : (l.T + 255) / 256);
-  if (wide >= sms / 2 * 3 / 4) return launch_pair<E4M3, TO>(a, l, sms, s);
   const int64_t per = l.offsets ? (l.T + l.G - 1) / l.G : l.T;
-  const int bn = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
+  if (per > 2 * kSplitTokens && wide >= sms / 6) return launch_pair<E4M3, TO>(a, l, sms, s);
+  const int bn = per <= 16 ? 16 : per <= 32 ? 32 : kSplitTokens;
   const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * (l.offsets ? l.T / bn + std::min(l.G, l.T) : (l.T + bn - 1) / bn);
-  int splits = (int)std::max<int64_t>(1, std::min<int64_t>(8, (bn <= 32 ? 2 : 1) * sms / tiles));
+  // Splits fill the SMs once where that takes four or more, else twice (two CTAs fit an SM)
+  int splits = (int)std::max<int64_t>(1, std::min<int64_t>(8, (sms / tiles >= 4 ? 1 : 2) * sms / tiles));
   splits = std::min(splits, std::max(1, l.nk / 2));
   return launch_split<E4M3, TO>(a, l, bn, splits, tiles, s);
 }
