@@ -24,28 +24,44 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-struct SumMax {
-  float s, m;
-};
-
-// Sum and NaN-keeping maximum over a block of up to 32 warps, the same value in every thread.
-__device__ __forceinline__ SumMax block_sum_max(SumMax v, SumMax* part) {
+// Sum of a and, as MAX says, NaN-keeping maximum or sum of b, over the G threads of a row (32, or
+// the whole block), the same values in every thread.
+template <int G, bool MAX>
+__device__ __forceinline__ void row_reduce(float& a, float& b, float2* part) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    v.s += __shfl_xor_sync(0xffffffffu, v.s, off);
-    v.m = max_nan(v.m, __shfl_xor_sync(0xffffffffu, v.m, off));
+    a += __shfl_xor_sync(0xffffffffu, a, off);
+    const float o = __shfl_xor_sync(0xffffffffu, b, off);
+    b = MAX ? max_nan(b, o) : b + o;
   }
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return v;
-  __syncthreads();                                   // `part` may still be read from the row before
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  if (G == 32) return;
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();                                   // `part` may still be read for the row before
+  if (lane == 0) part[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
-  SumMax a = part[0];
-  for (int i = 1; i < warps; ++i) {
-    a.s += part[i].s;
-    a.m = max_nan(a.m, part[i].m);
+  const float2 v = lane < warps ? part[lane] : make_float2(0.f, 0.f);
+  a = v.x;
+  b = v.y;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, off);
+    const float o = __shfl_xor_sync(0xffffffffu, b, off);
+    b = MAX ? max_nan(b, o) : b + o;
   }
-  return a;
+}
+
+// The gain of a unit of V columns (all ones without one); wide units start on 16 bytes.
+template <int V>
+__device__ __forceinline__ void load_gain(const float* gain, int c, float (&g)[V]) {
+  if constexpr (V == 1) {
+    g[0] = gain ? __ldg(gain + c) : 1.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 v = gain ? __ldg(reinterpret_cast<const float4*>(gain + c + i)) : make_float4(1.f, 1.f, 1.f, 1.f);
+      g[i] = v.x, g[i + 1] = v.y, g[i + 2] = v.z, g[i + 3] = v.w;
+    }
+  }
 }
 
 template <int V>
@@ -67,58 +83,70 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, const float (&v)[V]) {
   }
 }
 
-// One block per row.  The row stays in registers up to NV units a thread; what lies behind them
-// is read again.
-template <typename T, int V, int NV, bool Q>
-__global__ void __launch_bounds__(1024) add_rms_norm_kernel(Rows<const T> x, Rows<const T> res,
-                                                            const float* __restrict__ gain, float eps, int H,
-                                                            Rows<T> hout, Rows<T> y, Rows<uint8_t> q,
-                                                            float* __restrict__ scale) {
+// Bound by memory: one read of x and the residual, one write of h and y.  A row belongs to G
+// threads -- a warp (four rows a block) where it fits one, else a block -- and stays in their
+// registers, NV units a thread, all loads issued before the first is used; what lies behind
+// them is read again.
+template <typename T, int V, int NV, int G, bool Q>
+__global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, 1)
+    add_rms_norm_kernel(Rows<const T> x, Rows<const T> res, const float* __restrict__ gain, float eps, int T_, int H,
+                        Rows<T> hout, Rows<T> y, Rows<uint8_t> q, float* __restrict__ scale) {
   using RV = RowVec<T, V>;
-  __shared__ SumMax part[32];
+  __shared__ float2 part[32];
   ops_begin();
-  const long long t = blockIdx.x;
-  const int step = blockDim.x * V, c0 = threadIdx.x * V;
-  typename RV::Raw keep[NV];
-  SumMax a{0.f, 0.f};
-  auto sum = [&](int c) {
-    typename RV::Raw r = RV::load_rw(x.at(t) + c);
-    if (res.p) {
-      float v[V], o[V];
-      RV::unpack(r, v);
-      RV::unpack(RV::load_rw(res.at(t) + c), o);
+  const int threads = G == 32 ? 32 : blockDim.x, tid = G == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const long long t = G == 32 ? (long long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  if (t >= T_) return;                               // whole warps
+  const int step = threads * V, c0 = tid * V;
+  typename RV::Raw keep[NV], add[NV];
+  float ss = 0.f, mx = 0.f;
+  auto sum = [&](const typename RV::Raw& a, const typename RV::Raw& b) {
+    float v[V], o[V];
+    RV::unpack(a, v);
+    RV::unpack(b, o);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += o[i];
-      r = RV::pack(v);
-    }
-    return r;
+    for (int i = 0; i < V; ++i) v[i] += o[i];
+    return RV::pack(v);
   };
-  auto take = [&](int c) {
-    const typename RV::Raw r = sum(c);
+  auto take = [&](int c, const typename RV::Raw& r) {
     if (hout.p) RV::store(hout.at(t) + c, r);
-    float v[V];
+    float v[V], g[V];
     RV::unpack(r, v);
+    if (Q) load_gain<V>(gain, c, g);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      a.s = fmaf(v[i], v[i], a.s);
-      if (Q) a.m = max_nan(a.m, fabsf(gain ? v[i] * __ldg(gain + c + i) : v[i]));
+      ss = fmaf(v[i], v[i], ss);
+      if (Q) mx = max_nan(mx, fabsf(v[i] * g[i]));
     }
-    return r;
   };
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (c0 + j * step < H) keep[j] = take(c0 + j * step);
-  for (int c = c0 + NV * step; c < H; c += step) take(c);
-  a = block_sum_max(a, part);
-  const float r = 1.0f / sqrtf(a.s / (float)H + eps);
-  const float sc = max_nan(r * a.m * (1.0f / kE4m3Max), kMinScale), inv = 1.0f / sc;
-  if (Q && threadIdx.x == 0) scale[t] = sc;
+    if (c0 + j * step < H) {
+      keep[j] = RV::load_rw(x.at(t) + c0 + j * step);
+      if (res.p) add[j] = RV::load_rw(res.at(t) + c0 + j * step);
+    }
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (c0 + j * step < H) {
+      if (res.p) keep[j] = sum(keep[j], add[j]);
+      take(c0 + j * step, keep[j]);
+    }
+  auto again = [&](int c) {
+    const typename RV::Raw r = RV::load_rw(x.at(t) + c);
+    return res.p ? sum(r, RV::load_rw(res.at(t) + c)) : r;
+  };
+  for (int c = c0 + NV * step; c < H; c += step) take(c, again(c));
+  row_reduce<G, true>(ss, mx, part);
+  const float r = 1.0f / sqrtf(ss / (float)H + eps);
+  const float sc = max_nan(r * mx * (1.0f / kE4m3Max), kMinScale), inv = 1.0f / sc;
+  if (Q && tid == 0) scale[t] = sc;
   auto give = [&](int c, const typename RV::Raw& raw) {
-    float v[V];
+    float v[V], g[V];
     RV::unpack(raw, v);
+    load_gain<V>(gain, c, g);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      v[i] = (gain ? v[i] * __ldg(gain + c + i) : v[i]) * r;
+      v[i] = v[i] * g[i] * r;
       if (Q) v[i] *= inv;
     }
     if constexpr (Q)
@@ -130,71 +158,126 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(Rows<const T> x, Row
   for (int j = 0; j < NV; ++j)
     if (c0 + j * step < H) give(c0 + j * step, keep[j]);
   // h may have taken the place of x or of the residual: what this thread wrote is read
-  for (int c = c0 + NV * step; c < H; c += step) give(c, hout.p ? RV::load_rw(hout.at(t) + c) : sum(c));
+  for (int c = c0 + NV * step; c < H; c += step) give(c, hout.p ? RV::load_rw(hout.at(t) + c) : again(c));
 }
 
-// Rows blockIdx.x, + gridDim.x, ...; every block leaves the sum of grad_y * n over its rows in
-// its row of `partial` [gridDim.x, H].
-template <typename T, int V>
-__global__ void __launch_bounds__(256) rms_norm_backward_kernel(Rows<const T> gy, Rows<const T> h,
-                                                                const float* __restrict__ gain, float eps, int T_,
-                                                                int H, Rows<const T> gh, Rows<T> gx,
-                                                                float* __restrict__ partial) {
+// Rows blockIdx.x, + gridDim.x, ...  A thread keeps its columns: up to NV units of the row and of
+// the gain's gradient stay in its registers; every block leaves the sum of grad_y * n over its
+// rows in its row of `partial` [gridDim.x, H] (WIDE: columns behind those units are read again,
+// and added up there).
+template <typename T, int V, int NV, bool WIDE>
+__global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
+    rms_norm_backward_kernel(Rows<const T> gy, Rows<const T> h, const float* __restrict__ gain, float eps, int T_, int H,
+                             Rows<const T> gh, Rows<T> gx, float* __restrict__ partial) {
   using RV = RowVec<T, V>;
-  __shared__ SumMax part[32];
+  __shared__ float2 part[32];
   ops_begin();
   float* mine = partial ? partial + (size_t)blockIdx.x * H : nullptr;
-  bool first = true;
+  const int step = blockDim.x * V, c0 = threadIdx.x * V;
+  float acc[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
   for (long long t = blockIdx.x; t < T_; t += gridDim.x) {
-    SumMax a{0.f, 0.f}, b{0.f, 0.f};
-    for (int c = threadIdx.x * V; c < H; c += blockDim.x * V) {
-      float g[V], v[V];
-      RV::unpack(RV::load(gy.at(t) + c), g);
-      RV::unpack(RV::load(h.at(t) + c), v);
+    typename RV::Raw kg[NV], kh[NV], ke[NV];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        a.s = fmaf(v[i], v[i], a.s);
-        b.s = fmaf(gain ? g[i] * __ldg(gain + c + i) : g[i], v[i], b.s);
+    for (int j = 0; j < NV; ++j)
+      if (c0 + j * step < H) {
+        kg[j] = RV::load(gy.at(t) + c0 + j * step);
+        kh[j] = RV::load(h.at(t) + c0 + j * step);
+        if (gh.p) ke[j] = RV::load_rw(gh.at(t) + c0 + j * step);
       }
-    }
-    a = block_sum_max(a, part);
-    b = block_sum_max(b, part);
-    const float r = 1.0f / sqrtf(a.s / (float)H + eps);
-    const float m = r * (b.s / (float)H);            // mean(u n)
-    for (int c = threadIdx.x * V; c < H; c += blockDim.x * V) {
-      float g[V], v[V], o[V], e[V];
-      RV::unpack(RV::load(gy.at(t) + c), g);
-      RV::unpack(RV::load(h.at(t) + c), v);
-      if (gh.p) RV::unpack(RV::load_rw(gh.at(t) + c), e);
+    float ss = 0.f, su = 0.f;
+    auto take = [&](int c, const typename RV::Raw& rg, const typename RV::Raw& rh) {
+      float d[V], v[V], g[V];
+      RV::unpack(rg, d);
+      RV::unpack(rh, v);
+      load_gain<V>(gain, c, g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float n = v[i] * r, u = gain ? g[i] * __ldg(gain + c + i) : g[i];
-        o[i] = r * (u - n * m);
+        ss = fmaf(v[i], v[i], ss);
+        su = fmaf(d[i] * g[i], v[i], su);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (c0 + j * step < H) take(c0 + j * step, kg[j], kh[j]);
+    if (WIDE)
+      for (int c = c0 + NV * step; c < H; c += step) take(c, RV::load(gy.at(t) + c), RV::load(h.at(t) + c));
+    row_reduce<0, false>(ss, su, part);
+    const float r = 1.0f / sqrtf(ss / (float)H + eps);
+    const float m = r * (su / (float)H);             // mean(u n)
+    auto give = [&](int c, const typename RV::Raw& rg, const typename RV::Raw& rh, const typename RV::Raw& re, float (&dg)[V]) {
+      float d[V], v[V], g[V], e[V], o[V];
+      RV::unpack(rg, d);
+      RV::unpack(rh, v);
+      if (gh.p) RV::unpack(re, e);
+      load_gain<V>(gain, c, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float n = v[i] * r;
+        o[i] = r * (d[i] * g[i] - n * m);
         if (gh.p) o[i] += e[i];
-        if (mine) mine[c + i] = first ? g[i] * n : mine[c + i] + g[i] * n;
+        dg[i] = fmaf(d[i], n, dg[i]);
       }
       RV::store(gx.at(t) + c, RV::pack(o));
-    }
-    first = false;
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (c0 + j * step < H) give(c0 + j * step, kg[j], kh[j], ke[j], acc[j]);
+    if (WIDE)
+      for (int c = c0 + NV * step; c < H; c += step) {
+        float dg[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) dg[i] = mine && t != blockIdx.x ? mine[c + i] : 0.f;
+        const typename RV::Raw rg = RV::load(gy.at(t) + c);
+        give(c, rg, RV::load(h.at(t) + c), gh.p ? RV::load_rw(gh.at(t) + c) : rg, dg);
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) mine[c + i] = dg[i];
+        }
+      }
+  }
+  if (mine) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c0 + j * step < H) mine[c0 + j * step + i] = acc[j][i];
   }
 }
 
-__global__ void __launch_bounds__(256) sum_partials_kernel(const float* __restrict__ partial, int G, int H,
-                                                           float* __restrict__ out) {
+// out[c] = sum over G rows of partial: 32 columns a block, 32 groups of rows, joined in order.
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* __restrict__ partial, int G, int H,
+                                                            float* __restrict__ out) {
+  __shared__ float sum[32][33];
   ops_begin();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= H) return;
+  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float a = 0.f;
-  for (int g = 0; g < G; ++g) a += partial[(size_t)g * H + c];
-  out[c] = a;
+  if (c < H) {
+#pragma unroll 4
+    for (int g = grp; g < G; g += 32) a += partial[(size_t)g * H + c];
+  }
+  sum[grp][lane] = a;
+  __syncthreads();
+  a = warp_sum(sum[lane][grp]);                      // warp `grp`: column grp of the block
+  if (lane == 0 && blockIdx.x * 32 + grp < H) out[blockIdx.x * 32 + grp] = a;
 }
 
+// Units a thread keeps, and threads: a warp takes a row of up to 64 units; a block has at most 256
+// threads of up to 4 units where that holds the row, else as many as there may be.
 template <typename T, int V, bool Q>
 moe_status norm_launch(const Rows<const T>& x, const Rows<const T>& res, const float* gain, float eps, int T_, int H,
                        const Rows<T>& h, const Rows<T>& y, const Rows<uint8_t>& q, float* scale, void* s) {
   const int units = (H + V - 1) / V;
-  const int threads = std::min(1024, std::max(32, (units + 3) / 4 + 31 & ~31));
-  return launch_op(add_rms_norm_kernel<T, V, 4, Q>, dim3(T_), threads, 0, 1, s, x, res, gain, eps, H, h, y, q, scale);
+  if (units <= 64)
+    return launch_op(add_rms_norm_kernel<T, V, 2, 32, Q>, dim3((unsigned)((T_ + 3LL) / 4)), 128, 0, 1, s, x, res, gain, eps,
+                     T_, H, h, y, q, scale);
+  const int most = V == 1 ? 1024 : 512;
+  const int threads = std::min(most, ((units + 3) / 4 + 31) & ~31);
+  return launch_op(add_rms_norm_kernel<T, V, 4, 0, Q>, dim3(T_), threads, 0, 1, s, x, res, gain, eps, T_, H, h, y, q,
+                   scale);
 }
 
 template <typename T>
@@ -205,7 +288,8 @@ moe_status norm_dispatch(const void* x, int64_t ldx, const void* res, int64_t ld
   const Rows<T> hr{static_cast<T*>(h), ldh};
   const Rows<T> yr{scale ? nullptr : static_cast<T*>(y), ldy};
   const Rows<uint8_t> qr{scale ? static_cast<uint8_t*>(y) : nullptr, ldy};
-  const bool wide = H % N == 0 && rows16(x, ldx, sizeof(T)) && rows16(res, ldr, sizeof(T)) && rows16(h, ldh, sizeof(T));
+  const bool wide = H % N == 0 && rows16(x, ldx, sizeof(T)) && rows16(res, ldr, sizeof(T)) && rows16(h, ldh, sizeof(T)) &&
+                    aligned16(gain);
   if (scale) {
     if (wide && reinterpret_cast<uintptr_t>(y) % N == 0 && ldy % N == 0)
       return norm_launch<T, N, true>(xr, rr, gain, eps, T_, H, hr, yr, qr, scale, s);
@@ -216,9 +300,26 @@ moe_status norm_dispatch(const void* x, int64_t ldx, const void* res, int64_t ld
   return norm_launch<T, 1, false>(xr, rr, gain, eps, T_, H, hr, yr, qr, scale, s);
 }
 
-// Blocks of the backward pass: the rows of `partial`.
-constexpr int kNormBwdBlocks = 304;
-int norm_bwd_blocks(int T_) { return std::min(T_, kNormBwdBlocks); }
+// Blocks of the backward pass, the rows of `partial`: two an SM, more of them where rows are short.
+#ifndef NORM_BWD_BLOCKS
+#define NORM_BWD_BLOCKS 304
+#endif
+int norm_bwd_blocks(int T_, int H) { return std::min(T_, NORM_BWD_BLOCKS * std::max(1, std::min(8, 2048 / H))); }
+
+template <typename T, int V>
+moe_status norm_backward_launch(int G, const Rows<const T>& gy, const Rows<const T>& h, const float* gain, float eps, int T_,
+                                int H, const Rows<const T>& gh, const Rows<T>& gx, float* partial, void* s) {
+  const int units = (H + V - 1) / V, most = V == 1 ? 1024 : 512;
+  const int nv = units <= 256 ? 1 : units <= 512 ? 2 : 4;
+  const int threads = std::min(most, ((units + nv - 1) / nv + 31) & ~31);
+  auto go = [&](auto kernel) {
+    return launch_op(kernel, dim3(G), threads, 0, 1, s, gy, h, gain, eps, T_, H, gh, gx, partial);
+  };
+  if (units > 4 * most) return go(rms_norm_backward_kernel<T, V, 2, true>);
+  if (nv == 1) return go(rms_norm_backward_kernel<T, V, 1, false>);
+  if (nv == 2) return go(rms_norm_backward_kernel<T, V, 2, false>);
+  return go(rms_norm_backward_kernel<T, V, 4, false>);
+}
 
 template <typename T>
 moe_status norm_backward_dispatch(const void* gy, int64_t ldgy, const void* h, int64_t ldh, const float* gain, float eps,
@@ -228,16 +329,14 @@ moe_status norm_backward_dispatch(const void* gy, int64_t ldgy, const void* h, i
   const Rows<const T> a{static_cast<const T*>(gy), ldgy}, b{static_cast<const T*>(h), ldh},
       c{static_cast<const T*>(gh), ldgh};
   const Rows<T> o{static_cast<T*>(gx), ldgx};
-  const int G = norm_bwd_blocks(T_);
+  const int G = norm_bwd_blocks(T_, H);
   float* partial = ggain ? ws : nullptr;
   const bool wide = H % N == 0 && rows16(gy, ldgy, sizeof(T)) && rows16(h, ldh, sizeof(T)) &&
-                    rows16(gh, ldgh, sizeof(T)) && rows16(gx, ldgx, sizeof(T));
-  moe_status st = wide ? launch_op(rms_norm_backward_kernel<T, N>, dim3(G), 256, 0, 1, s, a, b, gain, eps, T_, H, c, o,
-                                   partial)
-                       : launch_op(rms_norm_backward_kernel<T, 1>, dim3(G), 256, 0, 1, s, a, b, gain, eps, T_, H, c, o,
-                                   partial);
+                    rows16(gh, ldgh, sizeof(T)) && rows16(gx, ldgx, sizeof(T)) && aligned16(gain);
+  const moe_status st = wide ? norm_backward_launch<T, N>(G, a, b, gain, eps, T_, H, c, o, partial, s)
+                             : norm_backward_launch<T, 1>(G, a, b, gain, eps, T_, H, c, o, partial, s);
   if (st != MOE_OK || !ggain) return st;
-  return launch_op(sum_partials_kernel, dim3((H + 255) / 256), 256, 0, 1, s, (const float*)ws, G, H, ggain);
+  return launch_op(sum_partials_kernel, dim3((H + 31) / 32), 1024, 0, 1, s, (const float*)ws, G, H, ggain);
 }
 
 }  // namespace
@@ -263,7 +362,7 @@ moe_status moe_async_add_rms_norm(int32_t dtype, const void* d_x, int64_t x_stri
 }
 
 int64_t moe_async_add_rms_norm_backward_workspace(int32_t T, int32_t H) {
-  return T < 1 || H < 1 ? 0 : (int64_t)norm_bwd_blocks(T) * H * (int64_t)sizeof(float);
+  return T < 1 || H < 1 ? 0 : (int64_t)norm_bwd_blocks(T, H) * H * (int64_t)sizeof(float);
 }
 
 moe_status moe_async_add_rms_norm_backward(int32_t dtype, const void* d_grad, int64_t grad_stride, const void* d_h,
