@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, 1)
   row_reduce<G, true>(ss, mx, part);
   const float r = 1.0f / sqrtf(ss / (float)H + eps);
   const float sc = max_nan(r * mx * (1.0f / kE4m3Max), kMinScale), inv = 1.0f / sc;
+  const float ri = Q && sc > kMinScale ? r * inv : r, last = Q && !(sc > kMinScale) ? inv : 1.f;   // r * inv stays finite
   if (Q && tid == 0) scale[t] = sc;
   auto give = [&](int c, const typename RV::Raw& raw) {
     float v[V], g[V];
@@ -146,8 +147,8 @@ __global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, 1)
     load_gain<V>(gain, c, g);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      v[i] = v[i] * g[i] * r;
-      if (Q) v[i] *= inv;
+      v[i] = v[i] * g[i] * ri;
+      if (Q && last != 1.f) v[i] *= last;
     }
     if constexpr (Q)
       store_e4m3<V>(q.at(t) + c, v);
@@ -163,31 +164,40 @@ __global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, 1)
 
 // Rows blockIdx.x, + gridDim.x, ...  A thread keeps its columns: up to NV units of the row and of
 // the gain's gradient stay in its registers; every block leaves the sum of grad_y * n over its
-// rows in its row of `partial` [gridDim.x, H] (WIDE: columns behind those units are read again,
-// and added up there).
+// rows in its row of `partial` [gridDim.x, H].  Bound by memory, so with NV <= 2 the next row is
+// asked for before this one is reduced.  WIDE: columns behind the NV units are read again, and
+// added up in `partial`.
 template <typename T, int V, int NV, bool WIDE>
 __global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
     rms_norm_backward_kernel(Rows<const T> gy, Rows<const T> h, const float* __restrict__ gain, float eps, int T_, int H,
                              Rows<const T> gh, Rows<T> gx, float* __restrict__ partial) {
   using RV = RowVec<T, V>;
+  constexpr bool kAhead = NV <= 2 && !WIDE;
   __shared__ float2 part[32];
   ops_begin();
   float* mine = partial ? partial + (size_t)blockIdx.x * H : nullptr;
   const int step = blockDim.x * V, c0 = threadIdx.x * V;
+  struct Row {
+    typename RV::Raw g[NV], h[NV], e[NV];
+  };
+  auto load = [&](Row& r, long long t) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (c0 + j * step < H && t < T_) {
+        r.g[j] = RV::load(gy.at(t) + c0 + j * step);
+        r.h[j] = RV::load(h.at(t) + c0 + j * step);
+        if (gh.p) r.e[j] = RV::load_rw(gh.at(t) + c0 + j * step);
+      }
+  };
   float acc[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
+  Row now, next;
+  load(now, blockIdx.x);
   for (long long t = blockIdx.x; t < T_; t += gridDim.x) {
-    typename RV::Raw kg[NV], kh[NV], ke[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (c0 + j * step < H) {
-        kg[j] = RV::load(gy.at(t) + c0 + j * step);
-        kh[j] = RV::load(h.at(t) + c0 + j * step);
-        if (gh.p) ke[j] = RV::load_rw(gh.at(t) + c0 + j * step);
-      }
+    if (kAhead) load(next, t + gridDim.x);
     float ss = 0.f, su = 0.f;
     auto take = [&](int c, const typename RV::Raw& rg, const typename RV::Raw& rh) {
       float d[V], v[V], g[V];
@@ -202,7 +212,7 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
     };
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (c0 + j * step < H) take(c0 + j * step, kg[j], kh[j]);
+      if (c0 + j * step < H) take(c0 + j * step, now.g[j], now.h[j]);
     if (WIDE)
       for (int c = c0 + NV * step; c < H; c += step) take(c, RV::load(gy.at(t) + c), RV::load(h.at(t) + c));
     row_reduce<0, false>(ss, su, part);
@@ -225,7 +235,7 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
     };
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (c0 + j * step < H) give(c0 + j * step, kg[j], kh[j], ke[j], acc[j]);
+      if (c0 + j * step < H) give(c0 + j * step, now.g[j], now.h[j], now.e[j], acc[j]);
     if (WIDE)
       for (int c = c0 + NV * step; c < H; c += step) {
         float dg[V];
@@ -238,6 +248,10 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
           for (int i = 0; i < V; ++i) mine[c + i] = dg[i];
         }
       }
+    if (kAhead)
+      now = next;
+    else
+      load(now, t + gridDim.x);
   }
   if (mine) {
 #pragma unroll
@@ -300,17 +314,15 @@ moe_status norm_dispatch(const void* x, int64_t ldx, const void* res, int64_t ld
   return norm_launch<T, 1, false>(xr, rr, gain, eps, T_, H, hr, yr, qr, scale, s);
 }
 
-// Blocks of the backward pass, the rows of `partial`: two an SM, more of them where rows are short.
-#ifndef NORM_BWD_BLOCKS
-#define NORM_BWD_BLOCKS 304
-#endif
-int norm_bwd_blocks(int T_, int H) { return std::min(T_, NORM_BWD_BLOCKS * std::max(1, std::min(8, 2048 / H))); }
+// Blocks of the backward pass, the rows of `partial`: one an SM for rows of 8192 columns, more where
+// they are short.
+int norm_bwd_blocks(int T_, int H) { return std::min(T_, 152 * std::max(1, std::min(16, 9216 / H))); }
 
 template <typename T, int V>
 moe_status norm_backward_launch(int G, const Rows<const T>& gy, const Rows<const T>& h, const float* gain, float eps, int T_,
                                 int H, const Rows<const T>& gh, const Rows<T>& gx, float* partial, void* s) {
   const int units = (H + V - 1) / V, most = V == 1 ? 1024 : 512;
-  const int nv = units <= 256 ? 1 : units <= 512 ? 2 : 4;
+  const int nv = units <= 128 ? 1 : units <= 2 * most ? 2 : 4;
   const int threads = std::min(most, ((units + nv - 1) / nv + 31) & ~31);
   auto go = [&](auto kernel) {
     return launch_op(kernel, dim3(G), threads, 0, 1, s, gy, h, gain, eps, T_, H, gh, gx, partial);

@@ -12,54 +12,86 @@
 // is the same on every run: no float atomics anywhere.
 #include <algorithm>
 #include "moe_ops.cuh"
+#include "moe_ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-
 // ------------------------------------------------------------------ sort_experts
 
-// One block, a stable counting sort: every warp owns a contiguous range of pairs and a histogram
-// of its own; an exclusive scan over (expert, warp) turns the histograms into first positions;
-// the warps walk their ranges again and hand out positions in pair order.  Bucket E holds the
-// pairs that belong to no expert here, behind all others.
-__global__ void __launch_bounds__(kSortThreads) sort_experts_kernel(const int32_t* __restrict__ expert, int P, int E,
-                                                                    int32_t* __restrict__ offsets,
-                                                                    int32_t* __restrict__ pos,
-                                                                    int32_t* __restrict__ pair) {
-  extern __shared__ int hist[];                      // [warps][E + 1]
-  __shared__ int wsum[kSortWarps];
-  const int NB = E + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * NB; i += kSortThreads) hist[i] = 0;
+// A stable counting sort in one launch by one cluster of C CTAs.  Every warp owns a contiguous range
+// of pairs and a histogram of its own; the scan over (expert, CTA, warp) turns the histograms into
+// first positions, the CTAs' totals passing through distributed shared memory; the warps walk
+// their ranges again and hand out positions in pair order.  Bucket E holds the pairs that belong
+// to no expert here, behind all others.  Bound by latency (2 M pairs are 25 MB): eight loads are in
+// flight per lane, and ranges of up to kKeep x 32 pairs stay in registers between the two walks.
+constexpr int kKeep = 8;
+constexpr int kSortCluster = 8;
+
+__global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __restrict__ expert, int P, int E, int per,
+                                                            int32_t* __restrict__ offsets, int32_t* __restrict__ pos,
+                                                            int32_t* __restrict__ pair) {
+  extern __shared__ int sh[];
+  __shared__ int wsum[32];
+  const int NB = E + 1, warps = blockDim.x >> 5;
+  int* hist = sh;                                    // [warps][E + 1]
+  int* total = sh + warps * NB;                      // [E + 1] each: this CTA's pairs, all CTAs', first positions
+  int* all = total + NB;
+  int* first = all + NB;
+  const int C = gridDim.x, rank = blockIdx.x;        // the grid is one cluster
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < warps * NB; i += blockDim.x) hist[i] = 0;
   ops_begin();
   __syncthreads();
-  const int per = ((P + kSortWarps - 1) / kSortWarps + 31) & ~31;
-  const long long p0 = (long long)warp * per;
-  const long long p1 = min((long long)P, p0 + per);
+  const long long p0 = min((long long)P, (long long)(rank * warps + warp) * per), p1 = min((long long)P, p0 + per);
   int* h = hist + warp * NB;
-  for (long long i = p0 + lane; i < p1; i += 32) {
-    const int e = expert[i];
-    atomicAdd(&h[e >= 0 && e < E ? e : E], 1);
+  auto bucket = [&](long long i) {
+    const int e = i < p1 ? __ldg(expert + i) : -1;
+    return e >= 0 && e < E ? e : E;
+  };
+  int keep[kKeep];                                   // the first kKeep x 32 of the range
+  for (long long i0 = p0; i0 < p1; i0 += 32 * kKeep) {
+    int b[kKeep];
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) b[u] = bucket(i0 + 32 * u + lane);
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+      if (i0 + 32 * u + lane < p1) atomicAdd(&h[b[u]], 1);
+      if (i0 == p0) keep[u] = b[u];
+    }
   }
   __syncthreads();
-  // exclusive scan in (bucket, warp) order: two buckets a thread cover 1025 of them
-  int tot[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int b = 2 * threadIdx.x + u;
+  // exclusive scan over the warps per bucket, and this CTA's totals
+  for (int b = tid; b < NB; b += blockDim.x) {
     int s = 0;
-    if (b < NB)
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = hist[w * NB + b];
-        hist[w * NB + b] = s;
-        s += c;
-      }
-    tot[u] = s;
+    for (int w = 0; w < warps; ++w) {
+      const int c = hist[w * NB + b];
+      hist[w * NB + b] = s;
+      s += c;
+    }
+    total[b] = s;
   }
-  int s = tot[0] + tot[1], incl = s;
+  if (C > 1) ptx::cluster_sync(); else __syncthreads();
+  for (int b = tid; b < NB; b += blockDim.x) {       // over all CTAs, and over those before this one
+    int n[kSortCluster], sum = 0, before = 0;
+#pragma unroll
+    for (int r = 0; r < kSortCluster; ++r)
+      n[r] = r < C ? (C > 1 ? ptx::ld_cluster_s32(ptx::mapa(ptx::smem_u32(total + b), r)) : total[b]) : 0;
+#pragma unroll
+    for (int r = 0; r < kSortCluster; ++r) {
+      sum += n[r];
+      if (r < rank) before += n[r];
+    }
+    all[b] = sum;
+    first[b] = before;
+  }
+  if (C > 1) ptx::cluster_arrive();
+  __syncthreads();
+  // a bucket's first position: everything in the buckets before it, then its pairs of the CTAs before
+  const int each = (NB + blockDim.x - 1) / blockDim.x;
+  int mine = 0;
+  for (int b = tid * each; b < min(NB, (tid + 1) * each); ++b) mine += all[b];
+  int incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int o = __shfl_up_sync(0xffffffffu, incl, off);
@@ -67,41 +99,48 @@ __global__ void __launch_bounds__(kSortThreads) sort_experts_kernel(const int32_
   }
   if (lane == 31) wsum[warp] = incl;
   __syncthreads();
-  int start = incl - s;
+  int start = incl - mine;
   for (int w = 0; w < warp; ++w) start += wsum[w];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int b = 2 * threadIdx.x + u;
-    if (b < NB) {
-      for (int w = 0; w < kSortWarps; ++w) hist[w * NB + b] += start;
-      offsets[b] = start;                           // bucket E starts where the last expert ends
-    }
-    start += tot[u];
+  for (int b = tid * each; b < min(NB, (tid + 1) * each); ++b) {
+    if (rank == 0) offsets[b] = start;               // bucket E starts where the last expert ends
+    first[b] += start;
+    start += all[b];
   }
   __syncthreads();
-  for (long long i0 = p0; i0 < p1; i0 += 32) {
-    const long long i = i0 + lane;
-    const int e = i < p1 ? expert[i] : -2;
-    const int b = i < p1 ? (e >= 0 && e < E ? e : E) : NB;
-    const unsigned same = __match_any_sync(0xffffffffu, b);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    int base = 0;
-    if (i < p1) base = h[b];
-    __syncwarp();
-    if (i < p1 && rank == 0) h[b] = base + __popc(same);
-    __syncwarp();
-    if (i < p1) {
-      pos[i] = b < E ? base + rank : -1;
-      pair[base + rank] = (int)i;
+  for (int b = tid; b < NB; b += blockDim.x)
+    for (int w = 0; w < warps; ++w) hist[w * NB + b] += first[b];
+  __syncthreads();
+  for (long long i0 = p0; i0 < p1; i0 += 32 * kKeep) {
+    int b[kKeep];
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) b[u] = i0 == p0 ? keep[u] : bucket(i0 + 32 * u + lane);
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) {
+      const long long i = i0 + 32 * u + lane;
+      if (i0 + 32 * u >= p1) break;
+      const int key = i < p1 ? b[u] : NB;            // lanes behind the range form a group of their own
+      const unsigned same = __match_any_sync(0xffffffffu, key);
+      const int at = __popc(same & ((1u << lane) - 1u));
+      const int base = i < p1 ? h[key] : 0;
+      __syncwarp();
+      if (i < p1 && at == 0) h[key] = base + __popc(same);
+      __syncwarp();
+      if (i < p1) {
+        pos[i] = key < E ? base + at : -1;
+        pair[base + at] = (int)i;
+      }
     }
   }
+  __syncwarp();
+  if (C > 1) ptx::cluster_wait();                    // no CTA ends while another reads its totals
 }
 
 // ------------------------------------------------------------------ sort_rows
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256;       // most threads of a block; a row's units are spread evenly over its blocks
 
-// Block (t, part): its part of token t's row, read once and written to the rows of its pairs.
+// Block (t, part): a thread reads one unit of token t's row and writes it to the rows of its pairs.
+// Bound by the writes.
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) sort_rows_kernel(Rows<const T> x, const int32_t* __restrict__ pos, int K,
                                                                 int H, long long R, Rows<T> rows) {
@@ -109,9 +148,8 @@ __global__ void __launch_bounds__(kRowThreads) sort_rows_kernel(Rows<const T> x,
   ops_begin();
   const long long t = blockIdx.x;
   const int32_t* pt = pos + t * K;
-  const T* src = x.at(t);
-  for (int c = (blockIdx.y * kRowThreads + threadIdx.x) * V; c < H; c += gridDim.y * kRowThreads * V) {
-    const typename RV::Raw v = RV::load(src + c);
+  for (long long c = ((long long)blockIdx.y * blockDim.x + threadIdx.x) * V; c < H; c += (long long)gridDim.y * blockDim.x * V) {
+    const typename RV::Raw v = RV::load(x.at(t) + c);
     for (int k = 0; k < K; ++k) {
       const int p = __ldg(pt + k);
       if (p >= 0 && p < R) RV::store(rows.at(p) + c, v);
@@ -122,8 +160,9 @@ __global__ void __launch_bounds__(kRowThreads) sort_rows_kernel(Rows<const T> x,
 // ------------------------------------------------------------------ merge_rows
 
 // Block (t, part): products and sums rounded in fp32 in ascending k, as in the collect kernel,
-// then the residual; rounded to T once.  w == nullptr: plain sum.
-template <typename T, int V>
+// then the residual; rounded to T once.  w == nullptr: plain sum.  A thread owns one unit of the
+// row and asks for KU result rows' units (and the residual's) before it uses the first.
+template <typename T, int V, int KU>
 __global__ void __launch_bounds__(kRowThreads) merge_rows_kernel(Rows<const T> rows, long long R,
                                                                  const int32_t* __restrict__ pos,
                                                                  const float* __restrict__ w, int K, int H,
@@ -131,23 +170,36 @@ __global__ void __launch_bounds__(kRowThreads) merge_rows_kernel(Rows<const T> r
   using RV = RowVec<T, V>;
   ops_begin();
   const long long t = blockIdx.x;
-  const int32_t* pt = pos + t * K;
-  for (int c = (blockIdx.y * kRowThreads + threadIdx.x) * V; c < H; c += gridDim.y * kRowThreads * V) {
+  for (long long c = ((long long)blockIdx.y * blockDim.x + threadIdx.x) * V; c < H; c += (long long)gridDim.y * blockDim.x * V) {
     float a[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) a[i] = 0.f;
-    for (int k = 0; k < K; ++k) {
-      const int p = __ldg(pt + k);
-      if (p < 0 || p >= R) continue;
-      float v[V];
-      RV::unpack(RV::load(rows.at(p) + c), v);
-      const float wk = w ? __ldg(w + t * K + k) : 1.f;
+    typename RV::Raw last;
+    if (residual.p) last = RV::load_rw(residual.at(t) + c);
+    for (int k0 = 0; k0 < K; k0 += KU) {
+      typename RV::Raw raw[KU];
+      int p[KU];
 #pragma unroll
-      for (int i = 0; i < V; ++i) a[i] = __fadd_rn(a[i], __fmul_rn(wk, v[i]));
+      for (int u = 0; u < KU; ++u) {
+        p[u] = k0 + u < K ? __ldg(pos + t * K + k0 + u) : -1;
+        if (p[u] >= R) p[u] = -1;
+      }
+#pragma unroll
+      for (int u = 0; u < KU; ++u)
+        if (p[u] >= 0) raw[u] = RV::load(rows.at(p[u]) + c);
+#pragma unroll
+      for (int u = 0; u < KU; ++u)
+        if (p[u] >= 0) {
+          float v[V];
+          RV::unpack(raw[u], v);
+          const float wk = w ? __ldg(w + t * K + k0 + u) : 1.f;
+#pragma unroll
+          for (int i = 0; i < V; ++i) a[i] = __fadd_rn(a[i], __fmul_rn(wk, v[i]));
+        }
     }
     if (residual.p) {
       float v[V];
-      RV::unpack(RV::load_rw(residual.at(t) + c), v);
+      RV::unpack(last, v);
 #pragma unroll
       for (int i = 0; i < V; ++i) a[i] = __fadd_rn(a[i], v[i]);
     }
@@ -155,36 +207,40 @@ __global__ void __launch_bounds__(kRowThreads) merge_rows_kernel(Rows<const T> r
   }
 }
 
-// Block t: grad_rows of its pairs and grad_w, kMergeK pairs at a time.
-constexpr int kMergeK = 8;
-template <typename T, int V>
+// Block t: grad_rows of its pairs and grad_w, KU pairs at a time, all their reads in flight.
+template <typename T, int V, int KU>
 __global__ void __launch_bounds__(kRowThreads)
     merge_rows_backward_kernel(Rows<const T> grad, Rows<const T> rows, long long R, const int32_t* __restrict__ pos,
                                const float* __restrict__ w, int K, int H, Rows<T> grad_rows,
                                float* __restrict__ grad_w) {
   using RV = RowVec<T, V>;
-  __shared__ float part[kRowThreads / 32][kMergeK];
+  __shared__ float part[kRowThreads / 32][KU];
   ops_begin();
   const long long t = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int k0 = 0; k0 < K; k0 += kMergeK) {
-    int p[kMergeK];
-    float wk[kMergeK], dot[kMergeK];
+  for (int k0 = 0; k0 < K; k0 += KU) {
+    int p[KU];
+    float wk[KU], dot[KU];
 #pragma unroll
-    for (int u = 0; u < kMergeK; ++u) {
+    for (int u = 0; u < KU; ++u) {
       p[u] = k0 + u < K ? __ldg(pos + t * K + k0 + u) : -1;
       if (p[u] >= R) p[u] = -1;
       wk[u] = k0 + u < K ? __ldg(w + t * K + k0 + u) : 0.f;
       dot[u] = 0.f;
     }
-    for (int c = threadIdx.x * V; c < H; c += kRowThreads * V) {
-      float g[V];
-      RV::unpack(RV::load(grad.at(t) + c), g);
+    for (int c = threadIdx.x * V; c < H; c += blockDim.x * V) {
+      const typename RV::Raw rg = RV::load(grad.at(t) + c);
+      typename RV::Raw raw[KU];
 #pragma unroll
-      for (int u = 0; u < kMergeK; ++u) {
+      for (int u = 0; u < KU; ++u)
+        if (p[u] >= 0) raw[u] = RV::load(rows.at(p[u]) + c);
+      float g[V];
+      RV::unpack(rg, g);
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
         if (p[u] >= 0) {
           float v[V], o[V];
-          RV::unpack(RV::load(rows.at(p[u]) + c), v);
+          RV::unpack(raw[u], v);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             dot[u] = fmaf(v[i], g[i], dot[u]);
@@ -195,14 +251,14 @@ __global__ void __launch_bounds__(kRowThreads)
       }
     }
 #pragma unroll
-    for (int u = 0; u < kMergeK; ++u) {
+    for (int u = 0; u < KU; ++u) {
       const float d = warp_sum(dot[u]);
       if (lane == 0) part[warp][u] = d;
     }
     __syncthreads();
-    if (threadIdx.x < kMergeK && k0 + threadIdx.x < K) {
+    if (threadIdx.x < KU && k0 + threadIdx.x < K) {
       float d = 0.f;
-      for (int i = 0; i < kRowThreads / 32; ++i) d += part[i][threadIdx.x];
+      for (int i = 0; i < (int)(blockDim.x >> 5); ++i) d += part[i][threadIdx.x];
       grad_w[t * K + k0 + threadIdx.x] = d;
     }
     __syncthreads();
@@ -240,46 +296,74 @@ bool valid_rows(int32_t dtype, int32_t T, int32_t K, int32_t H, int64_t R) {
          (int64_t)T * K <= INT32_MAX && R <= INT32_MAX;
 }
 
-// Blocks along a row: one covers kRowThreads vectors; few tokens spread their rows over more.
-int row_parts(int H, int v) { return std::max(1, std::min(65535, (H + kRowThreads * v - 1) / (kRowThreads * v))); }
+// A row's units over blocks of at most kRowThreads threads: blocks, and threads of each (whole warps).
+struct RowGrid {
+  int parts, threads;
+  RowGrid(int H, int v) {
+    const int units = (H + v - 1) / v;
+    parts = std::min(65535, (units + kRowThreads - 1) / kRowThreads);
+    threads = std::min(kRowThreads, ((units + parts - 1) / parts + 31) & ~31);
+  }
+};
+
+template <typename T, int V>
+moe_status sort_rows_launch(const Rows<const T>& x, const int32_t* pos, int T_, int K, int H, long long R, const Rows<T>& rows,
+                            void* s) {
+  const RowGrid g(H, V);
+  return launch_op(sort_rows_kernel<T, V>, dim3(T_, g.parts), g.threads, 0, 1, s, x, pos, K, H, R, rows);
+}
+
+template <typename T, int V>
+moe_status merge_rows_launch(const Rows<const T>& rows, long long R, const int32_t* pos, const float* w, int T_, int K, int H,
+                             const Rows<const T>& res, const Rows<T>& y, void* s) {
+  const RowGrid g(H, V);
+  const dim3 grid(T_, g.parts);
+  return K <= 4 ? launch_op(merge_rows_kernel<T, V, 4>, grid, g.threads, 0, 1, s, rows, R, pos, w, K, H, res, y)
+                : launch_op(merge_rows_kernel<T, V, 8>, grid, g.threads, 0, 1, s, rows, R, pos, w, K, H, res, y);
+}
+
+template <typename T, int V>
+moe_status merge_backward_launch(const Rows<const T>& grad, const Rows<const T>& rows, long long R, const int32_t* pos,
+                                 const float* w, int T_, int K, int H, const Rows<T>& grad_rows, float* grad_w, void* s) {
+  const RowGrid g(H, V);                             // one block: it takes the parts one after another
+  return K <= 4 ? launch_op(merge_rows_backward_kernel<T, V, 4>, dim3(T_), g.threads, 0, 1, s, grad, rows, R, pos, w, K, H,
+                            grad_rows, grad_w)
+                : launch_op(merge_rows_backward_kernel<T, V, 8>, dim3(T_), g.threads, 0, 1, s, grad, rows, R, pos, w, K, H,
+                            grad_rows, grad_w);
+}
 
 template <typename T>
-moe_status sort_rows_launch(const void* x, int64_t ldx, const int32_t* pos, int T_, int K, int H, int64_t R, void* rows,
-                            int64_t ldr, void* s) {
+moe_status sort_rows_dispatch(const void* x, int64_t ldx, const int32_t* pos, int T_, int K, int H, int64_t R, void* rows,
+                              int64_t ldr, void* s) {
   constexpr int N = Vec<T>::N;
   const Rows<const T> in{static_cast<const T*>(x), ldx};
   const Rows<T> out{static_cast<T*>(rows), ldr};
-  const long long r = R;
-  if (H % N == 0 && rows16(x, ldx, sizeof(T)) && rows16(rows, ldr, sizeof(T)))
-    return launch_op(sort_rows_kernel<T, N>, dim3(T_, row_parts(H, N)), kRowThreads, 0, 1, s, in, pos, K, H, r, out);
-  return launch_op(sort_rows_kernel<T, 1>, dim3(T_, row_parts(H, 1)), kRowThreads, 0, 1, s, in, pos, K, H, r, out);
+  return H % N == 0 && rows16(x, ldx, sizeof(T)) && rows16(rows, ldr, sizeof(T))
+             ? sort_rows_launch<T, N>(in, pos, T_, K, H, R, out, s)
+             : sort_rows_launch<T, 1>(in, pos, T_, K, H, R, out, s);
 }
 
 template <typename T>
-moe_status merge_rows_launch(const void* rows, int64_t ldr, int64_t R, const int32_t* pos, const float* w, int T_, int K,
-                             int H, const void* res, int64_t ldres, void* y, int64_t ldy, void* s) {
+moe_status merge_rows_dispatch(const void* rows, int64_t ldr, int64_t R, const int32_t* pos, const float* w, int T_, int K,
+                               int H, const void* res, int64_t ldres, void* y, int64_t ldy, void* s) {
   constexpr int N = Vec<T>::N;
   const Rows<const T> in{static_cast<const T*>(rows), ldr}, add{static_cast<const T*>(res), ldres};
   const Rows<T> out{static_cast<T*>(y), ldy};
-  const long long r = R;
-  if (H % N == 0 && rows16(rows, ldr, sizeof(T)) && rows16(res, ldres, sizeof(T)) && rows16(y, ldy, sizeof(T)))
-    return launch_op(merge_rows_kernel<T, N>, dim3(T_, row_parts(H, N)), kRowThreads, 0, 1, s, in, r, pos, w, K, H, add,
-                     out);
-  return launch_op(merge_rows_kernel<T, 1>, dim3(T_, row_parts(H, 1)), kRowThreads, 0, 1, s, in, r, pos, w, K, H, add,
-                   out);
+  return H % N == 0 && rows16(rows, ldr, sizeof(T)) && rows16(res, ldres, sizeof(T)) && rows16(y, ldy, sizeof(T))
+             ? merge_rows_launch<T, N>(in, R, pos, w, T_, K, H, add, out, s)
+             : merge_rows_launch<T, 1>(in, R, pos, w, T_, K, H, add, out, s);
 }
 
 template <typename T>
-moe_status merge_backward_launch(const void* grad, int64_t ldg, const void* rows, int64_t ldr, int64_t R,
-                                 const int32_t* pos, const float* w, int T_, int K, int H, void* grows, int64_t ldgr,
-                                 float* gw, void* s) {
+moe_status merge_backward_dispatch(const void* grad, int64_t ldg, const void* rows, int64_t ldr, int64_t R,
+                                   const int32_t* pos, const float* w, int T_, int K, int H, void* grows, int64_t ldgr,
+                                   float* gw, void* s) {
   constexpr int N = Vec<T>::N;
   const Rows<const T> g{static_cast<const T*>(grad), ldg}, in{static_cast<const T*>(rows), ldr};
   const Rows<T> out{static_cast<T*>(grows), ldgr};
-  const long long r = R;
-  if (H % N == 0 && rows16(grad, ldg, sizeof(T)) && rows16(rows, ldr, sizeof(T)) && rows16(grows, ldgr, sizeof(T)))
-    return launch_op(merge_rows_backward_kernel<T, N>, dim3(T_), kRowThreads, 0, 1, s, g, in, r, pos, w, K, H, out, gw);
-  return launch_op(merge_rows_backward_kernel<T, 1>, dim3(T_), kRowThreads, 0, 1, s, g, in, r, pos, w, K, H, out, gw);
+  return H % N == 0 && rows16(grad, ldg, sizeof(T)) && rows16(rows, ldr, sizeof(T)) && rows16(grows, ldgr, sizeof(T))
+             ? merge_backward_launch<T, N>(g, in, R, pos, w, T_, K, H, out, gw, s)
+             : merge_backward_launch<T, 1>(g, in, R, pos, w, T_, K, H, out, gw, s);
 }
 
 }  // namespace
@@ -292,12 +376,17 @@ moe_status moe_async_sort_experts(const int32_t* d_expert, int32_t T, int32_t K,
                                   int32_t* d_pos, int32_t* d_pair, void* stream) {
   if (T < 0 || K < 1 || K > 32 || E < 1 || E > kMaxExperts || (int64_t)T * K > INT32_MAX - 1024) return MOE_ERR_INVALID;
   if (!d_offsets || (T > 0 && (!d_expert || !d_pos || !d_pair))) return MOE_ERR_INVALID;
-  const size_t smem = (size_t)kSortWarps * (E + 1) * sizeof(int);
+  // 128 pairs a warp while that needs no more than 256 warps; over 32 of them, eight CTAs
+  const long long P = (long long)T * K;
+  const int all = (int)std::max<long long>(4, std::min<long long>(32 * kSortCluster, (P + 127) / 128));
+  const int ctas = all > 32 ? kSortCluster : 1, warps = (all + ctas - 1) / ctas;
+  const int per = (int)(((P + (long long)warps * ctas - 1) / ((long long)warps * ctas) + 31) & ~31LL);
+  const size_t smem = (size_t)(warps + 3) * (E + 1) * sizeof(int);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(sort_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
-  return launch_op(sort_experts_kernel, dim3(1), kSortThreads, smem, 1, stream, d_expert, T * K, E, d_offsets, d_pos,
-                   d_pair);
+  return launch_op(sort_experts_kernel, dim3(ctas), 32 * warps, smem, ctas, stream, d_expert, (int)P, E, per, d_offsets,
+                   d_pos, d_pair);
 }
 
 moe_status moe_async_sort_rows(int32_t dtype, const void* d_x, int64_t x_stride, const int32_t* d_pos, int32_t T,
@@ -306,8 +395,8 @@ moe_status moe_async_sort_rows(int32_t dtype, const void* d_x, int64_t x_stride,
   if (T == 0 || n_rows == 0) return MOE_OK;
   if (!d_x || !d_pos || !d_rows || x_stride < H || rows_stride < H) return MOE_ERR_INVALID;
   return dtype == MOE_BF16
-             ? sort_rows_launch<__nv_bfloat16>(d_x, x_stride, d_pos, T, K, H, n_rows, d_rows, rows_stride, stream)
-             : sort_rows_launch<float>(d_x, x_stride, d_pos, T, K, H, n_rows, d_rows, rows_stride, stream);
+             ? sort_rows_dispatch<__nv_bfloat16>(d_x, x_stride, d_pos, T, K, H, n_rows, d_rows, rows_stride, stream)
+             : sort_rows_dispatch<float>(d_x, x_stride, d_pos, T, K, H, n_rows, d_rows, rows_stride, stream);
 }
 
 moe_status moe_async_merge_rows(int32_t dtype, const void* d_rows, int64_t rows_stride, int64_t n_rows,
@@ -319,9 +408,9 @@ moe_status moe_async_merge_rows(int32_t dtype, const void* d_rows, int64_t rows_
   if ((n_rows > 0 && (!d_rows || rows_stride < H)) || !d_pos || !d_y || y_stride < H ||
       (d_residual && residual_stride < H))
     return MOE_ERR_INVALID;
-  return dtype == MOE_BF16 ? merge_rows_launch<__nv_bfloat16>(d_rows, rows_stride, n_rows, d_pos, d_w, T, K, H,
+  return dtype == MOE_BF16 ? merge_rows_dispatch<__nv_bfloat16>(d_rows, rows_stride, n_rows, d_pos, d_w, T, K, H,
                                                               d_residual, residual_stride, d_y, y_stride, stream)
-                           : merge_rows_launch<float>(d_rows, rows_stride, n_rows, d_pos, d_w, T, K, H, d_residual,
+                           : merge_rows_dispatch<float>(d_rows, rows_stride, n_rows, d_pos, d_w, T, K, H, d_residual,
                                                       residual_stride, d_y, y_stride, stream);
 }
 
@@ -335,9 +424,9 @@ moe_status moe_async_merge_rows_backward(int32_t dtype, const void* d_grad, int6
       (n_rows > 0 && (!d_rows || !d_grad_rows || rows_stride < H || grad_rows_stride < H)))
     return MOE_ERR_INVALID;
   return dtype == MOE_BF16
-             ? merge_backward_launch<__nv_bfloat16>(d_grad, grad_stride, d_rows, rows_stride, n_rows, d_pos, d_w, T, K,
+             ? merge_backward_dispatch<__nv_bfloat16>(d_grad, grad_stride, d_rows, rows_stride, n_rows, d_pos, d_w, T, K,
                                                     H, d_grad_rows, grad_rows_stride, d_grad_w, stream)
-             : merge_backward_launch<float>(d_grad, grad_stride, d_rows, rows_stride, n_rows, d_pos, d_w, T, K, H,
+             : merge_backward_dispatch<float>(d_grad, grad_stride, d_rows, rows_stride, n_rows, d_pos, d_w, T, K, H,
                                             d_grad_rows, grad_rows_stride, d_grad_w, stream);
 }
 
