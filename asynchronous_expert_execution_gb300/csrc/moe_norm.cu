@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 #include <algorithm>
 #include "moe_ops.cuh"
+#include "moe_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -24,19 +25,17 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Sum of a and, as MAX says, NaN-keeping maximum or sum of b, over the G threads of a row (32, or
-// the whole block), the same values in every thread.
-template <int G, bool MAX>
-__device__ __forceinline__ void row_reduce(float& a, float& b, float2* part) {
+// Sum of a and NaN-keeping maximum of b over the G threads of a row (32, or the whole block), the
+// same values in every thread.
+template <int G>
+__device__ __forceinline__ void row_sum_max(float& a, float& b, float2* part) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, off);
-    const float o = __shfl_xor_sync(0xffffffffu, b, off);
-    b = MAX ? max_nan(b, o) : b + o;
+    b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, off));
   }
   if (G == 32) return;
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();                                   // `part` may still be read for the row before
   if (lane == 0) part[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
   const float2 v = lane < warps ? part[lane] : make_float2(0.f, 0.f);
@@ -45,9 +44,31 @@ __device__ __forceinline__ void row_reduce(float& a, float& b, float2* part) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, off);
-    const float o = __shfl_xor_sync(0xffffffffu, b, off);
-    b = MAX ? max_nan(b, o) : b + o;
+    b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, off));
   }
+}
+
+// Four sums over the block at once, the same in every thread: the lanes hand each other half of
+// their values at a time, 6 shuffles instead of 20, and share the warps' sums alike.
+__device__ __forceinline__ void block_sum4(float (&v)[4], float (*part)[4]) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const bool hi = lane & 16, odd = lane & 8;
+  float a = hi ? v[2] : v[0], b = hi ? v[3] : v[1];
+  a += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+  b += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+  float c = odd ? b : a;
+  c += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
+  __syncthreads();                                   // `part` may still be read for the rows before
+  if ((lane & 7) == 0) part[threadIdx.x >> 5][lane >> 3] = c;
+  __syncthreads();
+  c = 0.f;
+  for (int w = lane >> 2; w < warps; w += 8) c += part[w][lane & 3];
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, c, i);
 }
 
 // The gain of a unit of V columns (all ones without one); wide units start on 16 bytes.
@@ -88,7 +109,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, const float (&v)[V]) {
 // registers, NV units a thread, all loads issued before the first is used; what lies behind
 // them is read again.
 template <typename T, int V, int NV, int G, bool Q>
-__global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, 1)
+__global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, G == 32 ? 8 : V == 1 ? 1 : 2)
     add_rms_norm_kernel(Rows<const T> x, Rows<const T> res, const float* __restrict__ gain, float eps, int T_, int H,
                         Rows<T> hout, Rows<T> y, Rows<uint8_t> q, float* __restrict__ scale) {
   using RV = RowVec<T, V>;
@@ -136,7 +157,7 @@ __global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, 1)
     return res.p ? sum(r, RV::load_rw(res.at(t) + c)) : r;
   };
   for (int c = c0 + NV * step; c < H; c += step) take(c, again(c));
-  row_reduce<G, true>(ss, mx, part);
+  row_sum_max<G>(ss, mx, part);
   const float r = 1.0f / sqrtf(ss / (float)H + eps);
   const float sc = max_nan(r * mx * (1.0f / kE4m3Max), kMinScale), inv = 1.0f / sc;
   const float ri = Q && sc > kMinScale ? r * inv : r, last = Q && !(sc > kMinScale) ? inv : 1.f;   // r * inv stays finite
@@ -162,96 +183,132 @@ __global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, 1)
   for (int c = c0 + NV * step; c < H; c += step) give(c, hout.p ? RV::load_rw(hout.at(t) + c) : again(c));
 }
 
-// Rows blockIdx.x, + gridDim.x, ...  A thread keeps its columns: up to NV units of the row and of
-// the gain's gradient stay in its registers; every block leaves the sum of grad_y * n over its
-// rows in its row of `partial` [gridDim.x, H].  Bound by memory, so with NV <= 2 the next row is
-// asked for before this one is reduced.  WIDE: columns behind the NV units are read again, and
-// added up in `partial`.
-template <typename T, int V, int NV, bool WIDE>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
+// Rows blockIdx.x, + gridDim.x, ..., two at a time.  A thread keeps its columns: up to NV units of
+// the rows and of the gain's gradient stay in its registers; every block leaves the sum of
+// grad_y * n over its rows in its row of `partial` [gridDim.x, H].  Bound by memory, and close
+// behind by the instructions between a row's reads and its writes: hence two rows in flight and
+// one reduction for both (one row at a time: 8192 x 2880 in 60 us, asking for the next one ahead
+// 58).  WIDE: columns behind the NV units are read again, and added up in `partial`.
+template <typename T, int V, int NV, bool WIDE, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS <= 384 ? 3 : 1)
     rms_norm_backward_kernel(Rows<const T> gy, Rows<const T> h, const float* __restrict__ gain, float eps, int T_, int H,
                              Rows<const T> gh, Rows<T> gx, float* __restrict__ partial) {
   using RV = RowVec<T, V>;
-  constexpr bool kAhead = NV <= 2 && !WIDE;
-  __shared__ float2 part[32];
+  using Raw = typename RV::Raw;
+  __shared__ float part[32][4];
   ops_begin();
   float* mine = partial ? partial + (size_t)blockIdx.x * H : nullptr;
   const int step = blockDim.x * V, c0 = threadIdx.x * V;
-  struct Row {
-    typename RV::Raw g[NV], h[NV], e[NV];
-  };
-  auto load = [&](Row& r, long long t) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (c0 + j * step < H && t < T_) {
-        r.g[j] = RV::load(gy.at(t) + c0 + j * step);
-        r.h[j] = RV::load(h.at(t) + c0 + j * step);
-        if (gh.p) r.e[j] = RV::load_rw(gh.at(t) + c0 + j * step);
-      }
-  };
   float acc[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
-  Row now, next;
-  load(now, blockIdx.x);
-  for (long long t = blockIdx.x; t < T_; t += gridDim.x) {
-    if (kAhead) load(next, t + gridDim.x);
-    float ss = 0.f, su = 0.f;
-    auto take = [&](int c, const typename RV::Raw& rg, const typename RV::Raw& rh) {
-      float d[V], v[V], g[V];
+  for (long long t0 = blockIdx.x; t0 < T_; t0 += 2LL * gridDim.x) {
+    Raw kg[2][NV], kh[2][NV], ke[2][NV];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const long long t = t0 + k * gridDim.x;
+        const int c = c0 + j * step;
+        if (c < H && t < T_) {
+          kg[k][j] = RV::load(gy.at(t) + c);
+          kh[k][j] = RV::load(h.at(t) + c);
+          if (gh.p) ke[k][j] = RV::load_rw(gh.at(t) + c);
+        }
+      }
+    // the next two rows into L2 while these are reduced: no registers, and every SM keeps reading
+    if (V > 1 && threadIdx.x % 8 == 0) {
+#pragma unroll
+      for (int k = 2; k < 4; ++k) {
+        const long long t = t0 + k * (long long)gridDim.x;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int c = c0 + j * step;
+          if (c < H && t < T_) {
+            ptx::prefetch_l2(gy.at(t) + c);
+            ptx::prefetch_l2(h.at(t) + c);
+            if (gh.p) ptx::prefetch_l2(gh.at(t) + c);
+          }
+        }
+      }
+    }
+    float s[4] = {0.f, 0.f, 0.f, 0.f};               // per row: sum of h^2, sum of u h
+    auto take = [&](int k, const float (&g)[V], const Raw& rg, const Raw& rh) {
+      float d[V], v[V];
       RV::unpack(rg, d);
       RV::unpack(rh, v);
-      load_gain<V>(gain, c, g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        ss = fmaf(v[i], v[i], ss);
-        su = fmaf(d[i] * g[i], v[i], su);
+        s[2 * k] = fmaf(v[i], v[i], s[2 * k]);
+        s[2 * k + 1] = fmaf(d[i] * g[i], v[i], s[2 * k + 1]);
       }
     };
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (c0 + j * step < H) take(c0 + j * step, now.g[j], now.h[j]);
+      if (c0 + j * step < H) {
+        float g[V];
+        load_gain<V>(gain, c0 + j * step, g);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (t0 + k * gridDim.x < T_) take(k, g, kg[k][j], kh[k][j]);
+      }
     if (WIDE)
-      for (int c = c0 + NV * step; c < H; c += step) take(c, RV::load(gy.at(t) + c), RV::load(h.at(t) + c));
-    row_reduce<0, false>(ss, su, part);
-    const float r = 1.0f / sqrtf(ss / (float)H + eps);
-    const float m = r * (su / (float)H);             // mean(u n)
-    auto give = [&](int c, const typename RV::Raw& rg, const typename RV::Raw& rh, const typename RV::Raw& re, float (&dg)[V]) {
-      float d[V], v[V], g[V], e[V], o[V];
+      for (int c = c0 + NV * step; c < H; c += step) {
+        float g[V];
+        load_gain<V>(gain, c, g);
+        for (int k = 0; k < 2; ++k) {
+          const long long t = t0 + k * gridDim.x;
+          if (t < T_) take(k, g, RV::load(gy.at(t) + c), RV::load(h.at(t) + c));
+        }
+      }
+    block_sum4(s, part);
+    float r[2], m[2];                                // 1 / rms; its square times mean(u h), which is mean(u n) / rms
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      r[k] = 1.0f / sqrtf(s[2 * k] / (float)H + eps);
+      m[k] = r[k] * r[k] * (s[2 * k + 1] / (float)H);
+    }
+    auto give = [&](int k, int c, const float (&g)[V], const Raw& rg, const Raw& rh, const Raw& re, float (&dg)[V]) {
+      float d[V], v[V], e[V], o[V];
       RV::unpack(rg, d);
       RV::unpack(rh, v);
       if (gh.p) RV::unpack(re, e);
-      load_gain<V>(gain, c, g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float n = v[i] * r;
-        o[i] = r * (d[i] * g[i] - n * m);
+        o[i] = r[k] * (d[i] * g[i] - v[i] * m[k]);
         if (gh.p) o[i] += e[i];
-        dg[i] = fmaf(d[i], n, dg[i]);
+        dg[i] = fmaf(d[i], v[i] * r[k], dg[i]);
       }
-      RV::store(gx.at(t) + c, RV::pack(o));
+      RV::store(gx.at(t0 + k * gridDim.x) + c, RV::pack(o));
     };
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (c0 + j * step < H) give(c0 + j * step, now.g[j], now.h[j], now.e[j], acc[j]);
+      if (c0 + j * step < H) {
+        float g[V];
+        load_gain<V>(gain, c0 + j * step, g);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (t0 + k * gridDim.x < T_) give(k, c0 + j * step, g, kg[k][j], kh[k][j], ke[k][j], acc[j]);
+      }
     if (WIDE)
       for (int c = c0 + NV * step; c < H; c += step) {
-        float dg[V];
+        float g[V], dg[V];
+        load_gain<V>(gain, c, g);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dg[i] = mine && t != blockIdx.x ? mine[c + i] : 0.f;
-        const typename RV::Raw rg = RV::load(gy.at(t) + c);
-        give(c, rg, RV::load(h.at(t) + c), gh.p ? RV::load_rw(gh.at(t) + c) : rg, dg);
+        for (int i = 0; i < V; ++i) dg[i] = mine && t0 != blockIdx.x ? mine[c + i] : 0.f;
+        for (int k = 0; k < 2; ++k) {
+          const long long t = t0 + k * gridDim.x;
+          if (t >= T_) break;
+          const Raw rg = RV::load(gy.at(t) + c);
+          give(k, c, g, rg, RV::load(h.at(t) + c), gh.p ? RV::load_rw(gh.at(t) + c) : rg, dg);
+        }
         if (mine) {
 #pragma unroll
           for (int i = 0; i < V; ++i) mine[c + i] = dg[i];
         }
       }
-    if (kAhead)
-      now = next;
-    else
-      load(now, t + gridDim.x);
   }
   if (mine) {
 #pragma unroll
@@ -270,8 +327,13 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* __restr
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float a = 0.f;
   if (c < H) {
-#pragma unroll 4
-    for (int g = grp; g < G; g += 32) a += partial[(size_t)g * H + c];
+    for (int g0 = grp; g0 < G; g0 += 32 * 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = g0 + 32 * u < G ? __ldg(partial + (size_t)(g0 + 32 * u) * H + c) : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) a += v[u];
+    }
   }
   sum[grp][lane] = a;
   __syncthreads();
@@ -316,21 +378,24 @@ moe_status norm_dispatch(const void* x, int64_t ldx, const void* res, int64_t ld
 
 // Blocks of the backward pass, the rows of `partial`: one an SM for rows of 8192 columns, more where
 // they are short.
-int norm_bwd_blocks(int T_, int H) { return std::min(T_, 152 * std::max(1, std::min(16, 9216 / H))); }
+int norm_bwd_blocks(int T_, int H) { return std::min(T_, 152 * std::max(1, std::min(8, 9216 / H))); }
 
 template <typename T, int V>
 moe_status norm_backward_launch(int G, const Rows<const T>& gy, const Rows<const T>& h, const float* gain, float eps, int T_,
                                 int H, const Rows<const T>& gh, const Rows<T>& gx, float* partial, void* s) {
-  const int units = (H + V - 1) / V, most = V == 1 ? 1024 : 512;
-  const int nv = units <= 128 ? 1 : units <= 2 * most ? 2 : 4;
-  const int threads = std::min(most, ((units + nv - 1) / nv + 31) & ~31);
+  const int units = (H + V - 1) / V;
+  const int threads = units <= 1024 ? (units + 31) & ~31 : 512;
   auto go = [&](auto kernel) {
     return launch_op(kernel, dim3(G), threads, 0, 1, s, gy, h, gain, eps, T_, H, gh, gx, partial);
   };
-  if (units > 4 * most) return go(rms_norm_backward_kernel<T, V, 2, true>);
-  if (nv == 1) return go(rms_norm_backward_kernel<T, V, 1, false>);
-  if (nv == 2) return go(rms_norm_backward_kernel<T, V, 2, false>);
-  return go(rms_norm_backward_kernel<T, V, 4, false>);
+  if (units <= 384) return go(rms_norm_backward_kernel<T, V, 1, false, 384>);      // three blocks an SM
+  if (units <= 1024) return go(rms_norm_backward_kernel<T, V, 1, false, 1024>);
+  if constexpr (V > 1) {
+    return go(rms_norm_backward_kernel<T, V, 2, true, 512>);        // four units spill
+  } else {
+    if (units <= 2048) return go(rms_norm_backward_kernel<T, V, 4, false, 512>);
+    return go(rms_norm_backward_kernel<T, V, 4, true, 512>);
+  }
 }
 
 template <typename T>
