@@ -129,7 +129,7 @@ def load():
         "moe_async_add_rms_norm": [I32, P, I64, P, I64, F32P, F32, I32, I32, P, I64, P, I64, F32P, P],
         "moe_async_add_rms_norm_backward": [I32, P, I64, P, I64, F32P, F32, I32, I32, P, I64, P, I64, F32P, P, I64, P],
         "moe_async_add_rms_norm_backward_workspace": [I32, I32],
-        "moe_async_linear": [P, P],                     # moe_async_linear_args, by reference or packed
+        "moe_async_linear": [ctypes.POINTER(LinearArgs), P],
         "moe_async_ops_status": [P],
     }
     restype = {"moe_async_status_string": ctypes.c_char_p, "moe_async_add_rms_norm_backward_workspace": I64}

@@ -5,13 +5,16 @@ compiled with MOE_DEBUG_BOUNDS, which checks every bucket, slot and k index the 
 back from device state and latches MOE_ERR_BOUNDS instead of touching memory out of range
 (loaded when the environment sets MOE_DEBUG_BOUNDS=1).  nvcc compiles every translation unit
 of both under ``csrc/`` in parallel and links each set into one shared object next to this
-file.  A rebuild is skipped when a library is newer than every source and header.
+file.  ``_ops.so`` is the Python binding of the stateless operators (g++ against torch, no
+device code; it calls whichever library was loaded).  A rebuild is skipped when a library is
+newer than every source and header.
 """
 import glob
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe_async.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_async_debug.so")
+BINDING = os.path.join(HERE, "_ops.so")
+BINDING_SRC = os.path.join(CSRC, "moe_binding.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 VARIANTS = {"release": (LIB, []), "debug": (LIB_DEBUG, ["-DMOE_DEBUG_BOUNDS=1"])}
 
@@ -45,18 +50,34 @@ def _stale(lib):
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [BINDING_SRC]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _binding_cmd(out):
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [x for p in cpp_extension.include_paths("cuda") for x in ("-isystem", p)]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *inc, "-I", sysconfig.get_paths()["include"], BINDING_SRC, "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu",
+            "-ltorch", "-lc10", "-lc10_cuda"]
 
 
 def build(force=False, verbose=False, variants=("release", "debug")):
     """Compile and link the requested libraries (all translation units of all of them in
     parallel); returns the release library's path."""
     todo = [v for v in variants if force or _stale(VARIANTS[v][0])]
-    if not todo:
+    binding = force or _stale(BINDING)
+    if not todo and not binding:
         return LIB
-    nvcc = _nvcc()
     procs, objs = [], {}
+    if binding:
+        cmd = _binding_cmd(BINDING + ".tmp")
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        procs.append((BINDING_SRC, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    nvcc = _nvcc() if todo else None
     for v in todo:
         bdir = os.path.join(BUILD_DIR, v)
         os.makedirs(bdir, exist_ok=True)
@@ -78,7 +99,9 @@ def build(force=False, verbose=False, variants=("release", "debug")):
             print(out.decode(errors="replace"), file=sys.stderr)
     if failed:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"compilation failed:\n{msg}")
+    if binding:
+        os.replace(BINDING + ".tmp", BINDING)
     for v in todo:
         lib = VARIANTS[v][0]
         tmp = lib + ".tmp"

@@ -83,16 +83,6 @@ def test_linear_refusals(nat):
         assert call(**kw) == N.MOE_ERR_UNSUPPORTED, kw
 
 
-def test_packed_linear_arguments_match_the_struct(nat):
-    """The binding packs the call's arguments itself: same size and places as the C struct."""
-    N, _ = nat
-    from asynchronous_expert_execution_gb300 import ops
-    values = list(range(1, 1 + len(N.LinearArgs._fields_)))
-    a = N.LinearArgs.from_buffer_copy(ops._LINEAR_ARGS.pack(*values))
-    assert ops._LINEAR_ARGS.size == ctypes.sizeof(N.LinearArgs)
-    assert [getattr(a, f) for f, _ in N.LinearArgs._fields_] == values
-
-
 def test_tensors_off_the_gpu_are_refused(nat):
     import asynchronous_expert_execution_gb300 as moe
     x, pos, w = torch.zeros((2, 8)), torch.zeros((2, 1), dtype=torch.int32), torch.zeros((2, 1))
