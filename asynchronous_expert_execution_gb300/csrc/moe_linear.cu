@@ -15,8 +15,8 @@
 // threads per 16 tokens, 17,000).
 //
 // Two kernels, chosen by linear_launch:
-//   pair   persistent, tiles of 256 features x up to 256 tokens over two SMs (cta_group::2): each
-//          SM stages half of both operands, which halves the shared-memory traffic per product.
+//   pair   persistent, tiles of 256 features x up to 256 tokens (128 for fp32 results) over two SMs
+//          (cta_group::2): each SM stages half of both operands, which halves the shared-memory traffic per product.
 //   split  one tile of 128 features x up to 64 tokens per cluster of up to 8 CTAs, K split over
 //          them; partials meet through distributed shared memory in rank order (no workspace,
 //          no atomics).  For few tiles: a lone SM streams weights far below the HBM rate.
@@ -41,6 +41,12 @@ constexpr int kBKBytes = 128;                      // K of a k-block (one swizzl
 constexpr int kABlock = kBM * kBKBytes;            // 16 KB
 constexpr int kThreads = 256;                      // warps: TMA, MMA, TMEM, spare, 4 x epilogue
 constexpr unsigned long long kLimitNs = 2000000000ull;
+// The tensor cores' fp32 sums cut what does not fit, so their error grows with the length of a sum
+// (bf16, 7168 deep, of the result's norm: 2.6e-6 in one sum, 1.4e-6 in sums of 22 k-blocks, 8.6e-7 in
+// sums of 14; plain fp32 products 2e-7 to 9e-7).  Results that are kept in fp32 are therefore summed in
+// chunks of up to this many k-blocks, which the epilogue adds with rounding (2048 x 7168 x 7168: 131 ->
+// 224 us, most of it the narrower tile); a bf16 result's own rounding is 1,000 times larger.
+constexpr int kChunkBlocks = 14;
 
 struct LinearParams {
   const float* bias;
@@ -236,7 +242,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.splits > 1 ? (int)cluster_rank() : 0;
   const int tile = blockIdx.x / p.splits;
-  const uint32_t cols = max(32, p.bn);
+  // fp32 results: K in up to four chunks with an accumulator each (see kChunkBlocks)
+  constexpr int kAccs = sizeof(TO) == 4 ? 4 : 1;
+  const uint32_t cols = max(32, kAccs * p.bn);
 
   if (threadIdx.x == 0) {
     prefetch_map(&p.w);
@@ -301,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
   const uint32_t tmem = s->tmem;
   const int kb0 = (int)((long long)l.nk * rank / p.splits), kb1 = (int)((long long)l.nk * (rank + 1) / p.splits);
   constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
+  const int chunks = min(kAccs, (kb1 - kb0 + kChunkBlocks - 1) / kChunkBlocks);
 
   if (nj > 0 && warp == 0 && lane == 0) {
     for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
@@ -314,14 +323,16 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
   } else if (nj > 0 && warp == 1 && lane == 0) {
     const uint32_t idesc = mma_desc<E4M3>(kBM, p.bn);
     bool ok = true;
-    for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
-      const int st = it % p.stages;
+    for (int kb = kb0, it = 0, chunk = -1; kb < kb1; ++kb, ++it) {
+      const int st = it % p.stages, now = it * chunks / (kb1 - kb0);
+      const bool first = now != chunk;
+      chunk = now;
       if (!(ok = wait(&s->full[st], (it / p.stages) & 1, abort_flag))) break;
       tc_after();
       const uint32_t a = smem_u32(smem + st * stage_bytes);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        mma<1, E4M3>(tmem, operand_desc(a + 32 * k), operand_desc(a + kABlock + 32 * k), idesc, kb > kb0 || k > 0);
+        mma<1, E4M3>(tmem + chunk * p.bn, operand_desc(a + 32 * k), operand_desc(a + kABlock + 32 * k), idesc, !first || k > 0);
       commit<1>(&s->empty[st]);
     }
     if (ok) commit<1>(&s->done);
@@ -339,6 +350,12 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
       for (int c = 0; c < nj; c += 16) {
         float v[16];
         tmem_ld16(t + c, v);
+        for (int ch = 1; ch < chunks; ++ch) {
+          float o[16];
+          tmem_ld16(t + ch * p.bn + c, o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] += o[j];
+        }
 #pragma unroll
         for (int j = 0; j < 16; ++j) own[(c + j) * kBM + row] = v[j];
       }
@@ -379,7 +396,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
 
 // ------------------------------------------------------------------ pair kernel
 
-constexpr int kPairTokens = 256;
+// tokens of a tile: two accumulators of 256 columns, or three of 128 that take the chunks of fp32 sums in
+// turn and 128 columns for the chunks' sum
+template <typename TO> constexpr int kPairTokens = sizeof(TO) == 4 ? 128 : 256;
 constexpr int kPairStages = 3;
 constexpr int kPairStage = 64 * 1024;                // 2 k-blocks of a full tile, 3 of a narrow one
 constexpr int kPairKpsMax = 3;
@@ -395,18 +414,20 @@ struct PairParams {
 };
 
 struct PairTail {
-  uint64_t full[kPairStages], empty[kPairStages], tfull[2], tempty[2];
+  uint64_t full[kPairStages], empty[kPairStages], tfull[4], tempty[4];
   uint32_t tmem;
   int abort_flag;
   int finishing;                    // tiles whose epilogue has begun
 };
 
 struct PairTile {
-  int g, row0, nj, fti, nmma, box, kps;
+  int g, row0, nj, fti, nmma, box, kps, chunk;   // chunk: k-blocks summed in one accumulator
 };
 
 // The tiles of a pair of CTAs, in order: t, t + pairs, ..  Every role walks the groups by itself.
+template <typename TO>
 struct PairWalk {
+  static constexpr int kTokens = kPairTokens<TO>;
   int t, g, base;                   // next tile; its group or an earlier one, and that group's first tile
   Span sp;
   __device__ PairWalk(const PairParams& p) : t(blockIdx.x / 2), g(0), base(0), sp(group_rows(p.l, 0)) {}
@@ -414,7 +435,7 @@ struct PairWalk {
   __device__ __forceinline__ bool next(const PairParams& p, PairTile& tl) {
     int ntt;
     while (true) {
-      ntt = (sp.n + kPairTokens - 1) / kPairTokens;
+      ntt = (sp.n + kTokens - 1) / kTokens;
       if (t - base < ntt * p.nft) break;
       base += ntt * p.nft;
       if (++g >= p.l.G) return false;
@@ -427,13 +448,14 @@ struct PairWalk {
     const int width = min(8, ntt - 8 * band);
     tl.g = g;
     tl.fti = local / width;
-    const int j0 = (8 * band + local % width) * kPairTokens;
+    const int j0 = (8 * band + local % width) * kTokens;
     tl.row0 = sp.a + j0;
-    tl.nj = min(kPairTokens, sp.n - j0);
+    tl.nj = min(kTokens, sp.n - j0);
     tl.nmma = (tl.nj + 31) & ~31;
     const int half = tl.nmma / 2;                    // token rows each CTA stages: a box that holds them
     tl.box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
     tl.kps = min(kPairKpsMax, kPairStage / (kABlock + (16 << tl.box) * kBKBytes));
+    tl.chunk = sizeof(TO) == 4 ? kChunkBlocks / tl.kps * tl.kps : p.l.nk;
     t += gridDim.x / 2;
     return true;
   }
@@ -449,7 +471,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const LinearParams& l = p.l;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
-  constexpr uint32_t kCols = 2 * kPairTokens;
+  constexpr int kTokens = kPairTokens<TO>, kAccs = sizeof(TO) == 4 ? 3 : 2;
+  constexpr uint32_t kCols = 512;
 
   if (threadIdx.x == 0) {
     prefetch_map(&p.w);
@@ -458,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(&s->full[i], 1);                     // the leader's producer, for both CTAs' bytes
       mbar_init(&s->empty[i], 1);                    // the MMA's commit, in both CTAs
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAccs; ++b) {
       mbar_init(&s->tfull[b], 1);
       mbar_init(&s->tempty[b], 16);                  // the epilogue warps of both CTAs, at the leader
     }
@@ -473,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_after();
   const uint32_t tmem = s->tmem;
-  PairWalk walk(p);
+  PairWalk<TO> walk(p);
   PairTile tl;
   constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
 
@@ -498,14 +521,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1 && lane == 0 && rank == 0) {
     uint32_t it = 0, acc = 0;
     bool ok = true;
-    for (; ok && walk.next(p, tl); ++acc) {
+    while (ok && walk.next(p, tl)) {
       const int block = kABlock + (16 << tl.box) * kBKBytes;
       const uint32_t idesc = mma_desc<E4M3>(2 * kBM, tl.nmma);
-      const int buf = acc & 1;
-      if (!(ok = wait(&s->tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag))) break;
-      tc_after();
-      const uint32_t d = tmem + buf * kPairTokens;
+      int buf = 0;
       for (int kb = 0; kb < l.nk; kb += tl.kps, ++it) {
+        if (kb % tl.chunk == 0) {
+          if (kb > 0) commit<2>(&s->tfull[buf]);
+          buf = acc % kAccs;
+          if (!(ok = wait(&s->tempty[buf], ((acc / kAccs) & 1) ^ 1, abort_flag))) break;
+          tc_after();
+          ++acc;
+        }
+        const uint32_t d = tmem + buf * kTokens;
         const int st = it % kPairStages, nv = min(tl.kps, l.nk - kb);
         if (!(ok = wait(&s->full[st], (it / kPairStages) & 1, abort_flag))) break;
         tc_after();
@@ -514,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const uint32_t a = a0 + j * block;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma<2, E4M3>(d, operand_desc(a + 32 * k), operand_desc(a + kABlock + 32 * k), idesc, kb + j > 0 || k > 0);
+            mma<2, E4M3>(d, operand_desc(a + 32 * k), operand_desc(a + kABlock + 32 * k), idesc, kb % tl.chunk + j > 0 || k > 0);
         }
         commit<2>(&s->empty[st]);
       }
@@ -540,16 +568,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..; two warps share a quarter's columns
     float* turn = reinterpret_cast<float*>(smem + kPairStages * kPairStage) + (warp - 4) * kTurn;
     uint32_t acc = 0;
-    for (; walk.next(p, tl); ++acc) {
-      if (threadIdx.x == 128) *reinterpret_cast<volatile int*>(&s->finishing) = acc + 1;
-      const int buf = acc & 1, f = tl.fti * 2 * kBM + rank * kBM + 32 * q;
-      const uint32_t d = tmem + ((uint32_t)(32 * q) << 16) + buf * kPairTokens;
+    // a warp's tokens: every other block of 32
+    constexpr bool kSums = sizeof(TO) == 4;
+    constexpr int kStep = 2 * kChunk;
+    auto acc_wait = [&](int buf, uint32_t n) {
+      const bool ok = wait(&s->tfull[buf], (n / kAccs) & 1, abort_flag);
+      const bool all = __all_sync(0xffffffffu, ok);
+      tc_after();
+      return all;
+    };
+    auto acc_done = [&](int buf) {
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&s->tempty[buf]), 0));
+    };
+    // `body(c)` for each of this warp's blocks of the tile, the block's sums in `turn`; false: a wait ran out
+    auto blocks = [&](auto body) {
+      const uint32_t d0 = tmem + ((uint32_t)(32 * q) << 16), sum = d0 + kAccs * kTokens;
+      const int chunks = kSums ? (l.nk + tl.chunk - 1) / tl.chunk : 1;
+      for (int ch = 0; ch + 1 < chunks; ++ch, ++acc) {         // all but the last chunk: into the sum's columns
+        const int buf = acc % kAccs;
+        if (!acc_wait(buf, acc)) return false;
+        for (int c = half * kChunk; c < tl.nj; c += c % kChunk ? kStep - 16 : 16) {
+          float v[16];
+          tmem_ld16(d0 + buf * kTokens + c, v);
+          if (ch > 0) {
+            float o[16];
+            tmem_ld16(sum + c, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += o[j];
+          }
+          tmem_st16(sum + c, v);
+        }
+        acc_done(buf);
+      }
+      const int buf = acc % kAccs;
+      if (!acc_wait(buf, acc)) return false;
+      ++acc;
+      for (int c = half * kChunk; c < tl.nj; c += kStep) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[16];
+          tmem_ld16(d0 + buf * kTokens + c + 16 * h, v);
+          if (kSums && chunks > 1) {
+            float o[16];
+            tmem_ld16(sum + c + 16 * h, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += o[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) turn[(16 * h + j) * 32 + (lane ^ ((j & 7) << 2))] = v[j];
+        }
+        __syncwarp();
+        body(c - half * kChunk);
+        __syncwarp();
+      }
+      acc_done(buf);
+      return true;
+    };
+    for (int tiles = 1; walk.next(p, tl); ++tiles) {
+      if (threadIdx.x == 128) *reinterpret_cast<volatile int*>(&s->finishing) = tiles;
+      const int f = tl.fti * 2 * kBM + rank * kBM + 32 * q;
+      bool ok;
       if (l.wide) {
         // 32 features x 32 tokens turned in the warp's own shared memory: lane i then holds 8
         // features (i % 4) of tokens i / 4 + 8 u, u < 4.  16-byte chunks of a token's row lie at
         // chunk ^ (token & 7): neither the writes nor the reads meet a bank twice.  mul and
         // residual are asked for kAt units ahead, the first ones before the products are done.
-        constexpr int kAt = sizeof(TO) == 2 ? 4 : 2;
+        constexpr int kAt = kSums ? 2 : 4;
         const int f8 = lane % 4, tk = lane / 4;
         const Finish<TO, 8> finish(l, tl.g, f + f8 * 8, 1);
         const Place<TO> place(l, tl.row0 + half * kChunk + tk, f + f8 * 8);
@@ -557,18 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         typename Finish<TO, 8>::Ahead a[kAt];
 #pragma unroll
         for (int u = 0; u < kAt; ++u) finish.ahead(a[u], place, 8 * u, 8 * u < mine);
-        const bool ok = wait(&s->tfull[buf], (acc >> 1) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_after();
-        for (int c = 0; c < kPairTokens && c + half * kChunk < tl.nj; c += 2 * kChunk) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float v[16];
-            tmem_ld16(d + c + half * kChunk + 16 * h, v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) turn[(16 * h + j) * 32 + (lane ^ ((j & 7) << 2))] = v[j];
-          }
-          __syncwarp();
+        ok = blocks([&](int c) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const float* row = turn + (tk + 8 * u) * 32;
@@ -576,40 +651,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const float4 y = *reinterpret_cast<const float4*>(row + ((2 * f8 + 1) ^ tk) * 4);
             float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
             if (c + 8 * u < mine) finish(w, place.y + (c + 8 * u) * l.ldy, a[u % kAt]);
-            const int nx = u + kAt < 4 ? c + 8 * (u + kAt) : c + 2 * kChunk + 8 * (u + kAt - 4);
+            const int nx = u + kAt < 4 ? c + 8 * (u + kAt) : c + kStep + 8 * (u + kAt - 4);
             finish.ahead(a[u % kAt], place, nx, nx < mine);
           }
-          __syncwarp();
-        }
+        });
       } else {
         // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens in flight
-        constexpr int kAt = 16;
+        constexpr int kAt = kSums ? 4 : 8;
         const Finish<TO, 1> finish(l, tl.g, f + lane, 1);
         const Place<TO> place(l, tl.row0 + half * kChunk, f + lane);
         const int mine = tl.nj - half * kChunk;
         typename Finish<TO, 1>::Ahead a[kAt];
 #pragma unroll
         for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, j, j < mine);
-        const bool ok = wait(&s->tfull[buf], (acc >> 1) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_after();
-        for (int c = 0; c < kPairTokens && c < mine;) {
-          const int next = c + (c % kChunk ? 2 * kChunk - 16 : 16);
-          float v[16];
-          tmem_ld16(d + c + half * kChunk, v);
+        ok = blocks([&](int c) {
+#pragma unroll 1
+          for (int j0 = 0; j0 < kChunk; j0 += kAt) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float w[1] = {v[j]};
-            if (c + j < mine) finish(w, place.y + (c + j) * l.ldy, a[j % kAt]);
-            const int nx = j + kAt < 16 ? c + j + kAt : next + j + kAt - 16;
-            finish.ahead(a[j % kAt], place, nx, nx < mine);
+            for (int j = 0; j < kAt; ++j) {
+              float w[1] = {turn[(j0 + j) * 32 + (lane ^ (((j0 + j) & 7) << 2))]};
+              if (c + j0 + j < mine) finish(w, place.y + (c + j0 + j) * l.ldy, a[j]);
+              const int nx = (j0 + kAt < kChunk ? c + j0 + kAt : c + kStep) + j;
+              finish.ahead(a[j], place, nx, nx < mine);
+            }
           }
-          c = next;
-        }
+        });
       }
-      tc_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&s->tempty[buf]), 0));
+      if (!ok) break;
     }
   }
   __syncwarp();
@@ -708,7 +776,9 @@ moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, 
   // tiles of 7168 deep 42.7 / 47.3, 56 of them 43.5 / 93, 24 of 2880 deep 21.6 / 21.8, 48 of them 21.9 /
   // 44; but 8 of 7168 deep 40.8 / 18.0, 16 of 592 deep 19.7 / 8.7), if the tiles are more than half full
   // (28 of 7168 deep: 128 tokens 37 / 29, one token 30.4 / 21.5).  Groups count at most one ragged tile each.
-  const int64_t wide = (int64_t)((l.N + 255) / 256) * (l.offsets ? l.T / 256 + std::min(l.G, l.T) : (l.T + 255) / 256);
+  constexpr int kTokens = kPairTokens<TO>;
+  const int64_t wide = (int64_t)((l.N + 255) / 256) *
+                       (l.offsets ? l.T / kTokens + std::min(l.G, l.T) : (l.T + kTokens - 1) / kTokens);
   const int64_t per = l.offsets ? (l.T + l.G - 1) / l.G : l.T;
   if (per > 2 * kSplitTokens && wide >= sms / 6) return launch_pair<E4M3, TO>(a, l, sms, s);
   const int bn = per <= 16 ? 16 : per <= 32 ? 32 : kSplitTokens;
