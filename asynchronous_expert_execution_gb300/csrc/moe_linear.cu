@@ -101,7 +101,7 @@ struct Place {
 // The end of the epilogue for one thread, which owns C features of every token it meets: first,
 // first + step, ...  C = 8, step = 1: rows of y, mul and residual move in 16-byte units; else
 // element by element.  Pointers are to a token's row at feature `first`.
-template <typename TO, int C>
+template <typename TO, int C, bool SCALED>
 struct Finish {
   static constexpr bool kWide = C == 8;
   static constexpr int kVecs = kWide ? C / Vec<TO>::N : C;
@@ -115,7 +115,7 @@ struct Finish {
     live = first >= q.N ? 0 : min(C, (q.N - first + step_ - 1) / step_);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      sw[i] = q.sw && i < live ? __ldg(q.sw + (size_t)g * q.N + first + i * step) : 1.f;
+      sw[i] = SCALED && i < live ? __ldg(q.sw + (size_t)g * q.N + first + i * step) : 1.f;
       bias[i] = q.bias && i < live ? __ldg(q.bias + (size_t)g * q.N + first + i * step) : 0.f;
     }
   }
@@ -128,7 +128,7 @@ struct Finish {
   __device__ __forceinline__ int at(int i) const { return kWide ? i * Vec<TO>::N : i * step; }
   // `token`: whether the token t behind the place's exists
   __device__ __forceinline__ void ahead(Ahead& a, const Place<TO>& place, int t, bool token) const {
-    a.sx = p.sx && token ? __ldg(place.sx + t) : 1.f;
+    if (SCALED) a.sx = token ? __ldg(place.sx + t) : 1.f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       if (p.mul && token && on(i)) a.m[i] = RV::load_rw(place.mul + t * p.ldmul + at(i));
@@ -136,7 +136,7 @@ struct Finish {
     }
   }
   __device__ __forceinline__ void operator()(float (&v)[C], TO* y, const Ahead& a) const {
-    if (p.sx) {
+    if (SCALED) {
 #pragma unroll
       for (int i = 0; i < C; ++i) v[i] *= a.sx * sw[i];
     }
@@ -196,15 +196,15 @@ struct SplitTail {                  // behind the stages
 
 // Tokens j0 + tk, + tks, .. < j1 of a tile at features f, f + step, ..: the ranks' partials summed in rank
 // order.  This rank's own lie at own [token][128], rank r's share for it at got + r * share [token - j0][128].
-template <typename TO, int C>
+template <typename TO, int C, bool SCALED>
 __device__ __forceinline__ void split_finish(const SplitParams& p, int g, int row0, int f0, const float* own, const float* got,
                                              int rank, int j0, int j1, int f, int step, int tk, int tks) {
   constexpr int kAt = C < 8 ? 4 : sizeof(TO) == 2 ? 2 : 1;              // tokens whose mul and residual are in flight
-  const Finish<TO, C> finish(p.l, g, f0 + f, step);
+  const Finish<TO, C, SCALED> finish(p.l, g, f0 + f, step);
   const Place<TO> place(p.l, row0 + j0, f0 + f);
   const int share = (j1 - j0) * kBM;
   for (int jb = tk; jb < j1 - j0; jb += kAt * tks) {
-    typename Finish<TO, C>::Ahead a[kAt];
+    typename Finish<TO, C, SCALED>::Ahead a[kAt];
 #pragma unroll
     for (int u = 0; u < kAt; ++u) finish.ahead(a[u], place, jb + u * tks, jb + u * tks < j1 - j0);
 #pragma unroll
@@ -380,9 +380,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
   }
   if (nj > 0) {                                      // every rank sums and finishes its share of the tokens
     if (l.wide)
-      split_finish<TO, 8>(p, g, row0, fti * kBM, own, got, rank, j0, j1, threadIdx.x % 16 * 8, 1, threadIdx.x / 16, kThreads / 16);
+      split_finish<TO, 8, E4M3>(p, g, row0, fti * kBM, own, got, rank, j0, j1, threadIdx.x % 16 * 8, 1, threadIdx.x / 16, kThreads / 16);
     else
-      split_finish<TO, 4>(p, g, row0, fti * kBM, own, got, rank, j0, j1, lane, 32, warp, kThreads / 32);
+      split_finish<TO, 4, E4M3>(p, g, row0, fti * kBM, own, got, rank, j0, j1, lane, 32, warp, kThreads / 32);
   }
   if (p.splits > 1) {
     __syncwarp();
@@ -637,10 +637,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // residual are asked for kAt units ahead, the first ones before the products are done.
         constexpr int kAt = kSums ? 2 : 4;
         const int f8 = lane % 4, tk = lane / 4;
-        const Finish<TO, 8> finish(l, tl.g, f + f8 * 8, 1);
+        const Finish<TO, 8, E4M3> finish(l, tl.g, f + f8 * 8, 1);
         const Place<TO> place(l, tl.row0 + half * kChunk + tk, f + f8 * 8);
         const int mine = tl.nj - half * kChunk - tk;           // tokens from this lane's first to the tile's end
-        typename Finish<TO, 8>::Ahead a[kAt];
+        typename Finish<TO, 8, E4M3>::Ahead a[kAt];
 #pragma unroll
         for (int u = 0; u < kAt; ++u) finish.ahead(a[u], place, 8 * u, 8 * u < mine);
         ok = blocks([&](int c) {
@@ -657,11 +657,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         });
       } else {
         // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens in flight
-        constexpr int kAt = kSums ? 4 : 8;
-        const Finish<TO, 1> finish(l, tl.g, f + lane, 1);
+        constexpr int kAt = kSums ? 4 : E4M3 ? 8 : 16;
+        const Finish<TO, 1, E4M3> finish(l, tl.g, f + lane, 1);
         const Place<TO> place(l, tl.row0 + half * kChunk, f + lane);
         const int mine = tl.nj - half * kChunk;
-        typename Finish<TO, 1>::Ahead a[kAt];
+        typename Finish<TO, 1, E4M3>::Ahead a[kAt];
 #pragma unroll
         for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, j, j < mine);
         ok = blocks([&](int c) {

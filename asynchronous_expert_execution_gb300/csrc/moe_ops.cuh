@@ -47,11 +47,11 @@ __device__ __forceinline__ void ops_begin() {
 }
 
 template <typename... KArgs, typename... Args>
-moe_status launch_op(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, int cluster, void* stream,
+moe_status launch_op(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster, void* stream,
                      Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
+  cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
