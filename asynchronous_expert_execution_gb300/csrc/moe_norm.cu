@@ -218,22 +218,6 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 384 ? 3 : 1)
           if (gh.p) ke[k][j] = RV::load_rw(gh.at(t) + c);
         }
       }
-    // the next two rows into L2 while these are reduced: no registers, and every SM keeps reading
-    if (V > 1 && threadIdx.x % 8 == 0) {
-#pragma unroll
-      for (int k = 2; k < 4; ++k) {
-        const long long t = t0 + k * (long long)gridDim.x;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int c = c0 + j * step;
-          if (c < H && t < T_) {
-            ptx::prefetch_l2(gy.at(t) + c);
-            ptx::prefetch_l2(h.at(t) + c);
-            if (gh.p) ptx::prefetch_l2(gh.at(t) + c);
-          }
-        }
-      }
-    }
     float s[4] = {0.f, 0.f, 0.f, 0.f};               // per row: sum of h^2, sum of u h
     auto take = [&](int k, const float (&g)[V], const Raw& rg, const Raw& rh) {
       float d[V], v[V];
@@ -319,6 +303,87 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 384 ? 3 : 1)
   }
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The same for rows of at most 1024 16-byte units: one unit a thread, which copies it for the next
+// two rows into its own slots of shared memory while it works on these (no barrier: nobody else
+// reads them), so every SM keeps reading, and holds no operand in registers across the reduction.
+template <typename T>
+__global__ void __launch_bounds__(1024, 1)
+    rms_norm_backward_ring_kernel(Rows<const T> gy, Rows<const T> h, const float* __restrict__ gain, float eps, int T_, int H,
+                                  Rows<const T> gh, Rows<T> gx, float* __restrict__ partial) {
+  constexpr int V = Vec<T>::N;
+  using RV = RowVec<T, V>;
+  extern __shared__ uint4 slots[];                   // [2 stages][2 rows][grad_y, h, grad_h][thread]
+  __shared__ float part[32][4];
+  ops_begin();
+  const int c = threadIdx.x * V;
+  const bool live = c < H;
+  auto slot = [&](int stage, int k, int o) { return slots + ((stage * 2 + k) * 3 + o) * blockDim.x + threadIdx.x; };
+  auto fetch = [&](int stage, long long t0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long t = t0 + k * (long long)gridDim.x;
+      if (live && t < T_) {
+        copy16(ptx::smem_u32(slot(stage, k, 0)), gy.at(t) + c);
+        copy16(ptx::smem_u32(slot(stage, k, 1)), h.at(t) + c);
+        if (gh.p) copy16(ptx::smem_u32(slot(stage, k, 2)), gh.at(t) + c);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float acc[V], g[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  if (live) load_gain<V>(gain, c, g);
+  int stage = 0;
+  fetch(0, blockIdx.x);
+  for (long long t0 = blockIdx.x; t0 < T_; t0 += 2LL * gridDim.x, stage ^= 1) {
+    fetch(stage ^ 1, t0 + 2LL * gridDim.x);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    float s[4] = {0.f, 0.f, 0.f, 0.f};               // per row: sum of h^2, sum of u h
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (live && t0 + k * (long long)gridDim.x < T_) {
+        float d[V], v[V];
+        RV::unpack(*slot(stage, k, 0), d);
+        RV::unpack(*slot(stage, k, 1), v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          s[2 * k] = fmaf(v[i], v[i], s[2 * k]);
+          s[2 * k + 1] = fmaf(d[i] * g[i], v[i], s[2 * k + 1]);
+        }
+      }
+    block_sum4(s, part);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long t = t0 + k * (long long)gridDim.x;
+      const float r = 1.0f / sqrtf(s[2 * k] / (float)H + eps);
+      const float m = r * r * (s[2 * k + 1] / (float)H);     // mean(u n) / rms
+      if (live && t < T_) {
+        float d[V], v[V], e[V], o[V];
+        RV::unpack(*slot(stage, k, 0), d);
+        RV::unpack(*slot(stage, k, 1), v);
+        if (gh.p) RV::unpack(*slot(stage, k, 2), e);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          o[i] = r * (d[i] * g[i] - v[i] * m);
+          if (gh.p) o[i] += e[i];
+          acc[i] = fmaf(d[i], v[i] * r, acc[i]);
+        }
+        RV::store(gx.at(t) + c, RV::pack(o));
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (partial && live) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) partial[(size_t)blockIdx.x * H + c + i] = acc[i];
+  }
+}
+
 // out[c] = sum over G rows of partial: 32 columns a block, 32 groups of rows, joined in order.
 __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* __restrict__ partial, int G, int H,
                                                             float* __restrict__ out) {
@@ -388,11 +453,18 @@ moe_status norm_backward_launch(int G, const Rows<const T>& gy, const Rows<const
   auto go = [&](auto kernel) {
     return launch_op(kernel, dim3(G), threads, 0, 1, s, gy, h, gain, eps, T_, H, gh, gx, partial);
   };
-  if (units <= 384) return go(rms_norm_backward_kernel<T, V, 1, false, 384>);      // three blocks an SM
-  if (units <= 1024) return go(rms_norm_backward_kernel<T, V, 1, false, 1024>);
   if constexpr (V > 1) {
+    if (units <= 1024) {
+      const size_t smem = (size_t)12 * 16 * threads;
+      if (cudaFuncSetAttribute(rms_norm_backward_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * 16 * 1024) !=
+          cudaSuccess)
+        return MOE_ERR_CUDA;
+      return launch_op(rms_norm_backward_ring_kernel<T>, dim3(G), threads, smem, 1, s, gy, h, gain, eps, T_, H, gh, gx, partial);
+    }
     return go(rms_norm_backward_kernel<T, V, 2, true, 512>);        // four units spill
   } else {
+    if (units <= 384) return go(rms_norm_backward_kernel<T, V, 1, false, 384>);    // three blocks an SM
+    if (units <= 1024) return go(rms_norm_backward_kernel<T, V, 1, false, 1024>);
     if (units <= 2048) return go(rms_norm_backward_kernel<T, V, 4, false, 512>);
     return go(rms_norm_backward_kernel<T, V, 4, true, 512>);
   }
