@@ -7,6 +7,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -133,35 +134,34 @@ Tensor output(PyObject* out, const char* name, int dev, ScalarType dtype, int64_
   return t;
 }
 
-// The call's device made current while it runs, and its stream.
+// The call's device and stream, made current while it runs: what the call allocates belongs to that
+// stream, so memory that other streams gave back is not written before they are done with it.
 struct On {
-  c10::DeviceIndex prev;
   int dev;
-  void* stream;
-  On(int d, PyObject* s) : prev(c10::cuda::current_device()), dev(d) {
+  cudaStream_t stream;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  c10::cuda::OptionalCUDAGuard device;
+  On(int d, PyObject* s) : dev(d) {
     if (s == Py_None) {
+      if (c10::cuda::current_device() != d) device.set_index(static_cast<c10::DeviceIndex>(d));
       stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(d)).stream();
-    } else {
-      PyObject* v = PyObject_GetAttrString(s, "cuda_stream");
-      if (!v) throw PythonError{};
-      stream = PyLong_AsVoidPtr(v);
-      Py_DECREF(v);
-      if (PyErr_Occurred()) throw PythonError{};
+      return;
     }
-    if (prev != dev) c10::cuda::set_device(static_cast<c10::DeviceIndex>(dev));
-  }
-  ~On() {
-    if (prev != dev) c10::cuda::set_device(prev);
+    PyObject* v = PyObject_GetAttrString(s, "cuda_stream");
+    if (!v) throw PythonError{};
+    stream = static_cast<cudaStream_t>(PyLong_AsVoidPtr(v));
+    Py_DECREF(v);
+    if (PyErr_Occurred()) throw PythonError{};
+    guard.reset_stream(c10::cuda::getStreamFromExternal(stream, static_cast<c10::DeviceIndex>(d)));
   }
 };
 
 template <typename F>
-void call(const char* what, int dev, PyObject* stream, F f) {
-  On on(dev, stream);
+void call(const char* what, const On& on, F f) {
   int status;
   PyThreadState* state = PyEval_SaveThread();        // a launch may wait for room in the stream
   try {
-    status = f(on.stream);
+    status = f(static_cast<void*>(on.stream));
   } catch (...) {
     PyEval_RestoreThread(state);
     throw;
@@ -191,12 +191,13 @@ PyObject* tuple(std::initializer_list<PyObject*> items) {
 PyObject* sort_experts(PyObject* const* a) {
   const Tensor& expert = tensor(a[0], "expert");
   const Lead l = lead(expert, "expert", {at::kInt});
+  const On on(l.dev, a[2]);
   if (!expert.is_contiguous()) bad("expert: expected contiguous", expert);
   const int64_t E = integer(a[1], "num_experts");
   if (E < 1) bad("num_experts: expected at least 1");
   const int32_t T = count(l.n, "tokens"), K = count(l.width, "top_k");
   Tensor offsets = empty({E + 1}, at::kInt, l.dev), pos = empty({T, K}, at::kInt, l.dev), pair = empty({l.n * l.width}, at::kInt, l.dev);
-  call("sort_experts", l.dev, a[2], [&](void* s) {
+  call("sort_experts", on, [&](void* s) {
     return lib.sort_experts(ptr<int32_t>(expert), T, K, static_cast<int32_t>(E), ptr<int32_t>(offsets), ptr<int32_t>(pos),
                             ptr<int32_t>(pair), s);
   });
@@ -207,11 +208,12 @@ PyObject* sort_experts(PyObject* const* a) {
 PyObject* sort_rows(PyObject* const* a) {
   const Tensor &x = tensor(a[0], "x"), &pos = tensor(a[1], "pos");
   const Lead l = lead(x, "x", {at::kFloat, at::kBFloat16});
+  const On on(l.dev, a[3]);
   const int64_t K = pairs(pos, l.dev);
   if (pos.size(0) != l.n) bad("pos: expected a row per row of x", pos);
   int64_t ldo, R = a[2] == Py_None ? l.n * K : tensor(a[2], "out").dim() == 2 ? tensor(a[2], "out").size(0) : 0;
   const Tensor out = output(a[2], "out", l.dev, l.dtype, R, l.width, ldo);
-  call("sort_rows", l.dev, a[3], [&](void* s) {
+  call("sort_rows", on, [&](void* s) {
     return lib.sort_rows(code(l.dtype), ptr(x), l.ld, ptr<int32_t>(pos), count(l.n, "tokens"), count(K, "top_k"),
                          count(l.width, "width"), ptr(out), ldo, R, s);
   });
@@ -223,12 +225,13 @@ PyObject* merge_rows(PyObject* const* a) {
   const Tensor &r = tensor(a[0], "rows"), &pos = tensor(a[1], "pos");
   const Tensor *w = maybe(a[2], "w"), *res = maybe(a[3], "residual");
   const Lead l = lead(r, "rows", {at::kFloat, at::kBFloat16});
+  const On on(l.dev, a[5]);
   const int64_t K = pairs(pos, l.dev), T = pos.size(0);
   if (w) whole(*w, "w", l.dev, at::kFloat, {T, K});
   const int64_t ldres = res ? rows(*res, "residual", l.dev, l.dtype, T, l.width) : l.width;
   int64_t ldo;
   const Tensor out = output(a[4], "out", l.dev, l.dtype, T, l.width, ldo);
-  call("merge_rows", l.dev, a[5], [&](void* s) {
+  call("merge_rows", on, [&](void* s) {
     return lib.merge_rows(code(l.dtype), ptr(r), l.ld, l.n, ptr<int32_t>(pos), ptr<float>(w), count(T, "tokens"), count(K, "top_k"),
                           count(l.width, "width"), ptr(res), ldres, ptr(out), ldo, s);
   });
@@ -239,13 +242,14 @@ PyObject* merge_rows(PyObject* const* a) {
 PyObject* merge_rows_backward(PyObject* const* a) {
   const Tensor &grad = tensor(a[0], "grad"), &r = tensor(a[1], "rows"), &pos = tensor(a[2], "pos"), &w = tensor(a[3], "w");
   const Lead l = lead(r, "rows", {at::kFloat, at::kBFloat16});
+  const On on(l.dev, a[5]);
   const int64_t K = pairs(pos, l.dev), T = pos.size(0);
   whole(w, "w", l.dev, at::kFloat, {T, K});
   const int64_t ldg = rows(grad, "grad", l.dev, l.dtype, T, l.width);
   int64_t ldo;
   const Tensor out = output(a[4], "out", l.dev, l.dtype, l.n, l.width, ldo);
   Tensor grad_w = empty({T, K}, at::kFloat, l.dev);
-  call("merge_rows_backward", l.dev, a[5], [&](void* s) {
+  call("merge_rows_backward", on, [&](void* s) {
     return lib.merge_rows_backward(code(l.dtype), ptr(grad), ldg, ptr(r), l.ld, l.n, ptr<int32_t>(pos), ptr<float>(w),
                                    count(T, "tokens"), count(K, "top_k"), count(l.width, "width"), ptr(out), ldo,
                                    ptr<float>(grad_w), s);
@@ -257,13 +261,14 @@ PyObject* merge_rows_backward(PyObject* const* a) {
 PyObject* route_backward(PyObject* const* a) {
   const Tensor &idx = tensor(a[0], "idx"), &w = tensor(a[1], "w"), &grad_w = tensor(a[2], "grad_w");
   const Lead l = lead(w, "w", {at::kFloat});
+  const On on(l.dev, a[4]);
   whole(w, "w", l.dev, at::kFloat, {l.n, l.width});
   whole(idx, "idx", l.dev, at::kInt, {l.n, l.width});
   whole(grad_w, "grad_w", l.dev, at::kFloat, {l.n, l.width});
   const int64_t E = integer(a[3], "num_experts");
   if (E < 1) bad("num_experts: expected at least 1");
   Tensor out = empty({l.n, E}, at::kFloat, l.dev);
-  call("route_backward", l.dev, a[4], [&](void* s) {
+  call("route_backward", on, [&](void* s) {
     return lib.route_backward(ptr<int32_t>(idx), ptr<float>(w), ptr<float>(grad_w), count(l.n, "tokens"), static_cast<int32_t>(E),
                               count(l.width, "top_k"), ptr<float>(out), s);
   });
@@ -283,6 +288,7 @@ PyObject* add_rms_norm(PyObject* const* a) {
   const float eps = real(a[3]);
   const bool e4m3 = a[7] == Py_True;
   const Lead l = lead(x, "x", {at::kFloat, at::kBFloat16});
+  const On on(l.dev, a[6]);
   const int64_t T = l.n, H = l.width;
   if (gain) whole(*gain, "gain", l.dev, at::kFloat, {H});
   int64_t ldr = H, ldh = H, ldo;
@@ -296,7 +302,7 @@ PyObject* add_rms_norm(PyObject* const* a) {
   const Tensor out = output(a[4], "out", l.dev, e4m3 ? at::kFloat8_e4m3fn : l.dtype, T, H, ldo);
   Tensor scale;
   if (e4m3) scale = empty({T}, at::kFloat, l.dev);
-  call("add_rms_norm", l.dev, a[6], [&](void* s) {
+  call("add_rms_norm", on, [&](void* s) {
     return lib.add_rms_norm(code(l.dtype), ptr(x), l.ld, ptr(res), ldr, ptr<float>(gain), eps, count(T, "rows"), count(H, "width"),
                             res ? ptr(h) : nullptr, ldh, ptr(out), ldo, e4m3 ? ptr<float>(scale) : nullptr, s);
   });
@@ -309,6 +315,7 @@ PyObject* add_rms_norm_backward(PyObject* const* a) {
   const Tensor *gain = maybe(a[2], "gain"), *gh = maybe(a[4], "grad_h");
   const float eps = real(a[3]);
   const Lead l = lead(h, "h", {at::kFloat, at::kBFloat16});
+  const On on(l.dev, a[6]);
   const int64_t T = l.n, H = l.width;
   const int64_t ldg = rows(grad, "grad", l.dev, l.dtype, T, H), ldgh = gh ? rows(*gh, "grad_h", l.dev, l.dtype, T, H) : H;
   int64_t ldo, size = 0;
@@ -320,15 +327,11 @@ PyObject* add_rms_norm_backward(PyObject* const* a) {
     size = lib.norm_workspace(count(T, "rows"), count(H, "width"));
     ws = empty({size}, at::kByte, l.dev);
   }
-  call("add_rms_norm_backward", l.dev, a[6], [&](void* s) {
+  call("add_rms_norm_backward", on, [&](void* s) {
     return lib.add_rms_norm_backward(code(l.dtype), ptr(grad), ldg, ptr(h), l.ld, ptr<float>(gain), eps, count(T, "rows"),
                                      count(H, "width"), ptr(gh), ldgh, ptr(out), ldo, gain ? ptr<float>(grad_gain) : nullptr,
                                      gain ? ptr(ws) : nullptr, size, s);
   });
-  if (gain && a[6] != Py_None) {                     // the workspace is freed below, while the call may still run there
-    On on(l.dev, a[6]);
-    ws.record_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(on.stream), static_cast<c10::DeviceIndex>(l.dev)));
-  }
   return tuple({wrap(out), gain ? wrap(grad_gain) : same(Py_None)});
 }
 
@@ -339,6 +342,7 @@ PyObject* linear(PyObject* const* a) {
                *offsets = maybe(a[6], "offsets"), *sx = maybe(a[7], "x_scale"), *sw = maybe(a[8], "w_scale"),
                *given = maybe(a[10], "out");
   const Lead l = lead(x, "x", {at::kBFloat16, at::kFloat8_e4m3fn});
+  const On on(l.dev, a[11]);
   const bool e4m3 = l.dtype == at::kFloat8_e4m3fn;
   const int64_t T = l.n, F = l.width;
   moe_async_linear_args p = {};
@@ -392,7 +396,7 @@ PyObject* linear(PyObject* const* a) {
   p.d_residual = ptr(res);
   p.d_offsets = ptr<int32_t>(offsets);
   p.d_y = ptr(out);
-  call("linear", l.dev, a[11], [&](void* s) { return lib.linear(&p, s); });
+  call("linear", on, [&](void* s) { return lib.linear(&p, s); });
   return given ? same(a[10]) : wrap(out);
 }
 

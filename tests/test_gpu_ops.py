@@ -589,6 +589,82 @@ def test_given_stream_is_used(moe):
     assert bool(((y.float() - 1).abs() < 1e-2).all()) and bool((gg > 0).all())
 
 
+def test_outputs_of_a_given_stream_do_not_meet_the_current_stream(moe):
+    """stream=: what the call allocates comes from that stream's memory, not from what the current stream has
+    just given back while its kernels still read it."""
+    s = torch.cuda.Stream()
+    x = torch.ones((512, 4096), dtype=torch.bfloat16, device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        victim = torch.full((512, 4096), 5.0, dtype=torch.bfloat16, device="cuda")
+        torch.cuda._sleep(3_000_000)
+        keep = victim.clone()                        # reads victim when the sleep is over
+        del victim                                   # its memory is free again for the current stream only
+        y, _ = moe.add_rms_norm(x, stream=s)
+        s.synchronize()
+        assert bool((y == 1).all())
+        assert bool((keep == 5).all())
+
+
+BIG = [(300_000, 7200)]                              # 2.16e9 elements: offsets pass 32 bits
+
+
+@pytest.mark.parametrize("T,H", BIG)
+def test_offsets_beyond_32_bits(moe, T, H):
+    """The last rows of matrices of more than 2^31 elements."""
+    g = gen(21)
+    rows = torch.arange(T, device="cuda").remainder(97).to(torch.bfloat16)[:, None].expand(T, H).contiguous()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda").reshape(-1, 3)           # three pairs a token
+    w = torch.rand(pos.shape, generator=g, device="cuda")
+    y = moe.merge_rows(rows, pos, w)
+    ref = (rows[:, 0].double().reshape(-1, 3) * w.double()).sum(1)
+    assert float(((y[:, -1].double() - ref).abs() / (ref.abs() + 1e-9)).max()) < 2 ** -7 and torch.equal(y[:, 0], y[:, -1])
+    back = moe.sort_rows(y, pos)
+    assert torch.equal(back[:, -1], y[:, -1].repeat_interleave(3)) and torch.equal(back[-1], y[-1].clone())
+    del back
+    n, h = moe.add_rms_norm(rows, rows, out_h=rows)                                   # in place, twice the value
+    assert float(h[-1, -1]) == 2 * ((T - 1) % 97) and abs(float(n[-1, -1]) - 1) < 2 ** -7
+    del n, h, rows
+    x, wt = randn((T, 64), g, torch.bfloat16), randn((H, 64), g, torch.bfloat16)
+    out = moe.linear(x, wt)
+    ref = x[-300:].double() @ wt.double().T
+    close(out[-300:], ref, 65 * 2.0 ** -23 * (x[-300:].double().abs() @ wt.double().abs().T) + 2.0 ** -8 * 1.01 * ref.abs() + 1e-300, "far rows")
+    offsets = torch.tensor([0, 5, T - 1000, T], dtype=torch.int32, device="cuda")
+    w3 = torch.stack([wt, wt, 2 * wt])
+    out.zero_()
+    moe.linear(x, w3, offsets=offsets, out=out)
+    close(out[-300:], 2 * ref, 65 * 2.0 ** -22 * (x[-300:].double().abs() @ wt.double().abs().T) + 2.0 ** -7 * 1.01 * ref.abs() + 1e-300, "far group")
+
+
+def test_linear_with_many_groups(moe):
+    """1024 experts, most of them without a row."""
+    g = gen(22)
+    T, F, Nn, G = 700, 64, 40, 1024
+    of = torch.randint(0, G, (T,), generator=g, device="cuda").sort().values
+    of[:300] = 5                                     # one group of several tiles
+    of = of.sort().values
+    at = torch.searchsorted(of, torch.arange(G + 1, device="cuda")).to(torch.int32)
+    x, w = randn((T, F), g, torch.bfloat16), randn((G, Nn, F), g, torch.bfloat16)
+    for out in BOTH:
+        y = moe.linear(x, w, offsets=at, out_dtype=out)
+        ref = torch.einsum("tf,tnf->tn", x.double(), w.double()[of])
+        mag = torch.einsum("tf,tnf->tn", x.double().abs(), w.double().abs()[of])
+        close(y, ref, F * 2.0 ** -23 * mag + HALF[out] * 1.01 * ref.abs() + 1e-300, "many groups")
+
+
+@pytest.mark.parametrize("T,F,Nn", [(700, 7168, 2050), (1500, 2064, 1800), (300, 1040, 7168)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_long_fp32_sums_are_rounded_not_cut(moe, T, F, Nn, e4m3):
+    """fp32 results of long sums: the error of the whole matrix stays at rounded sums' level.  A chunk of at most 14
+    k-blocks is 56 matrix instructions, each of which may cut a whole step (2^-23) of its running sum: at most
+    56 / 2 steps on average over a growing sum, towards zero, and chunks add with rounding."""
+    g = gen(T)
+    x, w, kw = linear_inputs(T, F, Nn, e4m3, torch.float32, "", 0, g)
+    y = moe.linear(x, w, out_dtype=torch.float32, **kw)
+    ref, _ = linear_ref(x, w, kw, "none", torch.float32)
+    assert float((y.double() - ref).norm() / ref.norm()) <= 28 * 2.0 ** -23
+
+
 def test_no_wait_ran_out(moe):
     """After everything above: the operators' sticky device error is clear."""
     moe.ops_sync()
