@@ -61,7 +61,7 @@ def _binding_cmd(out):
     inc = [x for p in cpp_extension.include_paths("cuda") for x in ("-isystem", p)]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *inc, "-I", sysconfig.get_paths()["include"], BINDING_SRC, "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu",
-            "-ltorch", "-lc10", "-lc10_cuda"]
+            "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def build(force=False, verbose=False, variants=("release", "debug")):

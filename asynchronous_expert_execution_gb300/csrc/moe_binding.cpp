@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -120,7 +121,7 @@ int64_t pairs(const Tensor& pos, int dev) {
 }
 
 Tensor empty(at::IntArrayRef sizes, ScalarType dtype, int dev) {
-  return at::empty(sizes, at::TensorOptions().dtype(dtype).device(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev))));
+  return at::detail::empty_cuda(sizes, dtype, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
 }
 
 // `out` as handed in (checked), or a new matrix; its row stride in ld.
