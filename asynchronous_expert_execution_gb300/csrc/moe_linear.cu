@@ -5,7 +5,7 @@
 // x [T, F] and w [N, F] (or [G, N, F]: rows offsets[g] .. offsets[g + 1] of x meet w[g]) in bf16 or
 // e4m3, products summed in fp32, y in bf16 or fp32, rounded once.
 //
-// Weights are the MMA's 128 (or, over two SMs, 256) rows and tokens its columns, so one token and
+// Weights are the MMA's 128 (or, over two SMs, 256) rows and tokens its columns, so few tokens and
 // thousands run on the same tiles: D[feature, token], both operands K-major as they lie in
 // memory, tiles of 128 bytes of K by TMA, accumulators in TMEM.  The epilogue passes through
 // shared memory as [token][feature]: a thread of a TMEM lane writes its feature's column there,
@@ -14,12 +14,15 @@
 // of a 7168-deep e4m3 tile; turning a whole tile's features at once, with two barriers of 128
 // threads per 16 tokens, 17,000).
 //
-// Two kernels, chosen by linear_launch:
+// Three kernels, chosen by linear_launch:
 //   pair   persistent, tiles of 256 features x up to 256 tokens (128 for fp32 results) over two SMs
 //          (cta_group::2): each SM stages half of both operands, which halves the shared-memory traffic per product.
 //   split  one tile of 128 features x up to 64 tokens per cluster of up to 8 CTAs, K split over
 //          them; partials meet through distributed shared memory in rank order (no workspace,
 //          no atomics).  For few tiles: a lone SM streams weights far below the HBM rate.
+//   few    up to 16 tokens: weights straight into the registers of warp-wide matrix instructions.  Only
+//          the weights' bytes count there; barriers, TMEM and the exchange cost more than they bring
+//          (4 tokens on 2880 x 2880: 5.8 us against 7.8; 4096 x 16384 at 5.1 TB/s).
 //
 // Every wait is bounded (2 s): a wait that runs out stops all roles, latches MOE_ERR_TIMEOUT in
 // the operators' error word, and the CTA still frees its TMEM.
@@ -688,6 +691,141 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 2) tmem_dealloc<2>(tmem, kCols);
 }
 
+// ------------------------------------------------------------------ few tokens
+
+constexpr int kFewTokens = 16;
+constexpr int kFewThreads = 512;                     // at most
+
+struct FewParams {
+  const void* x;
+  const void* w;
+  int64_t ldx, ldw;
+  LinearParams l;
+};
+
+// c[16][8] += a b over 32 bytes of K, twice.  The 16 bytes that a lane loaded of each row (a, and a8 for the
+// rows 8 .. of the 16) stand for the same elements in both operands, and no order of K matters to the sum.
+template <bool E4M3>
+__device__ __forceinline__ void warp_mma(float (&c)[4], const uint4& a, const uint4& a8, const uint4& b) {
+#define MOE_WARP_MMA(SHAPE, A0, A1, A2, A3, B0, B1)                                                           \
+  asm("mma.sync.aligned." SHAPE " {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"                      \
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                                        \
+      : "r"(A0), "r"(A1), "r"(A2), "r"(A3), "r"(B0), "r"(B1))
+  if constexpr (E4M3) {
+    MOE_WARP_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32", a.x, a8.x, a.y, a8.y, b.x, b.y);
+    MOE_WARP_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32", a.z, a8.z, a.w, a8.w, b.z, b.w);
+  } else {
+    MOE_WARP_MMA("m16n8k16.row.col.f32.bf16.bf16.f32", a.x, a8.x, a.y, a8.y, b.x, b.y);
+    MOE_WARP_MMA("m16n8k16.row.col.f32.bf16.bf16.f32", a.z, a8.z, a.w, a8.w, b.z, b.w);
+  }
+#undef MOE_WARP_MMA
+}
+
+// An SM's share of HBM, 45 GB/s, wants some 40 KB under way: 512 threads ask for eight (FS + TS = 2), five or four
+// 16-byte units a row each before they use the first.  Sums on the CUDA cores instead took 6.5 us for one
+// token on 2880 x 2880 (5.8 here) and 17.6 for eight (6.0).
+// Block (b, i): 8 FS features of up to 8 TS tokens, those of the i-th group that has rows.  Each of its W
+// warps takes every W-th 64 bytes of K, kAhead of them in flight; their sums meet in shared memory and
+// are added in order.
+template <bool E4M3, typename TO, int TS, int FS>
+__global__ void __launch_bounds__(kFewThreads, 1) linear_few_kernel(const __grid_constant__ FewParams p) {
+  constexpr int kSize = E4M3 ? 1 : 2, kAhead = 16 / (TS + FS), kFeatures = 8 * FS;
+  __shared__ float part[kFewThreads / 32][8 * TS * kFeatures];
+  ops_begin();
+  const LinearParams& l = p.l;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  int g = 0, row0 = 0, nt = l.T;
+  if (l.offsets) {
+    int want = blockIdx.y;
+    nt = 0;
+    for (int g0 = 0; g0 < l.G && nt == 0; g0 += 32) {
+      const Span sp = g0 + lane < l.G ? group_rows(l, g0 + lane) : Span{0, 0};
+      unsigned with = __ballot_sync(0xffffffffu, sp.n > 0);
+      if (__popc(with) <= want) {
+        want -= __popc(with);
+        continue;
+      }
+      while (want-- > 0) with &= with - 1;
+      const int src = __ffs(with) - 1;
+      g = g0 + src;
+      row0 = __shfl_sync(0xffffffffu, sp.a, src);
+      nt = min(8 * TS, __shfl_sync(0xffffffffu, sp.n, src));
+    }
+    if (nt == 0) return;
+  }
+  // this thread's output, and what its epilogue reads
+  const int of = blockIdx.x * kFeatures + threadIdx.x % kFeatures, ot = threadIdx.x / kFeatures;
+  const bool out = ot < nt;
+  const Finish<TO, 1, E4M3> finish(l, g, out ? of : l.N, 1);
+  const Place<TO> place(l, row0 + ot, of);
+  typename Finish<TO, 1, E4M3>::Ahead ahead;
+  finish.ahead(ahead, place, 0, out);
+
+  // rows in units of 16 bytes; a row that does not exist is not read
+  const int units = (int)((int64_t)l.F * kSize / 16);
+  const uint4 *w[FS], *x[TS];
+  int wu[FS], xu[TS];
+#pragma unroll
+  for (int i = 0; i < FS; ++i) {
+    const int f = blockIdx.x * kFeatures + i * 8 + lane / 4;
+    wu[i] = f < l.N ? units : 0;
+    w[i] = static_cast<const uint4*>(p.w) + ((size_t)g * l.N + (f < l.N ? f : 0)) * (p.ldw * kSize / 16);
+  }
+#pragma unroll
+  for (int i = 0; i < TS; ++i) {
+    const int t = i * 8 + lane / 4;
+    xu[i] = t < nt ? units : 0;
+    x[i] = static_cast<const uint4*>(p.x) + (row0 + (t < nt ? t : 0)) * (size_t)(p.ldx * kSize / 16);
+  }
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  constexpr int kTiles = TS * FS == 4 ? 2 : 1;       // of 16 x 8 sums
+  float sum[kTiles][4] = {};
+  for (int k0 = warp * 4; k0 < units; k0 += kAhead * warps * 4) {
+    uint4 wv[FS][kAhead], xv[TS][kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + lane % 4 + u * warps * 4;
+#pragma unroll
+      for (int i = 0; i < FS; ++i) wv[i][u] = k < wu[i] ? __ldcs(w[i] + k) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + lane % 4 + u * warps * 4;
+#pragma unroll
+      for (int i = 0; i < TS; ++i) xv[i][u] = k < xu[i] ? __ldg(x[i] + k) : zero;
+    }
+    // the matrix instruction truncates as it adds: short sums there, their sum here
+    float c[kTiles][4] = {};
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if constexpr (FS == 2) {
+#pragma unroll
+        for (int i = 0; i < TS; ++i) warp_mma<E4M3>(c[i], wv[0][u], wv[1][u], xv[i][u]);
+      } else {
+        warp_mma<E4M3>(c[0], xv[0][u], TS == 2 ? xv[TS - 1][u] : zero, wv[0][u]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[i][j] += c[i][j];
+  }
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = lane / 4 + j / 2 * 8, q = i * 8 + lane % 4 * 2 + j % 2;
+      if (FS == 2) part[warp][q * kFeatures + r] = sum[i][j];
+      else if (TS == 2 || j < 2) part[warp][r * kFeatures + q] = sum[i][j];
+    }
+  __syncthreads();
+  if (out) {
+    float v[1] = {part[0][threadIdx.x]};
+    for (int i = 1; i < warps; ++i) v[0] += part[i][threadIdx.x];
+    finish(v, place.y, ahead);
+  }
+}
+
 // ------------------------------------------------------------------ host side
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -768,10 +906,33 @@ moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, i
   return launch_op(linear_split_kernel<E4M3, TO>, dim3((unsigned)(tiles * splits)), kThreads, smem, splits, s, p);
 }
 
+template <bool E4M3, typename TO, int TS, int FS>
+moe_status launch_few(const moe_async_linear_args* a, const LinearParams& l, int sms, void* s) {
+  const FewParams p{a->d_x, a->d_w, a->x_stride, a->w_stride, l};
+  const dim3 grid((unsigned)((l.N + 8 * FS - 1) / (8 * FS)), (unsigned)(l.offsets ? std::min(l.G, l.T) : 1));
+  // Twice the warps where a block has an SM to itself and half of them would take K in more than one pass (1 token on
+  // 7168 x 256: 4.4 us against 6.4; but on 512 x 256 2.0 against 1.7, on 2880 x 2880 7.9 against 5.8)
+  const bool one_pass = (int64_t)l.F * (E4M3 ? 1 : 2) <= kFewThreads / 64 * 64 * (16 / (TS + FS));
+  const int threads = one_pass || grid.x * grid.y > (unsigned)sms ? kFewThreads / 2 : kFewThreads;
+  return launch_op(linear_few_kernel<E4M3, TO, TS, FS>, grid, threads, 0, 1, s, p);
+}
+
 template <bool E4M3, typename TO>
 moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, void* s) {
   const int sms = sm_count();
   if (sms < 2) return MOE_ERR_CUDA;
+  // Up to 16 tokens the few kernel is ahead (bf16, few / split us: 1 token on 2880 x 2880 5.8 / 7.7, 7168 x 256 4.5 /
+  // 9.2, 6144 x 6144 16.8 / 25, 7168 x 7168 20.8 / 21.8; 8 tokens of 8 groups on 512 x 256 3.2 / 5.9) until its blocks
+  // are many and short (1 token on 128 x 152064 42 / 18; 8 groups of 2880 x 2880 27.9 / 26.3) or, above 8 tokens, their
+  // re-reads of x crowd long streams (16 tokens on 6144 x 6144 20.2 / 25.9, 7168 x 7168 23.5 / 22.5; e4m3 17.4 / 14.5).
+  const int64_t features = (int64_t)l.N * (l.offsets ? std::min(l.G, l.T) : 1);
+  if (l.T <= kFewTokens && features <= 128 * sms && (l.T <= 8 || features * l.F <= 40'000'000)) {
+    // 16 features a block re-read x half as often (1 token on 2880 x 2880 5.8 us against 7.2; 16 tokens 6.1 against
+    // 9.0), 8 make enough blocks of a small weight (1 token on 7168 x 1024 6.5 against 5.4)
+    const bool wide = features > 8 * sms;
+    return l.T > 8 ? wide ? launch_few<E4M3, TO, 2, 2>(a, l, sms, s) : launch_few<E4M3, TO, 2, 1>(a, l, sms, s)
+                   : wide ? launch_few<E4M3, TO, 1, 2>(a, l, sms, s) : launch_few<E4M3, TO, 1, 1>(a, l, sms, s);
+  }
   // A third of the pairs at work is enough for the pair kernel (measured, bf16, pair / split us: 28 wide
   // tiles of 7168 deep 42.7 / 47.3, 56 of them 43.5 / 93, 24 of 2880 deep 21.6 / 21.8, 48 of them 21.9 /
   // 44; but 8 of 7168 deep 40.8 / 18.0, 16 of 592 deep 19.7 / 8.7), if the tiles are more than half full
@@ -795,7 +956,8 @@ moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, 
 extern "C" moe_status moe_async_linear(const moe_async_linear_args* a, void* stream) {
   using namespace moe;
   if (!a) return MOE_ERR_INVALID;
-  if (a->rows < 0 || a->rows > INT32_MAX - 1024 || a->fan_in < 1 || a->fan_out < 1 || a->groups < 0 || a->groups > kMaxExperts ||
+  if (a->rows < 0 || a->rows > INT32_MAX - 1024 || a->fan_in < 1 || a->fan_in > INT32_MAX - 1024 ||
+      a->fan_out < 1 || a->fan_out > INT32_MAX - 1024 || a->groups < 0 || a->groups > kMaxExperts ||
       a->act < MOE_ACT_NONE || a->act > MOE_ACT_RELU || (a->groups > 0) != (a->d_offsets != nullptr) ||
       (a->out_dtype != MOE_F32 && a->out_dtype != MOE_BF16))
     return MOE_ERR_INVALID;

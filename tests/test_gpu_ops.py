@@ -393,6 +393,20 @@ def test_linear(moe, T, F, Nn, e4m3, out, act, extras):
     assert torch.equal(moe.linear(x, w, act=act, out_dtype=out, **kw), got)      # the same bits again
 
 
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 15, 16])
+@pytest.mark.parametrize("F,Nn", [(16, 9), (64, 20011), (1056, 1235), (2064, 1200), (4128, 130), (208, 2500), (20000, 8), (7168, 6000)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_linear_of_few_tokens(moe, T, F, Nn, e4m3):
+    """One to 16 rows, also on the sides of the sizes at which the kernel, its features a block and its warps change."""
+    g = gen(T + F + Nn)
+    out = torch.float32 if T % 2 else torch.bfloat16
+    x, w, kw = linear_inputs(T, F, Nn, e4m3, out, "bmr", 0, g, pad=T % 3)
+    got = moe.linear(strided(x, 32), strided(w, 16), act="silu", out_dtype=out, **kw)
+    ref, tol = linear_ref(x, w, kw, "silu", out)
+    close(got, ref, tol, "few tokens")
+    assert torch.equal(moe.linear(x, w, act="silu", out_dtype=out, out=kw["residual"], **kw), got)
+
+
 def test_linear_of_small_integers_is_exact(moe):
     """Integer operands whose sums stay below 2^24 leave no room for rounding: every product reaches its place."""
     g = gen(2)
@@ -422,7 +436,8 @@ def test_linear_strides_and_outputs_in_place(moe, e4m3):
 
 GROUP_CASES = [  # rows, fan_in, fan_out, rows of each group
     (10, 64, 40, [3, 0, 7]), (1, 128, 130, [0, 0, 1, 0]), (200, 592, 300, [0, 129, 1, 0, 64, 6]), (500, 256, 256, [256, 100, 144]),
-    (300, 144, 257, [40] * 7), (64, 2880, 150, [1] * 64), (900, 320, 500, [600, 3, 0, 250])]
+    (300, 144, 257, [40] * 7), (64, 2880, 150, [1] * 64), (900, 320, 500, [600, 3, 0, 250]),
+    (16, 320, 100, [0] * 40 + [3, 0, 9] + [0] * 50 + [4]), (13, 80, 33, [0, 13]), (8, 4128, 2000, [1, 0, 2, 0, 0, 5]), (16, 64, 1300, [1] * 16)]
 
 
 @pytest.mark.parametrize("T,F,Nn,counts", GROUP_CASES)

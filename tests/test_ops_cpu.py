@@ -73,7 +73,8 @@ def test_linear_refusals(nat):
     call = lambda **kw: lib.moe_async_linear(ctypes.byref(N.LinearArgs(**{**base, **kw})), None)   # noqa: E731
     assert lib.moe_async_linear(None, None) == N.MOE_ERR_INVALID
     assert call(rows=0) == N.MOE_OK
-    for kw in (dict(rows=-1), dict(fan_in=0), dict(fan_out=0), dict(groups=-1), dict(groups=3), dict(groups=1025, d_offsets=P), dict(d_offsets=P),
+    for kw in (dict(rows=-1), dict(fan_in=0), dict(fan_out=0), dict(fan_in=2 ** 31 - 16, x_stride=2 ** 31, w_stride=2 ** 31),
+               dict(fan_out=2 ** 31 - 1, y_stride=2 ** 31), dict(groups=-1), dict(groups=3), dict(groups=1025, d_offsets=P), dict(d_offsets=P),
                dict(act=4), dict(act=-1), dict(out_dtype=N.MOE_E4M3), dict(d_x=None), dict(d_w=None), dict(d_y=None), dict(x_stride=56),
                dict(w_stride=56), dict(y_stride=31), dict(d_mul=P, mul_stride=31), dict(d_residual=P, residual_stride=31), dict(d_x_scale=P),
                dict(d_w_scale=P), dict(dtype=N.MOE_E4M3), dict(dtype=N.MOE_E4M3, d_x_scale=P)):
