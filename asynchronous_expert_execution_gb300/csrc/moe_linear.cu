@@ -314,29 +314,30 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
   constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
   const int chunks = min(kAccs, (kb1 - kb0 + kChunkBlocks - 1) / kChunkBlocks);
 
-  if (nj > 0 && warp == 0 && lane == 0) {
-    for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
-      const int st = it % p.stages;
-      if (!wait(&s->empty[st], ((it / p.stages) & 1) ^ 1, abort_flag)) break;
+  if (nj > 0 && warp == 0 && elect()) {
+    uint32_t st = 0, phase = 1;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!wait(&s->empty[st], phase, abort_flag)) break;
       const uint32_t a = smem_u32(smem + st * stage_bytes);
       mbar_expect(&s->full[st], stage_bytes);
       tma_3d<1>(a, &p.w, smem_u32(&s->full[st]), kb * kElems, fti * kBM, g);
       tma_2d<1>(a + kABlock, &p.x, smem_u32(&s->full[st]), kb * kElems, row0);
+      if (++st == p.stages) st = 0, phase ^= 1;
     }
-  } else if (nj > 0 && warp == 1 && lane == 0) {
+  } else if (nj > 0 && warp == 1 && elect()) {
     const uint32_t idesc = mma_desc<E4M3>(kBM, p.bn);
     bool ok = true;
-    for (int kb = kb0, it = 0, chunk = -1; kb < kb1; ++kb, ++it) {
-      const int st = it % p.stages, now = it * chunks / (kb1 - kb0);
-      const bool first = now != chunk;
-      chunk = now;
-      if (!(ok = wait(&s->full[st], (it / p.stages) & 1, abort_flag))) break;
-      tc_after();
-      const uint32_t a = smem_u32(smem + st * stage_bytes);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma<1, E4M3>(tmem + chunk * p.bn, operand_desc(a + 32 * k), operand_desc(a + kABlock + 32 * k), idesc, !first || k > 0);
-      commit<1>(&s->empty[st]);
+    uint32_t st = 0, phase = 0;
+    for (int chunk = 0; chunk < chunks && ok; ++chunk) {
+      const int n = (kb1 - kb0) * (chunk + 1) / chunks - (kb1 - kb0) * chunk / chunks;
+      for (int i = 0; i < n; ++i) {
+        if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
+        tc_after();
+        const uint64_t a = operand_desc(smem_u32(smem + st * stage_bytes));
+        mma_block<1, E4M3>(tmem + chunk * p.bn, a, a + (kABlock >> 4), idesc, i > 0);
+        commit<1>(&s->empty[st]);
+        if (++st == p.stages) st = 0, phase ^= 1;
+      }
     }
     if (ok) commit<1>(&s->done);
   }
@@ -411,9 +412,10 @@ constexpr int kTurn = kChunk * 32;                   // floats: 32 tokens x 32 f
 constexpr int kStaging = 8 * kTurn * 4;
 
 struct PairParams {
-  CUtensorMap w, x[4];              // x: boxes of 16, 32, 64, 128 rows
+  CUtensorMap w, x[4];              // x: boxes of 16, 32, 64 and tokens / 2 rows
   LinearParams l;
   int nft;                          // feature tiles of 256
+  int tokens;                       // of a tile, a multiple of 32
 };
 
 struct PairTail {
@@ -424,13 +426,12 @@ struct PairTail {
 };
 
 struct PairTile {
-  int g, row0, nj, fti, nmma, box, kps, chunk;   // chunk: k-blocks summed in one accumulator
+  int g, row0, nj, fti, nmma, box, brows, kps, chunk;   // brows: token rows a CTA stages; chunk: k-blocks summed in one accumulator
 };
 
 // The tiles of a pair of CTAs, in order: t, t + pairs, ..  Every role walks the groups by itself.
 template <typename TO>
 struct PairWalk {
-  static constexpr int kTokens = kPairTokens<TO>;
   int t, g, base;                   // next tile; its group or an earlier one, and that group's first tile
   Span sp;
   __device__ PairWalk(const PairParams& p) : t(blockIdx.x / 2), g(0), base(0), sp(group_rows(p.l, 0)) {}
@@ -438,7 +439,7 @@ struct PairWalk {
   __device__ __forceinline__ bool next(const PairParams& p, PairTile& tl) {
     int ntt;
     while (true) {
-      ntt = (sp.n + kTokens - 1) / kTokens;
+      ntt = (sp.n + p.tokens - 1) / p.tokens;
       if (t - base < ntt * p.nft) break;
       base += ntt * p.nft;
       if (++g >= p.l.G) return false;
@@ -451,14 +452,16 @@ struct PairWalk {
     const int width = min(8, ntt - 8 * band);
     tl.g = g;
     tl.fti = local / width;
-    const int j0 = (8 * band + local % width) * kTokens;
+    const int j0 = (8 * band + local % width) * p.tokens;
     tl.row0 = sp.a + j0;
-    tl.nj = min(kTokens, sp.n - j0);
+    tl.nj = min(p.tokens, sp.n - j0);
     tl.nmma = (tl.nj + 31) & ~31;
     const int half = tl.nmma / 2;                    // token rows each CTA stages: a box that holds them
     tl.box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-    tl.kps = min(kPairKpsMax, kPairStage / (kABlock + (16 << tl.box) * kBKBytes));
-    tl.chunk = sizeof(TO) == 4 ? kChunkBlocks / tl.kps * tl.kps : p.l.nk;
+    if (16 << tl.box >= p.tokens / 2) tl.box = 3;
+    tl.brows = tl.box < 3 ? 16 << tl.box : p.tokens / 2;
+    tl.kps = min(kPairKpsMax, kPairStage / (kABlock + tl.brows * kBKBytes));
+    tl.chunk = sizeof(TO) == 4 ? kChunkBlocks / tl.kps * tl.kps : (p.l.nk + tl.kps - 1) / tl.kps * tl.kps;
     t += gridDim.x / 2;
     return true;
   }
@@ -503,15 +506,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   PairTile tl;
   constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
 
-  if (warp == 0 && lane == 0) {
-    uint32_t it = 0;
+  if (warp == 0 && elect()) {
+    uint32_t st = 0, phase = 1;
     bool ok = true;
     while (ok && walk.next(p, tl)) {
-      const int brows = 16 << tl.box, block = kABlock + brows * kBKBytes;
+      const int block = kABlock + tl.brows * kBKBytes;
       const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
-      for (int kb = 0; kb < l.nk; kb += tl.kps, ++it) {
-        const int st = it % kPairStages, nv = min(tl.kps, l.nk - kb);
-        if (!(ok = wait(&s->empty[st], ((it / kPairStages) & 1) ^ 1, abort_flag))) break;
+      for (int kb = 0; kb < l.nk; kb += tl.kps) {
+        const int nv = min(tl.kps, l.nk - kb);
+        if (!(ok = wait(&s->empty[st], phase, abort_flag))) break;
         const uint32_t a = smem_u32(smem + st * kPairStage);
         const uint32_t bar = mapa(smem_u32(&s->full[st]), 0);
         if (rank == 0) mbar_expect(&s->full[st], 2 * nv * block);
@@ -519,35 +522,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tma_3d<2>(a + j * block, &p.w, bar, (kb + j) * kElems, wrow, tl.g);
           tma_2d<2>(a + j * block + kABlock, &p.x[tl.box], bar, (kb + j) * kElems, xrow);
         }
+        if (++st == kPairStages) st = 0, phase ^= 1;
       }
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    uint32_t it = 0, acc = 0;
+  } else if (warp == 1 && rank == 0 && elect()) {
+    uint32_t st = 0, phase = 0, acc = 0;
     bool ok = true;
     while (ok && walk.next(p, tl)) {
-      const int block = kABlock + (16 << tl.box) * kBKBytes;
+      const int block = kABlock + tl.brows * kBKBytes;
       const uint32_t idesc = mma_desc<E4M3>(2 * kBM, tl.nmma);
-      int buf = 0;
-      for (int kb = 0; kb < l.nk; kb += tl.kps, ++it) {
-        if (kb % tl.chunk == 0) {
+      int buf = 0, left = 0;                         // left: k-blocks until this accumulator is full
+      for (int kb = 0; kb < l.nk; kb += tl.kps) {
+        if (left == 0) {
           if (kb > 0) commit<2>(&s->tfull[buf]);
           buf = acc % kAccs;
           if (!(ok = wait(&s->tempty[buf], ((acc / kAccs) & 1) ^ 1, abort_flag))) break;
           tc_after();
           ++acc;
         }
-        const uint32_t d = tmem + buf * kTokens;
-        const int st = it % kPairStages, nv = min(tl.kps, l.nk - kb);
-        if (!(ok = wait(&s->full[st], (it / kPairStages) & 1, abort_flag))) break;
+        bool more = left > 0;
+        left = (left > 0 ? left : tl.chunk) - tl.kps;
+        const int nv = min(tl.kps, l.nk - kb);
+        if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
         tc_after();
-        const uint32_t a0 = smem_u32(smem + st * kPairStage);
-        for (int j = 0; j < nv; ++j) {
-          const uint32_t a = a0 + j * block;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma<2, E4M3>(d, operand_desc(a + 32 * k), operand_desc(a + kABlock + 32 * k), idesc, kb % tl.chunk + j > 0 || k > 0);
-        }
+        uint64_t a = operand_desc(smem_u32(smem + st * kPairStage));
+        for (int j = 0; j < nv; ++j, a += block >> 4, more = true)
+          mma_block<2, E4M3>(tmem + buf * kTokens, a, a + (kABlock >> 4), idesc, more);
         commit<2>(&s->empty[st]);
+        if (++st == kPairStages) st = 0, phase ^= 1;
       }
       if (ok) commit<2>(&s->tfull[buf]);
     }
@@ -862,7 +864,7 @@ int sm_count() {
 }
 
 template <bool E4M3, typename TO>
-moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, int sms, void* s) {
+moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, int sms, int tokens, void* s) {
   constexpr int kSmem = kPairStages * kPairStage + kStaging + (int)sizeof(PairTail) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   constexpr int size = E4M3 ? 1 : 2;
@@ -870,8 +872,9 @@ moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, in
   p.l = l;
   p.nft = (l.N + 2 * kBM - 1) / (2 * kBM);
   if (!encode(&p.w, a->d_w, size, l.F, l.N, a->w_stride, l.G, kBM)) return MOE_ERR_CUDA;
+  p.tokens = tokens;
   for (int i = 0; i < 4; ++i)
-    if (!encode(&p.x[i], a->d_x, size, l.F, l.T, a->x_stride, 0, 16 << i)) return MOE_ERR_CUDA;
+    if (!encode(&p.x[i], a->d_x, size, l.F, l.T, a->x_stride, 0, i < 3 ? 16 << i : tokens / 2)) return MOE_ERR_CUDA;
   if (cudaFuncSetAttribute(linear_pair_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return MOE_ERR_CUDA;
   return launch_op(linear_pair_kernel<E4M3, TO>, dim3(sms / 2 * 2), kPairThreads, kSmem, 1, s, p);
@@ -941,7 +944,7 @@ moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, 
   const int64_t wide = (int64_t)((l.N + 255) / 256) *
                        (l.offsets ? l.T / kTokens + std::min(l.G, l.T) : (l.T + kTokens - 1) / kTokens);
   const int64_t per = l.offsets ? (l.T + l.G - 1) / l.G : l.T;
-  if (per > 2 * kSplitTokens && wide >= sms / 6) return launch_pair<E4M3, TO>(a, l, sms, s);
+  if (per > 2 * kSplitTokens && wide >= sms / 6) return launch_pair<E4M3, TO>(a, l, sms, kTokens, s);
   const int bn = per <= 16 ? 16 : per <= 32 ? 32 : kSplitTokens;
   const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * (l.offsets ? l.T / bn + std::min(l.G, l.T) : (l.T + bn - 1) / bn);
   // Splits fill the SMs once where that takes four or more, else twice (two CTAs fit an SM)

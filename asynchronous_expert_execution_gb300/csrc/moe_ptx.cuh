@@ -21,6 +21,14 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+// One lane of a whole warp.  TMA and tcgen05 take their operands from uniform registers, and only behind this
+// does the compiler know that one thread runs: behind `lane == 0` it wraps every such instruction in a
+// loop over the warp's lanes, and a tcgen05.mma took 277 cycles to issue instead of 40.
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one)::"memory");
+  return one != 0;
+}
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -146,6 +154,14 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
   if constexpr (CG == 2 && !E4M3) MOE_MMA("2", "f16");
   if constexpr (CG == 2 && E4M3) MOE_MMA("2", "f8f6f4");
 #undef MOE_MMA
+}
+// One k-block (128 bytes of each row): four MMAs.
+template <int CG, bool E4M3>
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  mma<CG, E4M3>(d, a, b, idesc, accumulate);
+  mma<CG, E4M3>(d, a + 2, b + 2, idesc, 1);        // 32 bytes on
+  mma<CG, E4M3>(d, a + 4, b + 4, idesc, 1);
+  mma<CG, E4M3>(d, a + 6, b + 6, idesc, 1);
 }
 // All MMAs issued so far by this thread arrive on `bar` when they are done; CG = 2: on the
 // barrier at the same place in both CTAs of the pair.
