@@ -403,9 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
 // tokens of a tile: two accumulators of 256 columns, or three of 128 that take the chunks of fp32 sums in
 // turn and 128 columns for the chunks' sum
 template <typename TO> constexpr int kPairTokens = sizeof(TO) == 4 ? 128 : 256;
-constexpr int kPairStages = 3;
-constexpr int kPairStage = 64 * 1024;                // 2 k-blocks of a full tile, 3 of a narrow one
-constexpr int kPairKpsMax = 3;
+constexpr int kPairRing = 192 * 1024;
 constexpr int kPairThreads = 384;                    // warps: TMA, MMA, TMEM, spare, 2 x 4 epilogue
 constexpr int kChunk = 32;                           // tokens an epilogue warp turns at a time
 constexpr int kTurn = kChunk * 32;                   // floats: 32 tokens x 32 features
@@ -416,17 +414,19 @@ struct PairParams {
   LinearParams l;
   int nft;                          // feature tiles of 256
   int tokens;                       // of a tile, a multiple of 32
+  int stages, stage_bytes;          // of the ring: a k-block of a full tile each
 };
 
 struct PairTail {
-  uint64_t full[kPairStages], empty[kPairStages], tfull[4], tempty[4];
+  static constexpr int kMaxStages = 10;
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[4], tempty[4];
   uint32_t tmem;
   int abort_flag;
   int finishing;                    // tiles whose epilogue has begun
 };
 
 struct PairTile {
-  int g, row0, nj, fti, nmma, box, brows, kps, chunk;   // brows: token rows a CTA stages; chunk: k-blocks summed in one accumulator
+  int g, row0, nj, fti, nmma, box, brows;   // brows: token rows a CTA stages
 };
 
 // The tiles of a pair of CTAs, in order: t, t + pairs, ..  Every role walks the groups by itself.
@@ -460,8 +460,6 @@ struct PairWalk {
     tl.box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
     if (16 << tl.box >= p.tokens / 2) tl.box = 3;
     tl.brows = tl.box < 3 ? 16 << tl.box : p.tokens / 2;
-    tl.kps = min(kPairKpsMax, kPairStage / (kABlock + tl.brows * kBKBytes));
-    tl.chunk = sizeof(TO) == 4 ? kChunkBlocks / tl.kps * tl.kps : (p.l.nk + tl.kps - 1) / tl.kps * tl.kps;
     t += gridDim.x / 2;
     return true;
   }
@@ -472,18 +470,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  PairTail* s = reinterpret_cast<PairTail*>(smem + kPairStages * kPairStage + kStaging);
+  PairTail* s = reinterpret_cast<PairTail*>(smem + kPairRing + kStaging);
   volatile int* abort_flag = &s->abort_flag;
   const LinearParams& l = p.l;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   constexpr int kTokens = kPairTokens<TO>, kAccs = sizeof(TO) == 4 ? 3 : 2;
   constexpr uint32_t kCols = 512;
+  const int chunk = sizeof(TO) == 4 ? kChunkBlocks : l.nk;      // k-blocks summed in one accumulator
 
   if (threadIdx.x == 0) {
     prefetch_map(&p.w);
     prefetch_map(&p.x[3]);
-    for (int i = 0; i < kPairStages; ++i) {
+    for (int i = 0; i < p.stages; ++i) {
       mbar_init(&s->full[i], 1);                     // the leader's producer, for both CTAs' bytes
       mbar_init(&s->empty[i], 1);                    // the MMA's commit, in both CTAs
     }
@@ -512,44 +511,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     while (ok && walk.next(p, tl)) {
       const int block = kABlock + tl.brows * kBKBytes;
       const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
-      for (int kb = 0; kb < l.nk; kb += tl.kps) {
-        const int nv = min(tl.kps, l.nk - kb);
+      for (int kb = 0; kb < l.nk; ++kb) {
         if (!(ok = wait(&s->empty[st], phase, abort_flag))) break;
-        const uint32_t a = smem_u32(smem + st * kPairStage);
-        const uint32_t bar = mapa(smem_u32(&s->full[st]), 0);
-        if (rank == 0) mbar_expect(&s->full[st], 2 * nv * block);
-        for (int j = 0; j < nv; ++j) {
-          tma_3d<2>(a + j * block, &p.w, bar, (kb + j) * kElems, wrow, tl.g);
-          tma_2d<2>(a + j * block + kABlock, &p.x[tl.box], bar, (kb + j) * kElems, xrow);
-        }
-        if (++st == kPairStages) st = 0, phase ^= 1;
+        const uint32_t a = smem_u32(smem + st * p.stage_bytes), bar = mapa(smem_u32(&s->full[st]), 0);
+        if (rank == 0) mbar_expect(&s->full[st], 2 * block);
+        tma_3d<2>(a, &p.w, bar, kb * kElems, wrow, tl.g);
+        tma_2d<2>(a + kABlock, &p.x[tl.box], bar, kb * kElems, xrow);
+        if (++st == p.stages) st = 0, phase ^= 1;
       }
     }
   } else if (warp == 1 && rank == 0 && elect()) {
     uint32_t st = 0, phase = 0, acc = 0;
     bool ok = true;
     while (ok && walk.next(p, tl)) {
-      const int block = kABlock + tl.brows * kBKBytes;
       const uint32_t idesc = mma_desc<E4M3>(2 * kBM, tl.nmma);
-      int buf = 0, left = 0;                         // left: k-blocks until this accumulator is full
-      for (int kb = 0; kb < l.nk; kb += tl.kps) {
-        if (left == 0) {
+      int buf = 0;
+      for (int kb = 0, in = chunk; kb < l.nk; ++kb, ++in) {      // in: k-blocks in this accumulator
+        if (in == chunk) {
           if (kb > 0) commit<2>(&s->tfull[buf]);
           buf = acc % kAccs;
           if (!(ok = wait(&s->tempty[buf], ((acc / kAccs) & 1) ^ 1, abort_flag))) break;
           tc_after();
           ++acc;
+          in = 0;
         }
-        bool more = left > 0;
-        left = (left > 0 ? left : tl.chunk) - tl.kps;
-        const int nv = min(tl.kps, l.nk - kb);
         if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
         tc_after();
-        uint64_t a = operand_desc(smem_u32(smem + st * kPairStage));
-        for (int j = 0; j < nv; ++j, a += block >> 4, more = true)
-          mma_block<2, E4M3>(tmem + buf * kTokens, a, a + (kABlock >> 4), idesc, more);
+        const uint64_t a = operand_desc(smem_u32(smem + st * p.stage_bytes));
+        mma_block<2, E4M3>(tmem + buf * kTokens, a, a + (kABlock >> 4), idesc, in > 0);
         commit<2>(&s->empty[st]);
-        if (++st == kPairStages) st = 0, phase ^= 1;
+        if (++st == p.stages) st = 0, phase ^= 1;
       }
       if (ok) commit<2>(&s->tfull[buf]);
     }
@@ -571,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..; two warps share a quarter's columns
-    float* turn = reinterpret_cast<float*>(smem + kPairStages * kPairStage) + (warp - 4) * kTurn;
+    float* turn = reinterpret_cast<float*>(smem + kPairRing) + (warp - 4) * kTurn;
     uint32_t acc = 0;
     // a warp's tokens: every other block of 32
     constexpr bool kSums = sizeof(TO) == 4;
@@ -590,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // `body(c)` for each of this warp's blocks of the tile, the block's sums in `turn`; false: a wait ran out
     auto blocks = [&](auto body) {
       const uint32_t d0 = tmem + ((uint32_t)(32 * q) << 16), sum = d0 + kAccs * kTokens;
-      const int chunks = kSums ? (l.nk + tl.chunk - 1) / tl.chunk : 1;
+      const int chunks = kSums ? (l.nk + chunk - 1) / chunk : 1;
       for (int ch = 0; ch + 1 < chunks; ++ch, ++acc) {         // all but the last chunk: into the sum's columns
         const int buf = acc % kAccs;
         if (!acc_wait(buf, acc)) return false;
@@ -865,7 +856,7 @@ int sm_count() {
 
 template <bool E4M3, typename TO>
 moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, int sms, int tokens, void* s) {
-  constexpr int kSmem = kPairStages * kPairStage + kStaging + (int)sizeof(PairTail) + 1024;
+  constexpr int kSmem = kPairRing + kStaging + (int)sizeof(PairTail) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   constexpr int size = E4M3 ? 1 : 2;
   PairParams p;
@@ -873,6 +864,8 @@ moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, in
   p.nft = (l.N + 2 * kBM - 1) / (2 * kBM);
   if (!encode(&p.w, a->d_w, size, l.F, l.N, a->w_stride, l.G, kBM)) return MOE_ERR_CUDA;
   p.tokens = tokens;
+  p.stage_bytes = kABlock + tokens / 2 * kBKBytes;
+  p.stages = std::min(PairTail::kMaxStages, kPairRing / p.stage_bytes);
   for (int i = 0; i < 4; ++i)
     if (!encode(&p.x[i], a->d_x, size, l.F, l.T, a->x_stride, 0, i < 3 ? 16 << i : tokens / 2)) return MOE_ERR_CUDA;
   if (cudaFuncSetAttribute(linear_pair_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
