@@ -29,6 +29,8 @@
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 #include "moe_ops.cuh"
 #include "moe_ptx.cuh"
 
@@ -45,11 +47,11 @@ constexpr int kABlock = kBM * kBKBytes;            // 16 KB
 constexpr int kThreads = 256;                      // warps: TMA, MMA, TMEM, spare, 4 x epilogue
 constexpr unsigned long long kLimitNs = 2000000000ull;
 // The tensor cores' fp32 sums cut what does not fit, so their error grows with the length of a sum
-// (bf16, 7168 deep, of the result's norm: 2.6e-6 in one sum, 1.4e-6 in sums of 22 k-blocks, 8.6e-7 in
-// sums of 14; plain fp32 products 2e-7 to 9e-7).  Results that are kept in fp32 are therefore summed in
-// chunks of up to this many k-blocks, which the epilogue adds with rounding (2048 x 7168 x 7168: 131 ->
-// 224 us, most of it the narrower tile); a bf16 result's own rounding is 1,000 times larger.
-constexpr int kChunkBlocks = 14;
+// (bf16, 7168 deep, of the result's norm: 2.6e-6 in one sum, 1.4e-6 in sums of 22 k-blocks, 7.2e-7 in
+// sums of 12, 4.8e-7 in sums of 8; plain fp32 products 2e-7 to 9e-7).  Results that are kept in fp32 are
+// therefore summed in chunks of up to this many k-blocks, which the epilogue adds with rounding (2048 x 7168 x
+// 7168: 142 us in chunks of 12, 157 in chunks of 8); a bf16 result's own rounding is 1,000 times larger.
+constexpr int kChunkBlocks = 12;
 
 struct LinearParams {
   const float* bias;
@@ -902,6 +904,69 @@ moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, i
   return launch_op(linear_split_kernel<E4M3, TO>, dim3((unsigned)(tiles * splits)), kThreads, smem, splits, s, p);
 }
 
+// CTAs of the split kernel, in clusters of s, that find an SM of their own: a cluster stays within its part of the
+// chip.  As many again share an SM with another.
+int split_capacity(int s, int sms) {
+  static std::atomic<int> known[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return sms;
+  int n = known[dev][s].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(s);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSplitSmem / 2;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = s;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const auto kernel = linear_split_kernel<false, __nv_bfloat16>;       // all forms share its limits
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem / 2) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
+    return sms;
+  known[dev][s].store(n * s, std::memory_order_relaxed);
+  return n * s;
+}
+
+struct LinearPlan {
+  bool pair;
+  int tokens, splits;               // of a tile; CTAs that share its K
+};
+
+// Kernel, tile and split with the least expected time, in ns.  The constants are fits to this GPU's timings (116
+// shapes of 24 to 8192 tokens on 512 to 7168 features, dense and in 8 to 64 groups; the choice's time is 0.5%
+// above the best one's on average, 15% at worst): a k-block costs a split CTA 280 (64 tokens) or 220, a
+// pair 185 to 300 by its tokens; the exchange 1,300 + 100 a rank, a second CTA on an SM 1,100 to 1,900, the
+// pair's epilogue 13.7 a token behind the last tile and 1,300 + 21.5 a token between two.  `bytes`: all operands; the
+// split kernel streams them at 6.4 TB/s, the pair kernel at 5.5.  Groups count half a tile each for their ends.
+template <typename TO>
+LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
+  const float groups = l.offsets ? std::min(l.G, l.T) : 1, per = l.T / groups;
+  auto token_tiles = [&](int t) { return l.offsets ? l.T / (float)t + 0.5f * groups : (float)((l.T + t - 1) / t); };
+  LinearPlan plan{false, per <= 16 ? 16 : per <= 32 ? 32 : kSplitTokens, 1};
+  float best = 1e30f;
+  const float block = plan.tokens <= 32 ? 220.f : 280.f, split_tiles = (l.N + kBM - 1) / kBM * token_tiles(plan.tokens);
+  for (int s = 1; s <= 8 && (s == 1 || 2 * s <= l.nk); ++s) {
+    const float ctas = split_tiles * s, own = (float)split_capacity(s, sms), waves = std::ceil(ctas / (2 * own));
+    if ((s > 1 && waves > 1.f) || (sizeof(TO) == 4 && l.nk > 4 * kChunkBlocks * s)) continue;
+    const float kb = (l.nk + s - 1) / s * block;
+    const float ns = (s > 1 ? 4900.f + 100.f * s : 3600.f) + (ctas > own ? s > 1 ? 1900.f : 1100.f : 0.f) +
+                     (l.wide ? 0.f : 1500.f / s) + waves * kb + (waves - 1) * 2000.f;
+    if (ns < best) best = ns, plan.splits = s;
+  }
+  best = std::max(best, 4000.f + bytes / 6400.f) + 0.05f * best;
+  for (int t = 64; t <= kPairTokens<TO>; t += l.offsets ? t : 32) {
+    const float tiles = (l.N + 2 * kBM - 1) / (2 * kBM) * token_tiles(t), rounds = tiles / (sms / 2);
+    const float kb = l.nk * std::max(185.f, 90.f + 0.83f * t), finish = l.wide ? 1300.f + 21.5f * t : 85.f * t;
+    float ns = 3600.f + (l.wide ? 13.7f : 80.f) * t + kb + std::max(0.f, (l.offsets ? rounds : std::ceil(rounds)) - 1.f) * std::max(kb, finish);
+    ns = std::max(ns, 5500.f + bytes / 5500.f) + 0.05f * ns;
+    if (ns < best) best = ns, plan = {true, t, 1};
+  }
+  return plan;
+}
+
 template <bool E4M3, typename TO, int TS, int FS>
 moe_status launch_few(const moe_async_linear_args* a, const LinearParams& l, int sms, void* s) {
   const FewParams p{a->d_x, a->d_w, a->x_stride, a->w_stride, l};
@@ -929,21 +994,10 @@ moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, 
     return l.T > 8 ? wide ? launch_few<E4M3, TO, 2, 2>(a, l, sms, s) : launch_few<E4M3, TO, 2, 1>(a, l, sms, s)
                    : wide ? launch_few<E4M3, TO, 1, 2>(a, l, sms, s) : launch_few<E4M3, TO, 1, 1>(a, l, sms, s);
   }
-  // A third of the pairs at work is enough for the pair kernel (measured, bf16, pair / split us: 28 wide
-  // tiles of 7168 deep 42.7 / 47.3, 56 of them 43.5 / 93, 24 of 2880 deep 21.6 / 21.8, 48 of them 21.9 /
-  // 44; but 8 of 7168 deep 40.8 / 18.0, 16 of 592 deep 19.7 / 8.7), if the tiles are more than half full
-  // (28 of 7168 deep: 128 tokens 37 / 29, one token 30.4 / 21.5).  Groups count at most one ragged tile each.
-  constexpr int kTokens = kPairTokens<TO>;
-  const int64_t wide = (int64_t)((l.N + 255) / 256) *
-                       (l.offsets ? l.T / kTokens + std::min(l.G, l.T) : (l.T + kTokens - 1) / kTokens);
-  const int64_t per = l.offsets ? (l.T + l.G - 1) / l.G : l.T;
-  if (per > 2 * kSplitTokens && wide >= sms / 6) return launch_pair<E4M3, TO>(a, l, sms, kTokens, s);
-  const int bn = per <= 16 ? 16 : per <= 32 ? 32 : kSplitTokens;
-  const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * (l.offsets ? l.T / bn + std::min(l.G, l.T) : (l.T + bn - 1) / bn);
-  // Splits fill the SMs once where that takes four or more, else twice (two CTAs fit an SM)
-  int splits = (int)std::max<int64_t>(1, std::min<int64_t>(8, (sms / tiles >= 4 ? 1 : 2) * sms / tiles));
-  splits = std::min(splits, std::max(1, l.nk / 2));
-  return launch_split<E4M3, TO>(a, l, bn, splits, tiles, s);
+  const LinearPlan plan = linear_plan<TO>(l, sms, ((float)features + l.T) * l.F * (E4M3 ? 1 : 2));
+  if (plan.pair) return launch_pair<E4M3, TO>(a, l, sms, plan.tokens, s);
+  const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * (l.offsets ? l.T / plan.tokens + std::min(l.G, l.T) : (l.T + plan.tokens - 1) / plan.tokens);
+  return launch_split<E4M3, TO>(a, l, plan.tokens, plan.splits, tiles, s);
 }
 
 }  // namespace
