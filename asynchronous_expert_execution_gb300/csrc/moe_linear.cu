@@ -91,6 +91,58 @@ __device__ __forceinline__ Span group_rows(const LinearParams& p, int g) {
   return {a, b - a};
 }
 
+// The tiles of all groups, where a group of n rows has tiles(n), looked up by a whole warp.  64 groups' offsets are
+// asked for at a time (1024 groups of 512 x 512 on 8192 rows: 203 us; 32 at a time 211, 128 201, but 32 groups of
+// 2880 x 2880 138 / 138 / 140).
+struct GroupTiles {
+  int g0 = -32, incl = 0;           // 32 groups, and their tiles up to this lane's
+  Span sp{0, 0};                    // this lane's group
+  int want;                         // the next tile, counted from these groups' first
+  __device__ __forceinline__ explicit GroupTiles(int first) : want(first) {}
+
+  // false: there are fewer tiles; then `want` counts from behind the last one
+  template <class Tiles>
+  __device__ __forceinline__ bool find(const LinearParams& p, Tiles tiles) {
+    if (__any_sync(0xffffffffu, want < incl)) return true;
+    want -= __shfl_sync(0xffffffffu, incl, 31);
+    constexpr int kAt = 2;
+    const int lane = threadIdx.x % 32;
+    for (int at = g0 + 32; at < p.G; at += 32 * kAt) {
+      Span got[kAt];
+#pragma unroll
+      for (int u = 0; u < kAt; ++u) got[u] = at + 32 * u + lane < p.G ? group_rows(p, at + 32 * u + lane) : Span{0, 0};
+#pragma unroll
+      for (int u = 0; u < kAt; ++u) {
+        incl = tiles(got[u].n);
+        const int all = __reduce_add_sync(0xffffffffu, incl);
+        if (want < all) {
+          g0 = at + 32 * u;
+          sp = got[u];
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+          }
+          return true;
+        }
+        want -= all;
+      }
+    }
+    g0 = -32;
+    incl = 0;
+    return false;
+  }
+  // after find: the tile's group, that group's rows, and the tile's number in it
+  template <class Tiles>
+  __device__ __forceinline__ int get(Tiles tiles, int& g, int& row0, int& n) const {
+    const int src = __ffs(__ballot_sync(0xffffffffu, want < incl)) - 1;
+    g = g0 + src;
+    row0 = __shfl_sync(0xffffffffu, sp.a, src);
+    n = __shfl_sync(0xffffffffu, sp.n, src);
+    return want - (__shfl_sync(0xffffffffu, incl, src) - tiles(n));
+  }
+};
+
 // A thread's place in the epilogue's operands: token row r, feature f.
 template <typename TO>
 struct Place {
@@ -275,28 +327,13 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
   } else {
     ops_begin();
     if (warp == 3) {                                 // token tile tile / nft of the groups' tiles
-      const int want = tile / p.nft;
-      int seen = 0;
-      g = -1;
-      for (int g0 = 0; g0 < l.G && g < 0; g0 += 32) {
-        const Span sp = g0 + lane < l.G ? group_rows(l, g0 + lane) : Span{0, 0};
-        const int nt = (sp.n + p.bn - 1) / p.bn;
-        int incl = nt;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += o;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, seen + incl > want);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          const int t = want - seen - __shfl_sync(0xffffffffu, incl - nt, src);
-          const int n = __shfl_sync(0xffffffffu, sp.n, src);
-          g = g0 + src;
-          row0 = __shfl_sync(0xffffffffu, sp.a, src) + t * p.bn;
-          nj = min(p.bn, n - t * p.bn);
-        }
-        seen += __shfl_sync(0xffffffffu, incl, 31);
+      const auto tiles = [&](int n) { return (n + p.bn - 1) / p.bn; };
+      GroupTiles at(tile / p.nft);
+      if (at.find(l, tiles)) {
+        int n;
+        const int t = at.get(tiles, g, row0, n);
+        row0 += t * p.bn;
+        nj = min(p.bn, n - t * p.bn);
       }
       if (lane == 0) {
         s->g = g;
@@ -431,38 +468,44 @@ struct PairTile {
   int g, row0, nj, fti, nmma, box, brows;   // brows: token rows a CTA stages
 };
 
-// The tiles of a pair of CTAs, in order: t, t + pairs, ..  Every role walks the groups by itself.
-template <typename TO>
+// The tiles of a pair of CTAs, in order: every `pairs`-th one.  Every role's warp walks the groups by itself.  Groups
+// with a full tile come first, then those with more than half of one: long tiles at the end would leave pairs idle
+// (2880 x 2880, 32 groups of 18 to 1151 rows: 138 us, in the groups' order 142; e4m3 88 and 92; 64 groups of 2048 x
+// 768 on 16384 rows 66 and 73).
 struct PairWalk {
-  int t, g, base;                   // next tile; its group or an earlier one, and that group's first tile
-  Span sp;
-  __device__ PairWalk(const PairParams& p) : t(blockIdx.x / 2), g(0), base(0), sp(group_rows(p.l, 0)) {}
+  GroupTiles at;
+  int pass = 0;
+  __device__ __forceinline__ PairWalk() : at(blockIdx.x / 2) {}
 
+  // by whole warps
   __device__ __forceinline__ bool next(const PairParams& p, PairTile& tl) {
-    int ntt;
-    while (true) {
-      ntt = (sp.n + p.tokens - 1) / p.tokens;
-      if (t - base < ntt * p.nft) break;
-      base += ntt * p.nft;
-      if (++g >= p.l.G) return false;
-      sp = group_rows(p.l, g);
+    int first = 0, n = p.l.T, local = at.want;
+    tl.g = 0;
+    if (p.l.offsets) {
+      const auto tiles = [&](int rows) {
+        const bool now = pass == (rows >= p.tokens ? 0 : 2 * rows > p.tokens ? 1 : 2);
+        return now ? (rows + p.tokens - 1) / p.tokens * p.nft : 0;
+      };
+      while (!at.find(p.l, tiles))
+        if (++pass > 2) return false;
+      local = at.get(tiles, tl.g, first, n);
     }
+    const int ntt = (n + p.tokens - 1) / p.tokens;
+    if (local >= ntt * p.nft) return false;
     // eight token tiles meet one feature tile before the next: what runs at one time shares operands in L2
-    int local = t - base;
     const int band = local / (8 * p.nft);
     local -= band * 8 * p.nft;
     const int width = min(8, ntt - 8 * band);
-    tl.g = g;
     tl.fti = local / width;
     const int j0 = (8 * band + local % width) * p.tokens;
-    tl.row0 = sp.a + j0;
-    tl.nj = min(p.tokens, sp.n - j0);
+    tl.row0 = first + j0;
+    tl.nj = min(p.tokens, n - j0);
     tl.nmma = (tl.nj + 31) & ~31;
     const int half = tl.nmma / 2;                    // token rows each CTA stages: a box that holds them
     tl.box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
     if (16 << tl.box >= p.tokens / 2) tl.box = 3;
     tl.brows = tl.box < 3 ? 16 << tl.box : p.tokens / 2;
-    t += gridDim.x / 2;
+    at.want += gridDim.x / 2;
     return true;
   }
 };
@@ -503,14 +546,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_after();
   const uint32_t tmem = s->tmem;
-  PairWalk<TO> walk(p);
+  PairWalk walk;
   PairTile tl;
   constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
 
-  if (warp == 0 && elect()) {
+  if (warp == 0) {
     uint32_t st = 0, phase = 1;
     bool ok = true;
-    while (ok && walk.next(p, tl)) {
+    while (__all_sync(0xffffffffu, ok) && walk.next(p, tl)) {
+      if (!elect()) continue;
       const int block = kABlock + tl.brows * kBKBytes;
       const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
       for (int kb = 0; kb < l.nk; ++kb) {
@@ -522,10 +566,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (++st == p.stages) st = 0, phase ^= 1;
       }
     }
-  } else if (warp == 1 && rank == 0 && elect()) {
+  } else if (warp == 1 && rank == 0) {
     uint32_t st = 0, phase = 0, acc = 0;
     bool ok = true;
-    while (ok && walk.next(p, tl)) {
+    while (__all_sync(0xffffffffu, ok) && walk.next(p, tl)) {
+      if (!elect()) continue;
       const uint32_t idesc = mma_desc<E4M3>(2 * kBM, tl.nmma);
       int buf = 0;
       for (int kb = 0, in = chunk; kb < l.nk; ++kb, ++in) {      // in: k-blocks in this accumulator
@@ -731,21 +776,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_few_kernel(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   int g = 0, row0 = 0, nt = l.T;
   if (l.offsets) {
-    int want = blockIdx.y;
     nt = 0;
-    for (int g0 = 0; g0 < l.G && nt == 0; g0 += 32) {
-      const Span sp = g0 + lane < l.G ? group_rows(l, g0 + lane) : Span{0, 0};
-      unsigned with = __ballot_sync(0xffffffffu, sp.n > 0);
-      if (__popc(with) <= want) {
-        want -= __popc(with);
-        continue;
-      }
-      while (want-- > 0) with &= with - 1;
-      const int src = __ffs(with) - 1;
-      g = g0 + src;
-      row0 = __shfl_sync(0xffffffffu, sp.a, src);
-      nt = min(8 * TS, __shfl_sync(0xffffffffu, sp.n, src));
-    }
+    const auto tiles = [](int n) { return n > 0 ? 1 : 0; };
+    GroupTiles at(blockIdx.y);
+    if (at.find(l, tiles)) at.get(tiles, g, row0, nt);
+    nt = min(8 * TS, nt);
     if (nt == 0) return;
   }
   // this thread's output, and what its epilogue reads
@@ -940,7 +975,7 @@ struct LinearPlan {
 // above the best one's on average, 15% at worst): a k-block costs a split CTA 280 (64 tokens) or 220, a
 // pair 185 to 300 by its tokens; the exchange 1,300 + 100 a rank, a second CTA on an SM 1,100 to 1,900, the
 // pair's epilogue 13.7 a token behind the last tile and 1,300 + 21.5 a token between two.  `bytes`: all operands; the
-// split kernel streams them at 6.4 TB/s, the pair kernel at 5.5.  Groups count half a tile each for their ends.
+// split kernel streams them at 6.4 TB/s, the pair kernel at 5.5; of the smaller of stream and sums, part shows.  Groups count half a tile each for their ends.
 template <typename TO>
 LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
   const float groups = l.offsets ? std::min(l.G, l.T) : 1, per = l.T / groups;
@@ -953,10 +988,10 @@ LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
     if ((s > 1 && waves > 1.f) || (sizeof(TO) == 4 && l.nk > 4 * kChunkBlocks * s)) continue;
     const float kb = (l.nk + s - 1) / s * block;
     const float ns = (s > 1 ? 4900.f + 100.f * s : 3600.f) + (ctas > own ? s > 1 ? 1900.f : 1100.f : 0.f) +
-                     (l.wide ? 0.f : 1500.f / s) + waves * kb + (waves - 1) * 2000.f;
+                     (l.wide ? 0.f : 1500.f / s) + kb + (waves - 1) * std::max(kb + 2000.f, 4600.f);
     if (ns < best) best = ns, plan.splits = s;
   }
-  best = std::max(best, 4000.f + bytes / 6400.f) + 0.05f * best;
+  best = std::max(best, 4000.f + bytes / 6400.f) + 0.15f * std::min(best, 4000.f + bytes / 6400.f);
   for (int t = 64; t <= kPairTokens<TO>; t += l.offsets ? t : 32) {
     const float tiles = (l.N + 2 * kBM - 1) / (2 * kBM) * token_tiles(t), rounds = tiles / (sms / 2);
     const float kb = l.nk * std::max(185.f, 90.f + 0.83f * t), finish = l.wide ? 1300.f + 21.5f * t : 85.f * t;

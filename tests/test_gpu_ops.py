@@ -459,6 +459,19 @@ def test_linear_per_expert(moe, T, F, Nn, counts, e4m3, out, act, extras):
     assert bool((y[at[-1]:] == 3.0).all())
 
 
+@pytest.mark.parametrize("T,F,Nn", [(1100, 1040, 520), (520, 2880, 300), (300, 208, 1000), (2600, 64, 96)])
+@pytest.mark.parametrize("out", BOTH)
+def test_linear_with_groups_of_every_size(moe, T, F, Nn, out):
+    """70 groups, some large, most small or empty: the tiles are not taken in the groups' order."""
+    g = gen(T + Nn)
+    share = torch.rand(70, generator=g, device="cuda") ** 6
+    at = torch.cat([torch.zeros(1, device="cuda"), (share.cumsum(0) / share.sum() * T)]).int()
+    at[-1] = T
+    x, w, kw = linear_inputs(T, F, Nn, False, out, "bmr", 70, g)
+    ref, tol = linear_ref(x, w, kw, "silu", out, torch.zeros((T, Nn), device="cuda"), at.tolist())
+    close(moe.linear(x, w, act="silu", offsets=at, out_dtype=out, **kw), ref, tol, "groups of every size")
+
+
 def test_linear_rows_before_the_first_group_and_bad_offsets(moe):
     """Groups may start behind row 0; offsets outside the rows are clipped, descending ones hold no rows."""
     g = gen(4)
