@@ -240,11 +240,10 @@ struct SplitParams {
   int bn, stages, splits, nft;      // tokens a tile, ring depth, CTAs a cluster, feature tiles
 };
 
-constexpr int kSplitSmem = 226 * 1024;              // of an SM: for two CTAs
-constexpr int kSplitTokens = 64;                    // most tokens a tile
+constexpr int kSplitSmem = 226 * 1024;              // of an SM: for one CTA or two
 
 struct SplitTail {                  // behind the stages
-  static constexpr int kMaxStages = 6;
+  static constexpr int kMaxStages = 12;
   uint64_t full[kMaxStages], empty[kMaxStages], done, got;
   uint32_t tmem;
   int abort_flag;
@@ -910,34 +909,16 @@ moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, in
   return launch_op(linear_pair_kernel<E4M3, TO>, dim3(sms / 2 * 2), kPairThreads, kSmem, 1, s, p);
 }
 
-// the ring of a split CTA holds its own partials and its share of up to 8 ranks' (which may round up by a token each)
-constexpr bool split_fits(int bn) {
-  const int stage = kABlock + bn * kBKBytes;
-  const int stages = (kSplitSmem / 2 - (int)sizeof(SplitTail) - 1024) / stage;
-  return stages <= SplitTail::kMaxStages && (bn + bn + 8) * kBM * 4 <= stages * stage;
+// k-blocks in the ring of a split CTA that has an SM to itself, or shares one
+constexpr int split_stages(int bn, bool own_sm) {
+  const int n = ((own_sm ? kSplitSmem : kSplitSmem / 2) - (int)sizeof(SplitTail) - 1024) / (kABlock + bn * kBKBytes);
+  return n < SplitTail::kMaxStages ? n : SplitTail::kMaxStages;
 }
-static_assert(split_fits(16) && split_fits(32) && split_fits(kSplitTokens), "shared memory of the split kernel");
-
-template <bool E4M3, typename TO>
-moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, int bn, int splits, int64_t tiles, void* s) {
-  constexpr int size = E4M3 ? 1 : 2;
-  SplitParams p;
-  p.l = l;
-  p.bn = bn;
-  p.splits = splits;
-  p.nft = (l.N + kBM - 1) / kBM;
-  // two CTAs an SM: their rings fill each other's gaps (64 tokens on 7168 x 7168: 23.4 us against 27.1 for one
-  // CTA with twice the ring)
-  const int stage = kABlock + bn * kBKBytes, rest = (int)sizeof(SplitTail) + 1024;
-  p.stages = (kSplitSmem / 2 - rest) / stage;
-  const int smem = p.stages * stage + rest;
-  if (!encode(&p.w, a->d_w, size, l.F, l.N, a->w_stride, l.G, kBM) ||
-      !encode(&p.x, a->d_x, size, l.F, l.T, a->x_stride, 0, bn))
-    return MOE_ERR_CUDA;
-  if (cudaFuncSetAttribute(linear_split_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem / 2) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  return launch_op(linear_split_kernel<E4M3, TO>, dim3((unsigned)(tiles * splits)), kThreads, smem, splits, s, p);
+// the ring holds the CTA's partials and its share of up to 8 ranks' (which may round up by a token each)
+constexpr bool split_fits(int bn, bool own_sm) {
+  return (bn + bn + 8) * kBM * 4 <= split_stages(bn, own_sm) * (kABlock + bn * kBKBytes);
 }
+static_assert(split_fits(16, false) && split_fits(32, false) && split_fits(64, false) && split_fits(128, true), "shared memory of the split kernel");
 
 // CTAs of the split kernel, in clusters of s, that find an SM of their own: a cluster stays within its part of the
 // chip.  As many again share an SM with another.
@@ -965,31 +946,58 @@ int split_capacity(int s, int sms) {
   return n * s;
 }
 
+template <bool E4M3, typename TO>
+moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, int bn, int splits, int64_t tiles, int sms, void* s) {
+  constexpr int size = E4M3 ? 1 : 2;
+  SplitParams p;
+  p.l = l;
+  p.bn = bn;
+  p.splits = splits;
+  p.nft = (l.N + kBM - 1) / kBM;
+  // Alone on its SM a CTA takes all of the shared memory where its K fills it, for loads in flight (512 x 7168 x 256: 10.7 ->
+  // 8.9 us); two CTAs on an SM fill each other's gaps.  128 tokens' accumulators and partials fit one CTA an SM only.
+  p.stages = split_stages(bn, false);
+  if (bn > 64 || (tiles * splits <= split_capacity(splits, sms) && l.nk > p.stages * splits)) p.stages = split_stages(bn, true);
+  const int stage = kABlock + bn * kBKBytes, rest = (int)sizeof(SplitTail) + 1024;
+  const int smem = p.stages * stage + rest;
+  if (!encode(&p.w, a->d_w, size, l.F, l.N, a->w_stride, l.G, kBM) ||
+      !encode(&p.x, a->d_x, size, l.F, l.T, a->x_stride, 0, bn))
+    return MOE_ERR_CUDA;
+  if (cudaFuncSetAttribute(linear_split_kernel<E4M3, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return launch_op(linear_split_kernel<E4M3, TO>, dim3((unsigned)(tiles * splits)), kThreads, smem, splits, s, p);
+}
+
 struct LinearPlan {
   bool pair;
   int tokens, splits;               // of a tile; CTAs that share its K
 };
 
-// Kernel, tile and split with the least expected time, in ns.  The constants are fits to this GPU's timings (116
+// Kernel, tile and split with the least expected time, in ns.  The constants are fits to this GPU's timings (124
 // shapes of 24 to 8192 tokens on 512 to 7168 features, dense and in 8 to 64 groups; the choice's time is 0.5%
-// above the best one's on average, 15% at worst): a k-block costs a split CTA 280 (64 tokens) or 220, a
-// pair 185 to 300 by its tokens; the exchange 1,300 + 100 a rank, a second CTA on an SM 1,100 to 1,900, the
-// pair's epilogue 13.7 a token behind the last tile and 1,300 + 21.5 a token between two.  `bytes`: all operands; the
-// split kernel streams them at 6.4 TB/s, the pair kernel at 5.5; of the smaller of stream and sums, part shows.  Groups count half a tile each for their ends.
-template <typename TO>
+// above the best one's on average, 28% at worst).  A k-block costs a split CTA 135 to 230 alone on its SM, by tokens
+// and type, and 220 or 280 beside another; a pair 185 to 300.  The exchange takes 1,300 + 100 a rank, a second CTA on an SM
+// 1,100 to 1,900, 128 tokens of a split CTA 2,100 to 3,100, the pair's epilogue 13.7 a token behind the last tile and 1,300 +
+// 21.5 a token between two.  `bytes`: all operands; the split kernel streams them at 6.4 TB/s, the pair kernel at 5.5; of the
+// smaller of stream and sums, part shows.  Groups count half a tile each for their ends.
+template <bool E4M3, typename TO>
 LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
   const float groups = l.offsets ? std::min(l.G, l.T) : 1, per = l.T / groups;
   auto token_tiles = [&](int t) { return l.offsets ? l.T / (float)t + 0.5f * groups : (float)((l.T + t - 1) / t); };
-  LinearPlan plan{false, per <= 16 ? 16 : per <= 32 ? 32 : kSplitTokens, 1};
+  const int least = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+  LinearPlan plan{false, least, 1};
   float best = 1e30f;
-  const float block = plan.tokens <= 32 ? 220.f : 280.f, split_tiles = (l.N + kBM - 1) / kBM * token_tiles(plan.tokens);
-  for (int s = 1; s <= 8 && (s == 1 || 2 * s <= l.nk); ++s) {
-    const float ctas = split_tiles * s, own = (float)split_capacity(s, sms), waves = std::ceil(ctas / (2 * own));
-    if ((s > 1 && waves > 1.f) || (sizeof(TO) == 4 && l.nk > 4 * kChunkBlocks * s)) continue;
-    const float kb = (l.nk + s - 1) / s * block;
-    const float ns = (s > 1 ? 4900.f + 100.f * s : 3600.f) + (ctas > own ? s > 1 ? 1900.f : 1100.f : 0.f) +
-                     (l.wide ? 0.f : 1500.f / s) + kb + (waves - 1) * std::max(kb + 2000.f, 4600.f);
-    if (ns < best) best = ns, plan.splits = s;
+  for (int bn = least; bn == least || (bn == 128 && per > 64); bn *= 2) {
+    const float tiles = (l.N + kBM - 1) / kBM * token_tiles(bn);
+    for (int s = 1; s <= 8 && (s == 1 || 2 * s <= l.nk); ++s) {
+      const float ctas = tiles * s, own = (float)split_capacity(s, sms), waves = std::ceil(ctas / (2 * own));
+      const bool alone = ctas <= own;
+      if ((s > 1 && waves > 1.f) || (bn == 128 && !alone) || (sizeof(TO) == 4 && l.nk > 4 * kChunkBlocks * s)) continue;
+      const float kb = (l.nk + s - 1) / s * (!alone ? bn == 64 ? 280.f : 220.f : E4M3 ? bn == 128 ? 230.f : 180.f : bn == 128 ? 157.f : bn == 64 ? 148.f : 135.f);
+      const float ns = (s > 1 ? 4900.f + 100.f * s : 3600.f) + (bn == 128 ? s > 1 ? 2100.f : 3100.f : 0.f) + (alone ? 0.f : s > 1 ? 1900.f : 1100.f) +
+                       (l.wide ? 0.f : 1500.f / s) + kb + (waves - 1) * std::max(kb + 2000.f, 4600.f);
+      if (ns < best) best = ns, plan.tokens = bn, plan.splits = s;
+    }
   }
   best = std::max(best, 4000.f + bytes / 6400.f) + 0.15f * std::min(best, 4000.f + bytes / 6400.f);
   for (int t = 64; t <= kPairTokens<TO>; t += l.offsets ? t : 32) {
@@ -1029,10 +1037,10 @@ moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, 
     return l.T > 8 ? wide ? launch_few<E4M3, TO, 2, 2>(a, l, sms, s) : launch_few<E4M3, TO, 2, 1>(a, l, sms, s)
                    : wide ? launch_few<E4M3, TO, 1, 2>(a, l, sms, s) : launch_few<E4M3, TO, 1, 1>(a, l, sms, s);
   }
-  const LinearPlan plan = linear_plan<TO>(l, sms, ((float)features + l.T) * l.F * (E4M3 ? 1 : 2));
+  const LinearPlan plan = linear_plan<E4M3, TO>(l, sms, ((float)features + l.T) * l.F * (E4M3 ? 1 : 2));
   if (plan.pair) return launch_pair<E4M3, TO>(a, l, sms, plan.tokens, s);
   const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * (l.offsets ? l.T / plan.tokens + std::min(l.G, l.T) : (l.T + plan.tokens - 1) / plan.tokens);
-  return launch_split<E4M3, TO>(a, l, plan.tokens, plan.splits, tiles, s);
+  return launch_split<E4M3, TO>(a, l, plan.tokens, plan.splits, tiles, sms, s);
 }
 
 }  // namespace
