@@ -14,15 +14,15 @@
 // of a 7168-deep e4m3 tile; turning a whole tile's features at once, with two barriers of 128
 // threads per 16 tokens, 17,000).
 //
-// Three kernels, chosen by linear_launch:
+// Three kernels, chosen by expected time (linear_launch, linear_plan):
 //   pair   persistent, tiles of 256 features x up to 256 tokens (128 for fp32 results) over two SMs
 //          (cta_group::2): each SM stages half of both operands, which halves the shared-memory traffic per product.
-//   split  one tile of 128 features x up to 64 tokens per cluster of up to 8 CTAs, K split over
+//   split  one tile of 128 features x up to 128 tokens per cluster of up to 8 CTAs, K split over
 //          them; partials meet through distributed shared memory in rank order (no workspace,
 //          no atomics).  For few tiles: a lone SM streams weights far below the HBM rate.
 //   few    up to 16 tokens: weights straight into the registers of warp-wide matrix instructions.  Only
 //          the weights' bytes count there; barriers, TMEM and the exchange cost more than they bring
-//          (4 tokens on 2880 x 2880: 5.8 us against 7.8; 4096 x 16384 at 5.1 TB/s).
+//          (4 tokens on 2880 x 2880: 5.8 us against 7.0).
 //
 // Every wait is bounded (2 s): a wait that runs out stops all roles, latches MOE_ERR_TIMEOUT in
 // the operators' error word, and the CTA still frees its TMEM.
@@ -1025,12 +1025,12 @@ template <bool E4M3, typename TO>
 moe_status linear_launch(const moe_async_linear_args* a, const LinearParams& l, void* s) {
   const int sms = sm_count();
   if (sms < 2) return MOE_ERR_CUDA;
-  // Up to 16 tokens the few kernel is ahead (bf16, few / split us: 1 token on 2880 x 2880 5.8 / 7.7, 7168 x 256 4.5 /
-  // 9.2, 6144 x 6144 16.8 / 25, 7168 x 7168 20.8 / 21.8; 8 tokens of 8 groups on 512 x 256 3.2 / 5.9) until its blocks
-  // are many and short (1 token on 128 x 152064 42 / 18; 8 groups of 2880 x 2880 27.9 / 26.3) or, above 8 tokens, their
-  // re-reads of x crowd long streams (16 tokens on 6144 x 6144 20.2 / 25.9, 7168 x 7168 23.5 / 22.5; e4m3 17.4 / 14.5).
+  // Up to 16 tokens the few kernel is ahead on small weights (bf16, few / split us: 1 token on 2880 x 2880 5.8 / 6.9, 7168 x
+  // 256 4.4 / 6.1, 512 x 256 1.7 / 3.9, 7168 x 4096 12.4 / 13.3; 16 tokens 6.1 / 7.2, 6.2 / 6.4, 1.8 / 3.9, 13.0 / 13.6;
+  // e4m3, 8 tokens of 8 of 128 groups on 2048 x 768 5.8 / 7.9), until its blocks are many (1 token on 512 x 30000 11.9 /
+  // 8.0) or its re-reads of x crowd a long stream (1 token on 6144 x 6144 17.3 / 15.9, 16 tokens 20.2 / 16.5).
   const int64_t features = (int64_t)l.N * (l.offsets ? std::min(l.G, l.T) : 1);
-  if (l.T <= kFewTokens && features <= 128 * sms && (l.T <= 8 || features * l.F <= 40'000'000)) {
+  if (l.T <= kFewTokens && features <= 64 * sms && features * l.F <= 32'000'000) {
     // 16 features a block re-read x half as often (1 token on 2880 x 2880 5.8 us against 7.2; 16 tokens 6.1 against
     // 9.0), 8 make enough blocks of a small weight (1 token on 7168 x 1024 6.5 against 5.4)
     const bool wide = features > 8 * sms;
