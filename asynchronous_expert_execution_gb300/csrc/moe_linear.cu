@@ -64,6 +64,7 @@ struct LinearParams {
   int64_t ldmul, ldres, ldy;
   int T, N, F, G, act, nk;
   bool wide;                        // y, mul and residual: 16-byte units
+  __host__ __device__ bool plain() const { return !mul && !res && act == MOE_ACT_NONE; }
 };
 
 // Bounded wait; false once it ran out or another role gave up.
@@ -157,8 +158,9 @@ struct Place {
 
 // The end of the epilogue for one thread, which owns C features of every token it meets: first,
 // first + step, ...  C = 8, step = 1: rows of y, mul and residual move in 16-byte units; else
-// element by element.  Pointers are to a token's row at feature `first`.
-template <typename TO, int C, bool SCALED>
+// element by element.  Pointers are to a token's row at feature `first`.  PLAIN: no mul, residual and activation (their tests
+// and loads cost a fifth of 4096 x 512 x 7168: 39.4 us, now 32.5).
+template <typename TO, int C, bool SCALED, bool PLAIN = false>
 struct Finish {
   static constexpr bool kWide = C == 8;
   static constexpr int kVecs = kWide ? C / Vec<TO>::N : C;
@@ -188,47 +190,59 @@ struct Finish {
     if (SCALED) a.sx = token ? __ldg(place.sx + t) : 1.f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      if (p.mul && token && on(i)) a.m[i] = RV::load_rw(place.mul + t * p.ldmul + at(i));
-      if (p.res && token && on(i)) a.e[i] = RV::load_rw(place.res + t * p.ldres + at(i));
+      if (!PLAIN && p.mul && token && on(i)) a.m[i] = RV::load_rw(place.mul + t * p.ldmul + at(i));
+      if (!PLAIN && p.res && token && on(i)) a.e[i] = RV::load_rw(place.res + t * p.ldres + at(i));
+    }
+  }
+  // U tokens' values
+  template <int U>
+  __device__ __forceinline__ void compute(float (&v)[U][C], const Ahead* a) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[u][i] = SCALED ? v[u][i] * (a[u].sx * sw[i]) + bias[i] : v[u][i] + bias[i];
+    if (!PLAIN && p.act != MOE_ACT_NONE) {
+      auto each_value = [&](auto f) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < C; ++i) v[u][i] = f(v[u][i]);
+      };
+      if (p.act == MOE_ACT_SILU)
+        each_value([](float x) { return __fdividef(x, 1.0f + __expf(-x)); });   // off by at most 2^-20 |x|
+      else if (p.act == MOE_ACT_GELU)
+        each_value([](float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678f)); });
+      else
+        each_value([](float x) { return x < 0.f ? 0.f : x; });                  // relu; NaN stays
+    }
+    constexpr int N = C / kVecs;
+    auto with = [&](auto raw, auto f) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          float t[N];
+          RV::unpack(raw(a[u])[i], t);
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[u][i * N + j] = f(v[u][i * N + j], t[j]);
+        }
+    };
+    if (!PLAIN && p.mul) with([](const Ahead& h) -> const Raw(&)[kVecs] { return h.m; }, [](float x, float t) { return x * t; });
+    if (!PLAIN && p.res) with([](const Ahead& h) -> const Raw(&)[kVecs] { return h.e; }, [](float x, float t) { return x + t; });
+  }
+  __device__ __forceinline__ void store(const float (&v)[C], TO* y) const {
+    constexpr int N = C / kVecs;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float o[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = v[i * N + j];
+      if (on(i)) RV::store(y + at(i), RV::pack(o));
     }
   }
   __device__ __forceinline__ void operator()(float (&v)[C], TO* y, const Ahead& a) const {
-    if (SCALED) {
-#pragma unroll
-      for (int i = 0; i < C; ++i) v[i] *= a.sx * sw[i];
-    }
-#pragma unroll
-    for (int i = 0; i < C; ++i) v[i] += bias[i];
-    if (p.act != MOE_ACT_NONE) {
-      if (p.act == MOE_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = __fdividef(v[i], 1.0f + __expf(-v[i]));   // off by at most 2^-20 |v|: a 7 us tile less than exact ones
-      } else if (p.act == MOE_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678f));
-      } else {
-#pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // relu; NaN stays
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      constexpr int N = C / kVecs;
-      float o[N], t[N];
-#pragma unroll
-      for (int j = 0; j < N; ++j) o[j] = v[i * N + j];
-      if (p.mul) {
-        RV::unpack(a.m[i], t);
-#pragma unroll
-        for (int j = 0; j < N; ++j) o[j] *= t[j];
-      }
-      if (p.res) {
-        RV::unpack(a.e[i], t);
-#pragma unroll
-        for (int j = 0; j < N; ++j) o[j] += t[j];
-      }
-      if (on(i)) RV::store(y + at(i), RV::pack(o));
-    }
+    compute(reinterpret_cast<float(&)[1][C]>(v), &a);
+    store(v, y);
   }
 };
 
@@ -592,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 3 && (l.mul || l.res)) {
     // mul and residual of a tile into L2 while the tile before is finished: the epilogue's 16 KB of
-    // reads in flight an SM then last L2's latency (4096 x 512 x 7168 with mul: 80 -> 62 us)
+    // reads in flight an SM then last L2's latency (4096 x 512 x 7168 with mul: 50 -> 45 us)
     volatile int* finishing = &s->finishing;
     for (int i = 0; walk.next(p, tl); ++i) {
       const unsigned long long t0 = now_ns();
@@ -672,31 +686,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (threadIdx.x == 128) *reinterpret_cast<volatile int*>(&s->finishing) = tiles;
       const int f = tl.fti * 2 * kBM + rank * kBM + 32 * q;
       bool ok;
-      if (l.wide) {
+      const auto wide = [&](auto plain) {
+        constexpr bool PLAIN = decltype(plain)::value;
         // 32 features x 32 tokens turned in the warp's own shared memory: lane i then holds 8
         // features (i % 4) of tokens i / 4 + 8 u, u < 4.  16-byte chunks of a token's row lie at
         // chunk ^ (token & 7): neither the writes nor the reads meet a bank twice.  mul and
         // residual are asked for kAt units ahead, the first ones before the products are done.
-        constexpr int kAt = kSums ? 2 : 4;
+        constexpr int kAt = kSums ? 2 : 4, kU = PLAIN ? 2 : 1;         // kU units at once: more would delay the next loads
         const int f8 = lane % 4, tk = lane / 4;
-        const Finish<TO, 8, E4M3> finish(l, tl.g, f + f8 * 8, 1);
+        const Finish<TO, 8, E4M3, PLAIN> finish(l, tl.g, f + f8 * 8, 1);
         const Place<TO> place(l, tl.row0 + half * kChunk + tk, f + f8 * 8);
         const int mine = tl.nj - half * kChunk - tk;           // tokens from this lane's first to the tile's end
-        typename Finish<TO, 8, E4M3>::Ahead a[kAt];
+        typename Finish<TO, 8, E4M3, PLAIN>::Ahead a[kAt];
 #pragma unroll
         for (int u = 0; u < kAt; ++u) finish.ahead(a[u], place, 8 * u, 8 * u < mine);
-        ok = blocks([&](int c) {
+        return blocks([&](int c) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float* row = turn + (tk + 8 * u) * 32;
-            const float4 x = *reinterpret_cast<const float4*>(row + ((2 * f8) ^ tk) * 4);
-            const float4 y = *reinterpret_cast<const float4*>(row + ((2 * f8 + 1) ^ tk) * 4);
-            float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            if (c + 8 * u < mine) finish(w, place.y + (c + 8 * u) * l.ldy, a[u % kAt]);
-            const int nx = u + kAt < 4 ? c + 8 * (u + kAt) : c + kStep + 8 * (u + kAt - 4);
-            finish.ahead(a[u % kAt], place, nx, nx < mine);
+          for (int u0 = 0; u0 < 4; u0 += kU) {
+            float w[kU][8];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              const float* row = turn + (tk + 8 * (u0 + u)) * 32;
+              const float4 x = *reinterpret_cast<const float4*>(row + ((2 * f8) ^ tk) * 4);
+              const float4 y = *reinterpret_cast<const float4*>(row + ((2 * f8 + 1) ^ tk) * 4);
+              w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w, w[u][4] = y.x, w[u][5] = y.y, w[u][6] = y.z, w[u][7] = y.w;
+            }
+            finish.compute(w, a + u0 % kAt);
+#pragma unroll
+            for (int u = u0; u < u0 + kU; ++u) {
+              if (c + 8 * u < mine) finish.store(w[u - u0], place.y + (c + 8 * u) * l.ldy);
+              const int nx = u + kAt < 4 ? c + 8 * (u + kAt) : c + kStep + 8 * (u + kAt - 4);
+              finish.ahead(a[u % kAt], place, nx, nx < mine);
+            }
           }
         });
+      };
+      if (l.wide) {
+        ok = l.plain() ? wide(std::true_type{}) : wide(std::false_type{});
       } else {
         // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens in flight
         constexpr int kAt = kSums ? 4 : E4M3 ? 8 : 16;
@@ -976,9 +1002,9 @@ struct LinearPlan {
 // Kernel, tile and split with the least expected time, in ns.  The constants are fits to this GPU's timings (124
 // shapes of 24 to 8192 tokens on 512 to 7168 features, dense and in 8 to 64 groups; the choice's time is 0.5%
 // above the best one's on average, 28% at worst).  A k-block costs a split CTA 135 to 230 alone on its SM, by tokens
-// and type, and 220 or 280 beside another; a pair 185 to 300.  The exchange takes 1,300 + 100 a rank, a second CTA on an SM
-// 1,100 to 1,900, 128 tokens of a split CTA 2,100 to 3,100, the pair's epilogue 13.7 a token behind the last tile and 1,300 +
-// 21.5 a token between two.  `bytes`: all operands; the split kernel streams them at 6.4 TB/s, the pair kernel at 5.5; of the
+// and type, and 220 or 280 beside another; a pair 185 to 300.  The exchange takes 100 to 1,300 + 100 a rank, a second CTA on an SM
+// 1,100 to 1,900, 128 tokens of a split CTA 2,100 to 3,100, the pair's epilogue 13.7 a token behind the last tile and, between
+// two, 700 + 15 a token without mul, residual and activation, else 1,300 + 21.5.  `bytes`: all operands; the split kernel streams them at 6.4 TB/s, the pair kernel at 5.5; of the
 // smaller of stream and sums, part shows.  Groups count half a tile each for their ends.
 template <bool E4M3, typename TO>
 LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
@@ -994,7 +1020,7 @@ LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
       const bool alone = ctas <= own;
       if ((s > 1 && waves > 1.f) || (bn == 128 && !alone) || (sizeof(TO) == 4 && l.nk > 4 * kChunkBlocks * s)) continue;
       const float kb = (l.nk + s - 1) / s * (!alone ? bn == 64 ? 280.f : 220.f : E4M3 ? bn == 128 ? 230.f : 180.f : bn == 128 ? 157.f : bn == 64 ? 148.f : 135.f);
-      const float ns = (s > 1 ? 4900.f + 100.f * s : 3600.f) + (bn == 128 ? s > 1 ? 2100.f : 3100.f : 0.f) + (alone ? 0.f : s > 1 ? 1900.f : 1100.f) +
+      const float ns = (s > 1 ? (bn <= 32 ? 3700.f : 4900.f) + 100.f * s : 3600.f) + (bn == 128 ? s > 1 ? 2100.f : 3100.f : 0.f) + (alone ? 0.f : s > 1 ? 1900.f : 1100.f) +
                        (l.wide ? 0.f : 1500.f / s) + kb + (waves - 1) * std::max(kb + 2000.f, 4600.f);
       if (ns < best) best = ns, plan.tokens = bn, plan.splits = s;
     }
@@ -1002,7 +1028,7 @@ LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
   best = std::max(best, 4000.f + bytes / 6400.f) + 0.15f * std::min(best, 4000.f + bytes / 6400.f);
   for (int t = 64; t <= kPairTokens<TO>; t += l.offsets ? t : 32) {
     const float tiles = (l.N + 2 * kBM - 1) / (2 * kBM) * token_tiles(t), rounds = tiles / (sms / 2);
-    const float kb = l.nk * std::max(185.f, 90.f + 0.83f * t), finish = l.wide ? 1300.f + 21.5f * t : 85.f * t;
+    const float kb = l.nk * std::max(185.f, 90.f + 0.83f * t), finish = !l.wide ? 85.f * t : l.plain() ? 700.f + 15.f * t : 1300.f + 21.5f * t;
     float ns = 3600.f + (l.wide ? 13.7f : 80.f) * t + kb + std::max(0.f, (l.offsets ? rounds : std::ceil(rounds)) - 1.f) * std::max(kb, finish);
     ns = std::max(ns, 5500.f + bytes / 5500.f) + 0.05f * ns;
     if (ns < best) best = ns, plan = {true, t, 1};
