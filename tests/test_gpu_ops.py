@@ -377,7 +377,11 @@ def linear_ref(x, w, kw, act, out, start=None, at=None):
 LINEAR_CASES = [  # tokens, fan_in, fan_out
     (1, 16, 1), (1, 2880, 2880), (2, 64, 7), (3, 48, 130), (4, 7168, 257), (7, 144, 997), (16, 1008, 128), (17, 512, 64), (33, 4112, 300),
     (64, 2880, 256), (65, 80, 1000), (127, 2064, 255), (128, 128, 128), (129, 256, 384), (200, 592, 416), (256, 1024, 512), (300, 992, 1000),
-    (777, 592, 997), (1025, 320, 1111)]
+    (777, 592, 997), (1025, 320, 1111),
+    # every width of the tiles over two SMs, and 128 tokens split one to six ways, on wide rows and others
+    (412, 80, 2824), (963, 1040, 2680), (966, 1040, 3304), (2472, 336, 912), (1003, 1040, 3360), (2251, 592, 1760), (273, 144, 3864),
+    (259, 6464, 3264), (2470, 2976, 1286), (1761, 1632, 1285), (1623, 1952, 1567), (2996, 6528, 137), (2529, 1152, 387),
+    (138, 2688, 3693), (2997, 3424, 136), (2657, 1888, 131), (70, 4240, 3640), (2961, 4416, 39), (2314, 6368, 9), (1968, 1136, 1032)]
 
 
 @pytest.mark.parametrize("T,F,Nn", LINEAR_CASES)
@@ -419,14 +423,17 @@ def test_linear_of_small_integers_is_exact(moe):
             assert torch.equal(y.double(), x.double() @ w.double().T), (T, F, Nn, dt)
 
 
+@pytest.mark.parametrize("T,F,Nn,out", [(77, 160, 201, torch.float32), (11, 160, 201, torch.bfloat16), (963, 1040, 2680, torch.bfloat16),
+                                        (963, 1040, 2680, torch.float32), (1623, 1952, 1567, torch.bfloat16), (1968, 1136, 1032, torch.bfloat16)])
 @pytest.mark.parametrize("e4m3", [False, True])
-def test_linear_strides_and_outputs_in_place(moe, e4m3):
+def test_linear_strides_and_outputs_in_place(moe, e4m3, T, F, Nn, out):
     g = gen(3)
-    T, F, Nn, out = 77, 160, 201, torch.float32
     x, w, kw = linear_inputs(T, F, Nn, e4m3, out, "bmr", 0, g, pad=3)
     want = moe.linear(x, w, out_dtype=out, **kw)
+    ref, tol = linear_ref(x, w, kw, "none", out)
+    close(want, ref, tol, "contiguous")
     xs, ws = strided(x, 16), strided(w, 32)
-    y = strided(torch.zeros((T, Nn), device="cuda"), 5)
+    y = strided(torch.zeros((T, Nn), device="cuda").to(out), 5)
     assert torch.equal(moe.linear(xs, ws, out=y, **kw), want)
     for name in ("mul", "residual"):
         k2 = dict(kw)
@@ -437,7 +444,8 @@ def test_linear_strides_and_outputs_in_place(moe, e4m3):
 GROUP_CASES = [  # rows, fan_in, fan_out, rows of each group
     (10, 64, 40, [3, 0, 7]), (1, 128, 130, [0, 0, 1, 0]), (200, 592, 300, [0, 129, 1, 0, 64, 6]), (500, 256, 256, [256, 100, 144]),
     (300, 144, 257, [40] * 7), (64, 2880, 150, [1] * 64), (900, 320, 500, [600, 3, 0, 250]),
-    (16, 320, 100, [0] * 40 + [3, 0, 9] + [0] * 50 + [4]), (13, 80, 33, [0, 13]), (8, 4128, 2000, [1, 0, 2, 0, 0, 5]), (16, 64, 1300, [1] * 16)]
+    (16, 320, 100, [0] * 40 + [3, 0, 9] + [0] * 50 + [4]), (13, 80, 33, [0, 13]), (8, 4128, 2000, [1, 0, 2, 0, 0, 5]), (16, 64, 1300, [1] * 16),
+    (2000, 512, 2000, [700, 0, 3, 256, 255, 129, 600, 57]), (1500, 2064, 1000, [1, 900, 128, 127, 0, 300]), (3000, 592, 1040, [250] * 11 + [2])]
 
 
 @pytest.mark.parametrize("T,F,Nn,counts", GROUP_CASES)
