@@ -277,27 +277,28 @@ __device__ __forceinline__ void split_finish(const SplitParams& p, int g, int ro
     typename Finish<TO, C, SCALED>::Ahead a[kAt];
 #pragma unroll
     for (int u = 0; u < kAt; ++u) finish.ahead(a[u], place, jb + u * tks, jb + u * tks < j1 - j0);
+    float v[kAt][C];
 #pragma unroll
     for (int u = 0; u < kAt; ++u) {
-      const int j = jb + u * tks;
-      if (j < j1 - j0) {
-        float v[C];
-        for (int r = 0; r < p.splits; ++r) {
-          const float* from = (r == rank ? own + j0 * kBM : got + r * share) + j * kBM + f;
-          float t[C];
-          if constexpr (C == 8) {
-            const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 4);
-            t[0] = x.x, t[1] = x.y, t[2] = x.z, t[3] = x.w, t[4] = y.x, t[5] = y.y, t[6] = y.z, t[7] = y.w;
-          } else {
+      const int j = min(jb + u * tks, j1 - j0 - 1);
+      for (int r = 0; r < p.splits; ++r) {
+        const float* from = (r == rank ? own + j0 * kBM : got + r * share) + j * kBM + f;
+        float t[C];
+        if constexpr (C == 8) {
+          const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 4);
+          t[0] = x.x, t[1] = x.y, t[2] = x.z, t[3] = x.w, t[4] = y.x, t[5] = y.y, t[6] = y.z, t[7] = y.w;
+        } else {
 #pragma unroll
-            for (int i = 0; i < C; ++i) t[i] = from[step * i];
-          }
-#pragma unroll
-          for (int i = 0; i < C; ++i) v[i] = r ? v[i] + t[i] : t[i];
+          for (int i = 0; i < C; ++i) t[i] = from[step * i];
         }
-        finish(v, place.y + j * p.l.ldy, a[u]);
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[u][i] = r ? v[u][i] + t[i] : t[i];
       }
     }
+    finish.compute(v, a);
+#pragma unroll
+    for (int u = 0; u < kAt; ++u)
+      if (jb + u * tks < j1 - j0) finish.store(v[u], place.y + (jb + u * tks) * p.l.ldy);
   }
 }
 
@@ -724,26 +725,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (l.wide) {
         ok = l.plain() ? wide(std::true_type{}) : wide(std::false_type{});
       } else {
-        // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens in flight
-        constexpr int kAt = kSums ? 4 : E4M3 ? 8 : 16;
-        const Finish<TO, 1, E4M3> finish(l, tl.g, f + lane, 1);
-        const Place<TO> place(l, tl.row0 + half * kChunk, f + lane);
-        const int mine = tl.nj - half * kChunk;
-        typename Finish<TO, 1, E4M3>::Ahead a[kAt];
+        // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens at once
+        const auto narrow = [&](auto plain) {
+          constexpr bool PLAIN = decltype(plain)::value;
+          constexpr int kAt = kSums ? E4M3 ? 2 : 4 : 8;
+          using F = Finish<TO, 1, E4M3, PLAIN>;
+          const F finish(l, tl.g, f + lane, 1);
+          const Place<TO> place(l, tl.row0 + half * kChunk, f + lane);
+          const int mine = tl.nj - half * kChunk;
+          typename F::Ahead a[kAt];
 #pragma unroll
-        for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, j, j < mine);
-        ok = blocks([&](int c) {
+          for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, j, j < mine);
+          return blocks([&](int c) {
 #pragma unroll 1
-          for (int j0 = 0; j0 < kChunk; j0 += kAt) {
+            for (int j0 = 0; j0 < kChunk; j0 += kAt) {
+              float w[kAt][1];
 #pragma unroll
-            for (int j = 0; j < kAt; ++j) {
-              float w[1] = {turn[(j0 + j) * 32 + (lane ^ (((j0 + j) & 7) << 2))]};
-              if (c + j0 + j < mine) finish(w, place.y + (c + j0 + j) * l.ldy, a[j]);
-              const int nx = (j0 + kAt < kChunk ? c + j0 + kAt : c + kStep) + j;
-              finish.ahead(a[j], place, nx, nx < mine);
+              for (int j = 0; j < kAt; ++j) w[j][0] = turn[(j0 + j) * 32 + (lane ^ (((j0 + j) & 7) << 2))];
+              finish.compute(w, a);
+              TO* y = place.y + (c + j0) * l.ldy;
+#pragma unroll
+              for (int j = 0; j < kAt; ++j, y += l.ldy)
+                if (c + j0 + j < mine) finish.store(w[j], y);
+              const int nx = j0 + kAt < kChunk ? c + j0 + kAt : c + kStep;
+#pragma unroll
+              for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, nx + j, nx + j < mine);
             }
-          }
-        });
+          });
+        };
+        ok = l.plain() ? narrow(std::true_type{}) : narrow(std::false_type{});
       }
       if (!ok) break;
     }
@@ -1004,7 +1014,8 @@ struct LinearPlan {
 // above the best one's on average, 28% at worst).  A k-block costs a split CTA 135 to 230 alone on its SM, by tokens
 // and type, and 220 or 280 beside another; a pair 185 to 300.  The exchange takes 100 to 1,300 + 100 a rank, a second CTA on an SM
 // 1,100 to 1,900, 128 tokens of a split CTA 2,100 to 3,100, the pair's epilogue 13.7 a token behind the last tile and, between
-// two, 700 + 15 a token without mul, residual and activation, else 1,300 + 21.5.  `bytes`: all operands; the split kernel streams them at 6.4 TB/s, the pair kernel at 5.5; of the
+// two, 700 + 15 a token without mul, residual and activation, else 1,300 + 21.5; element by element a
+// third more without them, else 57 or 74 a token.  `bytes`: all operands; the split kernel streams them at 6.4 TB/s, the pair kernel at 5.5; of the
 // smaller of stream and sums, part shows.  Groups count half a tile each for their ends.
 template <bool E4M3, typename TO>
 LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
@@ -1021,15 +1032,16 @@ LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
       if ((s > 1 && waves > 1.f) || (bn == 128 && !alone) || (sizeof(TO) == 4 && l.nk > 4 * kChunkBlocks * s)) continue;
       const float kb = (l.nk + s - 1) / s * (!alone ? bn == 64 ? 280.f : 220.f : E4M3 ? bn == 128 ? 230.f : 180.f : bn == 128 ? 157.f : bn == 64 ? 148.f : 135.f);
       const float ns = (s > 1 ? (bn <= 32 ? 3700.f : 4900.f) + 100.f * s : 3600.f) + (bn == 128 ? s > 1 ? 2100.f : 3100.f : 0.f) + (alone ? 0.f : s > 1 ? 1900.f : 1100.f) +
-                       (l.wide ? 0.f : 1500.f / s) + kb + (waves - 1) * std::max(kb + 2000.f, 4600.f);
+                       (l.wide ? 0.f : 1000.f / s) + kb + (waves - 1) * std::max(kb + 2000.f, 4600.f);
       if (ns < best) best = ns, plan.tokens = bn, plan.splits = s;
     }
   }
   best = std::max(best, 4000.f + bytes / 6400.f) + 0.15f * std::min(best, 4000.f + bytes / 6400.f);
+  const float narrow = sizeof(TO) == 4 ? 74.f : 57.f;      // a token's epilogue element by element
   for (int t = 64; t <= kPairTokens<TO>; t += l.offsets ? t : 32) {
     const float tiles = (l.N + 2 * kBM - 1) / (2 * kBM) * token_tiles(t), rounds = tiles / (sms / 2);
-    const float kb = l.nk * std::max(185.f, 90.f + 0.83f * t), finish = !l.wide ? 85.f * t : l.plain() ? 700.f + 15.f * t : 1300.f + 21.5f * t;
-    float ns = 3600.f + (l.wide ? 13.7f : 80.f) * t + kb + std::max(0.f, (l.offsets ? rounds : std::ceil(rounds)) - 1.f) * std::max(kb, finish);
+    const float kb = l.nk * std::max(185.f, 90.f + 0.83f * t), finish = l.plain() ? (700.f + 15.f * t) * (l.wide ? 1.f : 1.3f) : l.wide ? 1300.f + 21.5f * t : narrow * t;
+    float ns = 3600.f + (l.wide ? 13.7f : l.plain() ? 17.f : narrow) * t + kb + std::max(0.f, (l.offsets ? rounds : std::ceil(rounds)) - 1.f) * std::max(kb, finish);
     ns = std::max(ns, 5500.f + bytes / 5500.f) + 0.05f * ns;
     if (ns < best) best = ns, plan = {true, t, 1};
   }
