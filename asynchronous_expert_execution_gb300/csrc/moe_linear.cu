@@ -728,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens at once
         const auto narrow = [&](auto plain) {
           constexpr bool PLAIN = decltype(plain)::value;
-          constexpr int kAt = kSums ? E4M3 ? 2 : 4 : 8;
+          constexpr int kAt = kSums ? PLAIN || E4M3 ? 2 : 8 : PLAIN || E4M3 ? 8 : 16;
           using F = Finish<TO, 1, E4M3, PLAIN>;
           const F finish(l, tl.g, f + lane, 1);
           const Place<TO> place(l, tl.row0 + half * kChunk, f + lane);
@@ -1009,20 +1009,22 @@ struct LinearPlan {
   int tokens, splits;               // of a tile; CTAs that share its K
 };
 
-// Kernel, tile and split with the least expected time, in ns.  The constants are fits to this GPU's timings (124
-// shapes of 24 to 8192 tokens on 512 to 7168 features, dense and in 8 to 64 groups; the choice's time is 0.5%
-// above the best one's on average, 28% at worst).  A k-block costs a split CTA 135 to 230 alone on its SM, by tokens
-// and type, and 220 or 280 beside another; a pair 185 to 300.  The exchange takes 100 to 1,300 + 100 a rank, a second CTA on an SM
-// 1,100 to 1,900, 128 tokens of a split CTA 2,100 to 3,100, the pair's epilogue 13.7 a token behind the last tile and, between
-// two, 700 + 15 a token without mul, residual and activation, else 1,300 + 21.5; element by element a
-// third more without them, else 57 or 74 a token.  `bytes`: all operands; the split kernel streams them at 6.4 TB/s, the pair kernel at 5.5; of the
-// smaller of stream and sums, part shows.  Groups count half a tile each for their ends.
+// Kernel, tile and split with the least expected time, in ns.  The constants are fits to this GPU's timings (some
+// 340 shapes and epilogues of 17 to 8192 tokens on 128 to 7168 features, dense and in 8 to 64 groups; the choice's time is
+// 1.5% above the best one's on average, 28% at worst).  A k-block costs a split CTA 135 to 230 alone on its SM, by tokens and
+// type, and 220 or 280 beside another; a pair 185 to 300.  The exchange takes 100 to 1,300 + 100 a rank, a second CTA on an
+// SM 1,100 to 1,900, 128 tokens of a split CTA 2,100 to 3,100, the pair's epilogue 14 a token (30 to 85 element by element)
+// behind the last tile, a third more between two.  Neither the epilogue's operands nor strides count: x and w give the same
+// sums whatever is done with them.  `bytes`: all operands; the split kernel streams them at 6.4 TB/s, the pair kernel at
+// 5.5; of the smaller of stream and sums, part shows.  Groups count half a tile each for their ends.
 template <bool E4M3, typename TO>
 LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
   const float groups = l.offsets ? std::min(l.G, l.T) : 1, per = l.T / groups;
   auto token_tiles = [&](int t) { return l.offsets ? l.T / (float)t + 0.5f * groups : (float)((l.T + t - 1) / t); };
   const int least = per <= 16 ? 16 : per <= 32 ? 32 : 64;
   LinearPlan plan{false, least, 1};
+  const bool rows16 = l.N % 8 == 0;
+  const float wave = rows16 ? 6600.f : 8300.f;       // a further wave, at least
   float best = 1e30f;
   for (int bn = least; bn == least || (bn == 128 && per > 64); bn *= 2) {
     const float tiles = (l.N + kBM - 1) / kBM * token_tiles(bn);
@@ -1032,16 +1034,16 @@ LinearPlan linear_plan(const LinearParams& l, int sms, float bytes) {
       if ((s > 1 && waves > 1.f) || (bn == 128 && !alone) || (sizeof(TO) == 4 && l.nk > 4 * kChunkBlocks * s)) continue;
       const float kb = (l.nk + s - 1) / s * (!alone ? bn == 64 ? 280.f : 220.f : E4M3 ? bn == 128 ? 230.f : 180.f : bn == 128 ? 157.f : bn == 64 ? 148.f : 135.f);
       const float ns = (s > 1 ? (bn <= 32 ? 3700.f : 4900.f) + 100.f * s : 3600.f) + (bn == 128 ? s > 1 ? 2100.f : 3100.f : 0.f) + (alone ? 0.f : s > 1 ? 1900.f : 1100.f) +
-                       (l.wide ? 0.f : 1000.f / s) + kb + (waves - 1) * std::max(kb + 2000.f, 4600.f);
+                       (rows16 ? 0.f : 1700.f / s) + kb + (waves - 1) * std::max(kb + 2000.f, wave);
       if (ns < best) best = ns, plan.tokens = bn, plan.splits = s;
     }
   }
   best = std::max(best, 4000.f + bytes / 6400.f) + 0.15f * std::min(best, 4000.f + bytes / 6400.f);
-  const float narrow = sizeof(TO) == 4 ? 74.f : 57.f;      // a token's epilogue element by element
+  const float last = rows16 ? 13.7f : sizeof(TO) == 2 ? 30.f : E4M3 ? 85.f : 38.f;      // a token's epilogue
   for (int t = 64; t <= kPairTokens<TO>; t += l.offsets ? t : 32) {
     const float tiles = (l.N + 2 * kBM - 1) / (2 * kBM) * token_tiles(t), rounds = tiles / (sms / 2);
-    const float kb = l.nk * std::max(185.f, 90.f + 0.83f * t), finish = l.plain() ? (700.f + 15.f * t) * (l.wide ? 1.f : 1.3f) : l.wide ? 1300.f + 21.5f * t : narrow * t;
-    float ns = 3600.f + (l.wide ? 13.7f : l.plain() ? 17.f : narrow) * t + kb + std::max(0.f, (l.offsets ? rounds : std::ceil(rounds)) - 1.f) * std::max(kb, finish);
+    const float kb = l.nk * std::max(185.f, 90.f + 0.83f * t), finish = 1000.f + 1.3f * last * t;
+    float ns = 3600.f + last * t + kb + std::max(0.f, (l.offsets ? rounds : std::ceil(rounds)) - 1.f) * std::max(kb, finish);
     ns = std::max(ns, 5500.f + bytes / 5500.f) + 0.05f * ns;
     if (ns < best) best = ns, plan = {true, t, 1};
   }

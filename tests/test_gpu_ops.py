@@ -493,6 +493,19 @@ def test_linear_rows_before_the_first_group_and_bad_offsets(moe):
     assert torch.equal(y[:15], want[:15]) and torch.equal(y[20:], want[20:])
 
 
+@pytest.mark.parametrize("T,F,Nn", [(3, 1040, 700), (40, 592, 997), (300, 2064, 520), (512, 512, 3001), (1024, 1040, 2000), (2048, 592, 1999)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_linear_sums_do_not_depend_on_the_epilogue(moe, T, F, Nn, e4m3):
+    """The same operands give the same sums, whatever is added, multiplied or skipped and wherever the rows lie."""
+    g = gen(T + Nn)
+    x, w, kw = linear_inputs(T, F, Nn, e4m3, torch.float32, "", 0, g)
+    plain = moe.linear(x, w, out_dtype=torch.float32, **kw)
+    assert torch.equal(moe.linear(x, w, out_dtype=torch.float32, act="relu", **kw), plain.clamp(min=0))
+    one, zero = torch.ones((T, Nn), device="cuda"), torch.zeros((T, Nn), device="cuda")
+    assert torch.equal(moe.linear(x, w, out_dtype=torch.float32, mul=one, residual=zero, **kw), plain)
+    assert torch.equal(moe.linear(x, w, out=strided(zero, 3), mul=strided(one, 1), **kw), plain)
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_linear_keeps_nan_and_infinity_in_their_rows(moe, e4m3):
     """A NaN in one row reaches that row's outputs only; inf * 0 of another row stays there; relu keeps NaN."""
