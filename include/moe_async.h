@@ -499,6 +499,7 @@ typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 /* with erf 
  *   [G, fan_out, fan_in] (each matrix fan_out * w_stride elements), d_bias and d_w_scale are
  *   [G, fan_out], and rows d_offsets[g] .. d_offsets[g + 1] (device, int32, ascending, clipped to
  *   [0, rows]) meet matrix g; rows of no group are left as they were.
+ * The same d_x and d_w of the same sizes give the same sums whatever the epilogue and the strides.
  * fan_in, the bases and the strides of x and w are multiples of 16 bytes, else
  * MOE_ERR_UNSUPPORTED; fan_out and the other strides are free.  Asynchronous. */
 typedef struct {
