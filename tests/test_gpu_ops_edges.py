@@ -1,0 +1,56 @@
+"""The stateless operators at the edges of their ranges, against their definitions in 64 bits.
+
+Tolerances count half steps: u = 2^-24 for fp32, 2^-8 for a stored bf16 value, 2^-4 for a stored e4m3 value (and half its
+smallest value, 2^-10, below its normal range).
+"""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BOTH = (torch.bfloat16, torch.float32)
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__ as g
+    g.build()
+    import asynchronous_expert_execution_gb300 as pkg
+    return pkg
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def close(got, want, tol, what):
+    d = (got.double() - want).abs()
+    bad = ~(d <= tol)
+    assert not bool(bad.any()), (what, int(bad.sum()), float((d / tol.clamp(min=1e-300)).nan_to_num(1e30).max()))
+
+
+# ------------------------------------------------------------------ norm
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("H", [4, 64, 137, 2880, 20001])
+@pytest.mark.parametrize("size", [3e-40, 6e-39, 1e-37, 1e-36, 2e-36, 1e-20])
+def test_norm_in_8_bits_of_small_rows(moe, dtype, H, size):
+    """Rows far below eps keep their ratios: zeros, halves and signs in 8 bits, with a scale down to 2^-126."""
+    pattern = torch.tensor([1.0, 0.0, 0.5, -0.25], device="cuda").repeat(H // 4 + 1)[:H]
+    x = (torch.stack([pattern, -pattern, pattern.flip(0)]) * size).to(dtype)
+    gain = torch.full((H,), 1.5, device="cuda")
+    eps = 1e-6
+    q, scale, _ = moe.add_rms_norm_e4m3(x, gain=gain, eps=eps)
+    v = x.double()
+    y = v / (v.square().mean(1, keepdim=True) + eps).sqrt() * 1.5
+    want = (y.abs().amax(1) / 448).clamp(min=2.0 ** -126)
+    # a product h gain below 2^-126 is off by up to 2^-150, and 1 / rms is at most 1000
+    tiny = 1000 * 2.0 ** -150
+    close(scale, want, (H / 2 + 16) * U * want + tiny / 448 + 2.0 ** -149, "scale")
+    s = scale.double()[:, None]
+    close(q.double() * s, y, (2.0 ** -4 + (H + 24) * U) * y.abs() + 1.01 * 2.0 ** -10 * s + tiny, "q")
+    assert bool((q.float()[x == 0] == 0).all())
