@@ -167,9 +167,11 @@ __global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, G == 32 ?
     load_gain<V>(gain, c, g);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      // step by step: r / scale as one factor, 448 / max|h gain|, passes fp32 where that is below 1.3e-36.  1 / scale
-      // (at most 2^126) is taken once: a quotient per value took 42 us for 4096 x 7168, 36 so.
-      v[i] = Q ? v[i] * r * g[i] * inv : v[i] * g[i] * r;
+      // step by step, h / rms first, which is at most sqrt(H): h gain may pass fp32 where y does not, and so may r / scale
+      // as one factor, 448 / max|h gain|.  1 / scale (at most 2^126) is taken once: a quotient per value took 42 us
+      // for 4096 x 7168, 36 so.
+      v[i] = v[i] * r * g[i];
+      if (Q) v[i] *= inv;
     }
     if constexpr (Q)
       store_e4m3<V>(q.at(t) + c, v);

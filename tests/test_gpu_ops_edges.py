@@ -35,6 +35,18 @@ def close(got, want, tol, what):
 
 # ------------------------------------------------------------------ norm
 
+def test_norm_of_a_gain_whose_product_with_the_row_passes_fp32(moe):
+    """h / rms is near 1 whatever h's size: only its product with the gain has to fit."""
+    for H in (64, 137, 2880, 20001):
+        h = torch.full((3, H), 1e17, device="cuda")
+        h[1] *= 1e-3
+        gain = torch.full((H,), 1e22, device="cuda")
+        y, _ = moe.add_rms_norm(h, gain=gain)
+        v = h.double()
+        ref = v / (v.square().mean(1, keepdim=True) + 1e-6).sqrt() * gain.double()
+        close(y, ref, (H / 2 + 10) * U * ref, "y")
+
+
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("H", [4, 64, 137, 2880, 20001])
 @pytest.mark.parametrize("size", [3e-40, 6e-39, 1e-37, 1e-36, 2e-36, 1e-20])
