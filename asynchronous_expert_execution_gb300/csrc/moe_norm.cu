@@ -10,6 +10,7 @@
 // the same reduction.  Sums are fp32 in a fixed order (no atomics).
 #include <cuda_fp8.h>
 #include <algorithm>
+#include <cmath>
 #include "moe_ops.cuh"
 #include "moe_ptx.cuh"
 
@@ -159,7 +160,9 @@ __global__ void __launch_bounds__(G == 32 ? 128 : V == 1 ? 1024 : 512, G == 32 ?
   for (int c = c0 + NV * step; c < H; c += step) take(c, again(c));
   row_sum_max<G>(ss, mx, part);
   const float r = 1.0f / sqrtf(ss / (float)H + eps);
-  const float sc = max_nan(r * mx * (1.0f / kE4m3Max), kMinScale), inv = 1.0f / sc;
+  // a sum or a product beyond fp32 (or NaN): r is 0 or the scale infinite, and zeros in 8 bits would hide it
+  const bool lost = !(ss < INFINITY && r * mx < INFINITY);
+  const float sc = lost ? NAN : fmaxf(r * mx * (1.0f / kE4m3Max), kMinScale), inv = 1.0f / sc;
   if (Q && tid == 0) scale[t] = sc;
   auto give = [&](int c, const typename RV::Raw& raw) {
     float v[V], g[V];

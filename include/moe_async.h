@@ -463,9 +463,9 @@ moe_status moe_async_route_backward(const int32_t* d_idx, const float* d_w, cons
  *   d_h        : [T, H] out, the sum; may be NULL, d_x or d_residual
  *   d_scale    : NULL: y is [T, H] in dtype.  Else [T] fp32 out and y is [T, H] e4m3:
  *                scale = max(max|y| / 448, 2^-126), stored value y / scale, round to nearest
- * A NaN makes its row NaN, an infinity (or a sum of squares beyond fp32) makes finite columns 0
- * and itself NaN; in e4m3 either makes the whole row and its scale NaN.  dtype: MOE_F32 or
- * MOE_BF16. */
+ * A NaN makes its row NaN, an infinity makes finite columns 0 and itself NaN, and a row of finite
+ * values whose sum of squares is beyond fp32 becomes zeros; in e4m3 each of them, and an h * gain
+ * or a y beyond fp32, makes the whole row and its scale NaN.  dtype: MOE_F32 or MOE_BF16. */
 moe_status moe_async_add_rms_norm(int32_t dtype, const void* d_x, int64_t x_stride, const void* d_residual,
                                   int64_t residual_stride, const float* d_gain, float eps, int32_t T, int32_t H,
                                   void* d_h, int64_t h_stride, void* d_y, int64_t y_stride, float* d_scale,

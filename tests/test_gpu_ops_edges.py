@@ -66,3 +66,20 @@ def test_norm_in_8_bits_of_small_rows(moe, dtype, H, size):
     s = scale.double()[:, None]
     close(q.double() * s, y, (2.0 ** -4 + (H + 24) * U) * y.abs() + 1.01 * 2.0 ** -10 * s + tiny, "q")
     assert bool((q.float()[x == 0] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_norm_in_8_bits_of_rows_whose_squares_pass_fp32(moe, dtype):
+    """A finite row whose sum of squares is not: zeros in its own type, in 8 bits a row and a scale of NaN, and no other row."""
+    for H in (64, 137, 2880, 20001):
+        x = torch.randn((4, H), generator=gen(H), device="cuda").to(dtype)
+        x[1], x[2] = 1e20, -3e19
+        y, _ = moe.add_rms_norm(x)
+        assert not bool(y[1:3].any())
+        q, scale, _ = moe.add_rms_norm_e4m3(x)
+        assert bool(q[1:3].float().isnan().all()) and bool(scale[1:3].isnan().all())
+        assert bool(torch.isfinite(q[[0, 3]].float()).all()) and bool(torch.isfinite(scale[[0, 3]]).all())
+    x = torch.ones((2, 64), dtype=dtype, device="cuda")                      # likewise a product with the gain that passes fp32
+    x[1] = 1e10
+    q, scale, _ = moe.add_rms_norm_e4m3(x, gain=torch.full((64,), 1e30, device="cuda"))
+    assert bool(q[1].float().isnan().all()) and bool(scale[1].isnan()) and bool((q[0].float() == 448).all())
