@@ -253,11 +253,11 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 384 ? 3 : 1)
         }
       }
     block_sum4(s, part);
-    float r[2], m[2];                                // 1 / rms; its square times mean(u h), which is mean(u n) / rms
+    float r[2], m[2];                                // 1 / rms (its square may pass fp32) and mean(u n)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       r[k] = 1.0f / sqrtf(s[2 * k] / (float)H + eps);
-      m[k] = r[k] * r[k] * (s[2 * k + 1] / (float)H);
+      m[k] = r[k] * s[2 * k + 1] / (float)H;
     }
     auto give = [&](int k, int c, const float (&g)[V], const Raw& rg, const Raw& rh, const Raw& re, float (&dg)[V]) {
       float d[V], v[V], e[V], o[V];
@@ -266,9 +266,10 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 384 ? 3 : 1)
       if (gh.p) RV::unpack(re, e);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        o[i] = r[k] * (d[i] * g[i] - v[i] * m[k]);
+        const float n = v[i] * r[k];
+        o[i] = r[k] * (d[i] * g[i] - n * m[k]);
         if (gh.p) o[i] += e[i];
-        dg[i] = fmaf(d[i], v[i] * r[k], dg[i]);
+        dg[i] = fmaf(d[i], n, dg[i]);
       }
       RV::store(gx.at(t0 + k * gridDim.x) + c, RV::pack(o));
     };
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(1024, 1)
     for (int k = 0; k < 2; ++k) {
       const long long t = t0 + k * (long long)gridDim.x;
       const float r = 1.0f / sqrtf(s[2 * k] / (float)H + eps);
-      const float m = r * r * (s[2 * k + 1] / (float)H);     // mean(u n) / rms
+      const float m = r * s[2 * k + 1] / (float)H;            // mean(u n); r * r may pass fp32
       if (live && t < T_) {
         float d[V], v[V], e[V], o[V];
         RV::unpack(*slot(stage, k, 0), d);
@@ -374,9 +375,10 @@ __global__ void __launch_bounds__(1024, 1)
         if (gh.p) RV::unpack(*slot(stage, k, 2), e);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          o[i] = r * (d[i] * g[i] - v[i] * m);
+          const float n = v[i] * r;
+          o[i] = r * (d[i] * g[i] - n * m);
           if (gh.p) o[i] += e[i];
-          acc[i] = fmaf(d[i], v[i] * r, acc[i]);
+          acc[i] = fmaf(d[i], n, acc[i]);
         }
         RV::store(gx.at(t) + c, RV::pack(o));
       }

@@ -10,6 +10,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 BOTH = (torch.bfloat16, torch.float32)
 
 
@@ -83,3 +84,24 @@ def test_norm_in_8_bits_of_rows_whose_squares_pass_fp32(moe, dtype):
     x[1] = 1e10
     q, scale, _ = moe.add_rms_norm_e4m3(x, gain=torch.full((64,), 1e30, device="cuda"))
     assert bool(q[1].float().isnan().all()) and bool(scale[1].isnan()) and bool((q[0].float() == 448).all())
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("H", [32, 64, 1024, 16384])
+@pytest.mark.parametrize("power", [-74, -70, -65, -64, -30, 0, 40])
+def test_norm_backward_without_eps(moe, dtype, H, power):
+    """eps = 0 and rows of +-2^power: the mean square is a power of two (down to fp32's smallest value), so 1 / rms is
+    exact, and its square may pass fp32 where grad_x does not."""
+    g = gen(H)
+    sign = torch.where(torch.rand((4, H), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    h = (sign * 2.0 ** power).to(dtype)
+    grad = torch.randn((4, H), generator=g, device="cuda").to(dtype)
+    gain = 1 + 0.1 * torch.randn(H, generator=g, device="cuda")
+    gx, gg = moe.add_rms_norm_backward(grad, h, gain, eps=0.0)
+    n, u, r = sign.double(), grad.double() * gain.double(), 2.0 ** -power
+    m, mag = (u * n).mean(1, keepdim=True), (u * n).abs().mean(1, keepdim=True)
+    ref = r * (u - n * m)
+    tol = r * ((u.abs() + m.abs()) * 16 * U + mag * (H + 16) * U)
+    # u h below 2^-126 is off by up to 2^-150 a term: r times that in m
+    close(gx, ref, tol + r * r * 2.0 ** -150 + HALF[dtype] * (ref.abs() + tol), "grad_x")
+    close(gg, (grad.double() * n).sum(0), 16 * U * grad.double().abs().sum(0), "grad_gain")
