@@ -156,6 +156,16 @@ struct Place {
         res(static_cast<const TO*>(p.res) + r * p.ldres + f), y(static_cast<TO*>(p.y) + r * p.ldy + f) {}
 };
 
+// x / (1 + e^-x), written with e^-|x| so that nothing overflows on the way.  For fp32 results within 10 u (u = 2^-24: the
+// exponential and the quotient 4 u each); for bf16 results the fast exponential's 2 + 1.173 |x| steps move it by
+// at most 2^-16, 1/256 of their own rounding (4096 x 512 x 7168 with mul, cold caches: bf16 61 us, fp32 80, 75 with the
+// fast exponential).
+template <typename TO>
+__device__ __forceinline__ float silu(float x) {
+  const float e = sizeof(TO) == 4 ? expf(-fabsf(x)) : __expf(-fabsf(x));
+  return __fdividef(x < 0.f ? x * e : x, 1.0f + e);
+}
+
 // The end of the epilogue for one thread, which owns C features of every token it meets: first,
 // first + step, ...  C = 8, step = 1: rows of y, mul and residual move in 16-byte units; else
 // element by element.  Pointers are to a token's row at feature `first`.  PLAIN: no mul, residual and activation (their tests
@@ -209,7 +219,7 @@ struct Finish {
           for (int i = 0; i < C; ++i) v[u][i] = f(v[u][i]);
       };
       if (p.act == MOE_ACT_SILU)
-        each_value([](float x) { return __fdividef(x, 1.0f + __expf(-x)); });   // off by at most 2^-20 |x|
+        each_value([](float x) { return silu<TO>(x); });
       else if (p.act == MOE_ACT_GELU)
         each_value([](float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678f)); });
       else

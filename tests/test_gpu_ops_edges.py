@@ -105,3 +105,32 @@ def test_norm_backward_without_eps(moe, dtype, H, power):
     # u h below 2^-126 is off by up to 2^-150 a term: r times that in m
     close(gx, ref, tol + r * r * 2.0 ** -150 + HALF[dtype] * (ref.abs() + tol), "grad_x")
     close(gg, (grad.double() * n).sum(0), 16 * U * grad.double().abs().sum(0), "grad_gain")
+
+
+# ------------------------------------------------------------------ product
+
+def of_bias(moe, v, act, out, T):
+    """act(v) by a product of zeros: the pre-activation is exactly the bias."""
+    x, w = torch.zeros((T, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((v.numel(), 64), dtype=torch.bfloat16, device="cuda")
+    y = moe.linear(x, w, v, act=act, out_dtype=out)
+    assert all(torch.equal(y[0].nan_to_num(7.0), y[i].nan_to_num(7.0)) for i in (T // 2, T - 1))
+    return y[0]
+
+
+# For bf16 results the fast exponential may be used: it is off by at most 2 + 1.173 |argument| steps, each at most 2^-23.
+def fast(argument):
+    return (3 + 1.173 * argument.abs()) * 2 * U
+
+
+@pytest.mark.parametrize("out", BOTH)
+@pytest.mark.parametrize("T", [1, 16, 40, 300, 2500])
+def test_silu_is_rounded_once(moe, out, T):
+    """v / (1 + e^-v) to the smallest values: fp32 exponential 2 steps (4 u), sum u, quotient 2 steps (4 u), product u; an e^-|v|
+    below 2^-126 is off by up to 2 steps of 2^-149, |v| times that in the result.  bf16's values below 2^-126 are the multiples of
+    2^-133: half of that."""
+    v = torch.cat([torch.linspace(-100, 30, 1999, device="cuda"), torch.zeros(1, device="cuda")])
+    d = v.double()
+    ref = d * torch.sigmoid(d)
+    rel = 10.1 * U if out == torch.float32 else fast(d) + 6.1 * U + HALF[out]
+    least = 110 * 2.0 ** -148 + (2.0 ** -134 if out == torch.bfloat16 else 0.0)
+    close(of_bias(moe, v, "silu", out, T), ref, rel * ref.abs() + least, "silu")
