@@ -166,6 +166,37 @@ __device__ __forceinline__ float silu(float x) {
   return __fdividef(x < 0.f ? x * e : x, 1.0f + e);
 }
 
+// x times the normal distribution's integral up to x.  1 + erf of a large negative number cancels (at -5 a tenth of the result
+// is lost), so the tail is taken itself: 0.5 erfc(a / sqrt 2) = e^(-a^2 / 2) q(a) for a = |x|, where q falls slowly from 0.5
+// to 1 / (a sqrt(2 pi)).  q = t P(t), t = 1 / (1 + 0.35 a): P is a least-squares fit in 64 bits, reweighted until its
+// errors are level, and q's relative error stays below 0.6 u on [0, 14.5], past which the result is below fp32.  The
+// square's rounding is put back to first order, and fp32 results are within 20 u; for bf16 results neither that nor the
+// fast exponential shows (2^-15 together).  4096 x 512 x 7168 with mul, cold caches: bf16
+// 78 us, fp32 96; by 1 + erf 78 and 88, by erfc of the whole argument 103 and 120.
+template <typename TO>
+__device__ __forceinline__ float gelu(float x) {
+  const float a = fminf(fabsf(x), 16.f), s = a * a;
+  const float t = __fdividef(1.0f, fmaf(0.35f, a, 1.0f));
+  float p = -0.0291578844f;
+  p = fmaf(p, t, 0.144030929f);
+  p = fmaf(p, t, -0.25583902f);
+  p = fmaf(p, t, 0.159319729f);
+  p = fmaf(p, t, -0.0232123677f);
+  p = fmaf(p, t, 0.105552509f);
+  p = fmaf(p, t, 0.119821288f);
+  p = fmaf(p, t, 0.139863506f);
+  p = fmaf(p, t, 0.139621302f);
+  float e;
+  if constexpr (sizeof(TO) == 4) {
+    e = expf(-0.5f * s);
+    e = fmaf(-0.5f * fmaf(a, a, -s), e, e);
+  } else {
+    e = __expf(-0.5f * s);
+  }
+  const float tail = e * (p * t);
+  return x * (x < 0.f ? tail : 1.0f - tail);
+}
+
 // The end of the epilogue for one thread, which owns C features of every token it meets: first,
 // first + step, ...  C = 8, step = 1: rows of y, mul and residual move in 16-byte units; else
 // element by element.  Pointers are to a token's row at feature `first`.  PLAIN: no mul, residual and activation (their tests
@@ -221,7 +252,7 @@ struct Finish {
       if (p.act == MOE_ACT_SILU)
         each_value([](float x) { return silu<TO>(x); });
       else if (p.act == MOE_ACT_GELU)
-        each_value([](float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678f)); });
+        each_value([](float x) { return gelu<TO>(x); });
       else
         each_value([](float x) { return x < 0.f ? 0.f : x; });                  // relu; NaN stays
     }

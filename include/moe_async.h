@@ -486,9 +486,10 @@ moe_status moe_async_add_rms_norm_backward(int32_t dtype, const void* d_grad, in
                                            int64_t grad_x_stride, float* d_grad_gain, void* d_workspace,
                                            int64_t workspace_bytes, void* stream);
 
-/* silu is computed to within 10 * 2^-24 of its value for fp32 results, 2^-15 for bf16 ones (whose
- * own rounding is up to 2^-8). */
-typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 /* with erf */, MOE_ACT_RELU = 3 } moe_act;
+/* silu is computed to within 10 * 2^-24 of its value for fp32 results, gelu (x times the normal
+ * distribution's integral) to within 20 * 2^-24; for bf16 ones, whose own rounding is up to 2^-8,
+ * both to within 2^-15. */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_RELU = 3 } moe_act;
 
 /* y[t, n] = act(sx[t] sw[n] sum_k x[t, k] w[n, k] + bias[n]) * mul[t, n] + residual[t, n]
  *   dtype     : MOE_BF16, or MOE_E4M3 with d_x_scale [rows] and d_w_scale [fan_out] fp32 (NULL

@@ -3,6 +3,7 @@
 Tolerances count half steps: u = 2^-24 for fp32, 2^-8 for a stored bf16 value, 2^-4 for a stored e4m3 value (and half its
 smallest value, 2^-10, below its normal range).
 """
+import math
 
 import pytest
 import torch
@@ -134,3 +135,30 @@ def test_silu_is_rounded_once(moe, out, T):
     rel = 10.1 * U if out == torch.float32 else fast(d) + 6.1 * U + HALF[out]
     least = 110 * 2.0 ** -148 + (2.0 ** -134 if out == torch.bfloat16 else 0.0)
     close(of_bias(moe, v, "silu", out, T), ref, rel * ref.abs() + least, "silu")
+
+
+@pytest.mark.parametrize("out", BOTH)
+@pytest.mark.parametrize("T", [1, 16, 40, 300, 2500])
+def test_gelu_keeps_its_negative_tail(moe, out, T):
+    """v times the normal distribution's integral: fp32 exponential and its correction 6 u, the fit 0.6 u, its variable 5 u, nine steps
+    of a polynomial whose terms stay below twice its value 5 u, three products 3 u.  In bf16 the exponent, v^2 / 2, keeps its
+    rounding, and the fast exponential its error."""
+    v = torch.cat([torch.linspace(-12, 8, 1999, device="cuda"), torch.zeros(1, device="cuda")])
+    d = v.double()
+    ref = 0.5 * d * torch.erfc(-d / math.sqrt(2.0))
+    rel = 20 * U if out == torch.float32 else fast(d * d / 2) + (14 + d * d / 2) * U + HALF[out] * 1.01
+    close(of_bias(moe, v, "gelu", out, T), ref, rel * ref.abs(), "gelu")
+
+
+def test_activations_of_infinity_and_nan(moe):
+    """relu, silu and gelu at the ends: infinity, 0 or NaN as the formulas give them."""
+    inf, nan = float("inf"), float("nan")
+    v = torch.tensor([inf, -inf, nan, 1e30, -1e30, -0.0, 1e-30, -1e-30], device="cuda")
+    for T in (1, 40, 2500):
+        for out in BOTH:
+            y = {a: of_bias(moe, v, a, out, T).float() for a in ("relu", "silu", "gelu")}
+            small = v[6:].to(out).float()
+            for a in ("silu", "gelu"):
+                assert float(y[a][0]) == inf and bool(y[a][1].isnan()) and bool(y[a][2].isnan()) and float(y[a][3]) == float(v[3].to(out))
+                assert float(y[a][4]) == 0 and float(y[a][5]) == 0 and bool(((y[a][6:] - small / 2).abs() <= small.abs() * 2.0 ** -7).all())
+            assert float(y["relu"][0]) == inf and float(y["relu"][1]) == 0 and bool(y["relu"][2].isnan()) and not bool(y["relu"][[4, 5]].any())
