@@ -28,6 +28,7 @@ namespace {
 // expert find each other by ballots over the id's bits (524288 pairs: 86 us by matching whole ids, 61 so).
 constexpr int kKeep = 8;
 constexpr int kSortCluster = 8;
+constexpr int kSortSmem = (32 + 3) * (kMaxExperts + 1) * (int)sizeof(int);       // of a block, at most
 
 __global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __restrict__ expert, int P, int E, int per,
                                                             int32_t* __restrict__ offsets, int32_t* __restrict__ pos,
@@ -407,8 +408,9 @@ moe_status moe_async_sort_experts(const int32_t* d_expert, int32_t T, int32_t K,
   const int ctas = all > 32 ? kSortCluster : 1, warps = (all + ctas - 1) / ctas;
   const int per = (int)(((P + (long long)warps * ctas - 1) / ((long long)warps * ctas) + 31) & ~31LL);
   const size_t smem = (size_t)(warps + 3) * (E + 1) * sizeof(int);
+  // the limit belongs to the function, and another thread may launch it with more at any time: one limit for all calls
   if (smem > 48 * 1024 && cudaFuncSetAttribute(sort_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem) != cudaSuccess)
+                                               kSortSmem) != cudaSuccess)
     return MOE_ERR_CUDA;
   return launch_op(sort_experts_kernel, dim3(ctas), 32 * warps, smem, ctas, stream, d_expert, (int)P, E, per, d_offsets,
                    d_pos, d_pair);

@@ -4,6 +4,7 @@ Tolerances count half steps: u = 2^-24 for fp32, 2^-8 for a stored bf16 value, 2
 smallest value, 2^-10, below its normal range).
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -162,3 +163,47 @@ def test_activations_of_infinity_and_nan(moe):
                 assert float(y[a][0]) == inf and bool(y[a][1].isnan()) and bool(y[a][2].isnan()) and float(y[a][3]) == float(v[3].to(out))
                 assert float(y[a][4]) == 0 and float(y[a][5]) == 0 and bool(((y[a][6:] - small / 2).abs() <= small.abs() * 2.0 ** -7).all())
             assert float(y["relu"][0]) == inf and float(y["relu"][1]) == 0 and bool(y["relu"][2].isnan()) and not bool(y["relu"][[4, 5]].any())
+
+
+# ------------------------------------------------------------------ tensors, streams and threads
+
+def on_threads(jobs, seconds=4.0):
+    """Each job again and again on a host thread and a stream of its own; the first exception of any of them."""
+    errors, stop = [], threading.Event()
+    start = threading.Barrier(len(jobs))
+
+    def work(job):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                while not stop.is_set():
+                    job()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:                                               # noqa: BLE001
+            errors.append(e)
+            stop.set()
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    stop.wait(seconds)
+    stop.set()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return errors
+
+
+def test_sort_experts_of_different_sizes_on_two_threads(moe):
+    """Two host threads whose calls need different amounts of shared memory."""
+    jobs = []
+    for E in (512, 1024):
+        expert = torch.randint(0, E, (20000, 2), generator=gen(E), device="cuda").to(torch.int32)
+        want = [t.clone() for t in moe.sort_experts(expert, E)]
+
+        def job(expert=expert, E=E, want=want):
+            for _ in range(50):
+                got = moe.sort_experts(expert, E)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        jobs.append(job)
+    torch.cuda.synchronize()
+    assert not on_threads(jobs)
