@@ -1016,7 +1016,8 @@ int split_capacity(int s, int sms) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   const auto kernel = linear_split_kernel<false, __nv_bfloat16>;       // all forms share its limits
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem / 2) != cudaSuccess ||
+  // the limit of launch_split: another thread may be launching this kernel
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
     return sms;
   known[dev][s].store(n * s, std::memory_order_relaxed);

@@ -4,6 +4,9 @@ Tolerances count half steps: u = 2^-24 for fp32, 2^-8 for a stored bf16 value, 2
 smallest value, 2^-10, below its normal range).
 """
 import math
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -11,6 +14,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U = 2.0 ** -24
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 BOTH = (torch.bfloat16, torch.float32)
@@ -207,3 +211,30 @@ def test_sort_experts_of_different_sizes_on_two_threads(moe):
         jobs.append(job)
     torch.cuda.synchronize()
     assert not on_threads(jobs)
+
+
+def test_linear_of_different_lengths_on_two_threads(moe):
+    """Two host threads whose products take different kernels, tiles and amounts of shared memory, from the first call on."""
+    code = ("import sys, threading, torch\n"
+            "import asynchronous_expert_execution_gb300 as moe\n"
+            "g = torch.Generator(device='cuda').manual_seed(1)\n"
+            "r = lambda *s: torch.randn(s, generator=g, device='cuda').bfloat16()\n"
+            "ops = [(r(512, 7168), r(256, 7168)), (r(40, 128), r(300, 128)), (r(600, 1024), r(4096, 1024)), (r(4, 512), r(64, 512))]\n"
+            "want = [x.double() @ w.double().T for x, w in ops]\n"
+            "torch.cuda.synchronize()\n"
+            "bar, errors = threading.Barrier(4), []\n"
+            "def work(i):\n"
+            "    try:\n"
+            "        with torch.cuda.stream(torch.cuda.Stream()):\n"
+            "            bar.wait()\n"
+            "            for _ in range(300):\n"
+            "                y = moe.linear(*ops[i])\n"
+            "            assert float((y.double() - want[i]).norm() / want[i].norm()) < 2 ** -8\n"
+            "    except Exception as e:\n"
+            "        errors.append(e)\n"
+            "threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]\n"
+            "[t.start() for t in threads]; [t.join() for t in threads]\n"
+            "moe.ops_sync()\n"
+            "assert not errors, errors\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
