@@ -124,15 +124,6 @@ Tensor empty(at::IntArrayRef sizes, ScalarType dtype, int dev) {
   return at::detail::empty_cuda(sizes, dtype, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
 }
 
-// `sizes` elements of a tensor from element `first` on, as a tensor of its own: one allocation for several small
-// outputs (sort_experts' host side 4.6 -> 3.8 us)
-Tensor part(const Tensor& whole, int64_t first, at::IntArrayRef sizes) {
-  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
-  t.unsafeGetTensorImpl()->set_storage_offset(first);
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-  return t;
-}
-
 // `out` as handed in (checked), or a new matrix; its row stride in ld.
 Tensor output(PyObject* out, const char* name, int dev, ScalarType dtype, int64_t n, int64_t width, int64_t& ld) {
   if (out == Py_None) {
@@ -206,9 +197,7 @@ PyObject* sort_experts(PyObject* const* a) {
   const int64_t E = integer(a[1], "num_experts");
   if (E < 1) bad("num_experts: expected at least 1");
   const int32_t T = count(l.n, "tokens"), K = count(l.width, "top_k");
-  const int64_t n = l.n * l.width, room = (n + 63) / 64 * 64;                    // each on a 256-byte boundary
-  const Tensor whole = empty({2 * room + E + 1}, at::kInt, l.dev);
-  const Tensor pos = part(whole, 0, {T, K}), pair = part(whole, room, {n}), offsets = part(whole, 2 * room, {E + 1});
+  Tensor offsets = empty({E + 1}, at::kInt, l.dev), pos = empty({T, K}, at::kInt, l.dev), pair = empty({l.n * l.width}, at::kInt, l.dev);
   call("sort_experts", on, [&](void* s) {
     return lib.sort_experts(ptr<int32_t>(expert), T, K, static_cast<int32_t>(E), ptr<int32_t>(offsets), ptr<int32_t>(pos),
                             ptr<int32_t>(pair), s);

@@ -171,6 +171,18 @@ def test_activations_of_infinity_and_nan(moe):
 
 # ------------------------------------------------------------------ tensors, streams and threads
 
+def test_sort_experts_outputs_own_their_memory(moe):
+    """Three tensors, three allocations: growing one in place leaves the others alone."""
+    expert = torch.randint(0, 16, (200, 4), generator=gen(1), device="cuda").to(torch.int32)
+    offsets, pos, pair = moe.sort_experts(expert, 16)
+    assert len({t.untyped_storage().data_ptr() for t in (offsets, pos, pair)}) == 3
+    for t in (offsets, pos, pair):
+        assert t.storage_offset() == 0 and t.untyped_storage().nbytes() == t.numel() * 4
+    keep = offsets.clone(), pair.clone()
+    pos.resize_(2000, 4).fill_(-9)
+    assert torch.equal(offsets, keep[0]) and torch.equal(pair, keep[1])
+
+
 def on_threads(jobs, seconds=4.0):
     """Each job again and again on a host thread and a stream of its own; the first exception of any of them."""
     errors, stop = [], threading.Event()
