@@ -7,6 +7,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -55,7 +56,12 @@ std::string shape(int64_t rows, int64_t width) { return "[" + std::to_string(row
 
 const Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) bad(std::string(name) + ": expected a tensor");
-  return THPVariable_Unpack(o);
+  const Tensor& t = THPVariable_Unpack(o);
+  // nothing is recorded here: what autograd would follow has to be said to be left out
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    bad(std::string(name) + ": requires grad, which the operators do not record; detach it, or call under torch.no_grad() or in an "
+                            "autograd.Function with the *_backward functions");
+  return t;
 }
 const Tensor* maybe(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
 template <typename T = void>

@@ -13,7 +13,9 @@ For a caller that holds a whole routed batch (a prefill chunk, a training step):
 Every function runs on the device of its first tensor, on that device's current stream unless
 ``stream`` is given, allocates only the outputs it is not handed, and raises ``MoEError``
 (``MOE_ERR_INVALID``) for tensors that do not fit together.  Gradients are functions of their
-own (``*_backward``).  Matrices are [rows, width] with adjacent columns and any row stride.
+own (``*_backward``), for an ``autograd.Function`` to call; nothing is recorded here, so a tensor
+that requires grad is refused while grad mode is on.  Matrices are [rows, width] with adjacent
+columns and any row stride.
 """
 import ctypes
 

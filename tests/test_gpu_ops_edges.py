@@ -250,3 +250,31 @@ def test_linear_of_different_lengths_on_two_threads(moe):
             "assert not errors, errors\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_operators_refuse_to_drop_gradients(moe):
+    """The operators record nothing: a call whose result would need a gradient is refused, one without grad mode runs."""
+    x = torch.randn((4, 64), device="cuda").to(torch.bfloat16)
+    w = torch.randn((16, 64), device="cuda").to(torch.bfloat16)
+    gain, pos, wt = torch.ones(64, device="cuda"), torch.arange(8, dtype=torch.int32, device="cuda").reshape(4, 2), torch.ones((4, 2), device="cuda")
+    rows = moe.sort_rows(x, pos)
+    leaf = lambda t: t.clone().requires_grad_()                              # noqa: E731
+    calls = [lambda f: moe.sort_rows(f(x), pos), lambda f: moe.merge_rows(f(rows), pos, wt), lambda f: moe.merge_rows(rows, pos, f(wt)),
+             lambda f: moe.merge_rows(rows, pos, wt, f(x)), lambda f: moe.merge_rows_backward(f(x), rows, pos, wt),
+             lambda f: moe.merge_rows_backward(x, rows, pos, f(wt)), lambda f: moe.route_backward(pos, f(wt), wt, 16),
+             lambda f: moe.sort_rows_backward(f(rows), pos), lambda f: moe.add_rms_norm(f(x)), lambda f: moe.add_rms_norm(x, f(x)),
+             lambda f: moe.add_rms_norm(x, None, f(gain)), lambda f: moe.add_rms_norm_e4m3(x, x, f(gain)),
+             lambda f: moe.add_rms_norm_backward(f(x), x, gain), lambda f: moe.add_rms_norm_backward(x, x, f(gain)),
+             lambda f: moe.add_rms_norm_backward(x, x, gain, grad_h=f(x)), lambda f: moe.linear(f(x), w), lambda f: moe.linear(x, f(w)),
+             lambda f: moe.linear(x, w, f(torch.ones(16, device="cuda"))), lambda f: moe.linear(x, w, mul=f(x[:, :16].contiguous())),
+             lambda f: moe.linear(x, w, residual=f(x[:, :16].contiguous())), lambda f: moe.linear(x, w, out=f(x[:, :16].contiguous())),
+             lambda f: moe.add_rms_norm(x, x, out_h=f(x))]
+    for i, call in enumerate(calls):
+        with pytest.raises(moe.MoEError):
+            call(leaf)
+            raise AssertionError(f"call {i} was accepted")
+        with torch.no_grad():
+            call(leaf)
+        with torch.inference_mode():
+            call(lambda t: t.clone())
+        call(lambda t: leaf(t).detach())
