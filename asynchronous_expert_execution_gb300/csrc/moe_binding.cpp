@@ -141,6 +141,13 @@ Tensor output(PyObject* out, const char* name, int dev, ScalarType dtype, int64_
   return t;
 }
 
+// An output that was handed in has been written over: autograd finds it where it was saved before.
+void written(PyObject* out) {
+  if (out == Py_None) return;
+  const Tensor& t = THPVariable_Unpack(out);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();     // an inference tensor has no version
+}
+
 // The call's device and stream, made current while it runs: what the call allocates belongs to that
 // stream, so memory that other streams gave back is not written before they are done with it.
 struct On {
@@ -224,6 +231,7 @@ PyObject* sort_rows(PyObject* const* a) {
     return lib.sort_rows(code(l.dtype), ptr(x), l.ld, ptr<int32_t>(pos), count(l.n, "tokens"), count(K, "top_k"),
                          count(l.width, "width"), ptr(out), ldo, R, s);
   });
+  written(a[2]);
   return wrap(out);
 }
 
@@ -242,6 +250,7 @@ PyObject* merge_rows(PyObject* const* a) {
     return lib.merge_rows(code(l.dtype), ptr(r), l.ld, l.n, ptr<int32_t>(pos), ptr<float>(w), count(T, "tokens"), count(K, "top_k"),
                           count(l.width, "width"), ptr(res), ldres, ptr(out), ldo, s);
   });
+  written(a[4]);
   return wrap(out);
 }
 
@@ -261,6 +270,7 @@ PyObject* merge_rows_backward(PyObject* const* a) {
                                    count(T, "tokens"), count(K, "top_k"), count(l.width, "width"), ptr(out), ldo,
                                    ptr<float>(grad_w), s);
   });
+  written(a[4]);
   return tuple({wrap(out), wrap(grad_w)});
 }
 
@@ -313,6 +323,8 @@ PyObject* add_rms_norm(PyObject* const* a) {
     return lib.add_rms_norm(code(l.dtype), ptr(x), l.ld, ptr(res), ldr, ptr<float>(gain), eps, count(T, "rows"), count(H, "width"),
                             res ? ptr(h) : nullptr, ldh, ptr(out), ldo, e4m3 ? ptr<float>(scale) : nullptr, s);
   });
+  written(a[4]);
+  written(a[5]);
   return tuple({wrap(out), e4m3 ? wrap(scale) : same(Py_None), !res ? same(a[0]) : a[5] != Py_None ? same(a[5]) : wrap(h)});
 }
 
@@ -339,6 +351,7 @@ PyObject* add_rms_norm_backward(PyObject* const* a) {
                                      count(H, "width"), ptr(gh), ldgh, ptr(out), ldo, gain ? ptr<float>(grad_gain) : nullptr,
                                      gain ? ptr(ws) : nullptr, size, s);
   });
+  written(a[5]);
   return tuple({wrap(out), gain ? wrap(grad_gain) : same(Py_None)});
 }
 
@@ -404,6 +417,7 @@ PyObject* linear(PyObject* const* a) {
   p.d_offsets = ptr<int32_t>(offsets);
   p.d_y = ptr(out);
   call("linear", on, [&](void* s) { return lib.linear(&p, s); });
+  written(a[10]);
   return given ? same(a[10]) : wrap(out);
 }
 

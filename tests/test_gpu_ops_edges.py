@@ -278,3 +278,24 @@ def test_operators_refuse_to_drop_gradients(moe):
         with torch.inference_mode():
             call(lambda t: t.clone())
         call(lambda t: leaf(t).detach())
+
+
+def test_outputs_in_place_raise_their_version(moe):
+    """Autograd finds a saved tensor that an operator wrote over."""
+    x = torch.randn((4, 64), device="cuda").to(torch.bfloat16)
+    w = torch.randn((64, 64), device="cuda").to(torch.bfloat16)
+    pos, wt = torch.arange(8, dtype=torch.int32, device="cuda").reshape(4, 2), torch.ones((4, 2), device="cuda")
+    rows = torch.randn((8, 64), device="cuda").to(torch.bfloat16)
+    for write in (lambda t: moe.sort_rows(x, pos, out=t[:8]), lambda t: moe.merge_rows(rows, pos, wt, out=t[:4]),
+                  lambda t: moe.sort_rows_backward(rows, pos, out=t[:4]), lambda t: moe.merge_rows_backward(x, rows, pos, wt, out=t[:8]),
+                  lambda t: moe.add_rms_norm(x, x, out=t[:4]), lambda t: moe.add_rms_norm(x, x, out_h=t[:4]),
+                  lambda t: moe.add_rms_norm_backward(x, x, out=t[:4]), lambda t: moe.linear(x, w, out=t[:4])):
+        t = torch.randn((8, 64), device="cuda").to(torch.bfloat16)
+        a = t.clone().requires_grad_()
+        y = (a * t).sum()                                                    # saves t for a's gradient
+        write(t)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    with torch.inference_mode():
+        t = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    assert bool(moe.linear(x, w, out=t).any())                               # made without a version
