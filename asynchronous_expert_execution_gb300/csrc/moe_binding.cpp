@@ -166,6 +166,14 @@ struct On {
     stream = static_cast<cudaStream_t>(PyLong_AsVoidPtr(v));
     Py_DECREF(v);
     if (PyErr_Occurred()) throw PythonError{};
+    if (PyObject* index = PyObject_GetAttrString(s, "device_index")) {      // an object that names no device is taken at its word
+      const long at = PyLong_AsLong(index);
+      Py_DECREF(index);
+      if (at == -1 && PyErr_Occurred()) throw PythonError{};
+      if (at != d) bad("stream: on cuda:" + std::to_string(at) + ", the tensors on cuda:" + std::to_string(d));
+    } else {
+      PyErr_Clear();
+    }
     guard.reset_stream(c10::cuda::getStreamFromExternal(stream, static_cast<c10::DeviceIndex>(d)));
   }
 };

@@ -299,3 +299,16 @@ def test_outputs_in_place_raise_their_version(moe):
     with torch.inference_mode():
         t = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
     assert bool(moe.linear(x, w, out=t).any())                               # made without a version
+
+
+def test_a_stream_of_another_device_is_refused(moe):
+    class Other:
+        cuda_stream = torch.cuda.current_stream().cuda_stream
+        device = torch.device("cuda", torch.cuda.current_device() + 1)
+        device_index = device.index
+    x = torch.ones((4, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(moe.MoEError):
+        moe.add_rms_norm(x, stream=Other())
+    y, _ = moe.add_rms_norm(x, stream=torch.cuda.ExternalStream(torch.cuda.Stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert bool((y == 1).all())
