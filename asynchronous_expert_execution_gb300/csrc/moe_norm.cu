@@ -505,7 +505,7 @@ moe_status moe_async_add_rms_norm(int32_t dtype, const void* d_x, int64_t x_stri
                                   int64_t residual_stride, const float* d_gain, float eps, int32_t T, int32_t H,
                                   void* d_h, int64_t h_stride, void* d_y, int64_t y_stride, float* d_scale,
                                   void* stream) {
-  if ((dtype != MOE_F32 && dtype != MOE_BF16) || T < 0 || H < 1 || !(eps >= 0.f)) return MOE_ERR_INVALID;
+  if ((dtype != MOE_F32 && dtype != MOE_BF16) || T < 0 || H < 1 || H > kMaxWidth || !(eps >= 0.f)) return MOE_ERR_INVALID;
   if (T == 0) return MOE_OK;
   if (!d_x || !d_y || x_stride < H || y_stride < H || (d_residual && residual_stride < H) ||
       (d_h && (!d_residual || h_stride < H)))
@@ -526,7 +526,7 @@ moe_status moe_async_add_rms_norm_backward(int32_t dtype, const void* d_grad, in
                                            const void* d_grad_h, int64_t grad_h_stride, void* d_grad_x,
                                            int64_t grad_x_stride, float* d_grad_gain, void* d_workspace,
                                            int64_t workspace_bytes, void* stream) {
-  if ((dtype != MOE_F32 && dtype != MOE_BF16) || T < 0 || H < 1 || !(eps >= 0.f)) return MOE_ERR_INVALID;
+  if ((dtype != MOE_F32 && dtype != MOE_BF16) || T < 0 || H < 1 || H > kMaxWidth || !(eps >= 0.f)) return MOE_ERR_INVALID;
   if (T == 0) {
     if (!d_grad_gain) return MOE_OK;
     return cudaMemsetAsync(d_grad_gain, 0, (size_t)H * sizeof(float), static_cast<cudaStream_t>(stream)) == cudaSuccess

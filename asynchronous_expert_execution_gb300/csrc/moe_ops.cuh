@@ -32,6 +32,9 @@ template <typename T> struct Rows {
   __device__ __forceinline__ T* at(int64_t r) const { return p + r * ld; }
 };
 
+// Column indices are 32-bit and step past a row's end by up to a block's columns (at most 512 x 8 a step, four of them).
+constexpr int kMaxWidth = INT32_MAX - 65536;
+
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // 16-byte access to rows at p with row stride ld (elements of `size` bytes); a null p has no say.

@@ -312,7 +312,7 @@ __global__ void route_backward_kernel(const int32_t* __restrict__ idx, const flo
 }
 
 bool valid_rows(int32_t dtype, int32_t T, int32_t K, int32_t H, int64_t R) {
-  return (dtype == MOE_F32 || dtype == MOE_BF16) && T >= 0 && K >= 1 && K <= 32 && H >= 1 && R >= 0 &&
+  return (dtype == MOE_F32 || dtype == MOE_BF16) && T >= 0 && K >= 1 && K <= 32 && H >= 1 && H <= kMaxWidth && R >= 0 &&
          (int64_t)T * K <= INT32_MAX && R <= INT32_MAX;
 }
 
@@ -462,7 +462,7 @@ moe_status moe_async_route_backward(const int32_t* d_idx, const float* d_w, cons
   if (T < 0 || E < 1 || E > kMaxExperts || K < 1 || K > E || K > 32) return MOE_ERR_INVALID;
   if (T == 0) return MOE_OK;
   if (!d_idx || !d_w || !d_grad_w || !d_grad_logits) return MOE_ERR_INVALID;
-  return launch_op(route_backward_kernel, dim3((T + 7) / 8), 256, 0, 1, stream, d_idx, d_w, d_grad_w, T, E, K,
+  return launch_op(route_backward_kernel, dim3((unsigned)((T + 7LL) / 8)), 256, 0, 1, stream, d_idx, d_w, d_grad_w, T, E, K,
                    d_grad_logits);
 }
 

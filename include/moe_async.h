@@ -412,6 +412,8 @@ moe_status moe_async_forward_noalloc(int32_t T, int32_t E, int32_t K, int32_t H,
  *     adjacent.  Rows whose base and stride are multiples of 16 bytes, and whose width is a
  *     whole number of 16-byte units, move in such units; others element by element.
  *   - Parameter vectors (gain, bias, scales, routing weights) are fp32.
+ *   - Sizes are at least 1, but 0 rows (or tokens) are a call that does nothing; widths are at most
+ *     2^31 - 65537 (moe_async_linear: 2^31 - 1025).
  *   - Sums are fp32 in an order fixed by the sizes and the alignment (no atomics): equal calls
  *     give equal bits.
  *   - An output may share memory with an input only where stated. */

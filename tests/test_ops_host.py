@@ -2,6 +2,8 @@
 import os
 import re
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "asynchronous_expert_execution_gb300", "csrc")
 
@@ -19,3 +21,26 @@ def test_one_shared_memory_limit_a_kernel():
     for name, sizes in limits.items():
         assert len(sizes) == 1, (name, sizes)
         assert re.fullmatch(r"(k[A-Z]\w*|\d+)( [*+] (k[A-Z]\w*|\d+))*", next(iter(sizes))), (name, sizes)
+
+
+@pytest.fixture(scope="module")
+def nat():
+    import __graft_entry__ as g
+    g.build()
+    from asynchronous_expert_execution_gb300 import _native as N
+    return N, N.load()
+
+
+P = 256                                          # an address that is never looked at: every call returns early
+
+
+@pytest.mark.parametrize("H", [2 ** 31 - 1, 2 ** 31 - 8, 2 ** 31 - 65536])
+def test_widths_whose_columns_would_pass_32_bits_are_refused(nat, H):
+    """Column indices are 32-bit and step past the row's end by up to a block's columns: a width near 2^31 would wrap there."""
+    N, lib = nat
+    for dt in (N.MOE_F32, N.MOE_BF16):
+        assert lib.moe_async_add_rms_norm(dt, P, H, None, 0, None, 1e-6, 1, H, None, 0, P, H, None, None) == N.MOE_ERR_INVALID
+        assert lib.moe_async_add_rms_norm_backward(dt, P, H, P, H, None, 1e-6, 1, H, None, 0, P, H, None, None, 0, None) == N.MOE_ERR_INVALID
+        assert lib.moe_async_sort_rows(dt, P, H, P, 1, 1, H, P, H, 1, None) == N.MOE_ERR_INVALID
+        assert lib.moe_async_merge_rows(dt, P, H, 1, P, P, 1, 1, H, None, 0, P, H, None) == N.MOE_ERR_INVALID
+        assert lib.moe_async_merge_rows_backward(dt, P, H, P, H, 1, P, P, 1, 1, H, P, H, P, None) == N.MOE_ERR_INVALID
