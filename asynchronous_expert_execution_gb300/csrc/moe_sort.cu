@@ -139,7 +139,6 @@ __global__ void __launch_bounds__(1024) sort_experts_kernel(const int32_t* __res
       }
     }
   }
-  __syncwarp();
   if (C > 1) ptx::cluster_wait();                    // no CTA ends while another reads its totals
 }
 
