@@ -25,7 +25,7 @@
 //          (4 tokens on 2880 x 2880: 5.8 us against 7.0).
 //
 // Every wait is bounded (2 s): a wait that runs out stops all roles, latches MOE_ERR_TIMEOUT in
-// the operators' error word, and the CTA still frees its TMEM.
+// the operators' error word, and the CTA still lets what is in flight land and frees its TMEM.
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 #include <algorithm>
@@ -80,6 +80,15 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
       return false;
     }
   }
+}
+
+// After a wait that ran out, when all roles have stopped: copies, products and their arrivals on barriers may still be under
+// way, and must not reach shared memory or TMEM that the next CTA owns.  None of them takes a hundredth of this.
+constexpr unsigned long long kSettleNs = 10000000ull;
+__device__ __forceinline__ void settle(volatile int* abort_flag) {
+  if (threadIdx.x != 0 || !*abort_flag) return;
+  const unsigned long long t0 = now_ns();
+  while (now_ns() - t0 < kSettleNs) __nanosleep(1000);
 }
 
 // Rows [a, b) of group g, clipped to the rows there are.
@@ -440,8 +449,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
   const int j0 = nj * rank / p.splits, j1 = nj * (rank + 1) / p.splits;
   if (nj > 0 && warp >= 4) {
     const int q = warp & 3, row = 32 * q + lane;     // TMEM lane: a feature
-    const bool ok = wait(&s->done, 0, abort_flag);
-    __syncwarp();
+    const bool ok = __all_sync(0xffffffffu, wait(&s->done, 0, abort_flag));      // whole warps read TMEM
     tc_after();
     if (ok) {
       const uint32_t t = tmem + ((uint32_t)(32 * q) << 16);
@@ -482,10 +490,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
     else
       split_finish<TO, 4, E4M3>(p, g, row0, fti * kBM, own, got, rank, j0, j1, lane, 32, warp, kThreads / 32);
   }
-  if (p.splits > 1) {
-    __syncwarp();
-    cluster_sync();                                  // the copies out of a rank's memory have been received
-  }
+  settle(abort_flag);
+  if (p.splits > 1) cluster_sync();                  // the copies out of a rank's memory have been received
   tc_before();
   __syncthreads();
   tc_after();
@@ -802,6 +808,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncwarp();
   tc_before();
   __syncthreads();
+  settle(abort_flag);
   cluster_sync();                                    // neither CTA's shared memory goes while the other may use it
   tc_after();
   if (warp == 2) tmem_dealloc<2>(tmem, kCols);
