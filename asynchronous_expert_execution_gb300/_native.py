@@ -26,7 +26,8 @@ EXPORTS = ("moe_async_create", "moe_async_route", "moe_async_enqueue", "moe_asyn
            "moe_async_cancel", "moe_async_debug_append_record",
            "moe_async_sort_experts", "moe_async_sort_rows", "moe_async_merge_rows", "moe_async_merge_rows_backward",
            "moe_async_route_backward", "moe_async_add_rms_norm", "moe_async_add_rms_norm_backward",
-           "moe_async_add_rms_norm_backward_workspace", "moe_async_linear", "moe_async_ops_status")
+           "moe_async_add_rms_norm_backward_workspace", "moe_async_linear", "moe_async_ops_status",
+           "moe_async_debug_latch_ops_error")
 
 KERNEL_KINDS = ("enqueue", "schedule", "ffn1", "ffn2", "collect", "tick")
 
@@ -131,6 +132,7 @@ def load():
         "moe_async_add_rms_norm_backward_workspace": [I32, I32],
         "moe_async_linear": [ctypes.POINTER(LinearArgs), P],
         "moe_async_ops_status": [P],
+        "moe_async_debug_latch_ops_error": [P],
     }
     restype = {"moe_async_status_string": ctypes.c_char_p, "moe_async_add_rms_norm_backward_workspace": I64}
     for name, args in sig.items():

@@ -1175,5 +1175,25 @@ extern "C" moe_status moe_async_ops_status(void* stream) {
   if (cudaMemcpyFromSymbolAsync(&e, g_ops_error, sizeof(e), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess)
     return MOE_ERR_CUDA;
+  if (e == 0) return MOE_OK;
+  const unsigned int none = 0;                       // reported: the calls after this one start clear
+  if (cudaMemcpyToSymbolAsync(g_ops_error, &none, sizeof(none), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MOE_ERR_CUDA;
   return static_cast<moe_status>(e);
+}
+
+extern "C" moe_status moe_async_debug_latch_ops_error(void* stream) {
+#ifdef MOE_DEBUG_BOUNDS
+  using namespace moe;
+  const unsigned int e = MOE_ERR_TIMEOUT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cudaMemcpyToSymbolAsync(g_ops_error, &e, sizeof(e), 0, cudaMemcpyHostToDevice, s) == cudaSuccess &&
+                 cudaStreamSynchronize(s) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+#else
+  (void)stream;
+  return MOE_ERR_UNSUPPORTED;
+#endif
 }

@@ -122,7 +122,8 @@ def linear(x, weight, bias=None, act="none", mul=None, residual=None, offsets=No
 
 def ops_sync(device=None, stream=None):
     """Wait for `stream` (default: the device's current one) and raise MoEError if a stateless
-    operator found an error on the device (a wait in linear that exceeded its bound)."""
+    operator found an error on the device since the last report, on any stream (a wait in linear that
+    exceeded its bound).  Reported once: a call made after it starts clear."""
     with torch.cuda.device(device):
         s = torch.cuda.current_stream() if stream is None else stream
         N.check(N.load().moe_async_ops_status(s.cuda_stream), "ops_sync")

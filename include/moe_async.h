@@ -522,9 +522,9 @@ typedef struct {
 } moe_async_linear_args;
 moe_status moe_async_linear(const moe_async_linear_args* args, void* stream);
 
-/* Synchronise `stream` and return the sticky error of the stateless operators on the current
- * device: MOE_OK, or MOE_ERR_TIMEOUT once a device wait in moe_async_linear exceeded its 2 s
- * bound (that call's output is then undefined). */
+/* Synchronise `stream`, return the error of the stateless operators on the current device and clear
+ * it: MOE_OK, or MOE_ERR_TIMEOUT if a device wait in moe_async_linear exceeded its 2 s bound since
+ * the last report, on any stream (that call's output is then undefined). */
 moe_status moe_async_ops_status(void* stream);
 
 /* Bounds-checked build (libmoe_async_debug.so, compiled with MOE_DEBUG_BOUNDS): every bucket,
@@ -535,6 +535,10 @@ moe_status moe_async_ops_status(void* stream);
  * out of range.  Release builds return MOE_ERR_UNSUPPORTED and write nothing.  Asynchronous. */
 moe_status moe_async_debug_append_record(moe_async_t h, int32_t layer, int32_t bucket, int32_t record,
                                         void* stream);
+
+/* The bounds-checked build sets the error of moe_async_ops_status to MOE_ERR_TIMEOUT, so a test can see
+ * it reported without a wait that runs out.  Release builds return MOE_ERR_UNSUPPORTED. */
+moe_status moe_async_debug_latch_ops_error(void* stream);
 
 /* 1 if the kernels can write `n` bytes at host address `p` directly (pinned host memory
  * mapped into the device's address space at the same address), else 0.  A caller may then

@@ -312,3 +312,22 @@ def test_a_stream_of_another_device_is_refused(moe):
     y, _ = moe.add_rms_norm(x, stream=torch.cuda.ExternalStream(torch.cuda.Stream().cuda_stream))
     torch.cuda.synchronize()
     assert bool((y == 1).all())
+
+
+def test_a_reported_timeout_does_not_stay(moe):
+    """The bounds-checked build can latch the operators' error word: it is reported once, then clear."""
+    code = ("import torch, asynchronous_expert_execution_gb300 as moe\n"
+            "from asynchronous_expert_execution_gb300 import _native as N\n"
+            "x = torch.ones((4, 64), dtype=torch.bfloat16, device='cuda')\n"
+            "moe.add_rms_norm(x); moe.ops_sync()\n"
+            "for stream in (None, torch.cuda.Stream()):\n"
+            "    N.check(N.load().moe_async_debug_latch_ops_error(None), 'latch')\n"
+            "    torch.cuda.synchronize()\n"
+            "    try:\n"
+            "        moe.ops_sync(stream=stream)\n"
+            "        raise SystemExit('not reported')\n"
+            "    except moe.MoEError as e:\n"
+            "        assert e.status == N.MOE_ERR_TIMEOUT\n"
+            "    moe.ops_sync(); moe.ops_sync(stream=stream)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env={**os.environ, "MOE_DEBUG_BOUNDS": "1"}, capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr

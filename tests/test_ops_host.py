@@ -44,3 +44,11 @@ def test_widths_whose_columns_would_pass_32_bits_are_refused(nat, H):
         assert lib.moe_async_sort_rows(dt, P, H, P, 1, 1, H, P, H, 1, None) == N.MOE_ERR_INVALID
         assert lib.moe_async_merge_rows(dt, P, H, 1, P, P, 1, 1, H, None, 0, P, H, None) == N.MOE_ERR_INVALID
         assert lib.moe_async_merge_rows_backward(dt, P, H, P, H, 1, P, P, 1, 1, H, P, H, P, None) == N.MOE_ERR_INVALID
+
+
+def test_release_build_refuses_to_latch_an_error(nat):
+    """Only the bounds-checked build sets the operators' error word by hand."""
+    N, lib = nat
+    if N.DEBUG_BOUNDS:
+        pytest.skip("the bounds-checked build is loaded")
+    assert lib.moe_async_debug_latch_ops_error(None) == N.MOE_ERR_UNSUPPORTED
