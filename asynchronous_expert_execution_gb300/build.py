@@ -7,7 +7,7 @@ back from device state and latches MOE_ERR_BOUNDS instead of touching memory out
 of both under ``csrc/`` in parallel and links each set into one shared object next to this
 file.  ``_ops.so`` is the Python binding of the stateless operators (g++ against torch, no
 device code; it calls whichever library was loaded).  A rebuild is skipped when a library is
-newer than every source and header.
+newer than every source and header, and the binding was built for the torch and Python at hand.
 """
 import glob
 import os
@@ -25,6 +25,7 @@ LIB_DEBUG = os.path.join(HERE, "libmoe_async_debug.so")
 BINDING = os.path.join(HERE, "_ops.so")
 BINDING_SRC = os.path.join(CSRC, "moe_binding.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
+BINDING_TAG = os.path.join(BUILD_DIR, "binding.tag")
 VARIANTS = {"release": (LIB, []), "debug": (LIB_DEBUG, ["-DMOE_DEBUG_BOUNDS=1"])}
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -54,12 +55,26 @@ def _stale(lib):
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def binding_tag():
+    """What the binding is built against: it uses torch's C++ classes, whose layout changes between versions."""
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version_info.major}.{sys.version_info.minor}"
+
+
+def _binding_stale():
+    if _stale(BINDING) or not os.path.exists(BINDING_TAG):
+        return True
+    with open(BINDING_TAG) as f:
+        return f.read() != binding_tag()
+
+
 def _binding_cmd(out):
     import torch
     from torch.utils import cpp_extension
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     inc = [x for p in cpp_extension.include_paths("cuda") for x in ("-isystem", p)]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DMOE_BINDING_TAG="{binding_tag()}"',
             *inc, "-I", sysconfig.get_paths()["include"], BINDING_SRC, "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu",
             "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
@@ -68,11 +83,12 @@ def build(force=False, verbose=False, variants=("release", "debug")):
     """Compile and link the requested libraries (all translation units of all of them in
     parallel); returns the release library's path."""
     todo = [v for v in variants if force or _stale(VARIANTS[v][0])]
-    binding = force or _stale(BINDING)
+    binding = force or _binding_stale()
     if not todo and not binding:
         return LIB
     procs, objs = [], {}
     if binding:
+        os.makedirs(BUILD_DIR, exist_ok=True)
         cmd = _binding_cmd(BINDING + ".tmp")
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
@@ -102,6 +118,8 @@ def build(force=False, verbose=False, variants=("release", "debug")):
         raise RuntimeError(f"compilation failed:\n{msg}")
     if binding:
         os.replace(BINDING + ".tmp", BINDING)
+        with open(BINDING_TAG, "w") as f:
+            f.write(binding_tag())
     for v in todo:
         lib = VARIANTS[v][0]
         tmp = lib + ".tmp"

@@ -484,4 +484,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullp
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ops() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__ops() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", MOE_BINDING_TAG) < 0) Py_CLEAR(m);
+  return m;
+}

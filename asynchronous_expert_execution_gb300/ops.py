@@ -31,12 +31,16 @@ _bound = None
 def _bind():
     """The binding (built beside the library), bound to the library that _native loaded."""
     global _bound
+    from .build import binding_tag
     lib = N.load()
     try:
         from . import _ops
     except ImportError as e:
         raise RuntimeError("the operators' binding is missing or does not load: build it with "
                            "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    if _ops.built_for != binding_tag():
+        raise RuntimeError(f"the operators' binding was built for {_ops.built_for}, this is {binding_tag()}: build it again with "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`")
     _ops.bind(N.MoEError, *(ctypes.cast(getattr(lib, "moe_async_" + n), ctypes.c_void_p).value for n in _ORDER))
     _bound = _ops
     return _ops

@@ -52,3 +52,23 @@ def test_release_build_refuses_to_latch_an_error(nat):
     if N.DEBUG_BOUNDS:
         pytest.skip("the bounds-checked build is loaded")
     assert lib.moe_async_debug_latch_ops_error(None) == N.MOE_ERR_UNSUPPORTED
+
+
+def test_binding_of_another_torch_is_rebuilt_and_not_loaded(nat, monkeypatch):
+    """The binding uses torch's C++ classes: a binary of another version is stale whatever its file's time, and is refused."""
+    import torch
+    import asynchronous_expert_execution_gb300 as moe
+    from asynchronous_expert_execution_gb300 import build as b, ops
+    assert not b._binding_stale()
+    monkeypatch.setattr(ops, "_bound", None)
+    moe_error = None
+    try:
+        moe.add_rms_norm(torch.zeros((2, 8)))                                # binds, then refuses a CPU tensor
+    except moe.MoEError as e:
+        moe_error = e
+    assert moe_error is not None
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    assert b._binding_stale()
+    monkeypatch.setattr(ops, "_bound", None)
+    with pytest.raises(RuntimeError, match="built for"):
+        moe.add_rms_norm(torch.zeros((2, 8)))
