@@ -169,6 +169,22 @@ def test_activations_of_infinity_and_nan(moe):
             assert float(y["relu"][0]) == inf and float(y["relu"][1]) == 0 and bool(y["relu"][2].isnan()) and not bool(y["relu"][[4, 5]].any())
 
 
+@pytest.mark.parametrize("T,F,Nn", [(1, 7168, 64), (16, 7168, 500), (40, 28672, 130), (300, 28672, 256), (900, 28672, 256), (700, 14336, 2050),
+                                    (300, 7168, 2056)])
+def test_fp32_sums_do_not_drift(moe, T, F, Nn):
+    """Operands in [1, 2) with 6 bits behind the point: every sum of up to 1024 products is below 2^12 and a multiple of 2^-12, so
+    the tensor cores hold the sums of 12 k-blocks (768 products) exactly, however they cut; what is left is fp32 rounding, u of the
+    result for each addition on the longest way to it: the chunks, the partial sums of up to eight CTAs, or (up to 16 rows) four
+    rounds of loads and 16 warps.  One sum over all of F would cut multiples of 2^-12 to the step of the running sum, always the
+    same way (over two SMs it was off by 38 u at 7168 deep, 490 u at 14336)."""
+    g = gen(F)
+    six = lambda s: (1 + torch.randint(0, 64, s, generator=g, device="cuda") / 64).to(torch.bfloat16)   # noqa: E731
+    x, w = six((T, F)), six((Nn, F))
+    y = moe.linear(x, w, out_dtype=torch.float32)
+    additions = math.ceil(F / 64 / 12) + 8 if T > 16 else 4 + 16
+    close(y, x.double() @ w.double().T, additions * U * (x.double() @ w.double().T), "sums of one sign")
+
+
 # ------------------------------------------------------------------ tensors, streams and threads
 
 def test_sort_experts_outputs_own_their_memory(moe):
