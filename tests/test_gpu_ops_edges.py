@@ -185,6 +185,35 @@ def test_fp32_sums_do_not_drift(moe, T, F, Nn):
     close(y, x.double() @ w.double().T, additions * U * (x.double() @ w.double().T), "sums of one sign")
 
 
+@pytest.mark.parametrize("T,F,Nn,groups", [(1, 7168, 300, 0), (16, 7168, 520, 0), (33, 7168, 300, 0), (300, 7168, 520, 0), (1030, 7168, 777, 0),
+                                           (16, 4112, 130, 6), (200, 4112, 130, 6), (900, 7168, 264, 5), (3000, 592, 1040, 12)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("epilogue", [False, True])
+def test_linear_of_integers_with_epilogue_and_groups_is_exact(moe, T, F, Nn, groups, dt, epilogue):
+    """Integers whose sums stay below 2^24 leave no room for rounding: long sums, per expert, with bias, mul and residual."""
+    g = gen(T + F)
+    shape = (groups, Nn) if groups else (Nn,)
+    ints = lambda s, n: torch.randint(-n, n + 1, s, generator=g, device="cuda").float()   # noqa: E731
+    x, w = ints((T, F), 8).to(dt), ints((*shape, F), 8).to(dt)
+    kw = {} if dt == torch.bfloat16 else {"x_scale": torch.full((T,), 2.0, device="cuda"), "w_scale": torch.full(shape, 0.5, device="cuda")}
+    at = [0, T]
+    if groups:
+        cut = torch.sort(torch.randint(0, T + 1, (groups - 1,), generator=g, device="cuda")).values.tolist()
+        at = [0, *cut, T]
+        kw["offsets"] = torch.tensor(at, dtype=torch.int32, device="cuda")
+    if epilogue:
+        kw.update(bias=ints(shape, 50), mul=ints((T, Nn), 3), residual=ints((T, Nn), 100))
+    y = moe.linear(x, w, out_dtype=torch.float32, **kw)
+    ref = torch.zeros((T, Nn), dtype=torch.float64, device="cuda")
+    for e in range(max(groups, 1)):
+        i, j = at[e], at[e + 1]
+        v = x[i:j].double() @ (w[e] if groups else w).double().T
+        if epilogue:
+            v = (v + (kw["bias"][e] if groups else kw["bias"]).double()) * kw["mul"][i:j].double() + kw["residual"][i:j].double()
+        ref[i:j] = v
+    assert float(ref.abs().max()) < 2 ** 24 and torch.equal(y.double(), ref)
+
+
 # ------------------------------------------------------------------ tensors, streams and threads
 
 def test_sort_experts_outputs_own_their_memory(moe):
