@@ -128,6 +128,6 @@ def ops_sync(device=None, stream=None):
     """Wait for `stream` (default: the device's current one) and raise MoEError if a stateless
     operator found an error on the device since the last report, on any stream (a wait in linear that
     exceeded its bound).  Reported once: a call made after it starts clear."""
-    with torch.cuda.device(device):
+    with torch.cuda.device(getattr(stream, "device", None) if device is None else device):
         s = torch.cuda.current_stream() if stream is None else stream
         N.check(N.load().moe_async_ops_status(s.cuda_stream), "ops_sync")

@@ -72,3 +72,18 @@ def test_binding_of_another_torch_is_rebuilt_and_not_loaded(nat, monkeypatch):
     monkeypatch.setattr(ops, "_bound", None)
     with pytest.raises(RuntimeError, match="built for"):
         moe.add_rms_norm(torch.zeros((2, 8)))
+
+
+def test_ops_sync_looks_at_the_device_of_its_stream(monkeypatch):
+    """The error word is the device's: with a stream and no device, that is the stream's."""
+    import contextlib
+    import types
+    import torch
+    from asynchronous_expert_execution_gb300 import ops
+    seen = []
+    monkeypatch.setattr(ops.torch.cuda, "device", lambda d: seen.append(d) or contextlib.nullcontext())
+    monkeypatch.setattr(ops.N, "load", lambda: types.SimpleNamespace(moe_async_ops_status=lambda s: seen.append(s) or 0))
+    stream = types.SimpleNamespace(cuda_stream=7, device=torch.device("cuda", 1))
+    ops.ops_sync(stream=stream)
+    ops.ops_sync(0, stream)
+    assert seen == [torch.device("cuda", 1), 7, 0, 7]
