@@ -449,7 +449,8 @@ moe_status norm_dispatch(const void* x, int64_t ldx, const void* res, int64_t ld
 }
 
 // Blocks of the backward pass, the rows of `partial`: one an SM for rows of 8192 columns, more where
-// they are short.
+// they are short.  152 is written out: the workspace's size is asked without a device, and the order of
+// the gain's sums depends on sizes only.
 int norm_bwd_blocks(int T_, int H) { return std::min(T_, 152 * std::max(1, std::min(8, 9216 / H))); }
 
 template <typename T, int V>

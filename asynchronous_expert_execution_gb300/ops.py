@@ -57,7 +57,8 @@ def sort_experts(expert, num_experts, stream=None):
 
 def sort_rows(x, pos, out=None, stream=None):
     """rows[pos[t, k]] = x[t]: x [T, H] fp32 or bf16, pos int32 [T, K] -> rows [T * K, H] (or
-    `out` [R, H]); rows that no pair names are left as they were."""
+    `out` [R, H]); rows that no pair names are left as they were (in a new matrix: not set).  Each row
+    is named by at most one pair, as sort_experts names them."""
     return (_bound or _bind()).sort_rows(x, pos, out, stream)
 
 
@@ -75,8 +76,9 @@ def sort_rows_backward(grad_rows, pos, out=None, stream=None):
 
 def merge_rows_backward(grad, rows, pos, w, out=None, stream=None):
     """Gradients of merge_rows: (grad_rows, grad_w) with grad_rows[pos[t, k]] = w[t, k] grad[t]
-    ([R, H] or `out`; rows that no pair names are left as they were) and grad_w[t, k] =
-    <rows[pos[t, k]], grad[t]> (fp32, 0 for a pair without a row).  The residual's is `grad`."""
+    ([R, H] or `out`; rows that no pair names are left as they were, in a new matrix not set) and
+    grad_w[t, k] = <rows[pos[t, k]], grad[t]> (fp32, 0 for a pair without a row).  The residual's is
+    `grad`.  Each row is named by at most one pair."""
     return (_bound or _bind()).merge_rows_backward(grad, rows, pos, w, out, stream)
 
 
@@ -114,10 +116,10 @@ def linear(x, weight, bias=None, act="none", mul=None, residual=None, offsets=No
     x [T, F] and weight [N, F], both bf16, or both e4m3 with x_scale fp32 [T] and w_scale fp32
     [N]; F a multiple of 16 bytes, rows of x and weight on 16-byte boundaries.  bias fp32 [N]; mul
     and residual [T, N] in the type of the result (out's, out_dtype or bf16; fp32 or bf16); act
-    "none", "silu", "gelu" (erf) or "relu".  `out` may be mul or residual.
+    "none", "silu", "gelu" (the exact one) or "relu".  `out` may be mul or residual.
     With offsets (int32 [G + 1], as sort_experts gives them) weight is [G, N, F], bias and w_scale
     are [G, N], and rows offsets[g]:offsets[g + 1] of x meet weight[g]; other rows of `out` are
-    left as they were."""
+    left as they were (in a new matrix: not set)."""
     code = N.ACTS.get(act)
     if code is None:
         raise N.MoEError(N.MOE_ERR_INVALID, f"act: expected one of {tuple(N.ACTS)}, got {act!r}")

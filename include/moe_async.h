@@ -447,7 +447,7 @@ moe_status moe_async_merge_rows(int32_t dtype, const void* d_rows, int64_t rows_
 
 /* Gradients of moe_async_merge_rows: grad_rows[pos[t, k]] = w[t, k] grad[t] (other rows are left
  * as they were) and grad_w[t, k] = <rows[pos[t, k]], grad[t]> (0 for a pair without a row); the
- * residual's gradient is `grad` itself. */
+ * residual's gradient is `grad` itself.  Each row is named by at most one pair. */
 moe_status moe_async_merge_rows_backward(int32_t dtype, const void* d_grad, int64_t grad_stride, const void* d_rows,
                                          int64_t rows_stride, int64_t n_rows, const int32_t* d_pos, const float* d_w,
                                          int32_t T, int32_t K, int32_t H, void* d_grad_rows, int64_t grad_rows_stride,
