@@ -1,6 +1,6 @@
 // Python binding of the stateless operators: argument checks, outputs and the call, in C++ because
 // a small call is bound by its host side (a decode step's norm runs 3 us on the GPU; checked and
-// marshalled in Python it took 10.6 us, here 4.4).  Nothing is computed here: every function ends
+// marshalled in Python it took 10.6 us, here 4).  Nothing is computed here: every function ends
 // in one moe_async_* call of the library that _native.py loaded (bind() gets their addresses).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
