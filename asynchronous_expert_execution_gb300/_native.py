@@ -26,7 +26,8 @@ EXPORTS = ("moe_async_create", "moe_async_route", "moe_async_enqueue", "moe_asyn
            "moe_async_cancel", "moe_async_debug_append_record",
            "moe_async_sort_experts", "moe_async_sort_rows", "moe_async_merge_rows", "moe_async_merge_rows_backward",
            "moe_async_route_backward", "moe_async_add_rms_norm", "moe_async_add_rms_norm_backward",
-           "moe_async_add_rms_norm_backward_workspace", "moe_async_linear", "moe_async_ops_status",
+           "moe_async_add_rms_norm_backward_workspace", "moe_async_linear", "moe_async_linear_backward",
+           "moe_async_linear_backward_workspace", "moe_async_act_mul_backward", "moe_async_ops_status",
            "moe_async_debug_latch_ops_error")
 
 KERNEL_KINDS = ("enqueue", "schedule", "ffn1", "ffn2", "collect", "tick")
@@ -74,6 +75,14 @@ class LinearArgs(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("d_x", "d_w", "d_bias", "d_x_scale", "d_w_scale", "d_mul", "d_residual",
                                                "d_offsets", "d_y")] + \
                [(n, ctypes.c_int64) for n in ("x_stride", "w_stride", "mul_stride", "residual_stride", "y_stride")]
+
+
+class LinearBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("x_dtype", "w_dtype", "rows", "fan_in", "fan_out", "groups", "accumulate", "reserved")] + \
+               [(n, ctypes.c_void_p) for n in ("d_grad", "d_x", "d_w", "d_residual", "d_offsets", "d_grad_x", "d_grad_w", "d_grad_bias",
+                                               "d_workspace")] + \
+               [(n, ctypes.c_int64) for n in ("grad_stride", "x_stride", "w_stride", "residual_stride", "grad_x_stride", "grad_w_stride",
+                                              "workspace_bytes")]
 
 
 class MoEError(RuntimeError):
@@ -131,10 +140,14 @@ def load():
         "moe_async_add_rms_norm_backward": [I32, P, I64, P, I64, F32P, F32, I32, I32, P, I64, P, I64, F32P, P, I64, P],
         "moe_async_add_rms_norm_backward_workspace": [I32, I32],
         "moe_async_linear": [ctypes.POINTER(LinearArgs), P],
+        "moe_async_linear_backward": [ctypes.POINTER(LinearBackwardArgs), P],
+        "moe_async_linear_backward_workspace": [ctypes.POINTER(LinearBackwardArgs)],
+        "moe_async_act_mul_backward": [I32, I32, P, I64, P, I64, P, I64, I32, I32, P, I64, P, I64, P],
         "moe_async_ops_status": [P],
         "moe_async_debug_latch_ops_error": [P],
     }
-    restype = {"moe_async_status_string": ctypes.c_char_p, "moe_async_add_rms_norm_backward_workspace": I64}
+    restype = {"moe_async_status_string": ctypes.c_char_p, "moe_async_add_rms_norm_backward_workspace": I64,
+               "moe_async_linear_backward_workspace": I64}
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args

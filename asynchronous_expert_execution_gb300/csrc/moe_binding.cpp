@@ -34,6 +34,9 @@ struct Library {
   decltype(&moe_async_add_rms_norm_backward_workspace) norm_workspace;
   decltype(&moe_async_add_rms_norm_backward) add_rms_norm_backward;
   decltype(&moe_async_linear) linear;
+  decltype(&moe_async_linear_backward_workspace) linear_backward_workspace;
+  decltype(&moe_async_linear_backward) linear_backward;
+  decltype(&moe_async_act_mul_backward) act_mul_backward;
 } lib = {};
 PyObject* error_class = nullptr;
 
@@ -429,6 +432,128 @@ PyObject* linear(PyObject* const* a) {
   return given ? same(a[10]) : wrap(out);
 }
 
+// float32 or bfloat16 as asked for, as the output that was handed in has, or bfloat16
+ScalarType result_dtype(PyObject* asked, const Tensor* given, const char* name) {
+  ScalarType d = at::kBFloat16;
+  if (asked != Py_None) {
+    if (!THPDtype_Check(asked)) bad(std::string(name) + ": expected a dtype");
+    d = reinterpret_cast<THPDtype*>(asked)->scalar_type;
+  } else if (given) {
+    d = given->scalar_type();
+  }
+  if (d != at::kFloat && d != at::kBFloat16) bad(std::string(name) + ": expected float32 or bfloat16");
+  return d;
+}
+
+// grad, x, weight, offsets, bias, residual, out dtype, weight dtype, out_x, out_weight, out_bias, accumulate, stream
+// -> (grad_x, grad_weight, grad_bias), None for what was not asked for
+PyObject* linear_backward(PyObject* const* a) {
+  const Tensor& grad = tensor(a[0], "grad");
+  const Tensor *x = maybe(a[1], "x"), *weight = maybe(a[2], "weight"), *offsets = maybe(a[3], "offsets"), *res = maybe(a[5], "residual"),
+               *given_x = maybe(a[8], "out_x"), *given_w = maybe(a[9], "out_weight"), *given_b = maybe(a[10], "out_bias");
+  const int bias = PyObject_IsTrue(a[4]), add = PyObject_IsTrue(a[11]);
+  if (bias < 0 || add < 0) throw PythonError{};
+  const Lead l = lead(grad, "grad", {at::kBFloat16});
+  const On on(l.dev, a[12]);
+  const int64_t T = l.n, N = l.width;
+  if (!x && !weight && !bias) bad("x, weight, bias: nothing to compute");
+  if ((!weight && (given_x || res)) || (!x && given_w) || (!bias && given_b))
+    bad("out_x and residual need weight, out_weight needs x, out_bias needs bias=True");
+  if (add && ((x && !given_w) || (bias && !given_b))) bad("accumulate: needs out_weight and out_bias, as far as they are computed");
+  moe_async_linear_backward_args p = {};
+  int64_t G = 0, F = 8;
+  if (offsets) {
+    if (offsets->dim() != 1 || offsets->size(0) < 2) bad("offsets: expected [G + 1]", *offsets);
+    G = offsets->size(0) - 1;
+    whole(*offsets, "offsets", l.dev, at::kInt, {G + 1});
+  }
+  if (x) {
+    if (x->dim() != 2) bad("x: expected [T, fan_in]", *x);
+    F = x->size(1);
+    p.x_stride = rows(*x, "x", l.dev, at::kBFloat16, T, F);
+  } else if (weight) {
+    F = weight->dim() > 0 ? weight->size(-1) : 0;
+  }
+  p.x_dtype = p.w_dtype = MOE_BF16;
+  Tensor out_x, out_w, out_b;
+  if (weight) {
+    if (offsets) {
+      whole(*weight, "weight", l.dev, at::kBFloat16, {G, N, F});
+      p.w_stride = F;
+    } else {
+      p.w_stride = rows(*weight, "weight", l.dev, at::kBFloat16, N, F);
+    }
+    const ScalarType d = result_dtype(a[6], given_x, "out_dtype");
+    p.x_dtype = code(d);
+    p.residual_stride = res ? rows(*res, "residual", l.dev, d, T, F) : F;
+    out_x = output(a[8], "out_x", l.dev, d, T, F, p.grad_x_stride);
+  }
+  if (x) {
+    const ScalarType d = result_dtype(a[7], given_w, "weight_dtype");
+    p.w_dtype = code(d);
+    if (!offsets) {
+      out_w = output(a[9], "out_weight", l.dev, d, N, F, p.grad_w_stride);
+    } else {
+      if (given_w) whole(*given_w, "out_weight", l.dev, d, {G, N, F});
+      out_w = given_w ? *given_w : empty({G, N, F}, d, l.dev);
+      p.grad_w_stride = F;
+    }
+  }
+  if (bias) {
+    const int64_t per[2] = {offsets ? G : N, N};
+    const at::IntArrayRef vec(per, offsets ? 2 : 1);
+    if (given_b) whole(*given_b, "out_bias", l.dev, at::kFloat, vec);
+    out_b = given_b ? *given_b : empty(vec, at::kFloat, l.dev);
+  }
+  p.rows = count(T, "rows");
+  p.fan_in = count(F, "fan_in");
+  p.fan_out = count(N, "fan_out");
+  p.groups = count(G, "groups");
+  p.accumulate = add;
+  p.grad_stride = l.ld;
+  p.d_grad = ptr(grad);
+  p.d_x = ptr(x);
+  p.d_w = ptr(weight);
+  p.d_residual = ptr(res);
+  p.d_offsets = ptr<int32_t>(offsets);
+  p.d_grad_x = weight ? ptr(out_x) : nullptr;
+  p.d_grad_w = x ? ptr(out_w) : nullptr;
+  p.d_grad_bias = bias ? ptr<float>(out_b) : nullptr;
+  Tensor ws;
+  p.workspace_bytes = lib.linear_backward_workspace(&p);
+  if (p.workspace_bytes > 0) {
+    ws = empty({p.workspace_bytes}, at::kByte, l.dev);
+    p.d_workspace = ptr(ws);
+  }
+  call("linear_backward", on, [&](void* s) { return lib.linear_backward(&p, s); });
+  for (int i = 8; i < 11; ++i) written(a[i]);
+  const auto result = [&](PyObject* given, const Tensor& t, bool some) { return !some ? same(Py_None) : given != Py_None ? same(given) : wrap(t); };
+  return tuple({result(a[8], out_x, weight != nullptr), result(a[9], out_w, x != nullptr), result(a[10], out_b, bias != 0)});
+}
+
+// grad, z, mul, act code, out_z, out_mul, stream -> (grad_z, grad_mul or None)
+PyObject* act_mul_backward(PyObject* const* a) {
+  const Tensor &grad = tensor(a[0], "grad"), &z = tensor(a[1], "z");
+  const Tensor* mul = maybe(a[2], "mul");
+  const Lead l = lead(z, "z", {at::kFloat, at::kBFloat16});
+  const On on(l.dev, a[6]);
+  const int64_t T = l.n, H = l.width;
+  const int32_t act = static_cast<int32_t>(integer(a[3], "act"));
+  const int64_t ldg = rows(grad, "grad", l.dev, l.dtype, T, H), ldm = mul ? rows(*mul, "mul", l.dev, l.dtype, T, H) : H;
+  if (!mul && a[5] != Py_None) bad("out_mul: there is no gradient of mul without mul");
+  int64_t ldz, ldgm = H;
+  const Tensor out_z = output(a[4], "out_z", l.dev, l.dtype, T, H, ldz);
+  Tensor out_mul;
+  if (mul) out_mul = output(a[5], "out_mul", l.dev, l.dtype, T, H, ldgm);
+  call("act_mul_backward", on, [&](void* s) {
+    return lib.act_mul_backward(code(l.dtype), act, ptr(grad), ldg, ptr(z), l.ld, ptr(mul), ldm, count(T, "rows"), count(H, "width"), ptr(out_z), ldz,
+                                mul ? ptr(out_mul) : nullptr, ldgm, s);
+  });
+  written(a[4]);
+  written(a[5]);
+  return tuple({a[4] != Py_None ? same(a[4]) : wrap(out_z), !mul ? same(Py_None) : a[5] != Py_None ? same(a[5]) : wrap(out_mul)});
+}
+
 // ------------------------------------------------------------------ module
 
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -479,6 +604,8 @@ PyMethodDef methods[] = {{"bind", reinterpret_cast<PyCFunction>(reinterpret_cast
                          OP(add_rms_norm, 8),
                          OP(add_rms_norm_backward, 7),
                          OP(linear, 12),
+                         OP(linear_backward, 13),
+                         OP(act_mul_backward, 7),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

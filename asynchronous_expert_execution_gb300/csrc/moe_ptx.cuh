@@ -52,6 +52,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -82,6 +87,12 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 
@@ -163,13 +174,15 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
   if constexpr (CG == 2 && E4M3) MOE_MMA("2", "f8f6f4");
 #undef MOE_MMA
 }
-// One k-block (128 bytes of each row): four MMAs.
-template <int CG, bool E4M3>
+// One k-block: four MMAs over 32 bytes of K each (128 bytes of each row of a K-major operand, 64 rows of one that lies
+// across, AT or BT: 16 rows of 128 bytes on).
+template <int CG, bool E4M3, bool AT = false, bool BT = false>
 __device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  constexpr int kA = AT ? 128 : 2, kB = BT ? 128 : 2;
   mma<CG, E4M3>(d, a, b, idesc, accumulate);
-  mma<CG, E4M3>(d, a + 2, b + 2, idesc, 1);        // 32 bytes on
-  mma<CG, E4M3>(d, a + 4, b + 4, idesc, 1);
-  mma<CG, E4M3>(d, a + 6, b + 6, idesc, 1);
+  mma<CG, E4M3>(d, a + kA, b + kB, idesc, 1);
+  mma<CG, E4M3>(d, a + 2 * kA, b + 2 * kB, idesc, 1);
+  mma<CG, E4M3>(d, a + 3 * kA, b + 3 * kB, idesc, 1);
 }
 // All MMAs issued so far by this thread arrive on `bar` when they are done; CG = 2: on the
 // barrier at the same place in both CTAs of the pair.
@@ -221,11 +234,18 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 |
          (uint64_t)2 << 61;
 }
+// Shared-memory operand that lies across K (16-bit types): rows of K, 64 elements of M or N (128 bytes) each under the
+// 128-byte swizzle, groups of 8 rows 1024 bytes apart; the next 64 elements of M or N `next` bytes on.
+__device__ __forceinline__ uint64_t across_desc(uint32_t saddr, uint32_t next) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
 // Instruction descriptor: D fp32, A and B both bf16 (kind::f16, format 1) or both e4m3
-// (kind::f8f6f4, format 0), K-major.
-template <bool E4M3>
+// (kind::f8f6f4, format 0), K-major, or across K (AT, BT).
+template <bool E4M3, bool AT = false, bool BT = false>
 __device__ __forceinline__ uint32_t mma_desc(int M, int N) {
-  return (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+  return (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (AT ? 1u << 15 : 0u) | (BT ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
 }
 
 }  // namespace ptx

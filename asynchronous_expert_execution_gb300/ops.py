@@ -24,7 +24,8 @@ import torch
 from . import _native as N
 
 _ORDER = ("sort_experts", "sort_rows", "merge_rows", "merge_rows_backward", "route_backward", "add_rms_norm",
-          "add_rms_norm_backward_workspace", "add_rms_norm_backward", "linear")
+          "add_rms_norm_backward_workspace", "add_rms_norm_backward", "linear", "linear_backward_workspace", "linear_backward",
+          "act_mul_backward")
 _bound = None
 
 
@@ -109,6 +110,13 @@ def add_rms_norm_backward(grad, h, gain=None, eps=1e-6, grad_h=None, out=None, s
     return (_bound or _bind()).add_rms_norm_backward(grad, h, gain, eps, grad_h, out, stream)
 
 
+def _act(act):
+    code = N.ACTS.get(act)
+    if code is None:
+        raise N.MoEError(N.MOE_ERR_INVALID, f"act: expected one of {tuple(N.ACTS)}, got {act!r}")
+    return code
+
+
 def linear(x, weight, bias=None, act="none", mul=None, residual=None, offsets=None, x_scale=None, w_scale=None,
            out_dtype=None, out=None, stream=None):
     """act(x @ weight.T + bias) * mul + residual, products summed in fp32, rounded once.
@@ -120,15 +128,34 @@ def linear(x, weight, bias=None, act="none", mul=None, residual=None, offsets=No
     With offsets (int32 [G + 1], as sort_experts gives them) weight is [G, N, F], bias and w_scale
     are [G, N], and rows offsets[g]:offsets[g + 1] of x meet weight[g]; other rows of `out` are
     left as they were (in a new matrix: not set)."""
-    code = N.ACTS.get(act)
-    if code is None:
-        raise N.MoEError(N.MOE_ERR_INVALID, f"act: expected one of {tuple(N.ACTS)}, got {act!r}")
-    return (_bound or _bind()).linear(x, weight, bias, code, mul, residual, offsets, x_scale, w_scale, out_dtype, out, stream)
+    return (_bound or _bind()).linear(x, weight, bias, _act(act), mul, residual, offsets, x_scale, w_scale, out_dtype, out, stream)
+
+
+def linear_backward(grad, x=None, weight=None, offsets=None, bias=False, residual=None, out_dtype=None, weight_dtype=None, out_x=None,
+                    out_weight=None, out_bias=None, accumulate=False, stream=None):
+    """Gradients of x @ weight.T + bias from `grad`: (grad_x, grad_weight, grad_bias), each None if not asked for.
+
+    grad [T, N], x [T, F] and weight [N, F] in bf16 (F a multiple of 8, rows of x and weight on 16-byte boundaries):
+    grad_x = grad @ weight + residual [T, F], if weight is given; grad_weight = grad.T @ x [N, F], if x is given; grad_bias fp32
+    [N], if `bias`.  Sums in fp32, rounded once to out_x's type (or out_dtype, or bf16; the residual's too) and to out_weight's
+    (or weight_dtype, or bf16).  accumulate=True adds grad_weight and grad_bias to what out_weight and out_bias hold.
+    `out_x` may be `residual`.  With offsets (int32 [G + 1]) as in linear: weight and grad_weight [G, N, F], grad_bias [G, N];
+    rows of no group are not read, and in out_x left as they were (in a new matrix: not set).
+    An epilogue's gradient comes first: act_mul_backward."""
+    return (_bound or _bind()).linear_backward(grad, x, weight, offsets, bias, residual, out_dtype, weight_dtype, out_x, out_weight, out_bias,
+                                               accumulate, stream)
+
+
+def act_mul_backward(grad, z, mul=None, act="silu", out_z=None, out_mul=None, stream=None):
+    """Gradients of act(z) * mul (or act(z)): (grad_z, grad_mul) = (grad * mul * act'(z), grad * act(z)), the second None
+    without mul.  grad, z, mul [T, H] fp32 or bf16; act as in linear; relu's slope at 0 is 0.  `out_z` and `out_mul` may be
+    any of the three."""
+    return (_bound or _bind()).act_mul_backward(grad, z, mul, _act(act), out_z, out_mul, stream)
 
 
 def ops_sync(device=None, stream=None):
     """Wait for `stream` (default: the device's current one) and raise MoEError if a stateless
-    operator found an error on the device since the last report, on any stream (a wait in linear that
+    operator found an error on the device since the last report, on any stream (a wait in a product that
     exceeded its bound).  Reported once: a call made after it starts clear."""
     with torch.cuda.device(getattr(stream, "device", None) if device is None else device):
         s = torch.cuda.current_stream() if stream is None else stream

@@ -522,8 +522,50 @@ typedef struct {
 } moe_async_linear_args;
 moe_status moe_async_linear(const moe_async_linear_args* args, void* stream);
 
+/* Gradients of moe_async_linear without its epilogue, y[t, n] = sum_k x[t, k] w[n, k] + bias[n], from
+ * grad = dL/dy:
+ *   grad_x[t, k]    = sum_n grad[t, n] w[n, k] + residual[t, k]
+ *   grad_w[n, k]    = sum_t grad[t, n] x[t, k]
+ *   grad_bias[n]    = sum_t grad[t, n]
+ * (an epilogue's gradient comes first: moe_async_act_mul_backward).  Operands are bf16, sums fp32, results rounded
+ * once.  Each of the three is computed if its pointer is given; accumulate != 0 adds grad_w and grad_bias to what
+ * they hold.
+ *   d_grad : [rows, fan_out]     d_x : [rows, fan_in], for grad_w     d_w : [fan_out, fan_in], for grad_x
+ *   d_grad_x : [rows, fan_in] in x_dtype, d_residual in the same or NULL; it may be grad_x itself
+ *   d_grad_w : [fan_out, fan_in] in w_dtype           d_grad_bias : [fan_out] fp32
+ *   groups = G > 0: as in moe_async_linear; d_w and d_grad_w are [G, fan_out, fan_in] (matrices of fan_out * stride elements
+ *   one behind another), d_grad_bias [G, fan_out]; rows of no group are not read and their grad_x is left as it was; a group
+ *   without rows has a gradient of zeros.
+ * fan_in is a multiple of 8, the bases and strides of x and w of 16 bytes, else MOE_ERR_UNSUPPORTED; fan_out and the other strides
+ * are free, but rows of grad that do not start on 16-byte boundaries are copied first, into a workspace (16-byte aligned) of
+ * moe_async_linear_backward_workspace(args) bytes (0 if they do), the caller's until the call has run; calls that may run at
+ * once need one each.  Smaller: MOE_ERR_CAPACITY.  0 rows: grad_w and grad_bias are set to zeros, or left.  Asynchronous. */
+typedef struct {
+  int32_t x_dtype, w_dtype, rows, fan_in, fan_out, groups, accumulate, reserved;
+  const void* d_grad;
+  const void* d_x;
+  const void* d_w;
+  const void* d_residual;
+  const int32_t* d_offsets;
+  void* d_grad_x;
+  void* d_grad_w;
+  float* d_grad_bias;
+  void* d_workspace;
+  int64_t grad_stride, x_stride, w_stride, residual_stride, grad_x_stride, grad_w_stride, workspace_bytes;
+} moe_async_linear_backward_args;
+int64_t moe_async_linear_backward_workspace(const moe_async_linear_backward_args* args);
+moe_status moe_async_linear_backward(const moe_async_linear_backward_args* args, void* stream);
+
+/* Gradients of y = act(z) * mul (of y = act(z): d_mul and d_grad_mul NULL) from grad = dL/dy:
+ *   grad_z = grad * mul * act'(z), grad_mul = grad * act(z), each [T, H] in dtype (MOE_F32 or MOE_BF16), rounded once
+ * relu's slope is 0 at 0.  An output may be any of the inputs, in the same layout.  fp32 slopes of silu and gelu are within
+ * 16 and 24 * 2^-24 of the sum of their terms' absolute values; for bf16 results both within 2^-14.  Asynchronous. */
+moe_status moe_async_act_mul_backward(int32_t dtype, int32_t act, const void* d_grad, int64_t grad_stride, const void* d_z, int64_t z_stride,
+                                      const void* d_mul, int64_t mul_stride, int32_t T, int32_t H, void* d_grad_z, int64_t grad_z_stride,
+                                      void* d_grad_mul, int64_t grad_mul_stride, void* stream);
+
 /* Synchronise `stream`, return the error of the stateless operators on the current device and clear
- * it: MOE_OK, or MOE_ERR_TIMEOUT if a device wait in moe_async_linear exceeded its 2 s bound since
+ * it: MOE_OK, or MOE_ERR_TIMEOUT if a device wait in a product exceeded its 2 s bound since
  * the last report, on any stream (that call's output is then undefined). */
 moe_status moe_async_ops_status(void* stream);
 
