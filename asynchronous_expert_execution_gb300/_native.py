@@ -27,7 +27,8 @@ EXPORTS = ("moe_async_create", "moe_async_route", "moe_async_enqueue", "moe_asyn
            "moe_async_sort_experts", "moe_async_sort_rows", "moe_async_merge_rows", "moe_async_merge_rows_backward",
            "moe_async_route_backward", "moe_async_add_rms_norm", "moe_async_add_rms_norm_backward",
            "moe_async_add_rms_norm_backward_workspace", "moe_async_linear", "moe_async_linear_backward",
-           "moe_async_linear_backward_workspace", "moe_async_act_mul_backward", "moe_async_ops_status",
+           "moe_async_linear_backward_workspace", "moe_async_act_mul_backward", "moe_async_linear_blocks",
+           "moe_async_quantize_blocks", "moe_async_ops_status",
            "moe_async_debug_latch_ops_error")
 
 KERNEL_KINDS = ("enqueue", "schedule", "ffn1", "ffn2", "collect", "tick")
@@ -143,6 +144,8 @@ def load():
         "moe_async_linear_backward": [ctypes.POINTER(LinearBackwardArgs), P],
         "moe_async_linear_backward_workspace": [ctypes.POINTER(LinearBackwardArgs)],
         "moe_async_act_mul_backward": [I32, I32, P, I64, P, I64, P, I64, I32, I32, P, I64, P, I64, P],
+        "moe_async_linear_blocks": [ctypes.POINTER(LinearArgs), I64, I64, P],
+        "moe_async_quantize_blocks": [I32, P, I64, I32, I32, I32, I32, P, I64, F32P, I64, I64, P],
         "moe_async_ops_status": [P],
         "moe_async_debug_latch_ops_error": [P],
     }

@@ -33,7 +33,7 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompil
               "--expt-relaxed-constexpr", "-I", INCLUDE]
 # The tcgen05 kernels must not spill: one holds an SM's whole register file, and a build of a
 # variant that spilled faulted on the GPU.  ptxas turns a spill into a build error.
-FILE_FLAGS = {f: ["-Xptxas", "--warn-on-spills,--warning-as-error"] for f in ("moe_ffn_tc.cu", "moe_linear.cu", "moe_linear_backward.cu")}
+FILE_FLAGS = {f: ["-Xptxas", "--warn-on-spills,--warning-as-error"] for f in ("moe_ffn_tc.cu", "moe_linear.cu", "moe_linear_backward.cu", "moe_linear_blocks.cu")}
 
 
 def _nvcc():

@@ -37,6 +37,8 @@ struct Library {
   decltype(&moe_async_linear_backward_workspace) linear_backward_workspace;
   decltype(&moe_async_linear_backward) linear_backward;
   decltype(&moe_async_act_mul_backward) act_mul_backward;
+  decltype(&moe_async_linear_blocks) linear_blocks;
+  decltype(&moe_async_quantize_blocks) quantize_blocks;
 } lib = {};
 PyObject* error_class = nullptr;
 
@@ -403,7 +405,14 @@ PyObject* linear(PyObject* const* a) {
   }
   if (od != at::kFloat && od != at::kBFloat16) bad("out_dtype: expected float32 or bfloat16");
   if ((sx != nullptr) != e4m3 || (sw != nullptr) != e4m3) bad("x_scale, w_scale: both with e4m3 operands, none with bf16");
-  if (e4m3) {
+  const int64_t KB = (F + 127) / 128;
+  const bool blocks = e4m3 && sx->dim() == 2;        // a scale per 128 columns of a token and per 128 x 128 of a weight
+  if (blocks) {
+    if (sx->scalar_type() != at::kFloat || !sx->is_cuda() || sx->get_device() != l.dev || sx->size(0) != T || sx->size(1) != KB)
+      bad("x_scale: expected " + shape(T, KB) + " of float on cuda:" + std::to_string(l.dev), *sx);
+    const int64_t sizes[3] = {offsets ? per[0] : (N + 127) / 128, offsets ? (N + 127) / 128 : KB, KB};
+    whole(*sw, "w_scale", l.dev, at::kFloat, at::IntArrayRef(sizes, offsets ? 3 : 2));
+  } else if (e4m3) {
     whole(*sx, "x_scale", l.dev, at::kFloat, {T});
     whole(*sw, "w_scale", l.dev, at::kFloat, vec);
   }
@@ -427,7 +436,7 @@ PyObject* linear(PyObject* const* a) {
   p.d_residual = ptr(res);
   p.d_offsets = ptr<int32_t>(offsets);
   p.d_y = ptr(out);
-  call("linear", on, [&](void* s) { return lib.linear(&p, s); });
+  call("linear", on, [&](void* s) { return blocks ? lib.linear_blocks(&p, sx->stride(0), sx->stride(1), s) : lib.linear(&p, s); });
   written(a[10]);
   return given ? same(a[10]) : wrap(out);
 }
@@ -554,6 +563,56 @@ PyObject* act_mul_backward(PyObject* const* a) {
   return tuple({a[4] != Py_None ? same(a[4]) : wrap(out_z), !mul ? same(Py_None) : a[5] != Py_None ? same(a[5]) : wrap(out_mul)});
 }
 
+// x, out, stream -> (q, scale): a scale per 128 columns of a row
+PyObject* quantize_blocks(PyObject* const* a) {
+  const Tensor& x = tensor(a[0], "x");
+  const Lead l = lead(x, "x", {at::kFloat, at::kBFloat16});
+  const On on(l.dev, a[2]);
+  const int64_t T = l.n, F = l.width, KB = (F + 127) / 128;
+  int64_t ldo;
+  const Tensor q = output(a[1], "out", l.dev, at::kFloat8_e4m3fn, T, F, ldo);
+  const Tensor scale = empty({KB, T}, at::kFloat, l.dev).t();            // tokens adjacent: the product reads a block's together
+  call("quantize_blocks", on, [&](void* s) {
+    return lib.quantize_blocks(code(l.dtype), ptr(x), l.ld, 1, count(T, "rows"), count(F, "width"), 1, ptr(q), ldo, ptr<float>(scale), 1, T, s);
+  });
+  written(a[1]);
+  return tuple({a[1] != Py_None ? same(a[1]) : wrap(q), wrap(scale)});
+}
+
+// w, out, stream -> (q, scale): a scale per 128 x 128 of a matrix, or of each of several
+PyObject* quantize_weight_blocks(PyObject* const* a) {
+  const Tensor& w = tensor(a[0], "w");
+  if (w.dim() != 2 && w.dim() != 3) bad("w: expected [N, F] or [G, N, F]", w);
+  if ((w.scalar_type() != at::kFloat && w.scalar_type() != at::kBFloat16) || !w.is_cuda()) bad("w: expected CUDA matrices of Float BFloat16", w);
+  const int dev = w.get_device();
+  const On on(dev, a[2]);
+  const bool many = w.dim() == 3;
+  const int64_t G = many ? w.size(0) : 1, N = w.size(-2), F = w.size(-1), NB = (N + 127) / 128, KB = (F + 127) / 128;
+  int64_t ldw = F, ldo = F;
+  if (many)
+    whole(w, "w", dev, w.scalar_type(), {G, N, F});
+  else
+    ldw = rows(w, "w", dev, w.scalar_type(), N, F);
+  Tensor q;
+  if (!many) {
+    q = output(a[1], "out", dev, at::kFloat8_e4m3fn, N, F, ldo);
+  } else if (a[1] == Py_None) {
+    q = empty({G, N, F}, at::kFloat8_e4m3fn, dev);
+  } else {
+    q = tensor(a[1], "out");
+    whole(q, "out", dev, at::kFloat8_e4m3fn, {G, N, F});
+  }
+  const int64_t sizes[3] = {many ? G : NB, many ? NB : KB, KB};
+  const Tensor scale = empty(at::IntArrayRef(sizes, many ? 3 : 2), at::kFloat, dev);
+  if (G > 0 && N > 0)
+    call("quantize_weight_blocks", on, [&](void* s) {
+      return lib.quantize_blocks(code(w.scalar_type()), ptr(w), ldw, count(G, "groups"), count(N, "rows"), count(F, "width"), 128, ptr(q), ldo, ptr<float>(scale),
+                                 KB, 1, s);
+    });
+  written(a[1]);
+  return tuple({a[1] != Py_None ? same(a[1]) : wrap(q), wrap(scale)});
+}
+
 // ------------------------------------------------------------------ module
 
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -606,6 +665,8 @@ PyMethodDef methods[] = {{"bind", reinterpret_cast<PyCFunction>(reinterpret_cast
                          OP(linear, 12),
                          OP(linear_backward, 13),
                          OP(act_mul_backward, 7),
+                         OP(quantize_blocks, 3),
+                         OP(quantize_weight_blocks, 3),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

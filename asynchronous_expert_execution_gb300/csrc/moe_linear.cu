@@ -255,13 +255,14 @@ extern "C" moe_status moe_async_linear(const moe_async_linear_args* a, void* str
 namespace moe {
 // every set of product kernels has an error word of its own
 unsigned int* ops_error_backward();
+unsigned int* ops_error_blocks();
 }
 
 extern "C" moe_status moe_async_ops_status(void* stream) {
   using namespace moe;
   void* mine = nullptr;
   if (cudaGetSymbolAddress(&mine, g_ops_error) != cudaSuccess) return MOE_ERR_CUDA;
-  unsigned int* const words[] = {static_cast<unsigned int*>(mine), ops_error_backward()};
+  unsigned int* const words[] = {static_cast<unsigned int*>(mine), ops_error_backward(), ops_error_blocks()};
   constexpr int kWords = sizeof(words) / sizeof(words[0]);
   unsigned int e[kWords] = {};
   cudaStream_t s = static_cast<cudaStream_t>(stream);

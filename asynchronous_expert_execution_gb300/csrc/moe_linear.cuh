@@ -698,6 +698,84 @@ struct PairWalk {
   }
 };
 
+// The end of a tile's epilogue for one warp, which has 32 features from f on and every other block of 32 of the tile's nj
+// tokens, from block `half` on: blocks(body) brings each block's sums into `turn` and calls body(its place - half's).  false: a wait
+// ran out there.
+template <typename TO, bool SCALED, class Row, class Blocks>
+__device__ __forceinline__ bool pair_finish(const LinearParams& l, int g, Row first_row, int f, int nj, int half, const float* turn, Blocks blocks) {
+  constexpr bool kSums = sizeof(TO) == 4;
+  constexpr int kStep = 2 * kChunk;
+  const int lane = threadIdx.x & 31;
+  const auto wide = [&](auto plain) {
+    constexpr bool PLAIN = decltype(plain)::value;
+    // 32 features x 32 tokens turned in the warp's own shared memory: lane i then holds 8
+    // features (i % 4) of tokens i / 4 + 8 u, u < 4.  16-byte chunks of a token's row lie at
+    // chunk ^ (token & 7): neither the writes nor the reads meet a bank twice.  mul and
+    // residual are asked for kAt units ahead, the first ones before the products are done.
+    constexpr int kAt = kSums ? 2 : 4, kU = PLAIN ? 2 : 1;         // kU units at once: more would delay the next loads
+    const int f8 = lane % 4, tk = lane / 4;
+    const Finish<TO, 8, SCALED, PLAIN> finish(l, g, f + f8 * 8, 1);
+    const Place<TO> place(l, first_row + half * kChunk + tk, f + f8 * 8);
+    const int mine = nj - half * kChunk - tk;           // tokens from this lane's first to the tile's end
+    typename Finish<TO, 8, SCALED, PLAIN>::Ahead a[kAt];
+#pragma unroll
+    for (int u = 0; u < kAt; ++u) finish.ahead(a[u], place, 8 * u, 8 * u < mine);
+    return blocks([&](int c) {
+#pragma unroll
+      for (int u0 = 0; u0 < 4; u0 += kU) {
+        float w[kU][8];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const float* row = turn + (tk + 8 * (u0 + u)) * 32;
+          const float4 x = *reinterpret_cast<const float4*>(row + ((2 * f8) ^ tk) * 4);
+          const float4 y = *reinterpret_cast<const float4*>(row + ((2 * f8 + 1) ^ tk) * 4);
+          w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w, w[u][4] = y.x, w[u][5] = y.y, w[u][6] = y.z, w[u][7] = y.w;
+        }
+        finish.compute(w, a + u0 % kAt);
+#pragma unroll
+        for (int u = u0; u < u0 + kU; ++u) {
+          if (c + 8 * u < mine) finish.store(w[u - u0], place.y + (c + 8 * u) * l.ldy);
+          const int nx = u + kAt < 4 ? c + 8 * (u + kAt) : c + kStep + 8 * (u + kAt - 4);
+          finish.ahead(a[u % kAt], place, nx, nx < mine);
+        }
+      }
+    });
+  };
+  if (l.wide) {
+    return l.plain() ? wide(std::true_type{}) : wide(std::false_type{});
+  } else {
+    // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens at once
+    const auto narrow = [&](auto plain) {
+      constexpr bool PLAIN = decltype(plain)::value;
+      constexpr int kAt = kSums ? PLAIN || SCALED ? 2 : 8 : PLAIN || SCALED ? 8 : 16;
+      using F = Finish<TO, 1, SCALED, PLAIN>;
+      const F finish(l, g, f + lane, 1);
+      const Place<TO> place(l, first_row + half * kChunk, f + lane);
+      const int mine = nj - half * kChunk;
+      typename F::Ahead a[kAt];
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, j, j < mine);
+      return blocks([&](int c) {
+#pragma unroll 1
+        for (int j0 = 0; j0 < kChunk; j0 += kAt) {
+          float w[kAt][1];
+#pragma unroll
+          for (int j = 0; j < kAt; ++j) w[j][0] = turn[(j0 + j) * 32 + (lane ^ (((j0 + j) & 7) << 2))];
+          finish.compute(w, a);
+          TO* y = place.y + (c + j0) * l.ldy;
+#pragma unroll
+          for (int j = 0; j < kAt; ++j, y += l.ldy)
+            if (c + j0 + j < mine) finish.store(w[j], y);
+          const int nx = j0 + kAt < kChunk ? c + j0 + kAt : c + kStep;
+#pragma unroll
+          for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, nx + j, nx + j < mine);
+        }
+      });
+    };
+    return l.plain() ? narrow(std::true_type{}) : narrow(std::false_type{});
+  }
+}
+
 template <bool E4M3, typename TO, int MODE = kForward>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairParams p) {
@@ -912,75 +990,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (threadIdx.x == 128) *reinterpret_cast<volatile int*>(&s->finishing) = tiles;
       const int f = tl.fti * 2 * kBM + rank * kBM + 32 * q;
       const auto first_row = (kAcross ? (long long)tl.g * l.T : 0) + tl.row0;
-      bool ok;
-      const auto wide = [&](auto plain) {
-        constexpr bool PLAIN = decltype(plain)::value;
-        // 32 features x 32 tokens turned in the warp's own shared memory: lane i then holds 8
-        // features (i % 4) of tokens i / 4 + 8 u, u < 4.  16-byte chunks of a token's row lie at
-        // chunk ^ (token & 7): neither the writes nor the reads meet a bank twice.  mul and
-        // residual are asked for kAt units ahead, the first ones before the products are done.
-        constexpr int kAt = kSums ? 2 : 4, kU = PLAIN ? 2 : 1;         // kU units at once: more would delay the next loads
-        const int f8 = lane % 4, tk = lane / 4;
-        const Finish<TO, 8, E4M3, PLAIN> finish(l, tl.g, f + f8 * 8, 1);
-        const Place<TO> place(l, first_row + half * kChunk + tk, f + f8 * 8);
-        const int mine = tl.nj - half * kChunk - tk;           // tokens from this lane's first to the tile's end
-        typename Finish<TO, 8, E4M3, PLAIN>::Ahead a[kAt];
-#pragma unroll
-        for (int u = 0; u < kAt; ++u) finish.ahead(a[u], place, 8 * u, 8 * u < mine);
-        return blocks([&](int c) {
-#pragma unroll
-          for (int u0 = 0; u0 < 4; u0 += kU) {
-            float w[kU][8];
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              const float* row = turn + (tk + 8 * (u0 + u)) * 32;
-              const float4 x = *reinterpret_cast<const float4*>(row + ((2 * f8) ^ tk) * 4);
-              const float4 y = *reinterpret_cast<const float4*>(row + ((2 * f8 + 1) ^ tk) * 4);
-              w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w, w[u][4] = y.x, w[u][5] = y.y, w[u][6] = y.z, w[u][7] = y.w;
-            }
-            finish.compute(w, a + u0 % kAt);
-#pragma unroll
-            for (int u = u0; u < u0 + kU; ++u) {
-              if (c + 8 * u < mine) finish.store(w[u - u0], place.y + (c + 8 * u) * l.ldy);
-              const int nx = u + kAt < 4 ? c + 8 * (u + kAt) : c + kStep + 8 * (u + kAt - 4);
-              finish.ahead(a[u % kAt], place, nx, nx < mine);
-            }
-          }
-        });
-      };
-      if (l.wide) {
-        ok = l.plain() ? wide(std::true_type{}) : wide(std::false_type{});
-      } else {
-        // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens at once
-        const auto narrow = [&](auto plain) {
-          constexpr bool PLAIN = decltype(plain)::value;
-          constexpr int kAt = kSums ? PLAIN || E4M3 ? 2 : 8 : PLAIN || E4M3 ? 8 : 16;
-          using F = Finish<TO, 1, E4M3, PLAIN>;
-          const F finish(l, tl.g, f + lane, 1);
-          const Place<TO> place(l, first_row + half * kChunk, f + lane);
-          const int mine = tl.nj - half * kChunk;
-          typename F::Ahead a[kAt];
-#pragma unroll
-          for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, j, j < mine);
-          return blocks([&](int c) {
-#pragma unroll 1
-            for (int j0 = 0; j0 < kChunk; j0 += kAt) {
-              float w[kAt][1];
-#pragma unroll
-              for (int j = 0; j < kAt; ++j) w[j][0] = turn[(j0 + j) * 32 + (lane ^ (((j0 + j) & 7) << 2))];
-              finish.compute(w, a);
-              TO* y = place.y + (c + j0) * l.ldy;
-#pragma unroll
-              for (int j = 0; j < kAt; ++j, y += l.ldy)
-                if (c + j0 + j < mine) finish.store(w[j], y);
-              const int nx = j0 + kAt < kChunk ? c + j0 + kAt : c + kStep;
-#pragma unroll
-              for (int j = 0; j < kAt; ++j) finish.ahead(a[j], place, nx + j, nx + j < mine);
-            }
-          });
-        };
-        ok = l.plain() ? narrow(std::true_type{}) : narrow(std::false_type{});
-      }
+      const bool ok = pair_finish<TO, E4M3>(l, tl.g, first_row, f, tl.nj, half, turn, blocks);
       if (!ok) break;
     }
   }

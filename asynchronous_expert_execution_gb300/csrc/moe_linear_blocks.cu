@@ -1,0 +1,712 @@
+// The product of e4m3 operands with a scale per 128 columns of a token and per 128 x 128 block of a weight, dense or
+// per expert on sorted rows, and the quantisers that make such operands:
+//
+//   v[t, n] = sum_b sx[t, b] sw[n / 128, b] sum_{k in block b} x[t, k] w[n, k],   b = k / 128
+//
+// then the epilogue of the forward product (moe_linear.cuh): act(v + bias) * mul + residual.
+//
+// 128 e4m3 columns are one k-block (128 bytes, one swizzle atom), so every k-block's sum stands under one scale a token
+// and feature block.  The tensor cores sum a k-block into a TMEM buffer of its own, and the epilogue warps, while the
+// next ones are summed, bring it into their registers times sx sw: the sum over blocks is rounded in fp32 (the tensor
+// cores' own sums of four instructions are too short for their cut to show).  Features are the MMA's rows, as in the forward
+// product: a CTA's 128 features are one block of w's scales, so sx sw is one number a token, which a warp
+// lays into shared memory ahead of use, and the multiply-adds run on pairs of tokens.
+//
+//   pair   persistent, 256 features x up to 128 tokens over two SMs
+//   split  128 features x up to 64 tokens, K split over a cluster of up to 8 CTAs
+#include "moe_linear.cuh"
+
+namespace moe {
+namespace {
+
+// acc += d * s on two fp32 at once
+__device__ __forceinline__ void fma2(unsigned long long& acc, float d0, float d1, unsigned long long s) {
+  unsigned long long d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(d0), "f"(d1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(s));
+}
+__device__ __forceinline__ float2 halves(unsigned long long v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+
+// acc[0 .. 8) += 16 columns at `taddr` times their tokens' factors
+__device__ __forceinline__ void take16(unsigned long long* acc, uint32_t taddr, const float* factor) {
+  float d[16];
+  tmem_ld16(taddr, d);
+#pragma unroll
+  for (int j = 0; j < 16; j += 4) {
+    const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(factor + j);
+    fma2(acc[j / 2], d[j], d[j + 1], s.x);
+    fma2(acc[j / 2 + 1], d[j + 2], d[j + 3], s.y);
+  }
+}
+
+// Scales of x, [rows][blocks] with any strides, and of w, [groups][feature blocks][blocks].
+struct Scales {
+  const float* x;
+  const float* w;
+  int64_t row, block;
+  int nfb;
+};
+
+// A warp lays sx sw of `n` tokens from `row` on into slot after slot, kBatch k-blocks' loads in flight.
+template <int SLOTS, int TOKENS, int kBatch, class Ready>
+__device__ __forceinline__ void lay_factors(const Scales& sc, const LinearParams& l, int g, int fb, int row, int n, int kb0, int kb1, float (*slot)[TOKENS],
+                                            uint64_t* full, uint32_t& at, Ready wait_empty) {
+  constexpr int kPer = (TOKENS + 31) / 32;
+  const int lane = threadIdx.x & 31;
+  const float* sw = sc.w + ((size_t)g * sc.nfb + min(fb, sc.nfb - 1)) * l.nk;
+  const float* sx = sc.x + (int64_t)row * sc.row;
+  for (int kb = kb0; kb < kb1; kb += kBatch) {
+    float v[kBatch][kPer], w[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const bool on = kb + b < kb1;
+      w[b] = on ? __ldg(sw + kb + b) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[b][i] = on && lane + 32 * i < n ? __ldg(sx + (lane + 32 * i) * sc.row + (kb + b) * sc.block) : 0.f;
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (kb + b >= kb1) break;
+      const int s = at % SLOTS;
+      if (!wait_empty(s, ((at / SLOTS) & 1) ^ 1)) return;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (TOKENS % 32 == 0 || lane + 32 * i < TOKENS) slot[s][lane + 32 * i] = v[b][i] * w[b];
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(smem_u32(&full[s]));
+      ++at;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ pair kernel
+
+constexpr int kBlockTokens = 128;
+constexpr int kBlockRing = 160 * 1024;
+constexpr int kFactorSlots = 8;
+// registers: the launch gives every thread 168; the epilogue's warps, which hold a tile's sums, take from the others
+constexpr int kLaunchRegs = 168, kFewRegs = 72, kManyRegs = 216;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kPairThreads * kLaunchRegs, "the warps' registers are those of the launch");
+
+struct BlockPairParams {
+  PairParams p;
+  Scales s;
+};
+
+struct BlockPairTail {
+  static constexpr int kMaxStages = 8;
+  float factor[kFactorSlots][kBlockTokens];
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[4], tempty[4], sfull[kFactorSlots], sempty[kFactorSlots];
+  uint32_t tmem;
+  int abort_flag;
+  int finishing;
+};
+constexpr int kBlockPairSmem = kBlockRing + kStaging + (int)sizeof(BlockPairTail) + 1024;
+static_assert(kBlockPairSmem <= 227 * 1024, "shared memory of a CTA");
+
+template <typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_blocks_pair_kernel(const __grid_constant__ BlockPairParams bp) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  BlockPairTail* s = reinterpret_cast<BlockPairTail*>(smem + kBlockRing + kStaging);
+  volatile int* abort_flag = &s->abort_flag;
+  const PairParams& p = bp.p;
+  const LinearParams& l = p.l;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int accs = p.tokens > 128 ? 2 : 4, acc_cols = 512 / accs;
+  constexpr uint32_t kCols = 512;
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&p.w);
+    prefetch_map(&p.x[3]);
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&s->full[i], 1);                     // the leader's producer, for both CTAs' bytes
+      mbar_init(&s->empty[i], 1);                    // the MMA's commit, in both CTAs
+    }
+    for (int b = 0; b < accs; ++b) {
+      mbar_init(&s->tfull[b], 1);
+      mbar_init(&s->tempty[b], 16);                  // the epilogue warps of both CTAs, at the leader
+    }
+    for (int i = 0; i < kFactorSlots; ++i) {
+      mbar_init(&s->sfull[i], 1);
+      mbar_init(&s->sempty[i], 8);
+    }
+    s->abort_flag = 0;
+    s->finishing = 0;
+    mbar_init_fence();
+  }
+  if (warp == 2) tmem_alloc<2>(&s->tmem, kCols);
+  ops_begin();
+  tc_before();
+  __syncthreads();
+  cluster_sync();
+  tc_after();
+  const uint32_t tmem = s->tmem;
+  PairWalk walk;
+  PairTile tl;
+
+  if (warp < 4) {
+    regs_give<kFewRegs>();
+    if (warp == 0) {
+      uint32_t st = 0, phase = 1;
+      bool ok = true;
+      while (__all_sync(0xffffffffu, ok) && walk.next<kForward>(p, tl)) {
+        if (!elect()) continue;
+        const int block = kABlock + tl.brows * kBKBytes;
+        const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
+        for (int kb = 0; kb < l.nk; ++kb) {
+          if (!(ok = wait(&s->empty[st], phase, abort_flag))) break;
+          const uint32_t a = smem_u32(smem + st * p.stage_bytes), bar = mapa(smem_u32(&s->full[st]), 0);
+          if (rank == 0) mbar_expect(&s->full[st], 2 * block);
+          tma_3d<2>(a, &p.w, bar, kb * kBKBytes, wrow, tl.g);
+          tma_2d<2>(a + kABlock, &p.x[tl.box], bar, kb * kBKBytes, xrow);
+          if (++st == p.stages) st = 0, phase ^= 1;
+        }
+      }
+    } else if (warp == 1 && rank == 0) {
+      uint32_t st = 0, phase = 0, acc = 0;
+      bool ok = true;
+      while (__all_sync(0xffffffffu, ok) && walk.next<kForward>(p, tl)) {
+        if (!elect()) continue;
+        const uint32_t idesc = mma_desc<true>(2 * kBM, tl.nmma);
+        for (int kb = 0; kb < l.nk; ++kb, ++acc) {
+          const int buf = acc % accs;
+          if (!(ok = wait(&s->tempty[buf], ((acc / accs) & 1) ^ 1, abort_flag))) break;
+          if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
+          tc_after();
+          product_block<2, kForward, true>(tmem + buf * acc_cols, smem_u32(smem + st * p.stage_bytes), idesc, false, kBoxRows);
+          commit<2>(&s->empty[st]);
+          commit<2>(&s->tfull[buf]);
+          if (++st == p.stages) st = 0, phase ^= 1;
+        }
+      }
+    } else if (warp == 2) {
+      uint32_t at = 0;
+      bool ok = true;
+      while (ok && walk.next<kForward>(p, tl))
+        lay_factors<kFactorSlots, kBlockTokens, 4>(bp.s, l, tl.g, tl.fti * 2 + rank, tl.row0, tl.nj, 0, l.nk, s->factor, s->sfull, at,
+                                                   [&](int slot, uint32_t parity) {
+                                                     return ok = __all_sync(0xffffffffu, wait(&s->sempty[slot], parity, abort_flag));
+                                                   });
+    } else if (warp == 3 && (l.mul || l.res)) {
+      // mul and residual of a tile into L2 while it is summed
+      volatile int* finishing = &s->finishing;
+      for (int i = 0; walk.next<kForward>(p, tl); ++i) {
+        const unsigned long long t0 = now_ns();
+        while (*finishing < i && !*abort_flag && now_ns() - t0 < kLimitNs) __nanosleep(200);
+        const int f = tl.fti * 2 * kBM + rank * kBM, n = min(kBM, l.N - f) * (int)sizeof(TO), lines = kBM * (int)sizeof(TO) / 128;
+        for (int j = lane / lines; j < tl.nj; j += 32 / lines) {
+          const int64_t r = tl.row0 + j;
+          if (lane % lines * 128 < n) {
+            if (l.mul) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.mul) + r * l.ldmul + f) + lane % lines * 128);
+            if (l.res) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.res) + r * l.ldres + f) + lane % lines * 128);
+          }
+        }
+      }
+    }
+  } else {
+    regs_take<kManyRegs>();
+    const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..; two warps share a quarter's columns
+    float* turn = reinterpret_cast<float*>(smem + kBlockRing) + (warp - 4) * kTurn;
+    const uint32_t d0 = tmem + ((uint32_t)(32 * q) << 16);
+    constexpr int kMine = kBlockTokens / kChunk / 2;           // a warp's blocks of 32 tokens: every other one
+    uint32_t n = 0;
+    for (int tiles = 1; walk.next<kForward>(p, tl); ++tiles) {
+      unsigned long long acc[kMine][kChunk / 2];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+#pragma unroll
+        for (int j = 0; j < kChunk / 2; ++j) acc[i][j] = 0;
+      bool ok = true;
+      for (int kb = 0; kb < l.nk; ++kb, ++n) {
+        const int buf = n % accs, slot = n % kFactorSlots;
+        ok = wait(&s->sfull[slot], (n / kFactorSlots) & 1, abort_flag) && wait(&s->tfull[buf], (n / accs) & 1, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_after();
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int c = (2 * i + half) * kChunk;
+          if (c < tl.nj) {
+            take16(acc[i], d0 + buf * acc_cols + c, s->factor[slot] + c);
+            take16(acc[i] + 8, d0 + buf * acc_cols + c + 16, s->factor[slot] + c + 16);
+          }
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster(mapa(smem_u32(&s->tempty[buf]), 0));
+          mbar_arrive_cluster(smem_u32(&s->sempty[slot]));
+        }
+      }
+      if (!ok) break;
+      if (threadIdx.x == 128) *reinterpret_cast<volatile int*>(&s->finishing) = tiles;
+      pair_finish<TO, false>(l, tl.g, tl.row0, tl.fti * 2 * kBM + rank * kBM + 32 * q, tl.nj, half, turn, [&](auto body) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int c = (2 * i + half) * kChunk;
+          if (c < tl.nj) {
+#pragma unroll
+            for (int j = 0; j < kChunk; j += 2) {
+              const float2 v = halves(acc[i][j / 2]);
+              turn[j * 32 + (lane ^ ((j & 7) << 2))] = v.x;
+              turn[(j + 1) * 32 + (lane ^ (((j + 1) & 7) << 2))] = v.y;
+            }
+            __syncwarp();
+            body(c - half * kChunk);
+            __syncwarp();
+          }
+        }
+        return true;
+      });
+    }
+  }
+  __syncwarp();
+  tc_before();
+  __syncthreads();
+  settle(abort_flag);
+  cluster_sync();                                    // neither CTA's shared memory goes while the other may use it
+  tc_after();
+  if (warp == 2) tmem_dealloc<2>(tmem, kCols);
+}
+
+// ------------------------------------------------------------------ split kernel
+
+struct BlockSplitParams {
+  SplitParams p;
+  Scales s;
+};
+
+template <int BN> struct BlockSplitTail {
+  static constexpr int kMaxStages = 12, kSlots = 16;
+  float factor[kSlots][BN];
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[4], tempty[4], sfull[kSlots], sempty[kSlots], got;
+  uint32_t tmem;
+  int abort_flag;
+  int g, row0, nj;                  // this cluster's tile; nj = 0: none
+};
+
+template <typename TO, int BN>
+__global__ void __launch_bounds__(kThreads, 2) linear_blocks_split_kernel(const __grid_constant__ BlockSplitParams sp) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  using Tail = BlockSplitTail<BN>;
+  const SplitParams& p = sp.p;
+  constexpr int kStage = kABlock + BN * kBKBytes;
+  Tail* s = reinterpret_cast<Tail*>(smem + p.stages * kStage);
+  volatile int* abort_flag = &s->abort_flag;
+  const LinearParams& l = p.l;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.splits > 1 ? (int)cluster_rank() : 0;
+  const int tile = blockIdx.x / p.splits;
+  constexpr int kAccs = 4;
+  constexpr uint32_t kCols = kAccs * BN < 32 ? 32 : kAccs * BN;
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&p.w);
+    prefetch_map(&p.x);
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&s->full[i], 1);
+      mbar_init(&s->empty[i], 1);
+    }
+    for (int i = 0; i < kAccs; ++i) {
+      mbar_init(&s->tfull[i], 1);
+      mbar_init(&s->tempty[i], 4);
+    }
+    for (int i = 0; i < Tail::kSlots; ++i) {
+      mbar_init(&s->sfull[i], 1);
+      mbar_init(&s->sempty[i], 4);
+    }
+    mbar_init(&s->got, 1);
+    s->abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 2) tmem_alloc<1>(&s->tmem, kCols);
+  int g = 0, nj = 0, row0 = tile / p.nft * BN;
+  const int fti = tile % p.nft;
+  if (!l.offsets) {                                  // dense: the tile is known before the inputs are
+    nj = min(BN, l.T - row0);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    ops_begin();
+  } else {
+    ops_begin();
+    if (warp == 3) {                                 // token tile tile / nft of the groups' tiles
+      const auto tiles = [&](int n) { return (n + BN - 1) / BN; };
+      GroupTiles at(tile / p.nft);
+      if (at.find(l, tiles)) {
+        int n;
+        const int t = at.get(tiles, g, row0, n);
+        row0 += t * BN;
+        nj = min(BN, n - t * BN);
+      }
+      if (lane == 0) {
+        s->g = g;
+        s->row0 = row0;
+        s->nj = nj;
+      }
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    g = s->g;
+    row0 = s->row0;
+    nj = s->nj;
+  }
+  const uint32_t tmem = s->tmem;
+  const int kb0 = (int)((long long)l.nk * rank / p.splits), kb1 = (int)((long long)l.nk * (rank + 1) / p.splits);
+  float* own = reinterpret_cast<float*>(smem);       // [token][feature]: the ring is idle by then
+  float* got = own + BN * kBM;                       // the other ranks' partials of this rank's share
+  const int j0 = nj * rank / p.splits, j1 = nj * (rank + 1) / p.splits;
+
+  if (nj > 0 && warp == 0 && elect()) {
+    uint32_t st = 0, phase = 1;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!wait(&s->empty[st], phase, abort_flag)) break;
+      const uint32_t a = smem_u32(smem + st * kStage);
+      mbar_expect(&s->full[st], kStage);
+      tma_3d<1>(a, &p.w, smem_u32(&s->full[st]), kb * kBKBytes, fti * kBM, g);
+      tma_2d<1>(a + kABlock, &p.x, smem_u32(&s->full[st]), kb * kBKBytes, row0);
+      if (++st == p.stages) st = 0, phase ^= 1;
+    }
+  } else if (nj > 0 && warp == 1 && elect()) {
+    const uint32_t idesc = mma_desc<true>(kBM, BN);
+    uint32_t st = 0, phase = 0;
+    for (int i = 0; i < kb1 - kb0; ++i) {
+      const int buf = i % kAccs;
+      if (!wait(&s->tempty[buf], ((i / kAccs) & 1) ^ 1, abort_flag) || !wait(&s->full[st], phase, abort_flag)) break;
+      tc_after();
+      product_block<1, kForward, true>(tmem + buf * BN, smem_u32(smem + st * kStage), idesc, false, kBoxRows);
+      commit<1>(&s->empty[st]);
+      commit<1>(&s->tfull[buf]);
+      if (++st == p.stages) st = 0, phase ^= 1;
+    }
+  } else if (nj > 0 && warp == 3) {
+    uint32_t at = 0;
+    lay_factors<Tail::kSlots, BN, 8>(sp.s, l, g, fti, row0, nj, kb0, kb1, s->factor, s->sfull, at, [&](int slot, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait(&s->sempty[slot], parity, abort_flag));
+    });
+  } else if (nj > 0 && warp >= 4) {
+    const int q = warp & 3, row = 32 * q + lane;     // TMEM lane: a feature
+    const uint32_t t = tmem + ((uint32_t)(32 * q) << 16);
+    unsigned long long acc[BN / 2];
+#pragma unroll
+    for (int j = 0; j < BN / 2; ++j) acc[j] = 0;
+    bool ok = true;
+    for (int i = 0; i < kb1 - kb0; ++i) {
+      const int buf = i % kAccs, slot = i % Tail::kSlots;
+      ok = wait(&s->sfull[slot], (i / Tail::kSlots) & 1, abort_flag) && wait(&s->tfull[buf], (i / kAccs) & 1, abort_flag);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;                  // whole warps read TMEM
+      tc_after();
+#pragma unroll
+      for (int c = 0; c < BN; c += 16)
+        if (c < nj) take16(acc + c / 2, t + buf * BN + c, s->factor[slot] + c);
+      tc_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_cluster(smem_u32(&s->tempty[buf]));
+        mbar_arrive_cluster(smem_u32(&s->sempty[slot]));
+      }
+    }
+    // all warps' last buffers are full: no product reads the ring any more
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < BN; j += 2) {
+        const float2 v = halves(acc[j / 2]);
+        own[j * kBM + row] = v.x;
+        own[(j + 1) * kBM + row] = v.y;
+      }
+    }
+    if (p.splits > 1) fence_async();
+    if (p.splits > 1 && threadIdx.x == 128) mbar_expect(&s->got, (p.splits - 1) * (j1 - j0) * kBM * 4);
+  }
+  __syncwarp();
+  if (p.splits > 1) {
+    cluster_sync();                                  // all rings are idle, all partials written
+    if (nj > 0 && warp == 0 && lane < p.splits && lane != rank) {
+      const int i0 = nj * lane / p.splits, i1 = nj * (lane + 1) / p.splits, share = (i1 - i0) * kBM;
+      if (share > 0)
+        bulk_to_cluster(mapa(smem_u32(got + rank * share), lane), smem_u32(own + i0 * kBM), share * 4, mapa(smem_u32(&s->got), lane));
+    }
+    if (nj > 0) wait(&s->got, 0, abort_flag);
+  } else {
+    __syncthreads();
+  }
+  if (nj > 0) {                                      // every rank sums and finishes its share of the tokens
+    if (l.wide)
+      split_finish<TO, 8, false>(p, g, row0, fti * kBM, own, got, rank, j0, j1, threadIdx.x % 16 * 8, 1, threadIdx.x / 16, kThreads / 16);
+    else
+      split_finish<TO, 4, false>(p, g, row0, fti * kBM, own, got, rank, j0, j1, lane, 32, warp, kThreads / 32);
+  }
+  settle(abort_flag);
+  if (p.splits > 1) cluster_sync();                  // the copies out of a rank's memory have been received
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 2) tmem_dealloc<1>(tmem, kCols);
+}
+
+// ------------------------------------------------------------------ quantisers
+
+constexpr float kE4M3Max = 448.f;
+constexpr int kQuantBlock = 128;
+
+// The scale of a block whose largest |value| has these bits (NaN above infinity), and what its values are multiplied by.
+__device__ __forceinline__ float block_scale(uint32_t bits, float& inverse) {
+  float scale = fmaxf(__fdiv_rn(__uint_as_float(bits), kE4M3Max), 1.17549435e-38f);
+  if (bits >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);         // an infinity or a NaN: all of the block is NaN
+  inverse = __frcp_rn(scale);
+  return scale;
+}
+
+// 8 elements of a row from column c; those at `width` and behind are zeros.  WIDE: in 16-byte units.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t width, float (&v)[8]) {
+  if constexpr (WIDE) {
+    constexpr int N = Vec<T>::N;
+#pragma unroll
+    for (int i = 0; i < 8; i += N) {
+      float t[N];
+      if (c + i < width) {
+        unpack16<T>(__ldg(reinterpret_cast<const uint4*>(row + c + i)), t);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) t[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i + j] = t[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < width ? to_f(row[c + i]) : 0.f;
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t width, const float (&v)[8]) {
+  if constexpr (WIDE) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3) |
+             (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
+    if (c < width) *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < width) row[c + i] = __nv_cvt_float_to_fp8(v[i], __NV_SATFINITE, __NV_E4M3);
+  }
+}
+__device__ __forceinline__ uint32_t largest(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return m;
+}
+
+template <typename T> struct QuantParams {
+  Rows<const T> x;
+  Rows<uint8_t> q;
+  float* scale;
+  int64_t scale_row, scale_block, rows, width;
+  int blocks;                       // of 128 columns
+};
+
+// 1 x 128: sixteen lanes take a block of a row, 8 elements each; a thread asks for kU blocks before it uses the first.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams<T> p) {
+  constexpr int kU = 4;
+  ops_begin();
+  const int sub = threadIdx.x / 16, at = threadIdx.x % 16 * 8;
+  const int64_t total = p.rows * p.blocks, first = (int64_t)blockIdx.x * 16 * kU + sub;
+  float v[kU][8];
+  int64_t row[kU];
+  int col[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int64_t i = first + u * 16;
+    row[u] = i / p.blocks;
+    col[u] = (int)(i - row[u] * p.blocks);
+    if (i < total) load8<T, WIDE>(p.x.at(row[u]), (int64_t)col[u] * kQuantBlock + at, p.width, v[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const bool on = first + u * 16 < total;
+    uint32_t m = on ? largest(v[u]) : 0;
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (!on) continue;
+    float inverse;
+    const float scale = block_scale(m, inverse);
+    if (at == 0) p.scale[row[u] * p.scale_row + col[u] * p.scale_block] = scale;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] *= inverse;
+    store8<WIDE>(p.q.at(row[u]), (int64_t)col[u] * kQuantBlock + at, p.width, v[u]);
+  }
+}
+
+// 128 x 128: a block of 256 threads takes a block of the matrix, which stays in its registers between maximum and quotient.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(256) quantize_weight_kernel(const QuantParams<T> p) {
+  __shared__ uint32_t part[8];
+  ops_begin();
+  constexpr int kRows = kQuantBlock / 16;            // of a thread
+  const int sub = threadIdx.x / 16;
+  const int64_t rb = (p.rows + kQuantBlock - 1) / kQuantBlock;
+  const int64_t b = blockIdx.x, g = b / (rb * p.blocks), in = b - g * rb * p.blocks;
+  const int64_t row0 = in / p.blocks * kQuantBlock, c = in % p.blocks * kQuantBlock + threadIdx.x % 16 * 8;
+  float v[kRows][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    load8<T, WIDE>(p.x.at(g * p.rows + min(row0 + sub + 16 * i, p.rows - 1)), c, p.width, v[i]);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) m = max(m, largest(v[i]));             // a row behind the last is the last one again
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+  float inverse;
+  const float scale = block_scale(m, inverse);
+  if (threadIdx.x == 0) p.scale[b] = scale;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (row0 + sub + 16 * i >= p.rows) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] *= inverse;
+    store8<WIDE>(p.q.at(g * p.rows + row0 + sub + 16 * i), c, p.width, v[i]);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+template <typename TO>
+moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, const Scales& sc, int sms, int tokens, void* s) {
+  // the warps wait for registers that the launch does not have if the compiler gave it fewer
+  static const bool fits = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, linear_blocks_pair_kernel<TO>) == cudaSuccess && at.numRegs >= kLaunchRegs;
+  }();
+  if (!fits) return MOE_ERR_CUDA;
+  BlockPairParams b;
+  PairParams& p = b.p;
+  b.s = sc;
+  p.l = l;
+  p.nft = (l.N + 2 * kBM - 1) / (2 * kBM);
+  if (!encode(&p.w, a->d_w, 1, l.F, l.N, a->w_stride, l.G, kBM)) return MOE_ERR_CUDA;
+  p.tokens = tokens;
+  p.stage_bytes = kABlock + tokens / 2 * kBKBytes;
+  p.stages = std::min(BlockPairTail::kMaxStages, kBlockRing / p.stage_bytes);
+  for (int i = 0; i < 4; ++i)
+    if (!encode(&p.x[i], a->d_x, 1, l.F, l.T, a->x_stride, 0, i < 3 ? 16 << i : tokens / 2)) return MOE_ERR_CUDA;
+  if (cudaFuncSetAttribute(linear_blocks_pair_kernel<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockPairSmem) != cudaSuccess) return MOE_ERR_CUDA;
+  return launch_op(linear_blocks_pair_kernel<TO>, dim3(sms / 2 * 2), kPairThreads, kBlockPairSmem, 1, s, b);
+}
+
+template <int BN>
+constexpr int block_split_stages(bool own_sm) {
+  const int n = ((own_sm ? kSplitSmem : kSplitSmem / 2) - (int)sizeof(BlockSplitTail<BN>) - 1024) / (kABlock + BN * kBKBytes);
+  return n < BlockSplitTail<BN>::kMaxStages ? n : BlockSplitTail<BN>::kMaxStages;
+}
+
+template <typename TO, int BN>
+moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, const Scales& sc, int sms, int splits, int64_t tiles, void* s) {
+  // the ring holds the CTA's partials and its share of up to 8 ranks' (which may round up by a token each)
+  static_assert((BN + BN + 8) * kBM * 4 <= block_split_stages<BN>(false) * (kABlock + BN * kBKBytes), "shared memory of the split kernel");
+  BlockSplitParams b;
+  SplitParams& p = b.p;
+  b.s = sc;
+  p.l = l;
+  p.bn = BN;
+  p.splits = splits;
+  p.nft = (l.N + kBM - 1) / kBM;
+  p.stages = block_split_stages<BN>(tiles * splits <= sms && l.nk > block_split_stages<BN>(false) * splits);
+  const int smem = p.stages * (kABlock + BN * kBKBytes) + (int)sizeof(BlockSplitTail<BN>) + 1024;
+  if (!encode(&p.w, a->d_w, 1, l.F, l.N, a->w_stride, l.G, kBM) || !encode(&p.x, a->d_x, 1, l.F, l.T, a->x_stride, 0, BN)) return MOE_ERR_CUDA;
+  if (cudaFuncSetAttribute(linear_blocks_split_kernel<TO, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem) != cudaSuccess) return MOE_ERR_CUDA;
+  return launch_op(linear_blocks_split_kernel<TO, BN>, dim3((unsigned)(tiles * splits)), kThreads, smem, splits, s, b);
+}
+
+template <typename TO>
+moe_status blocks_launch(const moe_async_linear_args* a, const LinearParams& l, const Scales& sc, void* s) {
+  const int sms = sm_count();
+  if (sms < 2) return MOE_ERR_CUDA;
+  const int groups = l.offsets ? std::min(l.G, l.T) : 1;
+  const float per = l.T / (float)groups;
+  if (per <= 64) {
+    const int bn = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+    const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * (l.offsets ? l.T / bn + groups : (l.T + bn - 1) / bn);
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= sms && l.nk >= 4 * splits) splits *= 2;
+    return bn == 16 ? launch_split<TO, 16>(a, l, sc, sms, splits, tiles, s) : bn == 32 ? launch_split<TO, 32>(a, l, sc, sms, splits, tiles, s)
+                                                                               : launch_split<TO, 64>(a, l, sc, sms, splits, tiles, s);
+  }
+  return launch_pair<TO>(a, l, sc, sms, kBlockTokens, s);
+}
+
+template <typename T>
+moe_status quantize(const void* x, int64_t ldx, int32_t G, int32_t rows, int32_t width, void* q, int64_t ldq, float* scale, int64_t sr, int64_t sb, bool weight,
+                    void* s) {
+  QuantParams<T> p{{static_cast<const T*>(x), ldx}, {static_cast<uint8_t*>(q), ldq}, scale, sr, sb, rows, width, (int)(((int64_t)width + kQuantBlock - 1) / kQuantBlock)};
+  const bool wide = width % 8 == 0 && rows16(x, ldx, sizeof(T)) && reinterpret_cast<uintptr_t>(q) % 8 == 0 && ldq % 8 == 0;
+  if (weight) {
+    const int64_t blocks = (int64_t)G * ((rows + kQuantBlock - 1) / kQuantBlock) * p.blocks;
+    if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    return launch_op(wide ? quantize_weight_kernel<T, true> : quantize_weight_kernel<T, false>, dim3((unsigned)blocks), 256, 0, 1, s, p);
+  }
+  const int64_t blocks = ((int64_t)rows * p.blocks + 63) / 64;
+  if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  return launch_op(wide ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>, dim3((unsigned)blocks), 256, 0, 1, s, p);
+}
+
+}  // namespace
+
+unsigned int* ops_error_blocks() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_ops_error) == cudaSuccess ? static_cast<unsigned int*>(p) : nullptr;
+}
+
+}  // namespace moe
+
+extern "C" moe_status moe_async_linear_blocks(const moe_async_linear_args* a, int64_t x_scale_row, int64_t x_scale_block, void* stream) {
+  using namespace moe;
+  if (!a) return MOE_ERR_INVALID;
+  if (a->rows < 0 || a->rows > INT32_MAX - 1024 || a->fan_in < 1 || a->fan_in > INT32_MAX - 1024 ||
+      a->fan_out < 1 || a->fan_out > INT32_MAX - 1024 || a->groups < 0 || a->groups > kMaxExperts ||
+      a->act < MOE_ACT_NONE || a->act > MOE_ACT_RELU || (a->groups > 0) != (a->d_offsets != nullptr) ||
+      (a->out_dtype != MOE_F32 && a->out_dtype != MOE_BF16) || x_scale_row < 0 || x_scale_block < 0)
+    return MOE_ERR_INVALID;
+  if (a->dtype != MOE_E4M3) return MOE_ERR_UNSUPPORTED;
+  if (a->rows == 0) return MOE_OK;
+  if (!a->d_x || !a->d_w || !a->d_y || !a->d_x_scale || !a->d_w_scale || a->x_stride < a->fan_in || a->w_stride < a->fan_in || a->y_stride < a->fan_out ||
+      (a->d_mul && a->mul_stride < a->fan_out) || (a->d_residual && a->residual_stride < a->fan_out))
+    return MOE_ERR_INVALID;
+  // the operands move in 16-byte units
+  if (a->fan_in % 16 || !rows16(a->d_x, a->x_stride, 1) || !rows16(a->d_w, a->w_stride, 1)) return MOE_ERR_UNSUPPORTED;
+  const int os = dtype_size(a->out_dtype);
+  const bool wide = a->fan_out % 8 == 0 && rows16(a->d_y, a->y_stride, os) && rows16(a->d_mul, a->mul_stride, os) &&
+                    rows16(a->d_residual, a->residual_stride, os);
+  const LinearParams l{a->d_bias,     nullptr,     nullptr,      a->d_mul,   a->d_residual, a->d_y,
+                       a->d_offsets,  a->mul_stride, a->residual_stride, a->y_stride, a->rows, a->fan_out,
+                       a->fan_in,     std::max(1, a->groups), a->act, (a->fan_in + kBKBytes - 1) / kBKBytes, wide};
+  const Scales sc{a->d_x_scale, a->d_w_scale, x_scale_row, x_scale_block, (a->fan_out + kBM - 1) / kBM};
+  return a->out_dtype == MOE_BF16 ? blocks_launch<__nv_bfloat16>(a, l, sc, stream) : blocks_launch<float>(a, l, sc, stream);
+}
+
+extern "C" moe_status moe_async_quantize_blocks(int32_t dtype, const void* d_x, int64_t x_stride, int32_t G, int32_t rows, int32_t width, int32_t block_rows,
+                                                void* d_q, int64_t q_stride, float* d_scale, int64_t scale_row, int64_t scale_block, void* stream) {
+  using namespace moe;
+  if (rows < 0 || width < 1 || width > kMaxWidth || (block_rows != 1 && block_rows != kQuantBlock) || G < 1 || (block_rows == 1 && G != 1) ||
+      (dtype != MOE_F32 && dtype != MOE_BF16))
+    return MOE_ERR_INVALID;
+  if (rows == 0) return MOE_OK;
+  if (!d_x || !d_q || !d_scale || x_stride < width || q_stride < width || scale_row < 0 || scale_block < 0) return MOE_ERR_INVALID;
+  return dtype == MOE_F32 ? quantize<float>(d_x, x_stride, G, rows, width, d_q, q_stride, d_scale, scale_row, scale_block, block_rows != 1, stream)
+                          : quantize<__nv_bfloat16>(d_x, x_stride, G, rows, width, d_q, q_stride, d_scale, scale_row, scale_block, block_rows != 1, stream);
+}

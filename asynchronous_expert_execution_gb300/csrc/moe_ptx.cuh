@@ -46,6 +46,12 @@ __device__ __forceinline__ unsigned long long now_ns() {
   return t;
 }
 
+// By all warps of a warpgroup: registers of a thread, out of those that the block was launched with.
+template <int N>
+__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // --------------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;

@@ -25,7 +25,7 @@ from . import _native as N
 
 _ORDER = ("sort_experts", "sort_rows", "merge_rows", "merge_rows_backward", "route_backward", "add_rms_norm",
           "add_rms_norm_backward_workspace", "add_rms_norm_backward", "linear", "linear_backward_workspace", "linear_backward",
-          "act_mul_backward")
+          "act_mul_backward", "linear_blocks", "quantize_blocks")
 _bound = None
 
 
@@ -127,8 +127,24 @@ def linear(x, weight, bias=None, act="none", mul=None, residual=None, offsets=No
     "none", "silu", "gelu" (the exact one) or "relu".  `out` may be mul or residual.
     With offsets (int32 [G + 1], as sort_experts gives them) weight is [G, N, F], bias and w_scale
     are [G, N], and rows offsets[g]:offsets[g + 1] of x meet weight[g]; other rows of `out` are
-    left as they were (in a new matrix: not set)."""
+    left as they were (in a new matrix: not set).
+    Scales per block: x_scale [T, ceil(F / 128)], any strides (tokens adjacent, as quantize_blocks leaves them, are read fastest),
+    and w_scale [ceil(N / 128), ceil(F / 128)], with offsets [G, ..]: element (t, k) of x stands for x[t, k] *
+    x_scale[t, k // 128], element (n, k) of weight for weight[n, k] * w_scale[n // 128, k // 128]."""
     return (_bound or _bind()).linear(x, weight, bias, _act(act), mul, residual, offsets, x_scale, w_scale, out_dtype, out, stream)
+
+
+def quantize_blocks(x, out=None, stream=None):
+    """(q, scale): x [T, F] fp32 or bf16 in e4m3 with a scale per 128 columns of a row, the operands x and x_scale of linear:
+    scale = max(max|x| / 448, 2^-126) of each block, q = x / scale, round to nearest.  scale is [T, ceil(F / 128)] with the tokens
+    adjacent in memory.  A block with an infinity or a NaN is NaN, and its scale."""
+    return (_bound or _bind()).quantize_blocks(x, out, stream)
+
+
+def quantize_weight_blocks(w, out=None, stream=None):
+    """(q, scale): w [N, F] or [G, N, F] fp32 or bf16 in e4m3 with a scale per 128 x 128 block, [.., ceil(N / 128), ceil(F / 128)]: the
+    operands weight and w_scale of linear; else as quantize_blocks."""
+    return (_bound or _bind()).quantize_weight_blocks(w, out, stream)
 
 
 def linear_backward(grad, x=None, weight=None, offsets=None, bias=False, residual=None, out_dtype=None, weight_dtype=None, out_x=None,

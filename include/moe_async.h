@@ -522,6 +522,23 @@ typedef struct {
 } moe_async_linear_args;
 moe_status moe_async_linear(const moe_async_linear_args* args, void* stream);
 
+/* moe_async_linear with a scale per block of 128 (MOE_E4M3 only; anything else returns MOE_ERR_UNSUPPORTED):
+ *   v[t, n] = sum_k (x[t, k] sx[t, k / 128]) (w[n, k] sw[n / 128, k / 128]), then act(v + bias) * mul + residual
+ *   d_x_scale : fp32, element (t, b) at t * x_scale_row + b * x_scale_block (tokens adjacent, x_scale_row = 1, is read
+ *               fastest), b < ceil(fan_in / 128)
+ *   d_w_scale : [ceil(fan_out / 128), ceil(fan_in / 128)] fp32, with groups [G, ..]
+ * Each block's products are summed on their own and added, scaled, with rounding in fp32.  Everything else as there. */
+moe_status moe_async_linear_blocks(const moe_async_linear_args* args, int64_t x_scale_row, int64_t x_scale_block, void* stream);
+
+/* The operands of moe_async_linear_blocks: each block's scale = max(max|x| / 448, 2^-126), stored value x / scale (times 1 / scale,
+ * to nearest).  A block with an infinity or a NaN becomes NaN, and its scale.
+ *   block_rows = 1   : blocks of 1 x 128; x [rows, width] (G = 1), scale of (t, b) at t * scale_row + b * scale_block
+ *   block_rows = 128 : blocks of 128 x 128 of G matrices [rows, width], one behind another (rows * stride elements each), scale
+ *                      [G, ceil(rows / 128), ceil(width / 128)] contiguous (scale_row and scale_block are not looked at)
+ * dtype: MOE_F32 or MOE_BF16; blocks at an edge are as wide or high as the matrix lets them. */
+moe_status moe_async_quantize_blocks(int32_t dtype, const void* d_x, int64_t x_stride, int32_t G, int32_t rows, int32_t width, int32_t block_rows,
+                                     void* d_q, int64_t q_stride, float* d_scale, int64_t scale_row, int64_t scale_block, void* stream);
+
 /* Gradients of moe_async_linear without its epilogue, y[t, n] = sum_k x[t, k] w[n, k] + bias[n], from
  * grad = dL/dy:
  *   grad_x[t, k]    = sum_n grad[t, n] w[n, k] + residual[t, k]
