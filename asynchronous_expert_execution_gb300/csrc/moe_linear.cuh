@@ -72,10 +72,13 @@ struct LinearParams {
 
 // Bounded wait; false once it ran out or another role gave up.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try(bar, parity)) return true;
+  constexpr int kTries = 16;                         // between two looks at the clock, which is slow to read
+  for (int i = 0; i < kTries; ++i)
+    if (mbar_try(bar, parity)) return true;
   const unsigned long long t0 = now_ns();
   while (true) {
-    if (mbar_try(bar, parity)) return true;
+    for (int i = 0; i < kTries; ++i)
+      if (mbar_try(bar, parity)) return true;
     if (*abort_flag) return false;
     if (now_ns() - t0 > kLimitNs) {
       *abort_flag = 1;
@@ -701,7 +704,8 @@ struct PairWalk {
 // The end of a tile's epilogue for one warp, which has 32 features from f on and every other block of 32 of the tile's nj
 // tokens, from block `half` on: blocks(body) brings each block's sums into `turn` and calls body(its place - half's).  false: a wait
 // ran out there.
-template <typename TO, bool SCALED, class Row, class Blocks>
+// AHEAD: units of mul and residual asked for ahead, where the registers are another's (0: as many as pay).
+template <typename TO, bool SCALED, int AHEAD = 0, class Row, class Blocks>
 __device__ __forceinline__ bool pair_finish(const LinearParams& l, int g, Row first_row, int f, int nj, int half, const float* turn, Blocks blocks) {
   constexpr bool kSums = sizeof(TO) == 4;
   constexpr int kStep = 2 * kChunk;
@@ -712,7 +716,7 @@ __device__ __forceinline__ bool pair_finish(const LinearParams& l, int g, Row fi
     // features (i % 4) of tokens i / 4 + 8 u, u < 4.  16-byte chunks of a token's row lie at
     // chunk ^ (token & 7): neither the writes nor the reads meet a bank twice.  mul and
     // residual are asked for kAt units ahead, the first ones before the products are done.
-    constexpr int kAt = kSums ? 2 : 4, kU = PLAIN ? 2 : 1;         // kU units at once: more would delay the next loads
+    constexpr int kAt = AHEAD ? AHEAD : kSums ? 2 : 4, kU = PLAIN && kAt > 1 ? 2 : 1;         // kU units at once: more would delay the next loads
     const int f8 = lane % 4, tk = lane / 4;
     const Finish<TO, 8, SCALED, PLAIN> finish(l, g, f + f8 * 8, 1);
     const Place<TO> place(l, first_row + half * kChunk + tk, f + f8 * 8);
@@ -747,7 +751,7 @@ __device__ __forceinline__ bool pair_finish(const LinearParams& l, int g, Row fi
     // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens at once
     const auto narrow = [&](auto plain) {
       constexpr bool PLAIN = decltype(plain)::value;
-      constexpr int kAt = kSums ? PLAIN || SCALED ? 2 : 8 : PLAIN || SCALED ? 8 : 16;
+      constexpr int kAt = AHEAD ? 2 * AHEAD : kSums ? PLAIN || SCALED ? 2 : 8 : PLAIN || SCALED ? 8 : 16;
       using F = Finish<TO, 1, SCALED, PLAIN>;
       const F finish(l, g, f + lane, 1);
       const Place<TO> place(l, first_row + half * kChunk, f + lane);
@@ -866,7 +870,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (live % 16) clear_rows(stage, 2 + tl.brows / 64, live);
         }
         if (rank == 1) {
-          if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&s->peer[st]), 0));
+          const uint32_t bar = mapa(smem_u32(&s->peer[st]), 0);
+          if (lane == 0 && live % 16)
+            mbar_arrive_cluster(bar);                // behind the zeros
+          else if (lane == 0)
+            mbar_arrive_light(bar);
         } else {
           if (!(ok = __all_sync(0xffffffffu, wait(&s->peer[st], phase, abort_flag)))) break;
           tc_after();

@@ -10,36 +10,25 @@
 // next ones are summed, bring it into their registers times sx sw: the sum over blocks is rounded in fp32 (the tensor
 // cores' own sums of four instructions are too short for their cut to show).  Features are the MMA's rows, as in the forward
 // product: a CTA's 128 features are one block of w's scales, so sx sw is one number a token, which a warp
-// lays into shared memory ahead of use, and the multiply-adds run on pairs of tokens.
+// lays into shared memory ahead of use.
 //
-//   pair   persistent, 256 features x up to 128 tokens over two SMs
+//   pair   persistent, 256 features x up to 256 tokens over two SMs
 //   split  128 features x up to 64 tokens, K split over a cluster of up to 8 CTAs
 #include "moe_linear.cuh"
 
 namespace moe {
 namespace {
 
-// acc += d * s on two fp32 at once
-__device__ __forceinline__ void fma2(unsigned long long& acc, float d0, float d1, unsigned long long s) {
-  unsigned long long d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(d0), "f"(d1));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(s));
-}
-__device__ __forceinline__ float2 halves(unsigned long long v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-
-// acc[0 .. 8) += 16 columns at `taddr` times their tokens' factors
-__device__ __forceinline__ void take16(unsigned long long* acc, uint32_t taddr, const float* factor) {
-  float d[16];
-  tmem_ld16(taddr, d);
+// acc[0 .. 16) += 16 columns times their tokens' factors, which lie in shared memory.  (Multiply-adds on pairs, fma.f32x2, run no
+// faster, and bringing what was read from TMEM into pairs cost more than they: 128 columns by two warps of a scheduler 1,035 cycles,
+// so 356.)
+__device__ __forceinline__ void take(float* acc, const float (&d)[16], uint32_t factor) {
 #pragma unroll
   for (int j = 0; j < 16; j += 4) {
-    const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(factor + j);
-    fma2(acc[j / 2], d[j], d[j + 1], s.x);
-    fma2(acc[j / 2 + 1], d[j + 2], d[j + 3], s.y);
+    float f[4];
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(factor + 4 * j));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j + i] = fmaf(d[j + i], f[i], acc[j + i]);
   }
 }
 
@@ -51,94 +40,115 @@ struct Scales {
   int nfb;
 };
 
-// A warp lays sx sw of `n` tokens from `row` on into slot after slot, kBatch k-blocks' loads in flight.
-template <int SLOTS, int TOKENS, int kBatch, class Ready>
-__device__ __forceinline__ void lay_factors(const Scales& sc, const LinearParams& l, int g, int fb, int row, int n, int kb0, int kb1, float (*slot)[TOKENS],
-                                            uint64_t* full, uint32_t& at, Ready wait_empty) {
+constexpr int kBatch = 4;
+
+// A warp lays sx sw of `n` tokens from `row` on into shared memory, kBatch k-blocks to a slot, whose loads are in flight together.
+template <int SLOTS, int TOKENS, class Ready>
+__device__ __forceinline__ void lay_factors(const Scales& sc, const LinearParams& l, int g, int fb, int row, int n, int kb0, int kb1,
+                                            float (*slot)[kBatch][TOKENS], uint64_t* full, uint32_t& at, Ready wait_empty) {
   constexpr int kPer = (TOKENS + 31) / 32;
   const int lane = threadIdx.x & 31;
   const float* sw = sc.w + ((size_t)g * sc.nfb + min(fb, sc.nfb - 1)) * l.nk;
-  const float* sx = sc.x + (int64_t)row * sc.row;
-  for (int kb = kb0; kb < kb1; kb += kBatch) {
-    float v[kBatch][kPer], w[kBatch];
+  const float* sx = sc.x + (int64_t)(row + lane) * sc.row;
+  for (int kb = kb0; kb < kb1; kb += kBatch, ++at) {
+    float v[kBatch][kPer];
+    const float mine = lane < kBatch && kb + lane < kb1 ? __ldg(sw + kb + lane) : 0.f;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const bool on = kb + b < kb1;
-      w[b] = on ? __ldg(sw + kb + b) : 0.f;
+      const float* from = sx + (kb + b) * sc.block;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[b][i] = on && lane + 32 * i < n ? __ldg(sx + (lane + 32 * i) * sc.row + (kb + b) * sc.block) : 0.f;
+      for (int i = 0; i < kPer; ++i, from += 32 * sc.row) v[b][i] = kb + b < kb1 && lane + 32 * i < n ? __ldg(from) : 0.f;
     }
+    const int s = at % SLOTS;
+    if (!wait_empty(s, ((at / SLOTS) & 1) ^ 1)) return;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      if (kb + b >= kb1) break;
-      const int s = at % SLOTS;
-      if (!wait_empty(s, ((at / SLOTS) & 1) ^ 1)) return;
+      const float w = __shfl_sync(0xffffffffu, mine, b);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (TOKENS % 32 == 0 || lane + 32 * i < TOKENS) slot[s][lane + 32 * i] = v[b][i] * w[b];
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(smem_u32(&full[s]));
-      ++at;
+        if (TOKENS % 32 == 0 || lane + 32 * i < TOKENS) slot[s][b][lane + 32 * i] = v[b][i] * w;
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[s]);
   }
 }
 
 // ------------------------------------------------------------------ pair kernel
 
-constexpr int kBlockTokens = 128;
+// Tokens are the MMA's rows here, and so the lanes of TMEM: a thread has one token, and one factor for all of a k-block's 128
+// features that it adds.  With features on the lanes, as in the split kernel, every column has a factor of its own, and their reads of
+// shared memory (one of 16 bytes for four columns a warp) held a k-block of 256 x 256 to 965 cycles where the products take some 570.
+// The price is that a group's last tile is summed as if it were full.
 constexpr int kBlockRing = 160 * 1024;
-constexpr int kFactorSlots = 8;
+constexpr int kTileSlots = 4;
 // registers: the launch gives every thread 168; the epilogue's warps, which hold a tile's sums, take from the others
-constexpr int kLaunchRegs = 168, kFewRegs = 72, kManyRegs = 216;
+constexpr int kLaunchRegs = 168, kFewRegs = 56, kManyRegs = 224;
 static_assert(128 * kFewRegs + 256 * kManyRegs <= kPairThreads * kLaunchRegs, "the warps' registers are those of the launch");
 
 struct BlockPairParams {
-  PairParams p;
+  PairParams p;                     // x[3]: boxes of 128 tokens
   Scales s;
 };
 
 struct BlockPairTail {
-  static constexpr int kMaxStages = 8;
-  float factor[kFactorSlots][kBlockTokens];
-  uint64_t full[kMaxStages], empty[kMaxStages], tfull[4], tempty[4], sfull[kFactorSlots], sempty[kFactorSlots];
+  static constexpr int kStages = kBlockRing / (2 * kABlock);
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], told[kTileSlots], heard[kTileSlots];
+  int4 tile[kTileSlots];            // g, first row, rows, feature tile; no rows: there are no more
   uint32_t tmem;
   int abort_flag;
-  int finishing;
 };
 constexpr int kBlockPairSmem = kBlockRing + kStaging + (int)sizeof(BlockPairTail) + 1024;
 static_assert(kBlockPairSmem <= 227 * 1024, "shared memory of a CTA");
+
+__device__ __forceinline__ void scale16(float* acc, const float (&d)[16], float f) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) acc[j] = fmaf(d[j], f, acc[j]);
+}
+
+// The scales of a token and of 128 features in kBatch k-blocks, asked for while those before are used.
+struct Factors {
+  const float* x;                   // null: no token
+  const float* w;                   // a k-block a lane
+  float sx[kBatch], sw;
+  __device__ __forceinline__ void ask(int left, int64_t step) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) sx[b] = b < left && x ? __ldg(x + b * step) : 0.f;
+    const int lane = threadIdx.x & 31;
+    sw = lane < min(kBatch, left) ? __ldg(w) : 0.f;
+  }
+};
 
 template <typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_blocks_pair_kernel(const __grid_constant__ BlockPairParams bp) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  BlockPairTail* s = reinterpret_cast<BlockPairTail*>(smem + kBlockRing + kStaging);
+  using Tail = BlockPairTail;
+  Tail* s = reinterpret_cast<Tail*>(smem + kBlockRing + kStaging);
   volatile int* abort_flag = &s->abort_flag;
   const PairParams& p = bp.p;
   const LinearParams& l = p.l;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
-  const int accs = p.tokens > 128 ? 2 : 4, acc_cols = 512 / accs;
-  constexpr uint32_t kCols = 512;
+  constexpr uint32_t kCols = 512, kAccCols = 256;
+  constexpr int kStage = 2 * kABlock;
 
   if (threadIdx.x == 0) {
     prefetch_map(&p.w);
     prefetch_map(&p.x[3]);
-    for (int i = 0; i < p.stages; ++i) {
+    for (int i = 0; i < Tail::kStages; ++i) {
       mbar_init(&s->full[i], 1);                     // the leader's producer, for both CTAs' bytes
       mbar_init(&s->empty[i], 1);                    // the MMA's commit, in both CTAs
     }
-    for (int b = 0; b < accs; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&s->tfull[b], 1);
       mbar_init(&s->tempty[b], 16);                  // the epilogue warps of both CTAs, at the leader
     }
-    for (int i = 0; i < kFactorSlots; ++i) {
-      mbar_init(&s->sfull[i], 1);
-      mbar_init(&s->sempty[i], 8);
+    for (int i = 0; i < kTileSlots; ++i) {
+      mbar_init(&s->told[i], 1);
+      mbar_init(&s->heard[i], 8);
     }
     s->abort_flag = 0;
-    s->finishing = 0;
     mbar_init_fence();
   }
   if (warp == 2) tmem_alloc<2>(&s->tmem, kCols);
@@ -148,62 +158,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_after();
   const uint32_t tmem = s->tmem;
-  PairWalk walk;
-  PairTile tl;
 
   if (warp < 4) {
     regs_give<kFewRegs>();
+    PairWalk walk;
+    PairTile tl;
     if (warp == 0) {
       uint32_t st = 0, phase = 1;
       bool ok = true;
       while (__all_sync(0xffffffffu, ok) && walk.next<kForward>(p, tl)) {
         if (!elect()) continue;
-        const int block = kABlock + tl.brows * kBKBytes;
-        const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
+        const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * kBM;
         for (int kb = 0; kb < l.nk; ++kb) {
           if (!(ok = wait(&s->empty[st], phase, abort_flag))) break;
-          const uint32_t a = smem_u32(smem + st * p.stage_bytes), bar = mapa(smem_u32(&s->full[st]), 0);
-          if (rank == 0) mbar_expect(&s->full[st], 2 * block);
-          tma_3d<2>(a, &p.w, bar, kb * kBKBytes, wrow, tl.g);
-          tma_2d<2>(a + kABlock, &p.x[tl.box], bar, kb * kBKBytes, xrow);
-          if (++st == p.stages) st = 0, phase ^= 1;
+          const uint32_t a = smem_u32(smem + st * kStage), bar = mapa(smem_u32(&s->full[st]), 0);
+          if (rank == 0) mbar_expect(&s->full[st], 2 * kStage);
+          tma_2d<2>(a, &p.x[3], bar, kb * kBKBytes, xrow);
+          tma_3d<2>(a + kABlock, &p.w, bar, kb * kBKBytes, wrow, tl.g);
+          if (++st == Tail::kStages) st = 0, phase ^= 1;
         }
       }
     } else if (warp == 1 && rank == 0) {
       uint32_t st = 0, phase = 0, acc = 0;
       bool ok = true;
+      const uint32_t idesc = mma_desc<true>(2 * kBM, 2 * kBM);
       while (__all_sync(0xffffffffu, ok) && walk.next<kForward>(p, tl)) {
         if (!elect()) continue;
-        const uint32_t idesc = mma_desc<true>(2 * kBM, tl.nmma);
         for (int kb = 0; kb < l.nk; ++kb, ++acc) {
-          const int buf = acc % accs;
-          if (!(ok = wait(&s->tempty[buf], ((acc / accs) & 1) ^ 1, abort_flag))) break;
+          const int buf = acc & 1;
+          if (!(ok = wait(&s->tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag))) break;
           if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
           tc_after();
-          product_block<2, kForward, true>(tmem + buf * acc_cols, smem_u32(smem + st * p.stage_bytes), idesc, false, kBoxRows);
+          product_block<2, kForward, true>(tmem + buf * kAccCols, smem_u32(smem + st * kStage), idesc, false, kBoxRows);
           commit<2>(&s->empty[st]);
           commit<2>(&s->tfull[buf]);
-          if (++st == p.stages) st = 0, phase ^= 1;
+          if (++st == Tail::kStages) st = 0, phase ^= 1;
         }
       }
     } else if (warp == 2) {
-      uint32_t at = 0;
+      // tells the epilogue its tiles, whose registers have no room for the walk
       bool ok = true;
-      while (ok && walk.next<kForward>(p, tl))
-        lay_factors<kFactorSlots, kBlockTokens, 4>(bp.s, l, tl.g, tl.fti * 2 + rank, tl.row0, tl.nj, 0, l.nk, s->factor, s->sfull, at,
-                                                   [&](int slot, uint32_t parity) {
-                                                     return ok = __all_sync(0xffffffffu, wait(&s->sempty[slot], parity, abort_flag));
-                                                   });
+      for (uint32_t n = 0, more = 1; more; ++n) {
+        const int slot = n % kTileSlots;
+        more = walk.next<kForward>(p, tl);
+        if (!(ok = __all_sync(0xffffffffu, wait(&s->heard[slot], ((n / kTileSlots) & 1) ^ 1, abort_flag)))) break;
+        if (lane == 0) {
+          s->tile[slot] = make_int4(tl.g, tl.row0, more ? tl.nj : 0, tl.fti);
+          mbar_arrive(&s->told[slot]);
+        }
+        __syncwarp();
+      }
     } else if (warp == 3 && (l.mul || l.res)) {
-      // mul and residual of a tile into L2 while it is summed
-      volatile int* finishing = &s->finishing;
-      for (int i = 0; walk.next<kForward>(p, tl); ++i) {
-        const unsigned long long t0 = now_ns();
-        while (*finishing < i && !*abort_flag && now_ns() - t0 < kLimitNs) __nanosleep(200);
-        const int f = tl.fti * 2 * kBM + rank * kBM, n = min(kBM, l.N - f) * (int)sizeof(TO), lines = kBM * (int)sizeof(TO) / 128;
-        for (int j = lane / lines; j < tl.nj; j += 32 / lines) {
+      // mul and residual of a tile into L2 while it is summed: the epilogue's reads in flight an SM then last L2's latency
+      for (int n = 0; walk.next<kForward>(p, tl); ++n) {
+        const int slot = n % kTileSlots;
+        if (!__all_sync(0xffffffffu, wait(&s->told[slot], (n / kTileSlots) & 1, abort_flag))) break;
+        const int f = tl.fti * 2 * kBM, width = min(2 * kBM, l.N - f) * (int)sizeof(TO), lines = 2 * kBM * (int)sizeof(TO) / 128;
+        for (int j = rank * kBM + lane / lines; j < min(tl.nj, (rank + 1) * kBM); j += 32 / lines) {
           const int64_t r = tl.row0 + j;
-          if (lane % lines * 128 < n) {
+          if (lane % lines * 128 < width) {
             if (l.mul) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.mul) + r * l.ldmul + f) + lane % lines * 128);
             if (l.res) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.res) + r * l.ldres + f) + lane % lines * 128);
           }
@@ -212,58 +225,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else {
     regs_take<kManyRegs>();
-    const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..; two warps share a quarter's columns
+    const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..: 32 tokens; 128 features
     float* turn = reinterpret_cast<float*>(smem + kBlockRing) + (warp - 4) * kTurn;
-    const uint32_t d0 = tmem + ((uint32_t)(32 * q) << 16);
-    constexpr int kMine = kBlockTokens / kChunk / 2;           // a warp's blocks of 32 tokens: every other one
-    uint32_t n = 0;
-    for (int tiles = 1; walk.next<kForward>(p, tl); ++tiles) {
-      unsigned long long acc[kMine][kChunk / 2];
+    const uint32_t tempty0 = mapa(smem_u32(&s->tempty[0]), 0);
+    uint32_t n = 0, tiles = 0;
+    Factors fac;
+    // tile `tiles`: its first scales; false: there is none.  What else of it is needed waits in shared memory for the finish.
+    auto hear = [&]() {
+      const int slot = tiles % kTileSlots;
+      if (!__all_sync(0xffffffffu, wait(&s->told[slot], (tiles / kTileSlots) & 1, abort_flag))) return false;
+      const int4 tile = s->tile[slot];
+      if (tile.z == 0) return false;
+      const int j = rank * kBM + 32 * q + lane;
+      fac.w = bp.s.w + ((size_t)tile.x * bp.s.nfb + min(tile.w * 2 + half, bp.s.nfb - 1)) * l.nk + lane;
+      fac.x = j < tile.z ? bp.s.x + (int64_t)(tile.y + j) * bp.s.row : nullptr;
+      fac.ask(l.nk, bp.s.block);
+      return true;
+    };
+    bool more = hear();
+    while (more) {
+      float acc[kBM];
 #pragma unroll
-      for (int i = 0; i < kMine; ++i)
-#pragma unroll
-        for (int j = 0; j < kChunk / 2; ++j) acc[i][j] = 0;
+      for (int j = 0; j < kBM; ++j) acc[j] = 0.f;
+      uint32_t d0 = 0;
       bool ok = true;
-      for (int kb = 0; kb < l.nk; ++kb, ++n) {
-        const int buf = n % accs, slot = n % kFactorSlots;
-        ok = wait(&s->sfull[slot], (n / kFactorSlots) & 1, abort_flag) && wait(&s->tfull[buf], (n / accs) & 1, abort_flag);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        tc_after();
+      for (int kb = 0; kb < l.nk; kb += kBatch) {
+        float f[kBatch];
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int c = (2 * i + half) * kChunk;
-          if (c < tl.nj) {
-            take16(acc[i], d0 + buf * acc_cols + c, s->factor[slot] + c);
-            take16(acc[i] + 8, d0 + buf * acc_cols + c + 16, s->factor[slot] + c + 16);
+        for (int b = 0; b < kBatch; ++b) f[b] = fac.sx[b] * __shfl_sync(0xffffffffu, fac.sw, b);
+        if (fac.x) fac.x += kBatch * bp.s.block;
+        fac.w += kBatch;
+        fac.ask(l.nk - kb - kBatch, bp.s.block);
+#pragma unroll 1
+        for (int b = 0; b < min(kBatch, l.nk - kb); ++b, ++n) {
+          const int buf = n & 1;
+          if (!(ok = __all_sync(0xffffffffu, wait(&s->tfull[buf], (n >> 1) & 1, abort_flag)))) break;
+          tc_after();
+          d0 = tmem + ((uint32_t)(32 * q) << 16) + buf * kAccCols + half * kBM;
+          // 16 columns are asked for while those before are added
+          float d[2][16];
+          tmem_ask16(d0, d[0]);
+#pragma unroll
+          for (int c = 0; c < kBM / 16; ++c) {
+            tmem_wait(d[c & 1]);
+            if (c + 1 < kBM / 16) tmem_ask16(d0 + 16 * (c + 1), d[(c + 1) & 1]);
+            // the buffer is the next k-block's but one's, unless it is the last: then the sums go there
+            if (c + 1 == kBM / 16 && kb + b + 1 < l.nk) {
+              tc_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_relaxed(tempty0 + buf * 8);
+            }
+            scale16(acc + 16 * c, d[c & 1], f[0]);
           }
+#pragma unroll
+          for (int i = 0; i + 1 < kBatch; ++i) f[i] = f[i + 1];
         }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster(mapa(smem_u32(&s->tempty[buf]), 0));
-          mbar_arrive_cluster(smem_u32(&s->sempty[slot]));
-        }
+        if (!ok) break;
       }
       if (!ok) break;
-      if (threadIdx.x == 128) *reinterpret_cast<volatile int*>(&s->finishing) = tiles;
-      pair_finish<TO, false>(l, tl.g, tl.row0, tl.fti * 2 * kBM + rank * kBM + 32 * q, tl.nj, half, turn, [&](auto body) {
+      // the sums go to the last k-block's buffer, which this warp has read: the registers are the finish's
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int c = (2 * i + half) * kChunk;
-          if (c < tl.nj) {
+      for (int c = 0; c < kBM; c += 16) {
+        float v[16];
 #pragma unroll
-            for (int j = 0; j < kChunk; j += 2) {
-              const float2 v = halves(acc[i][j / 2]);
-              turn[j * 32 + (lane ^ ((j & 7) << 2))] = v.x;
-              turn[(j + 1) * 32 + (lane ^ (((j + 1) & 7) << 2))] = v.y;
-            }
-            __syncwarp();
-            body(c - half * kChunk);
-            __syncwarp();
+        for (int j = 0; j < 16; ++j) v[j] = acc[c + j];
+        tmem_st16(d0 + c, v);
+      }
+      const int slot = tiles++ % kTileSlots;
+      more = hear();
+      const int4 tile = s->tile[slot];
+      const int first = rank * kBM + 32 * q, f0 = (tile.w * 2 + half) * kBM;
+#pragma unroll 1
+      for (int i = 0; i < kBM && f0 + i < l.N && first < tile.z; i += 32)
+        pair_finish<TO, false, sizeof(TO) == 2 ? 2 : 1>(l, tile.x, tile.y + first, f0 + i, min(32, tile.z - first), 0, turn, [&](auto body) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[16];
+            tmem_ld16(d0 + i + 16 * h, v);
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)          // as [token][32 features], 16-byte chunks at chunk ^ (token & 7)
+              *reinterpret_cast<float4*>(turn + lane * 32 + (((4 * h + j / 4) ^ (lane & 7)) * 4)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
           }
-        }
-        return true;
-      });
+          __syncwarp();
+          body(0);
+          __syncwarp();
+          return true;
+        });
+      tc_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_relaxed(tempty0 + ((n - 1) & 1) * 8);
+        mbar_arrive(&s->heard[slot]);
+      }
     }
   }
   __syncwarp();
@@ -283,8 +336,8 @@ struct BlockSplitParams {
 };
 
 template <int BN> struct BlockSplitTail {
-  static constexpr int kMaxStages = 12, kSlots = 16;
-  float factor[kSlots][BN];
+  static constexpr int kMaxStages = 12, kSlots = 4;
+  float factor[kSlots][kBatch][BN];
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[4], tempty[4], sfull[kSlots], sempty[kSlots], got;
   uint32_t tmem;
   int abort_flag;
@@ -389,39 +442,41 @@ __global__ void __launch_bounds__(kThreads, 2) linear_blocks_split_kernel(const 
     }
   } else if (nj > 0 && warp == 3) {
     uint32_t at = 0;
-    lay_factors<Tail::kSlots, BN, 8>(sp.s, l, g, fti, row0, nj, kb0, kb1, s->factor, s->sfull, at, [&](int slot, uint32_t parity) {
+    lay_factors<Tail::kSlots, BN>(sp.s, l, g, fti, row0, nj, kb0, kb1, s->factor, s->sfull, at, [&](int slot, uint32_t parity) {
       return __all_sync(0xffffffffu, wait(&s->sempty[slot], parity, abort_flag));
     });
   } else if (nj > 0 && warp >= 4) {
     const int q = warp & 3, row = 32 * q + lane;     // TMEM lane: a feature
     const uint32_t t = tmem + ((uint32_t)(32 * q) << 16);
-    unsigned long long acc[BN / 2];
+    float acc[BN];
 #pragma unroll
-    for (int j = 0; j < BN / 2; ++j) acc[j] = 0;
+    for (int j = 0; j < BN; ++j) acc[j] = 0.f;
     bool ok = true;
     for (int i = 0; i < kb1 - kb0; ++i) {
-      const int buf = i % kAccs, slot = i % Tail::kSlots;
-      ok = wait(&s->sfull[slot], (i / Tail::kSlots) & 1, abort_flag) && wait(&s->tfull[buf], (i / kAccs) & 1, abort_flag);
+      const int buf = i % kAccs, batch = i / kBatch, slot = batch % Tail::kSlots, in = i % kBatch;
+      if (in == 0) ok = wait(&s->sfull[slot], (batch / Tail::kSlots) & 1, abort_flag);
+      ok = ok && wait(&s->tfull[buf], (i / kAccs) & 1, abort_flag);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;                  // whole warps read TMEM
       tc_after();
+      const uint32_t factor = smem_u32(s->factor[slot][in]);
 #pragma unroll
       for (int c = 0; c < BN; c += 16)
-        if (c < nj) take16(acc + c / 2, t + buf * BN + c, s->factor[slot] + c);
+        if (c < nj) {
+          float d[16];
+          tmem_ld16(t + buf * BN + c, d);
+          take(acc + c, d, factor + 4 * c);
+        }
       tc_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_cluster(smem_u32(&s->tempty[buf]));
-        mbar_arrive_cluster(smem_u32(&s->sempty[slot]));
+        mbar_arrive_relaxed(smem_u32(&s->tempty[buf]));
+        if (in == kBatch - 1) mbar_arrive(&s->sempty[slot]);
       }
     }
     // all warps' last buffers are full: no product reads the ring any more
     if (ok) {
 #pragma unroll
-      for (int j = 0; j < BN; j += 2) {
-        const float2 v = halves(acc[j / 2]);
-        own[j * kBM + row] = v.x;
-        own[(j + 1) * kBM + row] = v.y;
-      }
+      for (int j = 0; j < BN; ++j) own[j * kBM + row] = acc[j];
     }
     if (p.splits > 1) fence_async();
     if (p.splits > 1 && threadIdx.x == 128) mbar_expect(&s->got, (p.splits - 1) * (j1 - j0) * kBM * 4);
@@ -587,7 +642,7 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const QuantParams<
 // ------------------------------------------------------------------ host side
 
 template <typename TO>
-moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, const Scales& sc, int sms, int tokens, void* s) {
+moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, const Scales& sc, int sms, void* s) {
   // the warps wait for registers that the launch does not have if the compiler gave it fewer
   static const bool fits = [] {
     cudaFuncAttributes at;
@@ -600,11 +655,8 @@ moe_status launch_pair(const moe_async_linear_args* a, const LinearParams& l, co
   p.l = l;
   p.nft = (l.N + 2 * kBM - 1) / (2 * kBM);
   if (!encode(&p.w, a->d_w, 1, l.F, l.N, a->w_stride, l.G, kBM)) return MOE_ERR_CUDA;
-  p.tokens = tokens;
-  p.stage_bytes = kABlock + tokens / 2 * kBKBytes;
-  p.stages = std::min(BlockPairTail::kMaxStages, kBlockRing / p.stage_bytes);
-  for (int i = 0; i < 4; ++i)
-    if (!encode(&p.x[i], a->d_x, 1, l.F, l.T, a->x_stride, 0, i < 3 ? 16 << i : tokens / 2)) return MOE_ERR_CUDA;
+  p.tokens = 2 * kBM;
+  if (!encode(&p.x[3], a->d_x, 1, l.F, l.T, a->x_stride, 0, kBM)) return MOE_ERR_CUDA;
   if (cudaFuncSetAttribute(linear_blocks_pair_kernel<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockPairSmem) != cudaSuccess) return MOE_ERR_CUDA;
   return launch_op(linear_blocks_pair_kernel<TO>, dim3(sms / 2 * 2), kPairThreads, kBlockPairSmem, 1, s, b);
 }
@@ -647,7 +699,7 @@ moe_status blocks_launch(const moe_async_linear_args* a, const LinearParams& l, 
     return bn == 16 ? launch_split<TO, 16>(a, l, sc, sms, splits, tiles, s) : bn == 32 ? launch_split<TO, 32>(a, l, sc, sms, splits, tiles, s)
                                                                                : launch_split<TO, 64>(a, l, sc, sms, splits, tiles, s);
   }
-  return launch_pair<TO>(a, l, sc, sms, kBlockTokens, s);
+  return launch_pair<TO>(a, l, sc, sms, s);
 }
 
 template <typename T>
