@@ -71,14 +71,13 @@ struct LinearParams {
 };
 
 // Bounded wait; false once it ran out or another role gave up.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   constexpr int kTries = 16;                         // between two looks at the clock, which is slow to read
-  for (int i = 0; i < kTries; ++i)
-    if (mbar_try(bar, parity)) return true;
   const unsigned long long t0 = now_ns();
   while (true) {
     for (int i = 0; i < kTries; ++i)
-      if (mbar_try(bar, parity)) return true;
+      if (mbar_try<CLUSTER>(bar, parity)) return true;
     if (*abort_flag) return false;
     if (now_ns() - t0 > kLimitNs) {
       *abort_flag = 1;
@@ -86,6 +85,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
       return false;
     }
   }
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  for (int i = 0; i < 4; ++i)
+    if (mbar_try<CLUSTER>(bar, parity)) return true;
+  return wait_on<CLUSTER>(bar, parity, abort_flag);
 }
 
 // After a wait that ran out, when all roles have stopped: copies, products and their arrivals on barriers may still be under
@@ -751,7 +756,7 @@ __device__ __forceinline__ bool pair_finish(const LinearParams& l, int g, Row fi
     // a lane keeps its feature: 32 adjacent elements of a token a warp, kAt tokens at once
     const auto narrow = [&](auto plain) {
       constexpr bool PLAIN = decltype(plain)::value;
-      constexpr int kAt = AHEAD ? 2 * AHEAD : kSums ? PLAIN || SCALED ? 2 : 8 : PLAIN || SCALED ? 8 : 16;
+      constexpr int kAt = AHEAD ? (kSums ? AHEAD : 2 * AHEAD) : kSums ? PLAIN || SCALED ? 2 : 8 : PLAIN || SCALED ? 8 : 16;
       using F = Finish<TO, 1, SCALED, PLAIN>;
       const F finish(l, g, f + lane, 1);
       const Place<TO> place(l, first_row + half * kChunk, f + lane);
@@ -876,7 +881,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           else if (lane == 0)
             mbar_arrive_light(bar);
         } else {
-          if (!(ok = __all_sync(0xffffffffu, wait(&s->peer[st], phase, abort_flag)))) break;
+          if (!(ok = __all_sync(0xffffffffu, wait<true>(&s->peer[st], phase, abort_flag)))) break;
           tc_after();
           if (elect()) {
             product_block<2, MODE, E4M3>(tmem + buf * kTokens, smem_u32(stage), idesc, in > 0, live);

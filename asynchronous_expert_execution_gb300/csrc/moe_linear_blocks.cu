@@ -80,9 +80,9 @@ __device__ __forceinline__ void lay_factors(const Scales& sc, const LinearParams
 // shared memory (one of 16 bytes for four columns a warp) held a k-block of 256 x 256 to 965 cycles where the products take some 570.
 // The price is that a group's last tile is summed as if it were full.
 constexpr int kBlockRing = 160 * 1024;
-constexpr int kTileSlots = 4;
+constexpr int kTileSlots = 4, kFactorSlots = 3;
 // registers: the launch gives every thread 168; the epilogue's warps, which hold a tile's sums, take from the others
-constexpr int kLaunchRegs = 168, kFewRegs = 56, kManyRegs = 224;
+constexpr int kLaunchRegs = 168, kFewRegs = 72, kManyRegs = 216;
 static_assert(128 * kFewRegs + 256 * kManyRegs <= kPairThreads * kLaunchRegs, "the warps' registers are those of the launch");
 
 struct BlockPairParams {
@@ -92,31 +92,14 @@ struct BlockPairParams {
 
 struct BlockPairTail {
   static constexpr int kStages = kBlockRing / (2 * kABlock);
-  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], told[kTileSlots], heard[kTileSlots];
+  float factor[kFactorSlots][kBatch][2][kBM];        // of either half's features and a token
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], told[kTileSlots], heard[kTileSlots], sfull[kFactorSlots], sempty[kFactorSlots];
   int4 tile[kTileSlots];            // g, first row, rows, feature tile; no rows: there are no more
   uint32_t tmem;
   int abort_flag;
 };
 constexpr int kBlockPairSmem = kBlockRing + kStaging + (int)sizeof(BlockPairTail) + 1024;
 static_assert(kBlockPairSmem <= 227 * 1024, "shared memory of a CTA");
-
-__device__ __forceinline__ void scale16(float* acc, const float (&d)[16], float f) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j) acc[j] = fmaf(d[j], f, acc[j]);
-}
-
-// The scales of a token and of 128 features in kBatch k-blocks, asked for while those before are used.
-struct Factors {
-  const float* x;                   // null: no token
-  const float* w;                   // a k-block a lane
-  float sx[kBatch], sw;
-  __device__ __forceinline__ void ask(int left, int64_t step) {
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) sx[b] = b < left && x ? __ldg(x + b * step) : 0.f;
-    const int lane = threadIdx.x & 31;
-    sw = lane < min(kBatch, left) ? __ldg(w) : 0.f;
-  }
-};
 
 template <typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
@@ -130,7 +113,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const LinearParams& l = p.l;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
-  constexpr uint32_t kCols = 512, kAccCols = 256;
+  constexpr uint32_t kCols = 512;
   constexpr int kStage = 2 * kABlock;
 
   if (threadIdx.x == 0) {
@@ -147,6 +130,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     for (int i = 0; i < kTileSlots; ++i) {
       mbar_init(&s->told[i], 1);
       mbar_init(&s->heard[i], 8);
+    }
+    for (int i = 0; i < kFactorSlots; ++i) {
+      mbar_init(&s->sfull[i], 1);
+      mbar_init(&s->sempty[i], 8);
     }
     s->abort_flag = 0;
     mbar_init_fence();
@@ -185,41 +172,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       while (__all_sync(0xffffffffu, ok) && walk.next<kForward>(p, tl)) {
         if (!elect()) continue;
         for (int kb = 0; kb < l.nk; ++kb, ++acc) {
+          if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
+          const uint64_t a = operand_desc(smem_u32(smem + st * kStage));
           const int buf = acc & 1;
           if (!(ok = wait(&s->tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag))) break;
-          if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
           tc_after();
-          product_block<2, kForward, true>(tmem + buf * kAccCols, smem_u32(smem + st * kStage), idesc, false, kBoxRows);
+          mma_block<2, true>(tmem + buf * 2 * kBM, a, a + (kABlock >> 4), idesc, false);
           commit<2>(&s->empty[st]);
           commit<2>(&s->tfull[buf]);
           if (++st == Tail::kStages) st = 0, phase ^= 1;
         }
       }
     } else if (warp == 2) {
-      // tells the epilogue its tiles, whose registers have no room for the walk
-      bool ok = true;
+      // tells the epilogue its tiles, whose registers have no room for the walk, and pulls a tile's mul and residual into L2 while it is
+      // summed: the epilogue's reads in flight an SM then last L2's latency
       for (uint32_t n = 0, more = 1; more; ++n) {
         const int slot = n % kTileSlots;
         more = walk.next<kForward>(p, tl);
-        if (!(ok = __all_sync(0xffffffffu, wait(&s->heard[slot], ((n / kTileSlots) & 1) ^ 1, abort_flag)))) break;
+        if (!__all_sync(0xffffffffu, wait(&s->heard[slot], ((n / kTileSlots) & 1) ^ 1, abort_flag))) break;
         if (lane == 0) {
           s->tile[slot] = make_int4(tl.g, tl.row0, more ? tl.nj : 0, tl.fti);
           mbar_arrive(&s->told[slot]);
         }
         __syncwarp();
-      }
-    } else if (warp == 3 && (l.mul || l.res)) {
-      // mul and residual of a tile into L2 while it is summed: the epilogue's reads in flight an SM then last L2's latency
-      for (int n = 0; walk.next<kForward>(p, tl); ++n) {
-        const int slot = n % kTileSlots;
-        if (!__all_sync(0xffffffffu, wait(&s->told[slot], (n / kTileSlots) & 1, abort_flag))) break;
-        const int f = tl.fti * 2 * kBM, width = min(2 * kBM, l.N - f) * (int)sizeof(TO), lines = 2 * kBM * (int)sizeof(TO) / 128;
-        for (int j = rank * kBM + lane / lines; j < min(tl.nj, (rank + 1) * kBM); j += 32 / lines) {
-          const int64_t r = tl.row0 + j;
-          if (lane % lines * 128 < width) {
-            if (l.mul) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.mul) + r * l.ldmul + f) + lane % lines * 128);
-            if (l.res) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.res) + r * l.ldres + f) + lane % lines * 128);
+        if (more && (l.mul || l.res)) {
+          const int f = tl.fti * 2 * kBM, width = min(2 * kBM, l.N - f) * (int)sizeof(TO), lines = 2 * kBM * (int)sizeof(TO) / 128;
+          for (int j = rank * kBM + lane / lines; j < min(tl.nj, (rank + 1) * kBM); j += 32 / lines) {
+            const int64_t r = tl.row0 + j;
+            if (lane % lines * 128 < width) {
+              if (l.mul) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.mul) + r * l.ldmul + f) + lane % lines * 128);
+              if (l.res) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.res) + r * l.ldres + f) + lane % lines * 128);
+            }
           }
+        }
+      }
+    } else if (warp == 3) {
+      // lays the factors of the CTA's tokens and either half's features, kBatch k-blocks to a slot, whose loads are in flight together.  (Asked
+      // for by the epilogue's own threads, the loads held up their reads of TMEM: a k-block in four took twice as long.)
+      uint32_t at = 0;
+      bool ok = true;
+      while (ok && walk.next<kForward>(p, tl)) {
+        const int fb = min(tl.fti * 2, bp.s.nfb - 1), have = tl.nj - rank * kBM - lane;
+        const float* sw = bp.s.w + ((size_t)tl.g * bp.s.nfb + (lane & 1 ? min(fb + 1, bp.s.nfb - 1) : fb)) * l.nk + lane / 2;      // a half and a k-block a lane
+        const float* sx = bp.s.x + (int64_t)(tl.row0 + rank * kBM + lane) * bp.s.row;
+        for (int left = l.nk; left > 0; left -= kBatch, ++at) {
+          float v[kBatch][4];
+          const float w = lane < 2 * min(kBatch, left) ? __ldg(sw) : 0.f;
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[b][i] = b < left && 32 * i < have ? __ldg(sx + b * bp.s.block + i * 32 * bp.s.row) : 0.f;
+          sw += kBatch;
+          sx += kBatch * bp.s.block;
+          const int slot = at % kFactorSlots;
+          if (!(ok = __all_sync(0xffffffffu, wait(&s->sempty[slot], ((at / kFactorSlots) & 1) ^ 1, abort_flag)))) break;
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float f = __shfl_sync(0xffffffffu, w, 2 * b + h);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s->factor[slot][b][h][lane + 32 * i] = v[b][i] * f;
+            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s->sfull[slot]);
         }
       }
     }
@@ -228,59 +244,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..: 32 tokens; 128 features
     float* turn = reinterpret_cast<float*>(smem + kBlockRing) + (warp - 4) * kTurn;
     const uint32_t tempty0 = mapa(smem_u32(&s->tempty[0]), 0);
-    uint32_t n = 0, tiles = 0;
-    Factors fac;
-    // tile `tiles`: its first scales; false: there is none.  What else of it is needed waits in shared memory for the finish.
-    auto hear = [&]() {
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * kBM;
+    uint32_t n = 0, batch = 0;
+    for (uint32_t tiles = 0;; ++tiles) {
       const int slot = tiles % kTileSlots;
-      if (!__all_sync(0xffffffffu, wait(&s->told[slot], (tiles / kTileSlots) & 1, abort_flag))) return false;
-      const int4 tile = s->tile[slot];
-      if (tile.z == 0) return false;
-      const int j = rank * kBM + 32 * q + lane;
-      fac.w = bp.s.w + ((size_t)tile.x * bp.s.nfb + min(tile.w * 2 + half, bp.s.nfb - 1)) * l.nk + lane;
-      fac.x = j < tile.z ? bp.s.x + (int64_t)(tile.y + j) * bp.s.row : nullptr;
-      fac.ask(l.nk, bp.s.block);
-      return true;
-    };
-    bool more = hear();
-    while (more) {
+      if (!__all_sync(0xffffffffu, wait(&s->told[slot], (tiles / kTileSlots) & 1, abort_flag))) break;
+      const volatile int4* tile = &s->tile[slot];
+      if (tile->z == 0) break;
       float acc[kBM];
 #pragma unroll
       for (int j = 0; j < kBM; ++j) acc[j] = 0.f;
       uint32_t d0 = 0;
       bool ok = true;
-      for (int kb = 0; kb < l.nk; kb += kBatch) {
-        float f[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) f[b] = fac.sx[b] * __shfl_sync(0xffffffffu, fac.sw, b);
-        if (fac.x) fac.x += kBatch * bp.s.block;
-        fac.w += kBatch;
-        fac.ask(l.nk - kb - kBatch, bp.s.block);
-#pragma unroll 1
-        for (int b = 0; b < min(kBatch, l.nk - kb); ++b, ++n) {
+      // Few instructions: what a k-block costs beside its multiply-adds, two warps of a scheduler do not hide.
+      for (int left = l.nk; left > 0; left -= kBatch, ++batch) {
+        const int from = batch % kFactorSlots;
+        if (!(ok = __all_sync(0xffffffffu, wait(&s->sfull[from], (batch / kFactorSlots) & 1, abort_flag)))) break;
+        const float* factor = &s->factor[from][0][half][32 * q + lane];
+        for (int end = left - min(kBatch, left), at = left; at > end; --at, ++n, factor += 2 * kBM) {
           const int buf = n & 1;
           if (!(ok = __all_sync(0xffffffffu, wait(&s->tfull[buf], (n >> 1) & 1, abort_flag)))) break;
           tc_after();
-          d0 = tmem + ((uint32_t)(32 * q) << 16) + buf * kAccCols + half * kBM;
-          // 16 columns are asked for while those before are added
-          float d[2][16];
-          tmem_ask16(d0, d[0]);
+          d0 = lanes + buf * 2 * kBM;
+          const float f = *factor;
 #pragma unroll
-          for (int c = 0; c < kBM / 16; ++c) {
-            tmem_wait(d[c & 1]);
-            if (c + 1 < kBM / 16) tmem_ask16(d0 + 16 * (c + 1), d[(c + 1) & 1]);
+          for (int c = 0; c < kBM; c += 32) {
+            float d[32];
+            tmem_ld32(d0 + c, d);
             // the buffer is the next k-block's but one's, unless it is the last: then the sums go there
-            if (c + 1 == kBM / 16 && kb + b + 1 < l.nk) {
+            if (c + 32 == kBM && at > 1) {
               tc_before();
-              __syncwarp();
               if (lane == 0) mbar_arrive_relaxed(tempty0 + buf * 8);
             }
-            scale16(acc + 16 * c, d[c & 1], f[0]);
-          }
 #pragma unroll
-          for (int i = 0; i + 1 < kBatch; ++i) f[i] = f[i + 1];
+            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(d[j], f, acc[c + j]);
+          }
         }
         if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->sempty[from]);
       }
       if (!ok) break;
       // the sums go to the last k-block's buffer, which this warp has read: the registers are the finish's
@@ -291,13 +293,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int j = 0; j < 16; ++j) v[j] = acc[c + j];
         tmem_st16(d0 + c, v);
       }
-      const int slot = tiles++ % kTileSlots;
-      more = hear();
-      const int4 tile = s->tile[slot];
-      const int first = rank * kBM + 32 * q, f0 = (tile.w * 2 + half) * kBM;
+      const int g = tile->x, first = rank * kBM + 32 * q, row = tile->y + first, f0 = (tile->w * 2 + half) * kBM, rows = tile->z - first;
 #pragma unroll 1
-      for (int i = 0; i < kBM && f0 + i < l.N && first < tile.z; i += 32)
-        pair_finish<TO, false, sizeof(TO) == 2 ? 2 : 1>(l, tile.x, tile.y + first, f0 + i, min(32, tile.z - first), 0, turn, [&](auto body) {
+      for (int i = 0; i < kBM && f0 + i < l.N && rows > 0; i += 32)
+        pair_finish<TO, false, 2>(l, g, row, f0 + i, min(32, rows), 0, turn, [&](auto body) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float v[16];
