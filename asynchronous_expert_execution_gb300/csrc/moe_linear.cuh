@@ -508,31 +508,45 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
       if (++st == p.stages) st = 0, phase ^= 1;
     }
   } else if (MODE == kWeightGrad && nj > 0 && warp == 1) {
-    // the whole warp, which clears what the last k-block holds behind the group's end
     const uint32_t idesc = mma_desc<E4M3, true, true>(kBM, p.bn);
+    // this rank's k-blocks, the group's last one with what lies behind its end cleared by the whole warp
+    const int live = sum.n - (nk - 1) * kBoxRows, last = kb1 == nk && kb1 > kb0 && live % 16 ? 1 : 0;
     bool ok = true;
     uint32_t st = 0, phase = 0;
-    int kb = kb0;
-    for (int chunk = 0; chunk < chunks && ok; ++chunk) {
-      const int n = (kb1 - kb0) * (chunk + 1) / chunks - (kb1 - kb0) * chunk / chunks;
-      for (int i = 0; i < n; ++i, ++kb) {
-        if (!(ok = __all_sync(0xffffffffu, wait(&s->full[st], phase, abort_flag)))) break;
-        uint8_t* stage = smem + st * stage_bytes;
-        int live = kBoxRows;
-        if (kb == nk - 1) {
-          live = sum.n - kb * kBoxRows;
-          if (live % 16) clear_rows(stage, 2 + p.bn / 64, live);
-        }
-        tc_after();
+    int chunk = 0, i = 0;                            // block i of the chunk
+    const auto block = [&](int rows) {
+      uint8_t* stage = smem + st * stage_bytes;
+      tc_after();
+      product_block<1, MODE, E4M3>(tmem + chunk * p.bn, smem_u32(stage), idesc, i > 0, rows);
+      commit<1>(&s->empty[st]);
+    };
+    const auto next = [&] {
+      if (++st == p.stages) st = 0, phase ^= 1;
+      if (++i == (kb1 - kb0) * (chunk + 1) / chunks - (kb1 - kb0) * chunk / chunks) ++chunk, i = 0;
+    };
+    if (elect()) {
+      for (int kb = kb0; kb < kb1 - last; ++kb) {
+        if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
+        block(kBoxRows);
+        next();
+      }
+      if (ok && !last) commit<1>(&s->done);
+    }
+    __syncwarp();
+    if (last) {
+      const int src = __ffs(__ballot_sync(0xffffffffu, i > 0 || chunk > 0 || st > 0)) - 1;      // the lane that issued, if one did
+      if (src >= 0) {
+        st = __shfl_sync(0xffffffffu, st, src), phase = __shfl_sync(0xffffffffu, phase, src);
+        chunk = __shfl_sync(0xffffffffu, chunk, src), i = __shfl_sync(0xffffffffu, i, src);
+      }
+      if (__all_sync(0xffffffffu, ok) && __all_sync(0xffffffffu, wait(&s->full[st], phase, abort_flag))) {
+        clear_rows(smem + st * stage_bytes, 2 + p.bn / 64, live);
         if (elect()) {
-          product_block<1, MODE, E4M3>(tmem + chunk * p.bn, smem_u32(stage), idesc, i > 0, live);
-          commit<1>(&s->empty[st]);
+          block(live);
+          commit<1>(&s->done);
         }
-        __syncwarp();
-        if (++st == p.stages) st = 0, phase ^= 1;
       }
     }
-    if (ok && elect()) commit<1>(&s->done);
   } else if (nj > 0 && warp == 1 && elect()) {
     const uint32_t idesc = mma_desc<E4M3, MODE != kForward>(kBM, p.bn);
     bool ok = true;
@@ -614,11 +628,26 @@ constexpr int kPairThreads = 384;                    // warps: TMA, MMA, TMEM, s
 constexpr int kChunk = 32;                           // tokens an epilogue warp turns at a time
 constexpr int kTurn = kChunk * 32;                   // floats: 32 tokens x 32 features
 constexpr int kStaging = 8 * kTurn * 4;
+// kWeightGrad: half a tile's tokens for 32 features a warp, which leave in one box
+constexpr int kBoxStaging = 2 * kStaging;
+constexpr int pair_ring(int mode) { return mode == kWeightGrad ? kPairRing + kStaging - kBoxStaging : kPairRing; }
+template <typename TO> constexpr int kBoxTokens = kPairTokens<TO> / 2;
+static_assert(kBoxTokens<float> * 32 * 4 * 8 == kBoxStaging && kBoxTokens<__nv_bfloat16> * 32 * 2 * 8 == kBoxStaging, "a box a warp");
+
+// Quotients by a number that the host knows: a division takes some 120 cycles, and every role of a CTA walks its tiles by itself.
+struct Divide {
+  uint32_t d, magic;                // floor(2^32 / d) + 1: exact while n d < 2^32; 0: d is one, or not small enough
+  static Divide by(int64_t d, int64_t most) { return {(uint32_t)d, d > 1 && d * most < (1ll << 32) ? (uint32_t)((1ll << 32) / d + 1) : 0}; }
+  __device__ __forceinline__ int operator()(int n) const { return magic ? (int)__umulhi((uint32_t)n, magic) : n / (int)d; }
+};
 
 struct PairParams {
   CUtensorMap w, x[4];              // x: boxes of 16, 32, 64 and tokens / 2 rows
   LinearParams l;
-  int nft;                          // feature tiles of 256
+  CUtensorMap y;                    // kWeightGrad, boxed: the result, boxes of half a tile's rows x 32 features
+  bool boxed;
+  Divide by_band, by_last;          // kWeightGrad: eight token tiles' feature tiles; the token tiles behind the last eight
+  int nft, ntt;                     // feature tiles of 256; kWeightGrad: token tiles a group
   int tokens;                       // of a tile, a multiple of 32
   int stages, stage_bytes;          // of the ring: a k-block of a full tile each
 };
@@ -626,7 +655,10 @@ struct PairParams {
 struct PairTail {
   static constexpr int kMaxStages = 10;
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[4], tempty[4];
-  uint64_t peer[kMaxStages];        // kWeightGrad, at the leader: the other CTA's k-block is in place
+  // kWeightGrad: this CTA's part of a k-block that has to be cleared, and the tiles that a warp tells the others
+  static constexpr int kTold = 4;
+  uint64_t own[kMaxStages], told[kTold], heard[kTold];
+  int4 tile[kTold][2];
   uint32_t tmem;
   int abort_flag;
   int finishing;                    // tiles whose epilogue has begun
@@ -646,29 +678,30 @@ struct PairWalk {
   int pass = 0;
   __device__ __forceinline__ PairWalk() : at(blockIdx.x / 2) {}
 
-  // kWeightGrad: all groups have the same tiles, and sums of different lengths
+  // kWeightGrad: all groups have the same tiles, and sums of different lengths.  at.g0: the group; at.want: the tile in it.
   __device__ __forceinline__ bool next_weight(const PairParams& p, PairTile& tl) {
-    const int ntt = (p.l.T + p.tokens - 1) / p.tokens, per = ntt * p.nft;
-    for (; at.want < per * p.l.G; at.want += gridDim.x / 2) {
-      tl.g = at.want / per;
-      const Span sp = group_rows(p.l, tl.g, p.l.F);
-      if (sp.n == 0 && p.l.res) continue;            // nothing to add
-      int local = at.want - tl.g * per;
-      const int band = local / (8 * p.nft);
-      local -= band * 8 * p.nft;
-      const int width = min(8, ntt - 8 * band);
-      tl.fti = local / width;
-      tl.row0 = (8 * band + local % width) * p.tokens;
-      tl.nj = min(p.tokens, p.l.T - tl.row0);
-      tl.nmma = p.tokens;
-      tl.brows = p.tokens / 2;
-      tl.sum0 = sp.a;
-      tl.sum = sp.n;
-      tl.nk = (sp.n + kBoxRows - 1) / kBoxRows;
-      at.want += gridDim.x / 2;
-      return true;
+    const int ntt = p.ntt, per = ntt * p.nft;
+    while (true) {
+      const int before = at.g0;
+      if (at.g0 < 0) at.g0 = 0;
+      for (; at.want >= per; at.want -= per) ++at.g0;
+      if (at.g0 >= p.l.G) return false;
+      if (at.g0 != before) at.sp = group_rows(p.l, at.g0, p.l.F);
+      if (at.sp.n > 0 || !p.l.res) break;
+      at.want += gridDim.x / 2;                      // nothing to add
     }
-    return false;
+    tl.g = at.g0;
+    const int band = p.by_band(at.want), in = at.want - band * 8 * p.nft, width = min(8, ntt - 8 * band);
+    tl.fti = width == 8 ? in >> 3 : p.by_last(in);
+    tl.row0 = (8 * band + in - tl.fti * width) * p.tokens;
+    tl.nj = min(p.tokens, p.l.T - tl.row0);
+    tl.nmma = p.tokens;
+    tl.brows = p.tokens / 2;
+    tl.sum0 = at.sp.a;
+    tl.sum = at.sp.n;
+    tl.nk = (at.sp.n + kBoxRows - 1) / kBoxRows;
+    at.want += gridDim.x / 2;
+    return true;
   }
 
   // by whole warps
@@ -790,6 +823,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  constexpr bool kAcross = MODE == kWeightGrad;
+  constexpr int kRing = pair_ring(MODE);
   PairTail* s = reinterpret_cast<PairTail*>(smem + kPairRing + kStaging);
   volatile int* abort_flag = &s->abort_flag;
   const LinearParams& l = p.l;
@@ -797,21 +832,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int rank = (int)cluster_rank();
   constexpr int kTokens = kPairTokens<TO>, kAccs = sizeof(TO) == 4 ? 3 : 2;
   constexpr uint32_t kCols = 512;
-  constexpr bool kAcross = MODE == kWeightGrad;
   const int chunk = sizeof(TO) == 4 ? kChunkBlocks : INT32_MAX; // k-blocks summed in one accumulator
 
   if (threadIdx.x == 0) {
     prefetch_map(&p.w);
     prefetch_map(&p.x[3]);
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&s->full[i], 1);                     // the leader's producer, for both CTAs' bytes (kWeightGrad: each CTA's for its own)
+      // the leader's producer, for both CTAs' bytes (kWeightGrad: twice, or either CTA's clearing warp)
+      mbar_init(&s->full[i], kAcross ? 2 : 1);
       mbar_init(&s->empty[i], 1);                    // the MMA's commit, in both CTAs
-      if (kAcross) mbar_init(&s->peer[i], 1);
+      if (kAcross) mbar_init(&s->own[i], 1);
     }
     for (int b = 0; b < kAccs; ++b) {
       mbar_init(&s->tfull[b], 1);
       mbar_init(&s->tempty[b], 16);                  // the epilogue warps of both CTAs, at the leader
     }
+    if (kAcross)
+      for (int i = 0; i < PairTail::kTold; ++i) {
+        mbar_init(&s->told[i], 1);
+        mbar_init(&s->heard[i], rank == 0 ? 11 : 10);              // all warps but the telling one and the second CTA's idle one
+      }
     s->abort_flag = 0;
     s->finishing = 0;
     mbar_init_fence();
@@ -824,13 +864,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_after();
   const uint32_t tmem = s->tmem;
   PairWalk walk;
-  PairTile tl;
+  PairTile tl = {};
   constexpr int kElems = E4M3 ? kBKBytes : kBKBytes / 2;
+  // The next tile.  kWeightGrad: as a warp tells it, for tiles may be a few k-blocks long and a walk's step takes a role 1,000 cycles.
+  uint32_t tiles_heard = 0;
+  const auto next_tile = [&]() {
+    if constexpr (!kAcross) {
+      return walk.template next<MODE>(p, tl);
+    } else {
+      const int slot = tiles_heard % PairTail::kTold;
+      if (!__all_sync(0xffffffffu, wait(&s->told[slot], (tiles_heard / PairTail::kTold) & 1, abort_flag))) return false;
+      ++tiles_heard;
+      const int4 t = s->tile[slot][0], u = s->tile[slot][1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s->heard[slot]);
+      tl.g = t.x, tl.row0 = t.y, tl.nj = t.z, tl.fti = t.w, tl.sum0 = u.x, tl.sum = u.y, tl.nk = u.z;
+      tl.nmma = p.tokens, tl.brows = p.tokens / 2;
+      return tl.nj > 0;
+    }
+  };
+  // mul and residual of this CTA's i-th tile into L2 while the tile before is finished: the epilogue's 16 KB of
+  // reads in flight an SM then last L2's latency (4096 x 512 x 7168 with mul: 50 -> 45 us)
+  const auto prefetch = [&](int i) {
+    volatile int* finishing = &s->finishing;
+    const unsigned long long t0 = now_ns();
+    while (!kAcross && *finishing < i && !*abort_flag && now_ns() - t0 < kLimitNs) __nanosleep(200);
+    const int f = tl.fti * 2 * kBM + rank * kBM, n = min(kBM, l.N - f) * (int)sizeof(TO), lines = kBM * (int)sizeof(TO) / 128;
+    for (int j = lane / lines; j < tl.nj; j += 32 / lines) {
+      const int64_t r = (kAcross ? (int64_t)tl.g * l.T : 0) + tl.row0 + j;
+      if (lane % lines * 128 < n) {
+        if (l.mul) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.mul) + r * l.ldmul + f) + lane % lines * 128);
+        if (l.res) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.res) + r * l.ldres + f) + lane % lines * 128);
+      }
+    }
+  };
 
   if (warp == 0) {
     uint32_t st = 0, phase = 1;
     bool ok = true;
-    while (__all_sync(0xffffffffu, ok) && walk.template next<MODE>(p, tl)) {
+    while (__all_sync(0xffffffffu, ok) && next_tile()) {
       if (!elect()) continue;
       const int block = kABlock + tl.brows * kBKBytes;
       const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
@@ -838,8 +910,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int kb = 0; kb < nk; ++kb) {
         if (!(ok = wait(&s->empty[st], phase, abort_flag))) break;
         const uint32_t a = smem_u32(smem + st * p.stage_bytes);
-        const uint32_t bar = kAcross ? smem_u32(&s->full[st]) : mapa(smem_u32(&s->full[st]), 0);
-        if (kAcross || rank == 0) mbar_expect(&s->full[st], kAcross ? block : 2 * block);
+        const bool clear = kAcross && kb == nk - 1 && tl.sum % 16;
+        const uint32_t bar = clear ? smem_u32(&s->own[st]) : mapa(smem_u32(&s->full[st]), 0);
+        if (clear) {
+          mbar_expect(&s->own[st], block);
+        } else if (rank == 0) {
+          if (kAcross) mbar_arrive(&s->full[st]);
+          mbar_expect(&s->full[st], 2 * block);
+        }
         load_a<2, MODE, E4M3>(a, &p.w, bar, kb, wrow, tl.g, kAcross ? tl.sum0 : 0);
         if constexpr (kAcross)
           load_across<2>(a + kABlock, &p.x[0], bar, kb, xrow, tl.brows, tl.sum0);
@@ -848,60 +926,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (++st == p.stages) st = 0, phase ^= 1;
       }
     }
-  } else if (kAcross && warp == 1) {
-    // Each CTA's own k-blocks land on its own barrier, so that it can clear what the last one holds behind the group's end;
-    // the second CTA then tells the first, whose warp issues the products.
-    uint32_t st = 0, phase = 0, acc = 0;
-    bool ok = true;
-    const uint32_t idesc = mma_desc<E4M3, true, true>(2 * kBM, p.tokens);
-    while (ok && walk.template next<MODE>(p, tl)) {
-      int buf = 0;
-      for (int kb = 0, in = chunk; kb < tl.nk; ++kb, ++in) {
-        if (in == chunk) {
-          if (rank == 0) {
-            if (kb > 0 && elect()) commit<2>(&s->tfull[buf]);
-            __syncwarp();
-            buf = acc % kAccs;
-            if (!(ok = __all_sync(0xffffffffu, wait(&s->tempty[buf], ((acc / kAccs) & 1) ^ 1, abort_flag)))) break;
-            ++acc;
-          }
-          in = 0;
-        }
-        if (!(ok = __all_sync(0xffffffffu, wait(&s->full[st], phase, abort_flag)))) break;
-        uint8_t* stage = smem + st * p.stage_bytes;
-        int live = kBoxRows;
-        if (kb == tl.nk - 1) {
-          live = tl.sum - kb * kBoxRows;
-          if (live % 16) clear_rows(stage, 2 + tl.brows / 64, live);
-        }
-        if (rank == 1) {
-          const uint32_t bar = mapa(smem_u32(&s->peer[st]), 0);
-          if (lane == 0 && live % 16)
-            mbar_arrive_cluster(bar);                // behind the zeros
-          else if (lane == 0)
-            mbar_arrive_light(bar);
-        } else {
-          if (!(ok = __all_sync(0xffffffffu, wait<true>(&s->peer[st], phase, abort_flag)))) break;
-          tc_after();
-          if (elect()) {
-            product_block<2, MODE, E4M3>(tmem + buf * kTokens, smem_u32(stage), idesc, in > 0, live);
-            commit<2>(&s->empty[st]);
-          }
-          __syncwarp();
-        }
-        if (++st == p.stages) st = 0, phase ^= 1;
+  } else if (kAcross && warp == 2) {
+    // A group's last k-block lands on each CTA's own barrier, if it ends inside 16 rows: what lies behind the end is cleared, and both
+    // CTAs tell the leader's barrier.
+    uint32_t at = 0, phases = 0;                     // k-blocks before; the stages' phases
+    while (next_tile()) {
+      at = (at + tl.nk) % p.stages;
+      if (tl.sum % 16 == 0) continue;
+      const uint32_t st = (at + p.stages - 1) % p.stages;
+      if (!__all_sync(0xffffffffu, wait(&s->own[st], phases >> st & 1, abort_flag))) break;
+      phases ^= 1u << st;
+      clear_rows(smem + st * p.stage_bytes, 2 + tl.brows / 64, tl.sum - (tl.nk - 1) * kBoxRows);
+      if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&s->full[st]), 0));
+    }
+  } else if (kAcross && warp == 3) {
+    bool more = true;
+    for (uint32_t n = 0; more; ++n) {
+      const int slot = n % PairTail::kTold;
+      more = walk.template next<MODE>(p, tl);
+      if (!__all_sync(0xffffffffu, wait(&s->heard[slot], ((n / PairTail::kTold) & 1) ^ 1, abort_flag))) break;
+      if (lane == 0) {
+        s->tile[slot][0] = make_int4(tl.g, tl.row0, more ? tl.nj : 0, tl.fti);
+        s->tile[slot][1] = make_int4(tl.sum0, tl.sum, tl.nk, 0);
+        mbar_arrive(&s->told[slot]);
       }
-      if (ok && rank == 0 && tl.nk > 0 && elect()) commit<2>(&s->tfull[buf]);
       __syncwarp();
+      if (more && l.res && !p.boxed) prefetch(0);
     }
   } else if (warp == 1 && rank == 0) {
     uint32_t st = 0, phase = 0, acc = 0;
     bool ok = true;
-    while (__all_sync(0xffffffffu, ok) && walk.template next<MODE>(p, tl)) {
+    while (__all_sync(0xffffffffu, ok) && next_tile()) {
       if (!elect()) continue;
-      const uint32_t idesc = mma_desc<E4M3, MODE != kForward>(2 * kBM, tl.nmma);
+      const uint32_t idesc = mma_desc<E4M3, MODE != kForward, kAcross>(2 * kBM, tl.nmma);
       int buf = 0;
-      for (int kb = 0, in = chunk; kb < l.nk; ++kb, ++in) {      // in: k-blocks in this accumulator
+      const int nk = kAcross ? tl.nk : l.nk;
+      for (int kb = 0, in = chunk; kb < nk; ++kb, ++in) {        // in: k-blocks in this accumulator
         if (in == chunk) {
           if (kb > 0) commit<2>(&s->tfull[buf]);
           buf = acc % kAccs;
@@ -910,35 +970,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           ++acc;
           in = 0;
         }
-        if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
+        const bool last = kAcross && kb == nk - 1;
+        if (!(ok = last ? wait<true>(&s->full[st], phase, abort_flag) : wait(&s->full[st], phase, abort_flag))) break;
         tc_after();
-        product_block<2, MODE, E4M3>(tmem + buf * kTokens, smem_u32(smem + st * p.stage_bytes), idesc, in > 0, kBoxRows);
+        product_block<2, MODE, E4M3>(tmem + buf * kTokens, smem_u32(smem + st * p.stage_bytes), idesc, in > 0,
+                                     last ? tl.sum - kb * kBoxRows : kBoxRows);
         commit<2>(&s->empty[st]);
         if (++st == p.stages) st = 0, phase ^= 1;
       }
-      if (ok) commit<2>(&s->tfull[buf]);
+      if (ok && nk > 0) commit<2>(&s->tfull[buf]);
     }
   } else if (warp == 3 && (l.mul || l.res)) {
-    // mul and residual of a tile into L2 while the tile before is finished: the epilogue's 16 KB of
-    // reads in flight an SM then last L2's latency (4096 x 512 x 7168 with mul: 50 -> 45 us)
-    volatile int* finishing = &s->finishing;
-    for (int i = 0; walk.template next<MODE>(p, tl); ++i) {
-      const unsigned long long t0 = now_ns();
-      while (*finishing < i && !*abort_flag && now_ns() - t0 < kLimitNs) __nanosleep(200);
-      const int f = tl.fti * 2 * kBM + rank * kBM, n = min(kBM, l.N - f) * (int)sizeof(TO), lines = kBM * (int)sizeof(TO) / 128;
-      for (int j = lane / lines; j < tl.nj; j += 32 / lines) {
-        const int64_t r = (kAcross ? (int64_t)tl.g * l.T : 0) + tl.row0 + j;
-        if (lane % lines * 128 < n) {
-          if (l.mul) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.mul) + r * l.ldmul + f) + lane % lines * 128);
-          if (l.res) prefetch_l2(reinterpret_cast<const char*>(static_cast<const TO*>(l.res) + r * l.ldres + f) + lane % lines * 128);
-        }
-      }
-    }
+    for (int i = 0; next_tile(); ++i) prefetch(i);
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..; two warps share a quarter's columns
-    float* turn = reinterpret_cast<float*>(smem + kPairRing) + (warp - 4) * kTurn;
+    float* turn = reinterpret_cast<float*>(smem + kRing + (warp - 4) * (kAcross ? kBoxStaging / 8 : kTurn * 4));
     uint32_t acc = 0;
-    // a warp's tokens: every other block of 32
+    // a warp's tokens: every other block of 32, or for boxes the tile's first or second half
     constexpr bool kSums = sizeof(TO) == 4;
     constexpr int kStep = 2 * kChunk;
     auto acc_wait = [&](int buf, uint32_t n) {
@@ -950,17 +998,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     auto acc_done = [&](int buf) {
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&s->tempty[buf]), 0));
+      if (lane == 0) mbar_arrive_relaxed(mapa(smem_u32(&s->tempty[buf]), 0));
     };
-    // `body(c)` for each of this warp's blocks of the tile, the block's sums in `turn`; false: a wait ran out
-    auto blocks = [&](auto body) {
+    // `take(c, v)` for every 16 of this warp's tokens of the tile, from token c on; false: a wait ran out
+    auto boxes = [&](auto halves, auto take) {
+      constexpr bool HALVES = decltype(halves)::value;
+      const int c0 = half * (HALVES ? kTokens / 2 : kChunk), c1 = HALVES ? min(tl.nj, c0 + kTokens / 2) : tl.nj;
+      const auto next = [](int c) { return HALVES || c % kChunk == 0 ? c + 16 : c + kStep - 16; };
       const uint32_t d0 = tmem + ((uint32_t)(32 * q) << 16), sum = d0 + kAccs * kTokens;
       const int chunks = kSums ? ((kAcross ? tl.nk : l.nk) + chunk - 1) / chunk : 1;
       const bool some = !kAcross || tl.nk > 0;                 // else the sums are of no rows: zeros
       for (int ch = 0; ch + 1 < chunks; ++ch, ++acc) {         // all but the last chunk: into the sum's columns
         const int buf = acc % kAccs;
         if (!acc_wait(buf, acc)) return false;
-        for (int c = half * kChunk; c < tl.nj; c += c % kChunk ? kStep - 16 : 16) {
+        for (int c = c0; c < c1; c = next(c)) {
           float v[16];
           tmem_ld16(d0 + buf * kTokens + c, v);
           if (ch > 0) {
@@ -978,7 +1029,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!acc_wait(buf, acc)) return false;
         ++acc;
       }
-      for (int c = half * kChunk; c < tl.nj; c += kStep) {
+      for (int c = c0; c < c1; c += HALVES ? 2 * 16 : kStep) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float v[16] = {};
@@ -989,23 +1040,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] += o[j];
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) turn[(16 * h + j) * 32 + (lane ^ ((j & 7) << 2))] = v[j];
+          take(c + 16 * h, v);
         }
-        __syncwarp();
-        body(c - half * kChunk);
-        __syncwarp();
       }
       if (some) acc_done(buf);
       return true;
     };
-    for (int tiles = 1; walk.template next<MODE>(p, tl); ++tiles) {
+    for (int tiles = 1; next_tile(); ++tiles) {
       if (threadIdx.x == 128) *reinterpret_cast<volatile int*>(&s->finishing) = tiles;
       const int f = tl.fti * 2 * kBM + rank * kBM + 32 * q;
       const auto first_row = (kAcross ? (long long)tl.g * l.T : 0) + tl.row0;
-      const bool ok = pair_finish<TO, E4M3>(l, tl.g, first_row, f, tl.nj, half, turn, blocks);
+      bool ok;
+      if (kAcross && p.boxed) {
+        // A warp's sums leave by TMA in one box, which leaves out what lies outside, and adds in fp32 where that is asked for.  (Through
+        // registers, as below, a tile of 256 x 128 in fp32 took 3.5 us.)
+        TO* box = reinterpret_cast<TO*>(turn);
+        if (lane == 0) store_wait_read<0>();         // the tile before
+        __syncwarp();
+        const int c0 = half * (kTokens / 2);
+        ok = boxes(std::true_type{}, [&](int c, const float (&v)[16]) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) box[(c - c0 + j) * 32 + lane] = from_f<TO>(v[j]);
+        });
+        fence_async();
+        __syncwarp();
+        if (lane == 0 && ok && f < l.N && c0 < tl.nj) {
+          if (sizeof(TO) == 4 && l.res)
+            tma_store_3d<true>(&p.y, smem_u32(box), f, tl.row0 + c0, tl.g);
+          else
+            tma_store_3d<false>(&p.y, smem_u32(box), f, tl.row0 + c0, tl.g);
+          store_commit();
+        }
+      } else {
+        ok = pair_finish<TO, E4M3>(l, tl.g, first_row, f, tl.nj, half, turn, [&](auto body) {
+          return boxes(std::false_type{}, [&](int c, const float (&v)[16]) {
+            const int h = c / 16 % 2;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) turn[(16 * h + j) * 32 + (lane ^ ((j & 7) << 2))] = v[j];
+            if (h == 0) return;
+            __syncwarp();
+            body(c - 16 - half * kChunk);
+            __syncwarp();
+          });
+        });
+      }
       if (!ok) break;
     }
+    if (kAcross && lane == 0) store_wait_all();
   }
   __syncwarp();
   tc_before();
@@ -1042,6 +1123,19 @@ bool encode(CUtensorMap* m, const void* base, int size, int width, int rows, int
   return fn(m, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups > 0 ? 3 : 2,
             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [groups][rows][width] results, boxes of kBoxTokens rows x 32 elements without swizzle.
+template <typename TO>
+bool encode_result(CUtensorMap* m, void* base, int width, int rows, int64_t ld, int groups) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)groups};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * sizeof(TO), (cuuint64_t)ld * sizeof(TO) * rows};
+  const cuuint32_t box[3] = {32, kBoxTokens<TO>, 1}, step[3] = {1, 1, 1};
+  return fn(m, sizeof(TO) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 int sm_count() {

@@ -21,8 +21,11 @@ moe_status launch_pair(PairParams& p, const LinearParams& l, int tokens, int sms
   p.l = l;
   p.nft = (l.N + 2 * kBM - 1) / (2 * kBM);
   p.tokens = tokens;
+  p.ntt = (l.T + tokens - 1) / tokens;
+  p.by_band = Divide::by(8 * p.nft, (int64_t)p.ntt * p.nft);
+  p.by_last = Divide::by(std::max(1, p.ntt % 8), 8 * p.nft);
   p.stage_bytes = kABlock + tokens / 2 * kBKBytes;
-  p.stages = std::min(PairTail::kMaxStages, kPairRing / p.stage_bytes);
+  p.stages = std::min(PairTail::kMaxStages, pair_ring(MODE) / p.stage_bytes);
   if (cudaFuncSetAttribute(linear_pair_kernel<false, TO, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return MOE_ERR_CUDA;
   return launch_op(linear_pair_kernel<false, TO, MODE>, dim3(sms / 2 * 2), kPairThreads, kSmem, 1, s, p);
@@ -77,6 +80,9 @@ moe_status weight_grad(const Args* a, const void* grad, int64_t grad_stride, int
   PairParams p;
   if (!encode(&p.w, a->d_x, 2, a->fan_in, a->rows, a->x_stride, 0, kBoxRows) || !encode(&p.x[0], grad, 2, a->fan_out, a->rows, grad_stride, 0, kBoxRows))
     return MOE_ERR_CUDA;
+  // by boxes, unless rows start off 16-byte boundaries, or what is added to would be rounded twice
+  p.boxed = wide && !(a->accumulate && sizeof(TO) == 2);
+  if (p.boxed && !encode_result<TO>(&p.y, a->d_grad_w, a->fan_in, a->fan_out, a->grad_w_stride, l.G)) return MOE_ERR_CUDA;
   return launch_pair<TO, kWeightGrad>(p, l, tokens, sms, s);
 }
 
