@@ -519,28 +519,35 @@ __device__ __forceinline__ float block_scale(uint32_t bits, float& inverse) {
   return scale;
 }
 
-// 8 elements of a row from column c; those at `width` and behind are zeros.  WIDE: in 16-byte units.
-template <typename T, bool WIDE>
-__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t width, float (&v)[8]) {
-  if constexpr (WIDE) {
-    constexpr int N = Vec<T>::N;
+// 8 elements of a row from column c, as they lie in memory; those at `width` and behind are zeros.  WIDE: in 16-byte units.
+template <typename T, bool WIDE> struct Eight {
+  T v[8];
+  __device__ __forceinline__ void load(const T* row, int64_t c, int64_t width) {
 #pragma unroll
-    for (int i = 0; i < 8; i += N) {
-      float t[N];
-      if (c + i < width) {
-        unpack16<T>(__ldg(reinterpret_cast<const uint4*>(row + c + i)), t);
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) t[j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[i + j] = t[j];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < width ? to_f(row[c + i]) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = c + i < width ? row[c + i] : from_f<T>(0.f);
   }
-}
+  __device__ __forceinline__ void get(float (&t)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = to_f(v[i]);
+  }
+};
+template <typename T> struct Eight<T, true> {
+  static constexpr int N = Vec<T>::N;
+  uint4 v[8 / N];
+  __device__ __forceinline__ void load(const T* row, int64_t c, int64_t width) {
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) v[i] = c < width ? __ldg(reinterpret_cast<const uint4*>(row + c) + i) : make_uint4(0, 0, 0, 0);   // width: a multiple of 8
+  }
+  __device__ __forceinline__ void get(float (&t)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) {
+      float u[N];
+      unpack16<T>(v[i], u);
+#pragma unroll
+      for (int j = 0; j < N; ++j) t[i * N + j] = u[j];
+    }
+  }
+};
 template <bool WIDE>
 __device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t width, const float (&v)[8]) {
   if constexpr (WIDE) {
@@ -571,56 +578,61 @@ template <typename T> struct QuantParams {
   int blocks;                       // of 128 columns
 };
 
-// 1 x 128: sixteen lanes take a block of a row, 8 elements each; a thread asks for kU blocks before it uses the first.
+// 1 x 128: sixteen lanes take a block of a row, 8 elements each; a thread asks for kU blocks before it uses the first.  A block of
+// threads takes kU * 16 blocks of 128 side by side of kRows rows, so that neither needs a division; the scales of a column of blocks,
+// whose rows lie side by side, are written kRows at a time.
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams<T> p) {
-  constexpr int kU = 4;
+  constexpr int kU = 4, kRows = 4;                   // blocks of a thread; rows of a block of threads
   ops_begin();
   const int sub = threadIdx.x / 16, at = threadIdx.x % 16 * 8;
-  const int64_t total = p.rows * p.blocks, first = (int64_t)blockIdx.x * 16 * kU + sub;
-  float v[kU][8];
-  int64_t row[kU];
-  int col[kU];
+  const int64_t row = (int64_t)blockIdx.y * kRows + sub % kRows + (int64_t)blockIdx.z * 65535 * kRows;
+  const int first = blockIdx.x * (kU * 16 / kRows) + sub / kRows;
+  Eight<T, WIDE> x[kU];
+  if (row < p.rows) {
 #pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const int64_t i = first + u * 16;
-    row[u] = i / p.blocks;
-    col[u] = (int)(i - row[u] * p.blocks);
-    if (i < total) load8<T, WIDE>(p.x.at(row[u]), (int64_t)col[u] * kQuantBlock + at, p.width, v[u]);
+    for (int u = 0; u < kU; ++u)
+      if (first + u * (16 / kRows) < p.blocks) x[u].load(p.x.at(row), (int64_t)(first + u * (16 / kRows)) * kQuantBlock + at, p.width);
   }
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
-    const bool on = first + u * 16 < total;
-    uint32_t m = on ? largest(v[u]) : 0;
+    const int col = first + u * (16 / kRows);
+    const bool on = row < p.rows && col < p.blocks;
+    float v[8];
+    x[u].get(v);
+    uint32_t m = on ? largest(v) : 0;
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
     if (!on) continue;
     float inverse;
     const float scale = block_scale(m, inverse);
-    if (at == 0) p.scale[row[u] * p.scale_row + col[u] * p.scale_block] = scale;
+    if (at == 0) p.scale[row * p.scale_row + col * p.scale_block] = scale;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[u][i] *= inverse;
-    store8<WIDE>(p.q.at(row[u]), (int64_t)col[u] * kQuantBlock + at, p.width, v[u]);
+    for (int i = 0; i < 8; ++i) v[i] *= inverse;
+    store8<WIDE>(p.q.at(row), (int64_t)col * kQuantBlock + at, p.width, v);
   }
 }
 
-// 128 x 128: a block of 256 threads takes a block of the matrix, which stays in its registers between maximum and quotient.
+// 128 x 128: a block of 256 threads takes a block of the matrix, which stays in its registers, as it was read, between maximum and
+// quotient.
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(256) quantize_weight_kernel(const QuantParams<T> p) {
+__global__ void __launch_bounds__(256, WIDE && sizeof(T) == 2 ? 4 : 2) quantize_weight_kernel(const QuantParams<T> p) {
   __shared__ uint32_t part[8];
   ops_begin();
   constexpr int kRows = kQuantBlock / 16;            // of a thread
   const int sub = threadIdx.x / 16;
-  const int64_t rb = (p.rows + kQuantBlock - 1) / kQuantBlock;
-  const int64_t b = blockIdx.x, g = b / (rb * p.blocks), in = b - g * rb * p.blocks;
-  const int64_t row0 = in / p.blocks * kQuantBlock, c = in % p.blocks * kQuantBlock + threadIdx.x % 16 * 8;
-  float v[kRows][8];
+  const int64_t row0 = (int64_t)blockIdx.y * kQuantBlock, g = blockIdx.z, c = (int64_t)blockIdx.x * kQuantBlock + threadIdx.x % 16 * 8;
+  Eight<T, WIDE> v[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)                    // a row behind the last is the last one again
+    v[i].load(p.x.at(g * p.rows + min(row0 + sub + 16 * i, p.rows - 1)), c, p.width);
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    load8<T, WIDE>(p.x.at(g * p.rows + min(row0 + sub + 16 * i, p.rows - 1)), c, p.width, v[i]);
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) m = max(m, largest(v[i]));             // a row behind the last is the last one again
+  for (int i = 0; i < kRows; ++i) {
+    float t[8];
+    v[i].get(t);
+    m = max(m, largest(t));
+  }
   m = __reduce_max_sync(0xffffffffu, m);
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
   __syncthreads();
@@ -628,13 +640,15 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const QuantParams<
   for (int i = 0; i < 8; ++i) m = max(m, part[i]);
   float inverse;
   const float scale = block_scale(m, inverse);
-  if (threadIdx.x == 0) p.scale[b] = scale;
+  if (threadIdx.x == 0) p.scale[(g * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = scale;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     if (row0 + sub + 16 * i >= p.rows) continue;
+    float t[8];
+    v[i].get(t);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] *= inverse;
-    store8<WIDE>(p.q.at(g * p.rows + row0 + sub + 16 * i), c, p.width, v[i]);
+    for (int j = 0; j < 8; ++j) t[j] *= inverse;
+    store8<WIDE>(p.q.at(g * p.rows + row0 + sub + 16 * i), c, p.width, t);
   }
 }
 
@@ -707,13 +721,13 @@ moe_status quantize(const void* x, int64_t ldx, int32_t G, int32_t rows, int32_t
   QuantParams<T> p{{static_cast<const T*>(x), ldx}, {static_cast<uint8_t*>(q), ldq}, scale, sr, sb, rows, width, (int)(((int64_t)width + kQuantBlock - 1) / kQuantBlock)};
   const bool wide = width % 8 == 0 && rows16(x, ldx, sizeof(T)) && reinterpret_cast<uintptr_t>(q) % 8 == 0 && ldq % 8 == 0;
   if (weight) {
-    const int64_t blocks = (int64_t)G * ((rows + kQuantBlock - 1) / kQuantBlock) * p.blocks;
-    if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-    return launch_op(wide ? quantize_weight_kernel<T, true> : quantize_weight_kernel<T, false>, dim3((unsigned)blocks), 256, 0, 1, s, p);
+    const int64_t rb = ((int64_t)rows + kQuantBlock - 1) / kQuantBlock;
+    if (rb > 65535 || G > 65535) return MOE_ERR_UNSUPPORTED;
+    return launch_op(wide ? quantize_weight_kernel<T, true> : quantize_weight_kernel<T, false>, dim3((unsigned)p.blocks, (unsigned)rb, (unsigned)G), 256, 0, 1, s, p);
   }
-  const int64_t blocks = ((int64_t)rows * p.blocks + 63) / 64;
-  if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  return launch_op(wide ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>, dim3((unsigned)blocks), 256, 0, 1, s, p);
+  const int64_t y = ((int64_t)rows + 3) / 4;
+  const dim3 grid((unsigned)((p.blocks + 15) / 16), (unsigned)std::min<int64_t>(y, 65535), (unsigned)((y + 65534) / 65535));
+  return launch_op(wide ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>, grid, 256, 0, 1, s, p);
 }
 
 }  // namespace

@@ -534,7 +534,8 @@ moe_status moe_async_linear_blocks(const moe_async_linear_args* args, int64_t x_
  * to nearest).  A block with an infinity or a NaN becomes NaN, and its scale.
  *   block_rows = 1   : blocks of 1 x 128; x [rows, width] (G = 1), scale of (t, b) at t * scale_row + b * scale_block
  *   block_rows = 128 : blocks of 128 x 128 of G matrices [rows, width], one behind another (rows * stride elements each), scale
- *                      [G, ceil(rows / 128), ceil(width / 128)] contiguous (scale_row and scale_block are not looked at)
+ *                      [G, ceil(rows / 128), ceil(width / 128)] contiguous (scale_row and scale_block are not looked at); G and
+ *                      rows / 128 at most 65,535, else MOE_ERR_UNSUPPORTED
  * dtype: MOE_F32 or MOE_BF16; blocks at an edge are as wide or high as the matrix lets them. */
 moe_status moe_async_quantize_blocks(int32_t dtype, const void* d_x, int64_t x_stride, int32_t G, int32_t rows, int32_t width, int32_t block_rows,
                                      void* d_q, int64_t q_stride, float* d_scale, int64_t scale_row, int64_t scale_block, void* stream);
