@@ -519,6 +519,13 @@ __device__ __forceinline__ float block_scale(uint32_t bits, float& inverse) {
   return scale;
 }
 
+__device__ __forceinline__ uint32_t largest(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return m;
+}
+
 // 8 elements of a row from column c, as they lie in memory; those at `width` and behind are zeros.  WIDE: in 16-byte units.
 template <typename T, bool WIDE> struct Eight {
   T v[8];
@@ -530,6 +537,11 @@ template <typename T, bool WIDE> struct Eight {
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = to_f(v[i]);
   }
+  __device__ __forceinline__ uint32_t most() const {
+    float t[8];
+    get(t);
+    return largest(t);
+  }
 };
 template <typename T> struct Eight<T, true> {
   static constexpr int N = Vec<T>::N;
@@ -537,6 +549,20 @@ template <typename T> struct Eight<T, true> {
   __device__ __forceinline__ void load(const T* row, int64_t c, int64_t width) {
 #pragma unroll
     for (int i = 0; i < 8 / N; ++i) v[i] = c < width ? __ldg(reinterpret_cast<const uint4*>(row + c) + i) : make_uint4(0, 0, 0, 0);   // width: a multiple of 8
+  }
+  // the bits of the largest |value|, as fp32 (NaN above infinity): two at a time in 16 bits
+  __device__ __forceinline__ uint32_t most() const {
+    if constexpr (N == 8) {
+      __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[0].x));
+      m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[0].y)));
+      m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[0].z)));
+      m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[0].w)));
+      return (uint32_t)__bfloat16_as_ushort(__hmax_nan(m.x, m.y)) << 16;
+    } else {
+      float t[8];
+      get(t);
+      return largest(t);
+    }
   }
   __device__ __forceinline__ void get(float (&t)[8]) const {
 #pragma unroll
@@ -563,13 +589,6 @@ __device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t width, c
       if (c + i < width) row[c + i] = __nv_cvt_float_to_fp8(v[i], __NV_SATFINITE, __NV_E4M3);
   }
 }
-__device__ __forceinline__ uint32_t largest(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  return m;
-}
-
 template <typename T> struct QuantParams {
   Rows<const T> x;
   Rows<uint8_t> q;
@@ -581,9 +600,10 @@ template <typename T> struct QuantParams {
 // 1 x 128: sixteen lanes take a block of a row, 8 elements each; a thread asks for kU blocks before it uses the first.  A block of
 // threads takes kU * 16 blocks of 128 side by side of kRows rows, so that neither needs a division; the scales of a column of blocks,
 // whose rows lie side by side, are written kRows at a time.
+constexpr int kQuantRows = 8;                        // 4096 x 7168 19.3 us, with 4 20.3
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams<T> p) {
-  constexpr int kU = 4, kRows = 4;                   // blocks of a thread; rows of a block of threads
+  constexpr int kU = 4, kRows = kQuantRows;          // blocks of a thread; rows of a block of threads
   ops_begin();
   const int sub = threadIdx.x / 16, at = threadIdx.x % 16 * 8;
   const int64_t row = (int64_t)blockIdx.y * kRows + sub % kRows + (int64_t)blockIdx.z * 65535 * kRows;
@@ -598,15 +618,15 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams<T>
   for (int u = 0; u < kU; ++u) {
     const int col = first + u * (16 / kRows);
     const bool on = row < p.rows && col < p.blocks;
-    float v[8];
-    x[u].get(v);
-    uint32_t m = on ? largest(v) : 0;
+    uint32_t m = on ? x[u].most() : 0;
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
     if (!on) continue;
     float inverse;
     const float scale = block_scale(m, inverse);
     if (at == 0) p.scale[row * p.scale_row + col * p.scale_block] = scale;
+    float v[8];
+    x[u].get(v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= inverse;
     store8<WIDE>(p.q.at(row), (int64_t)col * kQuantBlock + at, p.width, v);
@@ -628,11 +648,7 @@ __global__ void __launch_bounds__(256, WIDE && sizeof(T) == 2 ? 4 : 2) quantize_
     v[i].load(p.x.at(g * p.rows + min(row0 + sub + 16 * i, p.rows - 1)), c, p.width);
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    float t[8];
-    v[i].get(t);
-    m = max(m, largest(t));
-  }
+  for (int i = 0; i < kRows; ++i) m = max(m, v[i].most());
   m = __reduce_max_sync(0xffffffffu, m);
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
   __syncthreads();
@@ -725,8 +741,8 @@ moe_status quantize(const void* x, int64_t ldx, int32_t G, int32_t rows, int32_t
     if (rb > 65535 || G > 65535) return MOE_ERR_UNSUPPORTED;
     return launch_op(wide ? quantize_weight_kernel<T, true> : quantize_weight_kernel<T, false>, dim3((unsigned)p.blocks, (unsigned)rb, (unsigned)G), 256, 0, 1, s, p);
   }
-  const int64_t y = ((int64_t)rows + 3) / 4;
-  const dim3 grid((unsigned)((p.blocks + 15) / 16), (unsigned)std::min<int64_t>(y, 65535), (unsigned)((y + 65534) / 65535));
+  const int64_t y = ((int64_t)rows + kQuantRows - 1) / kQuantRows;
+  const dim3 grid((unsigned)((p.blocks + 7) / 8), (unsigned)std::min<int64_t>(y, 65535), (unsigned)((y + 65534) / 65535));
   return launch_op(wide ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>, grid, 256, 0, 1, s, p);
 }
 
