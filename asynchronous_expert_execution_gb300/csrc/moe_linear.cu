@@ -17,34 +17,6 @@ namespace {
 
 // ------------------------------------------------------------------ few tokens
 
-constexpr int kFewTokens = 16;
-constexpr int kFewThreads = 512;                     // at most
-
-struct FewParams {
-  const void* x;
-  const void* w;
-  int64_t ldx, ldw;
-  LinearParams l;
-};
-
-// c[16][8] += a b over 32 bytes of K, twice.  The 16 bytes that a lane loaded of each row (a, and a8 for the
-// rows 8 .. of the 16) stand for the same elements in both operands, and no order of K matters to the sum.
-template <bool E4M3>
-__device__ __forceinline__ void warp_mma(float (&c)[4], const uint4& a, const uint4& a8, const uint4& b) {
-#define MOE_WARP_MMA(SHAPE, A0, A1, A2, A3, B0, B1)                                                           \
-  asm("mma.sync.aligned." SHAPE " {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"                      \
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                                        \
-      : "r"(A0), "r"(A1), "r"(A2), "r"(A3), "r"(B0), "r"(B1))
-  if constexpr (E4M3) {
-    MOE_WARP_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32", a.x, a8.x, a.y, a8.y, b.x, b.y);
-    MOE_WARP_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32", a.z, a8.z, a.w, a8.w, b.z, b.w);
-  } else {
-    MOE_WARP_MMA("m16n8k16.row.col.f32.bf16.bf16.f32", a.x, a8.x, a.y, a8.y, b.x, b.y);
-    MOE_WARP_MMA("m16n8k16.row.col.f32.bf16.bf16.f32", a.z, a8.z, a.w, a8.w, b.z, b.w);
-  }
-#undef MOE_WARP_MMA
-}
-
 // An SM's share of HBM, 45 GB/s, wants some 40 KB under way: 512 threads ask for eight (FS + TS = 2), five or four
 // 16-byte units a row each before they use the first.  Sums on the CUDA cores instead took 6.5 us for one
 // token on 2880 x 2880 (5.8 here) and 17.6 for eight (6.0).

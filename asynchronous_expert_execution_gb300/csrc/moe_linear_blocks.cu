@@ -14,6 +14,7 @@
 //
 //   pair   persistent, 256 features x up to 256 tokens over two SMs
 //   split  128 features x up to 64 tokens, K split over a cluster of up to 8 CTAs
+//   few    up to 16 tokens on small weights, by warp-wide matrix instructions
 #include "moe_linear.cuh"
 
 namespace moe {
@@ -506,6 +507,120 @@ __global__ void __launch_bounds__(kThreads, 2) linear_blocks_split_kernel(const 
   if (warp == 2) tmem_dealloc<1>(tmem, kCols);
 }
 
+// ------------------------------------------------------------------ few tokens
+
+// As the forward product's kernel for up to 16 tokens: weights straight into the registers of warp-wide matrix instructions.  A warp
+// takes whole k-blocks, kBlocks of them in flight, so that their sums stand under one scale a token.  Block (b, i): 8 FS features of up
+// to 8 TS tokens, those of the i-th group that has rows.
+constexpr int few_blocks(int ts, int fs) { return ts + fs == 2 ? 4 : ts + fs == 3 ? 2 : 1; }
+template <typename TO, int TS, int FS>
+__global__ void __launch_bounds__(kFewThreads, 1) linear_blocks_few_kernel(const __grid_constant__ FewParams p, const __grid_constant__ Scales sc) {
+  constexpr int kBlocks = few_blocks(TS, FS), kFeatures = 8 * FS, kTiles = TS * FS == 4 ? 2 : 1;
+  __shared__ float part[kFewThreads / 32][8 * TS * kFeatures];
+  ops_begin();
+  const LinearParams& l = p.l;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  int g = 0, row0 = 0, nt = l.T;
+  if (l.offsets) {
+    nt = 0;
+    const auto tiles = [](int n) { return n > 0 ? 1 : 0; };
+    GroupTiles at(blockIdx.y);
+    if (at.find(l, tiles)) at.get(tiles, g, row0, nt);
+    nt = min(8 * TS, nt);
+    if (nt == 0) return;
+  }
+  // this thread's output, and what its epilogue reads
+  const int of = blockIdx.x * kFeatures + threadIdx.x % kFeatures, ot = threadIdx.x / kFeatures;
+  const bool out = ot < nt;
+  const Finish<TO, 1, false> finish(l, g, out ? of : l.N, 1);
+  const Place<TO> place(l, row0 + ot, of);
+  typename Finish<TO, 1, false>::Ahead ahead;
+  finish.ahead(ahead, place, 0, out);
+
+  // rows in units of 16 bytes; a row that does not exist is not read
+  const int units = l.F / 16;
+  const uint4 *w[FS], *x[TS];
+  int wu[FS], xu[TS];
+#pragma unroll
+  for (int i = 0; i < FS; ++i) {
+    const int f = blockIdx.x * kFeatures + i * 8 + lane / 4;
+    wu[i] = f < l.N ? units : 0;
+    w[i] = static_cast<const uint4*>(p.w) + ((size_t)g * l.N + (f < l.N ? f : 0)) * (p.ldw / 16);
+  }
+#pragma unroll
+  for (int i = 0; i < TS; ++i) {
+    const int t = i * 8 + lane / 4;
+    xu[i] = t < nt ? units : 0;
+    x[i] = static_cast<const uint4*>(p.x) + (row0 + (t < nt ? t : 0)) * (size_t)(p.ldx / 16);
+  }
+  // the tokens of this lane's sums: features on the instruction's rows (FS = 2), two adjacent columns a tile; else rows 8 apart
+  const int t0 = FS == 2 ? lane % 4 * 2 : lane / 4;
+  const auto token = [](int i, int j) { return FS == 2 ? i * 8 + j : 8 * j; };       // from t0
+  const float* sx = sc.x + (int64_t)(row0 + t0) * sc.row;
+  const float* sw = sc.w + ((size_t)g * sc.nfb + blockIdx.x * kFeatures / kBM) * l.nk;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  float sum[kTiles][4] = {};
+  for (int b0 = warp; b0 < l.nk; b0 += kBlocks * warps) {
+    uint4 wv[FS][kBlocks][2], xv[TS][kBlocks][2];
+    float f[kTiles][kBlocks][2], fw[kBlocks];
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = (b0 + u * warps) * 8 + h * 4 + lane % 4;
+#pragma unroll
+        for (int i = 0; i < FS; ++i) wv[i][u][h] = k < wu[i] ? __ldcs(w[i] + k) : zero;
+      }
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      const int b = b0 + u * warps;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < TS; ++i) xv[i][u][h] = b * 8 + h * 4 + lane % 4 < xu[i] ? __ldg(x[i] + b * 8 + h * 4 + lane % 4) : zero;
+      fw[u] = b < l.nk ? __ldg(sw + b) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f[i][u][j] = b < l.nk && t0 + token(i, j) < nt ? __ldg(sx + token(i, j) * sc.row + b * sc.block) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      float c[kTiles][4] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (FS == 2) {
+#pragma unroll
+          for (int i = 0; i < TS; ++i) warp_mma<true>(c[i], wv[0][u][h], wv[1][u][h], xv[i][u][h]);
+        } else {
+          warp_mma<true>(c[0], xv[0][u][h], TS == 2 ? xv[TS - 1][u][h] : zero, wv[0][u][h]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float s = f[i][u][FS == 2 ? j % 2 : j / 2] * fw[u];
+          if (b0 + u * warps < l.nk) sum[i][j] = fmaf(c[i][j], s, sum[i][j]);
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = lane / 4 + j / 2 * 8, q = i * 8 + lane % 4 * 2 + j % 2;
+      if (FS == 2) part[warp][q * kFeatures + r] = sum[i][j];
+      else if (TS == 2 || j < 2) part[warp][r * kFeatures + q] = sum[i][j];
+    }
+  __syncthreads();
+  if (out) {
+    float v[1] = {part[0][threadIdx.x]};
+    for (int i = 1; i < warps; ++i) v[0] += part[i][threadIdx.x];
+    finish(v, place.y, ahead);
+  }
+}
+
 // ------------------------------------------------------------------ quantisers
 
 constexpr float kE4M3Max = 448.f;
@@ -714,11 +829,27 @@ moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, c
   return launch_op(linear_blocks_split_kernel<TO, BN>, dim3((unsigned)(tiles * splits)), kThreads, smem, splits, s, b);
 }
 
+template <typename TO, int TS, int FS>
+moe_status launch_few(const moe_async_linear_args* a, const LinearParams& l, const Scales& sc, void* s) {
+  const FewParams p{a->d_x, a->d_w, a->x_stride, a->w_stride, l};
+  const dim3 grid((unsigned)((l.N + 8 * FS - 1) / (8 * FS)), (unsigned)(l.offsets ? std::min(l.G, l.T) : 1));
+  // half the warps where these take K in one pass all the same
+  const int threads = l.nk <= few_blocks(TS, FS) * (kFewThreads / 64) ? kFewThreads / 2 : kFewThreads;
+  return launch_op(linear_blocks_few_kernel<TO, TS, FS>, grid, threads, 0, 1, s, p, sc);
+}
+
 template <typename TO>
 moe_status blocks_launch(const moe_async_linear_args* a, const LinearParams& l, const Scales& sc, void* s) {
   const int sms = sm_count();
   if (sms < 2) return MOE_ERR_CUDA;
   const int groups = l.offsets ? std::min(l.G, l.T) : 1;
+  // as in the forward product: few tokens on small weights
+  const int64_t features = (int64_t)l.N * groups;
+  if (l.T <= kFewTokens && features <= 64 * sms && features * l.F <= 32'000'000) {
+    const bool wide_rows = features > 8 * sms;
+    return l.T > 8 ? wide_rows ? launch_few<TO, 2, 2>(a, l, sc, s) : launch_few<TO, 2, 1>(a, l, sc, s)
+                   : wide_rows ? launch_few<TO, 1, 2>(a, l, sc, s) : launch_few<TO, 1, 1>(a, l, sc, s);
+  }
   const float per = l.T / (float)groups;
   if (per <= 64) {
     const int bn = per <= 16 ? 16 : per <= 32 ? 32 : 64;

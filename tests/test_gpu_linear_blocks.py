@@ -146,8 +146,16 @@ def test_dense(moe, T, F, N, out, act, what, layout, pad):
     check(moe, T, F, N, 0, out, act, what, layout, pad=pad)
 
 
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 15, 16])
+@pytest.mark.parametrize("F,N", [(16, 9), (64, 9000), (1056, 1235), (2064, 1200), (4128, 130), (208, 2500), (7168, 2048), (7168, 6000)])
+def test_few_tokens(moe, T, F, N):
+    """One to 16 rows, also on the sides of the sizes at which the kernel and its tiles change."""
+    check(moe, T, F, N, 0, F32 if T % 2 else BF16, "silu", "bmr", ("tokens", "rows", "strided")[T % 3], pad=T % 3)
+
+
 GROUPED = [(1, 64, 64, 3), (5, 80, 33, 16), (64, 2880, 256, 32), (64, 128, 256, 2), (200, 592, 997, 16), (333, 208, 584, 24), (700, 64, 40, 1024), (1000, 512, 384, 7),
-           (1500, 2880, 160, 12), (4096, 256, 512, 32), (2500, 320, 2048, 5), (257, 2048, 1500, 4), (40, 7168, 520, 12)]
+           (1500, 2880, 160, 12), (4096, 256, 512, 32), (2500, 320, 2048, 5), (257, 2048, 1500, 4), (40, 7168, 520, 12), (16, 1040, 264, 5),
+           (7, 7168, 300, 20)]
 
 
 @pytest.mark.parametrize("T,F,N,G", GROUPED)
