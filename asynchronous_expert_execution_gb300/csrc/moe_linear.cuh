@@ -509,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
     }
   } else if (MODE == kWeightGrad && nj > 0 && warp == 1) {
     const uint32_t idesc = mma_desc<E4M3, true, true>(kBM, p.bn);
-    // this rank's k-blocks, the group's last one with what lies behind its end cleared by the whole warp
-    const int live = sum.n - (nk - 1) * kBoxRows, last = kb1 == nk && kb1 > kb0 && live % 16 ? 1 : 0;
+    // this rank's k-blocks; the group's last one, if it is not full, by the whole warp, which clears what lies behind the end
+    const int live = sum.n - (nk - 1) * kBoxRows, last = kb1 == nk && kb1 > kb0 && live < kBoxRows ? 1 : 0;
     bool ok = true;
     uint32_t st = 0, phase = 0;
     int chunk = 0, i = 0;                            // block i of the chunk
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
         chunk = __shfl_sync(0xffffffffu, chunk, src), i = __shfl_sync(0xffffffffu, i, src);
       }
       if (__all_sync(0xffffffffu, ok) && __all_sync(0xffffffffu, wait(&s->full[st], phase, abort_flag))) {
-        clear_rows(smem + st * stage_bytes, 2 + p.bn / 64, live);
+        if (live % 16) clear_rows(smem + st * stage_bytes, 2 + p.bn / 64, live);
         if (elect()) {
           block(live);
           commit<1>(&s->done);
