@@ -152,9 +152,10 @@ __device__ __forceinline__ void product_block(uint32_t d, uint32_t smem, uint32_
 // kWeightGrad, by a whole warp: the last k-block of a group holds `live` rows of it, and behind them rows of the next group or
 // of none, with any content.  Those that a product of 16 rows would still reach become zeros in both operands.
 __device__ __forceinline__ void clear_rows(uint8_t* stage, int boxes, int live) {
-  const int rows = (16 - live % 16) % 16, units = boxes * rows * 8;
-  for (int i = threadIdx.x % 32; i < units; i += 32)
-    *reinterpret_cast<uint4*>(stage + i / (8 * rows) * kBox + (live + i / 8 % rows) * kBKBytes + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+  // a row's eight units of 16 bytes by adjacent lanes, four rows at a time; no divisions: the products wait for this
+  const int lane = threadIdx.x % 32, end = (live + 15) / 16 * 16;
+  for (int r = live + lane / 8; r < end; r += 4)
+    for (int b = 0; b < boxes; ++b) *reinterpret_cast<uint4*>(stage + b * kBox + r * kBKBytes + lane % 8 * 16) = make_uint4(0, 0, 0, 0);
   fence_async();
   __syncwarp();
 }
@@ -658,6 +659,7 @@ struct PairTail {
   // kWeightGrad: this CTA's part of a k-block that has to be cleared, and the tiles that a warp tells the others
   static constexpr int kTold = 4;
   uint64_t own[kMaxStages], told[kTold], heard[kTold];
+  uint64_t old[8];                  // an epilogue warp's box of what is added to
   int4 tile[kTold][2];
   uint32_t tmem;
   int abort_flag;
@@ -852,6 +854,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         mbar_init(&s->told[i], 1);
         mbar_init(&s->heard[i], rank == 0 ? 11 : 10);              // all warps but the telling one and the second CTA's idle one
       }
+    if (kAcross)
+      for (int i = 0; i < 8; ++i) mbar_init(&s->old[i], 1);
     s->abort_flag = 0;
     s->finishing = 0;
     mbar_init_fence();
@@ -937,7 +941,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!__all_sync(0xffffffffu, wait(&s->own[st], phases >> st & 1, abort_flag))) break;
       phases ^= 1u << st;
       clear_rows(smem + st * p.stage_bytes, 2 + tl.brows / 64, tl.sum - (tl.nk - 1) * kBoxRows);
-      if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&s->full[st]), 0));
+      if (lane == 0 && rank == 0) mbar_arrive(&s->full[st]);
+      if (lane == 0 && rank == 1) mbar_arrive_cluster(mapa(smem_u32(&s->full[st]), 0));
     }
   } else if (kAcross && warp == 3) {
     bool more = true;
@@ -951,7 +956,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         mbar_arrive(&s->told[slot]);
       }
       __syncwarp();
-      if (more && l.res && !p.boxed) prefetch(0);
+      if (more && l.res && (sizeof(TO) == 2 || !p.boxed)) prefetch(0);
     }
   } else if (warp == 1 && rank == 0) {
     uint32_t st = 0, phase = 0, acc = 0;
@@ -985,7 +990,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp >> 2) - 1;  // TMEM lanes 32 q ..; two warps share a quarter's columns
     float* turn = reinterpret_cast<float*>(smem + kRing + (warp - 4) * (kAcross ? kBoxStaging / 8 : kTurn * 4));
-    uint32_t acc = 0;
+    uint32_t acc = 0, olds = 0;
     // a warp's tokens: every other block of 32, or for boxes the tile's first or second half
     constexpr bool kSums = sizeof(TO) == 4;
     constexpr int kStep = 2 * kChunk;
@@ -1054,17 +1059,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (kAcross && p.boxed) {
         // A warp's sums leave by TMA in one box, which leaves out what lies outside, and adds in fp32 where that is asked for.  (Through
         // registers, as below, a tile of 256 x 128 in fp32 took 3.5 us.)
+        // In bf16 what is added to comes first, for the sum is rounded once.
         TO* box = reinterpret_cast<TO*>(turn);
-        if (lane == 0) store_wait_read<0>();         // the tile before
-        __syncwarp();
+        constexpr int kBoxBytes = kBoxTokens<TO> * 32 * (int)sizeof(TO);
         const int c0 = half * (kTokens / 2);
-        ok = boxes(std::true_type{}, [&](int c, const float (&v)[16]) {
+        const bool here = f < l.N && c0 < tl.nj, add = sizeof(TO) == 2 && l.res && here;
+        if (lane == 0) store_wait_read<0>();         // the tile before
+        if (lane == 0 && add) {
+          mbar_expect(&s->old[warp - 4], kBoxBytes);
+          tma_3d<1>(smem_u32(box), &p.y, smem_u32(&s->old[warp - 4]), f, tl.row0 + c0, tl.g);
+        }
+        __syncwarp();
+        const auto put = [&](int c, const float (&v)[16]) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) box[(c - c0 + j) * 32 + lane] = from_f<TO>(v[j]);
-        });
+        };
+        if (add) {
+          bool first = true;
+          ok = boxes(std::true_type{}, [&](int c, float (&v)[16]) {
+            if (first) wait(&s->old[warp - 4], olds++ & 1, abort_flag);
+            first = false;
+            float o[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = to_f(box[(c - c0 + j) * 32 + lane]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += o[j];
+            put(c, v);
+          });
+        } else {
+          ok = boxes(std::true_type{}, put);
+        }
         fence_async();
         __syncwarp();
-        if (lane == 0 && ok && f < l.N && c0 < tl.nj) {
+        if (lane == 0 && ok && here) {
           if (sizeof(TO) == 4 && l.res)
             tma_store_3d<true>(&p.y, smem_u32(box), f, tl.row0 + c0, tl.g);
           else

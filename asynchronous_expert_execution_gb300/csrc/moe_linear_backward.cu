@@ -112,8 +112,7 @@ moe_status weight_grad(const Args* a, const void* grad, int64_t grad_stride, int
   PairParams p;
   if (!encode(&p.w, a->d_x, 2, a->fan_in, a->rows, a->x_stride, 0, kBoxRows) || !encode(&p.x[0], grad, 2, a->fan_out, a->rows, grad_stride, 0, kBoxRows))
     return MOE_ERR_CUDA;
-  // by boxes, unless rows start off 16-byte boundaries, or what is added to would be rounded twice
-  p.boxed = wide && !(a->accumulate && sizeof(TO) == 2);
+  p.boxed = wide;                                    // unless rows start off 16-byte boundaries
   if (p.boxed && !encode_result<TO>(&p.y, a->d_grad_w, a->fan_in, a->fan_out, a->grad_w_stride, l.G)) return MOE_ERR_CUDA;
   return launch_pair<TO, kWeightGrad>(p, l, plan.tokens, sms, s);
 }
@@ -121,10 +120,11 @@ moe_status weight_grad(const Args* a, const void* grad, int64_t grad_stride, int
 // ------------------------------------------------------------------ the bias's gradient
 
 constexpr int kBiasThreads = 256;
-constexpr int kBiasCols = 256;                       // columns of a block: 8 a lane, every warp the same
+constexpr int kBiasCols = 64;                        // columns of a block: 8 a lane, four rows a warp
 
-// Column sums of a group's rows, bound by their one read.  A cluster takes 256 columns of a group: every warp of its CTAs
-// each so-many-th row, four loads in flight; the warps' sums meet in shared memory, the CTAs' in the first one's, both in order.
+// Column sums of a group's rows, bound by their one read.  A cluster takes 64 columns of a group (128 bytes a row; 256 columns left 2048 x
+// 256 to eight CTAs, 6.2 us): every quarter of its warps each so-many-th row, eight loads in flight.  Quarters meet by shuffles, warps in
+// shared memory, CTAs in the first one's, all in a fixed order.
 __global__ void __launch_bounds__(kBiasThreads)
     grad_bias_kernel(const __nv_bfloat16* __restrict__ grad, int64_t ld, const LinearParams l, float* __restrict__ out, int add) {
   __shared__ float part[kBiasThreads / 32][kBiasCols];
@@ -132,13 +132,13 @@ __global__ void __launch_bounds__(kBiasThreads)
   const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kBiasThreads / 32;
   const int blocks = (l.T + kBiasCols - 1) / kBiasCols, at = blockIdx.x / ranks;
-  const int g = at / blocks, c = at % blocks * kBiasCols + lane * 8;
+  const int g = at / blocks, c = at % blocks * kBiasCols + lane % 8 * 8;
   const Span sp = group_rows(l, g, l.F);
   float v[8] = {};
-  const int step = ranks * warps;
+  const int step = ranks * warps * 4, first = (rank * warps + warp) * 4 + lane / 8;
   if (c + 8 <= l.T) {
-    constexpr int kAt = 4;
-    for (int r = rank * warps + warp; r < sp.n; r += kAt * step) {
+    constexpr int kAt = 8;
+    for (int r = first; r < sp.n; r += kAt * step) {
       uint4 u[kAt];
 #pragma unroll
       for (int i = 0; i < kAt; ++i)
@@ -152,41 +152,47 @@ __global__ void __launch_bounds__(kBiasThreads)
       }
     }
   } else {
-    for (int r = rank * warps + warp; r < sp.n; r += step)
+    for (int r = first; r < sp.n; r += step)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (c + j < l.T) v[j] += __bfloat162float(grad[(int64_t)(sp.a + r) * ld + c + j]);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) part[warp][lane * 8 + j] = v[j];
+  for (int j = 0; j < 8; ++j) {
+    v[j] += __shfl_xor_sync(0xffffffffu, v[j], 8);
+    v[j] += __shfl_xor_sync(0xffffffffu, v[j], 16);
+    if (lane < 8) part[warp][lane * 8 + j] = v[j];
+  }
   __syncthreads();
-  float sum = part[0][threadIdx.x];
-  for (int w = 1; w < warps; ++w) sum += part[w][threadIdx.x];
+  const int t = threadIdx.x;
+  float sum = 0.f;
+  if (t < kBiasCols)
+    for (int w = 0; w < warps; ++w) sum += part[w][t];
   if (ranks > 1) {
     __syncthreads();
-    part[0][threadIdx.x] = sum;
+    if (t < kBiasCols) part[0][t] = sum;
     cluster_sync();
-    if (rank == 0)
-      for (int r = 1; r < ranks; ++r) sum += ld_cluster_f32(mapa(smem_u32(&part[0][threadIdx.x]), r));
+    if (rank == 0 && t < kBiasCols)
+      for (int r = 1; r < ranks; ++r) sum += ld_cluster_f32(mapa(smem_u32(&part[0][t]), r));
     cluster_sync();                                  // the others' shared memory has been read
   }
-  const int n = at % blocks * kBiasCols + threadIdx.x;
-  if (rank == 0 && n < l.T) {
+  const int n = at % blocks * kBiasCols + t;
+  if (rank == 0 && t < kBiasCols && n < l.T) {
     float* o = out + (int64_t)g * l.T + n;
     *o = add ? *o + sum : sum;
   }
 }
 
-moe_status bias_grad(const Args* a, const void* grad, int64_t grad_stride, void* s) {
+moe_status bias_grad(const Args* a, const void* grad, int64_t grad_stride, int sms, void* s) {
   LinearParams l = {};
   l.T = a->fan_out;
   l.F = a->rows;
   l.G = std::max(1, a->groups);
   l.offsets = a->d_offsets;
   const int64_t blocks = (int64_t)((l.T + kBiasCols - 1) / kBiasCols) * l.G;
-  // a CTA for some 64 rows of an average group
+  // a CTA for some 64 rows of an average group, as long as there are few
   int ranks = 1;
-  while (ranks < 8 && (int64_t)a->rows / l.G > 64 * ranks) ranks *= 2;
+  while (ranks < 8 && (int64_t)a->rows / l.G > 64 * ranks && blocks * ranks < 4 * sms) ranks *= 2;
   return launch_op(grad_bias_kernel, dim3((unsigned)(blocks * ranks)), kBiasThreads, 0, ranks, s, static_cast<const __nv_bfloat16*>(grad), grad_stride, l,
                    a->d_grad_bias, a->accumulate);
 }
@@ -195,11 +201,17 @@ moe_status bias_grad(const Args* a, const void* grad, int64_t grad_stride, void*
 __global__ void __launch_bounds__(256)
     align_rows_kernel(const __nv_bfloat16* __restrict__ in, int64_t ld, __nv_bfloat16* __restrict__ out, int64_t ldo, int T, int N) {
   ops_begin();
-  const long long total = (long long)T * ldo;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
-    const long long t = i / ldo, c = i - t * ldo;
-    if (c < N) out[i] = in[t * ld + c];
-  }
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  constexpr int kRows = 4;
+  const int64_t row = ((int64_t)blockIdx.z * 65535 + blockIdx.y) * kRows;
+  if (c >= N) return;
+  __nv_bfloat16 v[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    if (row + i < T) v[i] = in[(row + i) * ld + c];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    if (row + i < T) out[(row + i) * ldo + c] = v[i];
 }
 
 int64_t aligned_stride(int32_t fan_out) { return ((int64_t)fan_out + 7) / 8 * 8; }
@@ -351,14 +363,15 @@ extern "C" moe_status moe_async_linear_backward(const moe_async_linear_backward_
   moe_status r = MOE_OK;
   if (need > 0) {
     ld = aligned_stride(a->fan_out);
-    const int64_t blocks = std::min<int64_t>((a->rows * ld + 1023) / 1024, 16 * sms);
-    r = launch_op(align_rows_kernel, dim3((unsigned)blocks), 256, 0, 1, s, static_cast<const __nv_bfloat16*>(grad), a->grad_stride,
+    const int64_t y = ((int64_t)a->rows + 3) / 4;
+    const dim3 grid((unsigned)((a->fan_out + 255) / 256), (unsigned)std::min<int64_t>(y, 65535), (unsigned)((y + 65534) / 65535));
+    r = launch_op(align_rows_kernel, grid, 256, 0, 1, s, static_cast<const __nv_bfloat16*>(grad), a->grad_stride,
                   static_cast<__nv_bfloat16*>(a->d_workspace), ld, a->rows, a->fan_out);
     grad = a->d_workspace;
   }
   if (r == MOE_OK && gx) r = a->x_dtype == MOE_F32 ? rows_grad<float>(a, grad, ld, sms, s) : rows_grad<__nv_bfloat16>(a, grad, ld, sms, s);
   if (r == MOE_OK && gw) r = a->w_dtype == MOE_F32 ? weight_grad<float>(a, grad, ld, sms, s) : weight_grad<__nv_bfloat16>(a, grad, ld, sms, s);
-  if (r == MOE_OK && gb) r = bias_grad(a, grad, ld, s);
+  if (r == MOE_OK && gb) r = bias_grad(a, grad, ld, sms, s);
   return r;
 }
 
