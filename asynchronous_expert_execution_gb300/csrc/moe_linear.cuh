@@ -838,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (threadIdx.x == 0) {
     prefetch_map(&p.w);
-    prefetch_map(&p.x[3]);
+    prefetch_map(&p.x[kAcross ? 0 : 3]);
     for (int i = 0; i < p.stages; ++i) {
       // the leader's producer, for both CTAs' bytes (kWeightGrad: twice, or either CTA's clearing warp)
       mbar_init(&s->full[i], kAcross ? 2 : 1);

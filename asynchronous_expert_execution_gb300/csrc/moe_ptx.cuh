@@ -29,7 +29,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive_light(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-// arrive without any order over memory: for a buffer in TMEM, which tcgen05's fences order
+// arrive without any order over memory: for a buffer in TMEM, behind tcgen05.wait::ld, when what was read is in registers
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }

@@ -10,6 +10,15 @@ For a caller that holds a whole routed batch (a prefill chunk, a training step):
     act = linear(rows, w1, act="silu", mul=up, offsets=offsets)
     out = merge_rows(linear(act, w2, offsets=offsets), pos, w, residual=h)
 
+and back, with z = linear(rows, w1, offsets=offsets) kept or computed again:
+
+    grad_ys, grad_w = merge_rows_backward(grad, ys, pos, w)
+    grad_act, grad_w2, _ = linear_backward(grad_ys, act, w2, offsets)
+    grad_z, grad_up = act_mul_backward(grad_act, z, up)
+    grad_rows, grad_w1, _ = linear_backward(grad_z, rows, w1, offsets)
+    grad_rows, grad_w3, _ = linear_backward(grad_up, rows, w3, offsets, residual=grad_rows)
+    grad_y = sort_rows_backward(grad_rows, pos)
+
 Every function runs on the device of its first tensor, on that device's current stream unless
 ``stream`` is given, allocates only the outputs it is not handed, and raises ``MoEError``
 (``MOE_ERR_INVALID``) for tensors that do not fit together.  Gradients are functions of their
@@ -156,7 +165,7 @@ def linear_backward(grad, x=None, weight=None, offsets=None, bias=False, residua
     [N], if `bias`.  Sums in fp32, rounded once to out_x's type (or out_dtype, or bf16; the residual's too) and to out_weight's
     (or weight_dtype, or bf16).  accumulate=True adds grad_weight and grad_bias to what out_weight and out_bias hold.
     `out_x` may be `residual`.  With offsets (int32 [G + 1]) as in linear: weight and grad_weight [G, N, F], grad_bias [G, N];
-    rows of no group are not read, and in out_x left as they were (in a new matrix: not set).
+    rows of no group count nowhere, and in out_x are left as they were (in a new matrix: not set).
     An epilogue's gradient comes first: act_mul_backward."""
     return (_bound or _bind()).linear_backward(grad, x, weight, offsets, bias, residual, out_dtype, weight_dtype, out_x, out_weight, out_bias,
                                                accumulate, stream)
