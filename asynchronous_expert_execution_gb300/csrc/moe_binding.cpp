@@ -571,7 +571,9 @@ PyObject* quantize_blocks(PyObject* const* a) {
   const int64_t T = l.n, F = l.width, KB = (F + 127) / 128;
   int64_t ldo;
   const Tensor q = output(a[1], "out", l.dev, at::kFloat8_e4m3fn, T, F, ldo);
-  const Tensor scale = empty({KB, T}, at::kFloat, l.dev).t();            // tokens adjacent: the product reads a block's together
+  const Tensor scale = empty({KB, T}, at::kFloat, l.dev);
+  const int64_t sizes[2] = {T, KB}, strides[2] = {1, T};                 // tokens adjacent: the product reads a block's together
+  scale.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(sizes, 2), at::IntArrayRef(strides, 2));
   call("quantize_blocks", on, [&](void* s) {
     return lib.quantize_blocks(code(l.dtype), ptr(x), l.ld, 1, count(T, "rows"), count(F, "width"), 1, ptr(q), ldo, ptr<float>(scale), 1, T, s);
   });
