@@ -67,6 +67,7 @@ struct LinearParams {
   int64_t ldmul, ldres, ldy;
   int T, N, F, G, act, nk;
   bool wide;                        // y, mul and residual: 16-byte units
+  bool beside;                      // kWeightGrad: runs beside the kernel before it (ops_beside)
   __host__ __device__ bool plain() const { return !mul && !res && act == MOE_ACT_NONE; }
 };
 
@@ -453,7 +454,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
     g = tile / p.nft / p.ntt;
     row0 = tile / p.nft % p.ntt * p.bn;
     nj = min(p.bn, l.T - row0);
-    ops_begin();
+    if (l.beside) ops_beside();
+    else ops_begin();
     sum = group_rows(l, g, l.F);
     if (sum.n == 0 && l.res) nj = 0;                 // nothing to add
     tc_before();
@@ -617,6 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
   __syncthreads();
   tc_after();
   if (warp == 2) tmem_dealloc<1>(tmem, cols);
+  if (MODE == kWeightGrad && l.beside) ops_end_beside();
 }
 
 // ------------------------------------------------------------------ pair kernel
@@ -861,7 +864,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mbar_init_fence();
   }
   if (warp == 2) tmem_alloc<2>(&s->tmem, kCols);
-  ops_begin();
+  if (kAcross && l.beside) ops_beside();
+  else ops_begin();
   tc_before();
   __syncthreads();
   cluster_sync();
@@ -1122,6 +1126,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();                                    // neither CTA's shared memory goes while the other may use it
   tc_after();
   if (warp == 2) tmem_dealloc<2>(tmem, kCols);
+  if (kAcross && l.beside) ops_end_beside();
 }
 
 // ------------------------------------------------------------------ few tokens

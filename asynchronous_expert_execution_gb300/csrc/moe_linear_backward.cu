@@ -96,11 +96,11 @@ LinearPlan weight_plan(const LinearParams& l, int sms) {
 }
 
 template <typename TO>
-moe_status weight_grad(const Args* a, const void* grad, int64_t grad_stride, int sms, void* s) {
+moe_status weight_grad(const Args* a, const void* grad, int64_t grad_stride, bool beside, int sms, void* s) {
   const bool wide = a->fan_in % 8 == 0 && rows16(a->d_grad_w, a->grad_w_stride, sizeof(TO));
   const LinearParams l{nullptr, nullptr, nullptr, nullptr, a->accumulate ? a->d_grad_w : nullptr, a->d_grad_w, a->d_offsets, 0,
                        a->grad_w_stride, a->grad_w_stride, a->fan_out, a->fan_in, a->rows, std::max(1, a->groups), MOE_ACT_NONE,
-                       (a->rows + kBoxRows - 1) / kBoxRows, wide};
+                       (a->rows + kBoxRows - 1) / kBoxRows, wide, beside};
   const LinearPlan plan = weight_plan<TO>(l, sms);
   const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * ((l.T + plan.tokens - 1) / plan.tokens) * l.G;
   if (!plan.pair) {
@@ -128,7 +128,8 @@ constexpr int kBiasCols = 64;                        // columns of a block: 8 a 
 __global__ void __launch_bounds__(kBiasThreads)
     grad_bias_kernel(const __nv_bfloat16* __restrict__ grad, int64_t ld, const LinearParams l, float* __restrict__ out, int add) {
   __shared__ float part[kBiasThreads / 32][kBiasCols];
-  ops_begin();
+  if (l.beside) ops_beside();
+  else ops_begin();
   const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kBiasThreads / 32;
   const int blocks = (l.T + kBiasCols - 1) / kBiasCols, at = blockIdx.x / ranks;
@@ -181,10 +182,12 @@ __global__ void __launch_bounds__(kBiasThreads)
     float* o = out + (int64_t)g * l.T + n;
     *o = add ? *o + sum : sum;
   }
+  if (l.beside) ops_end_beside();
 }
 
-moe_status bias_grad(const Args* a, const void* grad, int64_t grad_stride, int sms, void* s) {
+moe_status bias_grad(const Args* a, const void* grad, int64_t grad_stride, bool beside, int sms, void* s) {
   LinearParams l = {};
+  l.beside = beside;
   l.T = a->fan_out;
   l.F = a->rows;
   l.G = std::max(1, a->groups);
@@ -370,8 +373,10 @@ extern "C" moe_status moe_async_linear_backward(const moe_async_linear_backward_
     grad = a->d_workspace;
   }
   if (r == MOE_OK && gx) r = a->x_dtype == MOE_F32 ? rows_grad<float>(a, grad, ld, sms, s) : rows_grad<__nv_bfloat16>(a, grad, ld, sms, s);
-  if (r == MOE_OK && gw) r = a->w_dtype == MOE_F32 ? weight_grad<float>(a, grad, ld, sms, s) : weight_grad<__nv_bfloat16>(a, grad, ld, sms, s);
-  if (r == MOE_OK && gb) r = bias_grad(a, grad, ld, sms, s);
+  // The three need nothing of each other: the first waits for what came before, the others run beside it as it leaves room.
+  if (r == MOE_OK && gw)
+    r = a->w_dtype == MOE_F32 ? weight_grad<float>(a, grad, ld, gx, sms, s) : weight_grad<__nv_bfloat16>(a, grad, ld, gx, sms, s);
+  if (r == MOE_OK && gb) r = bias_grad(a, grad, ld, gx || gw, sms, s);
   return r;
 }
 

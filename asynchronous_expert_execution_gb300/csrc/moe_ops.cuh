@@ -49,6 +49,11 @@ __device__ __forceinline__ void ops_begin() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// For a kernel that needs nothing of the one before it in the stream, an operator of the same call that began by ops_begin: what
+// came before that one is complete by the time this one is let start.  It runs beside it, and is complete only after it.
+__device__ __forceinline__ void ops_beside() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void ops_end_beside() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <typename... KArgs, typename... Args>
 moe_status launch_op(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster, void* stream,
                      Args... args) {

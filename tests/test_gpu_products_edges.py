@@ -171,6 +171,40 @@ def test_two_graphs_replayed_at_once(moe):
             assert all(torch.equal(p, q) for p, q in zip(o, r))
 
 
+@pytest.mark.parametrize("T,F,N,G", [(300, 264, 520, 0), (2048, 1024, 256, 0), (700, 520, 333, 5), (64, 2048, 2048, 0)])
+def test_what_comes_before_and_after_in_the_stream(moe, T, F, N, G):
+    """The three gradients of a call run beside each other, behind what made their inputs, and what follows finds all of them done: inputs
+    written just before, and overwritten by other operators just after, eagerly and in a graph."""
+    g = gen(T + N)
+    src = [randn((T, N), g, BF16), randn((T, F), g, BF16)]
+    w = randn((G, N, F) if G else (N, F), g, BF16)
+    offsets = torch.linspace(0, T, G + 1).int().cuda() if G else None
+    want = moe.linear_backward(*src, w, offsets, True, weight_dtype=F32)
+    torch.cuda.synchronize()
+    grad, x = (torch.zeros_like(t) for t in src)
+
+    def step():
+        for a, b in ((grad, src[0]), (x, src[1])):
+            moe.act_mul_backward(b, b, act="none", out_z=a)                  # grad_z = grad: a copy, as the operator before
+        r = moe.linear_backward(grad, x, w, offsets, True, weight_dtype=F32)
+        for t in (grad, x):                                                  # in place, by the operator behind
+            moe.act_mul_backward(t, torch.full_like(t, -1.0), act="relu", out_z=t)
+        return r, [t.clone() for t in r]
+
+    for _ in range(20):
+        r, copies = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(r, want)) and all(torch.equal(p, q) for p, q in zip(copies, want))
+        assert not bool(grad.any()) and not bool(x.any())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r, copies = step()
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(r, want)) and all(torch.equal(p, q) for p, q in zip(copies, want))
+
+
 @pytest.mark.parametrize("T", [1, 17, 64, 65, 129, 255, 256, 257, 300, 511, 513])
 @pytest.mark.parametrize("N", [255, 256, 264, 384, 520, 2050])
 def test_blocks_around_a_tile(moe, T, N):
