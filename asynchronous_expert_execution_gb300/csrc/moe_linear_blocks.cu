@@ -8,13 +8,13 @@
 // 128 e4m3 columns are one k-block (128 bytes, one swizzle atom), so every k-block's sum stands under one scale a token
 // and feature block.  The tensor cores sum a k-block into a TMEM buffer of its own, and the epilogue warps, while the
 // next ones are summed, bring it into their registers times sx sw: the sum over blocks is rounded in fp32 (the tensor
-// cores' own sums of four instructions are too short for their cut to show).  Features are the MMA's rows, as in the forward
-// product: a CTA's 128 features are one block of w's scales, so sx sw is one number a token, which a warp
-// lays into shared memory ahead of use.
+// cores' own sums of four instructions are too short for their cut to show).  128 features are one block of w's scales, so
+// sx sw is one number a token, which a warp lays into shared memory ahead of use.
 //
-//   pair   persistent, 256 features x up to 256 tokens over two SMs
-//   split  128 features x up to 64 tokens, K split over a cluster of up to 8 CTAs
+//   pair   persistent, 256 tokens x 256 features over two SMs, tokens on the MMA's rows; for many tokens
+//   split  128 features x up to 64 tokens, features on the MMA's rows as in the forward product, K split over a cluster of up to 8 CTAs
 //   few    up to 16 tokens on small weights, by warp-wide matrix instructions
+// 4096 x 7168 x 7168 in bf16 takes 175 us (2.4 PFLOP/s, 64% of twice the measured bf16 rate), 256 x 7168 x 2048 16, 4 x 7168 x 2048 5.3.
 #include "moe_linear.cuh"
 
 namespace moe {
@@ -41,7 +41,7 @@ struct Scales {
   int nfb;
 };
 
-constexpr int kBatch = 4;
+constexpr int kBatch = 4;                            // k-blocks whose factors are loaded together
 
 // A warp lays sx sw of `n` tokens from `row` on into shared memory, kBatch k-blocks to a slot, whose loads are in flight together.
 template <int SLOTS, int TOKENS, class Ready>

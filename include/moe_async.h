@@ -577,7 +577,8 @@ moe_status moe_async_linear_backward(const moe_async_linear_backward_args* args,
 /* Gradients of y = act(z) * mul (of y = act(z): d_mul and d_grad_mul NULL) from grad = dL/dy:
  *   grad_z = grad * mul * act'(z), grad_mul = grad * act(z), each [T, H] in dtype (MOE_F32 or MOE_BF16), rounded once
  * relu's slope is 0 at 0.  An output may be any of the inputs, in the same layout.  fp32 slopes of silu and gelu are within
- * 16 and 24 * 2^-24 of the sum of their terms' absolute values; for bf16 results both within 2^-14.  Asynchronous. */
+ * 24 * 2^-24 of the sum of their terms' absolute values (s + |z| s (1 - s), and Phi + |z| phi); for bf16 results within 2^-14.
+ * Asynchronous. */
 moe_status moe_async_act_mul_backward(int32_t dtype, int32_t act, const void* d_grad, int64_t grad_stride, const void* d_z, int64_t z_stride,
                                       const void* d_mul, int64_t mul_stride, int32_t T, int32_t H, void* d_grad_z, int64_t grad_z_stride,
                                       void* d_grad_mul, int64_t grad_mul_stride, void* stream);
