@@ -1214,11 +1214,11 @@ constexpr bool split_fits(int bn, bool own_sm) {
 }
 static_assert(split_fits(16, false) && split_fits(32, false) && split_fits(64, false) && split_fits(128, true), "shared memory of the split kernel");
 
-// CTAs of the split kernel, in clusters of s, that find an SM of their own: a cluster stays within its part of the
-// chip.  As many again share an SM with another.
-template <int MODE>
-int split_capacity(int s, int sms) {
-  static std::atomic<int> known[64][9];
+// CTAs of a split kernel, in clusters of s, that find an SM of their own: a cluster stays within its part of the
+// chip.  As many again share an SM with another.  `known`: the answers so far, by device.
+using Capacities = std::atomic<int>[64][9];
+template <class Kernel>
+int capacity_of(Kernel kernel, Capacities& known, int s, int sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return sms;
   int n = known[dev][s].load(std::memory_order_relaxed);
@@ -1233,13 +1233,17 @@ int split_capacity(int s, int sms) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const auto kernel = linear_split_kernel<false, __nv_bfloat16, MODE>;       // all forms share its limits
-  // the limit of launch_split: another thread may be launching this kernel
+  // the limit of the launches: another thread may be launching this kernel
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
     return sms;
   known[dev][s].store(n * s, std::memory_order_relaxed);
   return n * s;
+}
+template <int MODE>
+int split_capacity(int s, int sms) {
+  static Capacities known;
+  return capacity_of(linear_split_kernel<false, __nv_bfloat16, MODE>, known, s, sms);      // all forms share its limits
 }
 
 struct LinearPlan {

@@ -839,8 +839,8 @@ moe_status launch_few(const moe_async_linear_args* a, const LinearParams& l, con
 }
 
 int blocks_split_capacity(int s, int sms) {
-  // as split_capacity: clusters of s stay within their part of the chip
-  return s == 1 ? sms : split_capacity<kForward>(s, sms);
+  static Capacities known;
+  return s == 1 ? sms : capacity_of(linear_blocks_split_kernel<__nv_bfloat16, 64>, known, s, sms);
 }
 
 // Kernel, tile and split with the least expected time, in ns, from 25 shapes of 17 to 4096 tokens on 256 to 7168 features, dense and in 32
