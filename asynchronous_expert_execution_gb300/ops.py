@@ -145,8 +145,9 @@ def linear(x, weight, bias=None, act="none", mul=None, residual=None, offsets=No
 
 def quantize_blocks(x, out=None, stream=None):
     """(q, scale): x [T, F] fp32 or bf16 in e4m3 with a scale per 128 columns of a row, the operands x and x_scale of linear:
-    scale = max(max|x| / 448, 2^-126) of each block, q = x / scale, round to nearest.  scale is [T, ceil(F / 128)] with the tokens
-    adjacent in memory.  A block with an infinity or a NaN is NaN, and its scale."""
+    scale = max(max|x| / 448, 2^-126) of each block, q = x / scale, rounded to fp32 and then to nearest, as dividing in fp32
+    gives it.  scale is [T, ceil(F / 128)] with the tokens adjacent in memory.  A block with an infinity or a NaN is NaN, and its
+    scale."""
     return (_bound or _bind()).quantize_blocks(x, out, stream)
 
 

@@ -530,8 +530,9 @@ moe_status moe_async_linear(const moe_async_linear_args* args, void* stream);
  * Each block's products are summed on their own and added, scaled, with rounding in fp32.  Everything else as there. */
 moe_status moe_async_linear_blocks(const moe_async_linear_args* args, int64_t x_scale_row, int64_t x_scale_block, void* stream);
 
-/* The operands of moe_async_linear_blocks: each block's scale = max(max|x| / 448, 2^-126), stored value x / scale (times 1 / scale,
- * to nearest).  A block with an infinity or a NaN becomes NaN, and its scale.
+/* The operands of moe_async_linear_blocks: each block's scale = max(max|x| / 448, 2^-126), stored value x / scale, the
+ * quotient's fp32 rounding rounded to nearest (as dividing in fp32 gives it).  A block with an infinity or a NaN becomes NaN, and its
+ * scale.
  *   block_rows = 1   : blocks of 1 x 128; x [rows, width] (G = 1), scale of (t, b) at t * scale_row + b * scale_block
  *   block_rows = 128 : blocks of 128 x 128 of G matrices [rows, width], one behind another (rows * stride elements each), scale
  *                      [G, ceil(rows / 128), ceil(width / 128)] contiguous (scale_row and scale_block are not looked at); G and

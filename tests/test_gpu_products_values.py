@@ -1,0 +1,91 @@
+"""Values of the products' companions where rounding or the ends of the range decide them."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__ as g
+    g.build()
+    import asynchronous_expert_execution_gb300 as pkg
+    return pkg
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(shape, g, dtype=F32, scale=1.0):
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+# ------------------------------------------------------------------ quantisers
+
+def divided(x, rows):
+    """What the quantisers document, by elementary operations: scale = max(max|x| / 448, 2^-126), q = x / scale, to nearest."""
+    n, f = x.shape[-2:]
+    v = torch.nn.functional.pad(x.float(), (0, -f % 128, 0, -n % rows))
+    v = v.reshape(*v.shape[:-2], v.shape[-2] // rows, rows, v.shape[-1] // 128, 128)
+    s = (v.abs().amax((-3, -1)) / torch.full((), 448.0, device="cuda")).clamp(min=2.0 ** -126)         # by a number torch multiplies
+    q = (v / s[..., :, None, :, None]).flatten(-4, -3).flatten(-2)[..., :n, :f].to(E4M3)
+    return q, s
+
+
+def same(moe, x, rows):
+    q, s = moe.quantize_blocks(x) if rows == 1 else moe.quantize_weight_blocks(x)
+    want, ws = divided(x, rows)
+    assert torch.equal(s, ws)
+    off = q.view(torch.uint8) != want.view(torch.uint8)
+    assert not bool(off.any()), (int(off.sum()), q[off][:4].tolist(), want[off][:4].tolist(), x[off][:4].tolist())
+
+
+@pytest.mark.parametrize("shape,rows", [((300, 1040), 1), ((777, 2880), 1), ((5, 20001), 1), ((384, 1040), 128), ((3, 200, 584), 128), ((130, 257), 128)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantisers_divide(moe, shape, rows, dtype):
+    """Bit for bit the quotient, rounded once to fp32 and then to e4m3, as whoever divides gets it.  Nothing is left to a tolerance."""
+    g = gen(sum(shape) + rows)
+    same(moe, (randn(shape, g) * torch.exp(randn((*shape[:-1], 1), g))).to(dtype), rows)
+
+
+def test_quantisers_divide_every_bf16(moe):
+    """Every bf16 mantissa of a block's largest value against every mantissa of another, at every exponent that reaches e4m3's range:
+    448 = 7 * 64, so exact ties are common."""
+    m = 1 + torch.arange(128, device="cuda") / 128.0
+    down = torch.exp2(-torch.arange(0, 22, device="cuda").float())
+    other = (m[:, None] * down).reshape(-1)                                  # 2816 values
+    other = torch.nn.functional.pad(other, (0, -other.numel() % 127)).reshape(-1, 127)
+    for exponent in (0, -60, 60, -110, 110, 126, -120):                      # the scales' own range too
+        big = 2.0 * m * 2.0 ** exponent if exponent < 126 else m * 2.0 ** exponent
+        x = torch.empty((128, other.shape[0], 128), device="cuda")
+        x[:, :, 0] = big[:, None]
+        x[:, :, 1:] = other * 2.0 ** exponent
+        x = x.reshape(-1, 128).to(BF16)
+        same(moe, x, 1)
+        same(moe, x.float(), 1)
+        w = x.reshape(128, -1, 128)[::9]                                     # one largest value a block of 128 rows
+        for block in w:
+            same(moe, block[:128].contiguous(), 128)
+
+
+def test_quantisers_divide_beside_every_tie(moe):
+    """fp32 values on both sides of every border between two e4m3 values, under scales of any mantissa, those next to powers of two
+    and of few bits among them."""
+    g = gen(4)
+    values = torch.arange(0, 127, dtype=torch.uint8, device="cuda").view(E4M3).double()
+    ties = (values[1:] + values[:-1]) / 2                                    # 126
+    scale = torch.cat([torch.rand(3000, generator=g, device="cuda") + 1, 1 + torch.arange(0, 64, device="cuda") * 2.0 ** -23,
+                       2 - torch.arange(1, 64, device="cuda") * 2.0 ** -23, 1 + torch.arange(0, 128, device="cuda") / 128.0])
+    largest = (scale.double() * 448).float()
+    s = (largest / torch.full((), 448.0, device="cuda")).double()
+    for step in (-2, -1, 0, 1, 2):
+        x = torch.zeros((scale.numel(), 128), device="cuda")
+        near = (ties * s[:, None]).float()
+        x[:, 1:127] = (near.view(torch.int32) + step).view(torch.float32)
+        x[:, 0] = largest
+        same(moe, x, 1)
