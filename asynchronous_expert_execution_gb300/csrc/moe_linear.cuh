@@ -72,14 +72,15 @@ struct LinearParams {
 };
 
 // Bounded wait; false once it ran out or another role gave up.
+template <Order O = kCta>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   for (int i = 0; i < 4; ++i)
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try<O>(bar, parity)) return true;
   constexpr int kTries = 16;                         // between two looks at the clock, which is slow to read
   const unsigned long long t0 = now_ns();
   while (true) {
     for (int i = 0; i < kTries; ++i)
-      if (mbar_try(bar, parity)) return true;
+      if (mbar_try<O>(bar, parity)) return true;
     if (*abort_flag) return false;
     if (now_ns() - t0 > kLimitNs) {
       *abort_flag = 1;
@@ -129,24 +130,36 @@ __device__ __forceinline__ void load_across(uint32_t dst, const CUtensorMap* m, 
   for (int i = 0; i < cols; i += 64) tma_2d<CG>(dst + i * kBKBytes, m, bar, c + i, row0 + kb * kBoxRows);
 }
 
+// kWeightGrad over two CTAs, a group's last k-block: `cols` columns from c of the group's last `live` rows, from `row` on, behind 64 - live
+// rows of zeros.  Behind the group's end lie rows of the next group or of none, with any content, so the copy itself has to know the end:
+// the map's rows are a window of 64 over all rows (encode_window), entered at a negative place, which brings zeros.  All of a pair's operands
+// come by copies that its leader waits for.  (The block as it lies there, and a warp of either CTA that clears the rows behind the end
+// and tells the leader, wants a release over the cluster, which waits for all that the thread has under way: 32 experts 8192 x 2880 x
+// 2880 took 287 us in fp32; boxes of 1, 2, 4 .. rows and of zeros 307.)
+__device__ __forceinline__ void load_end(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c, int cols, int row, int live) {
+  for (int i = 0; i < cols; i += 64) tma_3d<2>(dst + i * kBKBytes, m, bar, c + i, live - kBoxRows, row);
+}
+
 template <int MODE>
 __device__ __forceinline__ uint64_t a_desc(uint32_t saddr) { return MODE == kForward ? operand_desc(saddr) : across_desc(saddr, kBox); }
 template <int MODE>
 __device__ __forceinline__ uint64_t b_desc(uint32_t saddr) { return MODE == kWeightGrad ? across_desc(saddr, kBox) : operand_desc(saddr); }
 
-// The products of one k-block; `live`: rows of K that it holds (kWeightGrad: 16 a product, those behind are left out).
+// The products of one k-block; `live`: rows of K that it holds (kWeightGrad: 16 a product, the others are left out), its first ones in
+// one CTA, its last ones in a pair.
 template <int CG, int MODE, bool E4M3>
 __device__ __forceinline__ void product_block(uint32_t d, uint32_t smem, uint32_t idesc, bool accumulate, int live) {
   const uint64_t a = a_desc<MODE>(smem), b = b_desc<MODE>(smem + kABlock);
   if (MODE == kWeightGrad && live <= kBoxRows - 16) {
-    for (int i = 0; 16 * i < live; ++i) mma<CG, E4M3>(d, a + 128 * i, b + 128 * i, idesc, accumulate || i > 0);
+    const int n = (live + 15) / 16, first = CG == 2 ? kBoxRows / 16 - n : 0;
+    for (int i = first; i < first + n; ++i) mma<CG, E4M3>(d, a + 128 * i, b + 128 * i, idesc, accumulate || i > first);
   } else {
     mma_block<CG, E4M3, MODE != kForward, MODE == kWeightGrad>(d, a, b, idesc, accumulate);
   }
 }
 
-// kWeightGrad, by a whole warp: the last k-block of a group holds `live` rows of it, and behind them rows of the next group or
-// of none, with any content.  Those that a product of 16 rows would still reach become zeros in both operands.
+// kWeightGrad in one CTA, by a whole warp: the last k-block of a group holds `live` rows of it, and behind them rows of the next
+// group or of none, with any content.  Those that a product of 16 rows would still reach become zeros in both operands.
 __device__ __forceinline__ void clear_rows(uint8_t* stage, int boxes, int live) {
   // a row's eight units of 16 bytes by adjacent lanes, four rows at a time; no divisions: the products wait for this
   const int lane = threadIdx.x % 32, end = (live + 15) / 16 * 16;
@@ -597,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_split_kernel(const __grid_
         bulk_to_cluster(mapa(smem_u32(got + rank * share), lane), smem_u32(own + i0 * kBM), share * 4,
                         mapa(smem_u32(&s->got), lane));
     }
-    if (nj > 0) wait(&s->got, 0, abort_flag);
+    if (nj > 0) wait<kCluster>(&s->got, 0, abort_flag);
   } else {
     __syncthreads();
   }
@@ -641,7 +654,7 @@ struct Divide {
 };
 
 struct PairParams {
-  CUtensorMap w, x[4];              // x: boxes of 16, 32, 64 and tokens / 2 rows
+  CUtensorMap w, x[4];              // x: boxes of 16, 32, 64 and tokens / 2 rows; kWeightGrad: whole k-blocks, w's and x's last ones (load_end)
   LinearParams l;
   CUtensorMap y;                    // kWeightGrad, boxed: the result, boxes of half a tile's rows x 32 features
   bool boxed;
@@ -654,9 +667,8 @@ struct PairParams {
 struct PairTail {
   static constexpr int kMaxStages = 10;
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[4], tempty[4];
-  // kWeightGrad: this CTA's part of a k-block that has to be cleared, and the tiles that a warp tells the others
-  static constexpr int kTold = 4;
-  uint64_t own[kMaxStages], told[kTold], heard[kTold];
+  static constexpr int kTold = 4;                    // kWeightGrad: the tiles that a warp tells the others
+  uint64_t told[kTold], heard[kTold];
   uint64_t old[8];                  // an epilogue warp's box of what is added to
   int4 tile[kTold][2];
   uint32_t tmem;
@@ -838,10 +850,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     prefetch_map(&p.w);
     prefetch_map(&p.x[kAcross ? 0 : 3]);
     for (int i = 0; i < p.stages; ++i) {
-      // the leader's producer, for both CTAs' bytes (kWeightGrad: twice, or either CTA's clearing warp)
-      mbar_init(&s->full[i], kAcross ? 2 : 1);
+      mbar_init(&s->full[i], 1);                     // the leader's producer, for both CTAs' bytes
       mbar_init(&s->empty[i], 1);                    // the MMA's commit, in both CTAs
-      if (kAcross) mbar_init(&s->own[i], 1);
     }
     for (int b = 0; b < kAccs; ++b) {
       mbar_init(&s->tfull[b], 1);
@@ -850,7 +860,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (kAcross)
       for (int i = 0; i < PairTail::kTold; ++i) {
         mbar_init(&s->told[i], 1);
-        mbar_init(&s->heard[i], rank == 0 ? 11 : 10);              // all warps but the telling one and the second CTA's idle one
+        mbar_init(&s->heard[i], rank == 0 ? 10 : 9);               // all warps but the telling and the idle ones
       }
     if (kAcross)
       for (int i = 0; i < 8; ++i) mbar_init(&s->old[i], 1);
@@ -907,42 +917,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     while (__all_sync(0xffffffffu, ok) && next_tile()) {
       if (!elect()) continue;
-      const int block = kABlock + tl.brows * kBKBytes;
       const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
       const int nk = kAcross ? tl.nk : l.nk;
       for (int kb = 0; kb < nk; ++kb) {
-        if (!(ok = wait(&s->empty[st], phase, abort_flag))) break;
-        const uint32_t a = smem_u32(smem + st * p.stage_bytes);
-        const bool clear = kAcross && kb == nk - 1 && tl.sum % 16;
-        const uint32_t bar = clear ? smem_u32(&s->own[st]) : mapa(smem_u32(&s->full[st]), 0);
-        if (clear) {
-          mbar_expect(&s->own[st], block);
-        } else if (rank == 0) {
-          if (kAcross) mbar_arrive(&s->full[st]);
-          mbar_expect(&s->full[st], 2 * block);
+        if (!(ok = wait<kCluster>(&s->empty[st], phase, abort_flag))) break;
+        const uint32_t a = smem_u32(smem + st * p.stage_bytes), bar = mapa(smem_u32(&s->full[st]), 0);
+        if (rank == 0) mbar_expect(&s->full[st], 2 * (kABlock + tl.brows * kBKBytes));
+        if (kAcross && tl.sum - kb * kBoxRows < kBoxRows) {
+          load_end(a, &p.x[1], bar, wrow, kBM, tl.sum0 + kb * kBoxRows, tl.sum - kb * kBoxRows);
+          load_end(a + kABlock, &p.x[2], bar, xrow, tl.brows, tl.sum0 + kb * kBoxRows, tl.sum - kb * kBoxRows);
+        } else {
+          load_a<2, MODE, E4M3>(a, &p.w, bar, kb, wrow, tl.g, kAcross ? tl.sum0 : 0);
+          if constexpr (kAcross)
+            load_across<2>(a + kABlock, &p.x[0], bar, kb, xrow, tl.brows, tl.sum0);
+          else
+            tma_2d<2>(a + kABlock, &p.x[tl.box], bar, kb * kElems, xrow);
         }
-        load_a<2, MODE, E4M3>(a, &p.w, bar, kb, wrow, tl.g, kAcross ? tl.sum0 : 0);
-        if constexpr (kAcross)
-          load_across<2>(a + kABlock, &p.x[0], bar, kb, xrow, tl.brows, tl.sum0);
-        else
-          tma_2d<2>(a + kABlock, &p.x[tl.box], bar, kb * kElems, xrow);
         if (++st == p.stages) st = 0, phase ^= 1;
       }
-    }
-  } else if (kAcross && warp == 2) {
-    // A group's last k-block lands on each CTA's own barrier, if it ends inside 16 rows: what lies behind the end is cleared, and both
-    // CTAs tell the leader's barrier.
-    uint32_t at = 0, phases = 0;                     // k-blocks before; the stages' phases
-    while (next_tile()) {
-      at = (at + tl.nk) % p.stages;
-      if (tl.sum % 16 == 0) continue;
-      const uint32_t st = (at + p.stages - 1) % p.stages;
-      if (!__all_sync(0xffffffffu, wait(&s->own[st], phases >> st & 1, abort_flag))) break;
-      phases ^= 1u << st;
-      clear_rows(smem + st * p.stage_bytes, 2 + tl.brows / 64, tl.sum - (tl.nk - 1) * kBoxRows);
-      // behind the fence the zeros are in this CTA's shared memory, where the leader's products read them: no release over the cluster,
-      // which waited for all that this thread had under way (32 experts 8192 x 2880 x 2880: fp32 287 -> 243 us, bf16 180 -> 159)
-      if (lane == 0) mbar_arrive_light(mapa(smem_u32(&s->full[st]), 0));
     }
   } else if (kAcross && warp == 3) {
     bool more = true;
@@ -970,13 +962,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (in == chunk) {
           if (kb > 0) commit<2>(&s->tfull[buf]);
           buf = acc % kAccs;
-          if (!(ok = wait(&s->tempty[buf], ((acc / kAccs) & 1) ^ 1, abort_flag))) break;
+          if (!(ok = wait<kTmem>(&s->tempty[buf], ((acc / kAccs) & 1) ^ 1, abort_flag))) break;
           tc_after();
           ++acc;
           in = 0;
         }
         const bool last = kAcross && kb == nk - 1;
-        if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
+        if (!(ok = wait<kCluster>(&s->full[st], phase, abort_flag))) break;
         tc_after();
         product_block<2, MODE, E4M3>(tmem + buf * kTokens, smem_u32(smem + st * p.stage_bytes), idesc, in > 0,
                                      last ? tl.sum - kb * kBoxRows : kBoxRows);
@@ -995,7 +987,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     constexpr bool kSums = sizeof(TO) == 4;
     constexpr int kStep = 2 * kChunk;
     auto acc_wait = [&](int buf, uint32_t n) {
-      const bool ok = wait(&s->tfull[buf], (n / kAccs) & 1, abort_flag);
+      const bool ok = wait<kTmem>(&s->tfull[buf], (n / kAccs) & 1, abort_flag);
       const bool all = __all_sync(0xffffffffu, ok);
       tc_after();
       return all;
@@ -1181,6 +1173,17 @@ bool encode(CUtensorMap* m, const void* base, int size, int width, int rows, int
   return fn(m, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, groups > 0 ? 3 : 2,
             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Every row of a [rows][width] bf16 matrix as the first of a window of 64 rows, boxes of 128 bytes x a window, 128-byte swizzle, zeros
+// outside the window: element (c, a, b) is column c of row a + b.  (Windows that reach behind the last row are entered before it only.)
+bool encode_window(CUtensorMap* m, const void* base, int width, int rows, int64_t ld) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, kBoxRows, (cuuint64_t)rows}, strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t box[3] = {kBKBytes / 2, kBoxRows, 1}, step[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // [groups][rows][width] results, boxes of kBoxTokens rows x 32 elements without swizzle.

@@ -7,8 +7,7 @@
 //
 // Both products run on the forward product's kernels (moe_linear.cuh): w lies across grad_x's sum, and both
 // operands of grad_w across its own, so the operands stay as they lie in memory and the tensor cores read them
-// transposed.  grad_w's sum is as long as the group has rows: the last k-block's rows behind the group's end are
-// cleared in shared memory.
+// transposed.  grad_w's sum is as long as the group has rows: its last k-block is filled up with zeros.
 #include "moe_linear.cuh"
 
 namespace moe {
@@ -112,6 +111,7 @@ moe_status weight_grad(const Args* a, const void* grad, int64_t grad_stride, boo
   PairParams p;
   if (!encode(&p.w, a->d_x, 2, a->fan_in, a->rows, a->x_stride, 0, kBoxRows) || !encode(&p.x[0], grad, 2, a->fan_out, a->rows, grad_stride, 0, kBoxRows))
     return MOE_ERR_CUDA;
+  if (!encode_window(&p.x[1], a->d_x, a->fan_in, a->rows, a->x_stride) || !encode_window(&p.x[2], grad, a->fan_out, a->rows, grad_stride)) return MOE_ERR_CUDA;
   p.boxed = wide;                                    // unless rows start off 16-byte boundaries
   if (p.boxed && !encode_result<TO>(&p.y, a->d_grad_w, a->fan_in, a->fan_out, a->grad_w_stride, l.G)) return MOE_ERR_CUDA;
   return launch_pair<TO, kWeightGrad>(p, l, plan.tokens, sms, s);

@@ -158,7 +158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!elect()) continue;
         const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * kBM;
         for (int kb = 0; kb < l.nk; ++kb) {
-          if (!(ok = wait(&s->empty[st], phase, abort_flag))) break;
+          if (!(ok = wait<kCluster>(&s->empty[st], phase, abort_flag))) break;
           const uint32_t a = smem_u32(smem + st * kStage), bar = mapa(smem_u32(&s->full[st]), 0);
           if (rank == 0) mbar_expect(&s->full[st], 2 * kStage);
           tma_2d<2>(a, &p.x[3], bar, kb * kBKBytes, xrow);
@@ -173,10 +173,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       while (__all_sync(0xffffffffu, ok) && walk.next<kForward>(p, tl)) {
         if (!elect()) continue;
         for (int kb = 0; kb < l.nk; ++kb, ++acc) {
-          if (!(ok = wait(&s->full[st], phase, abort_flag))) break;
+          if (!(ok = wait<kCluster>(&s->full[st], phase, abort_flag))) break;
           const uint64_t a = operand_desc(smem_u32(smem + st * kStage));
           const int buf = acc & 1;
-          if (!(ok = wait(&s->tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag))) break;
+          if (!(ok = wait<kTmem>(&s->tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag))) break;
           tc_after();
           mma_block<2, true>(tmem + buf * 2 * kBM, a, a + (kABlock >> 4), idesc, false);
           commit<2>(&s->empty[st]);
@@ -264,7 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const float* factor = &s->factor[from][0][half][32 * q + lane];
         for (int end = left - min(kBatch, left), at = left; at > end; --at, ++n, factor += 2 * kBM) {
           const int buf = n & 1;
-          if (!(ok = __all_sync(0xffffffffu, wait(&s->tfull[buf], (n >> 1) & 1, abort_flag)))) break;
+          if (!(ok = __all_sync(0xffffffffu, wait<kTmem>(&s->tfull[buf], (n >> 1) & 1, abort_flag)))) break;
           tc_after();
           d0 = lanes + buf * 2 * kBM;
           const float f = *factor;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_blocks_split_kernel(const 
       if (share > 0)
         bulk_to_cluster(mapa(smem_u32(got + rank * share), lane), smem_u32(own + i0 * kBM), share * 4, mapa(smem_u32(&s->got), lane));
     }
-    if (nj > 0) wait(&s->got, 0, abort_flag);
+    if (nj > 0) wait<kCluster>(&s->got, 0, abort_flag);
   } else {
     __syncthreads();
   }

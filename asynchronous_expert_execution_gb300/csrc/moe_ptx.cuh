@@ -17,15 +17,14 @@ __device__ __forceinline__ void mbar_init_fence() { asm volatile("fence.mbarrier
 __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-// Arrive on a barrier of this CTA, or of any CTA of the cluster (address from mapa), behind reads and what this thread wrote to its own
-// shared memory.  No release over the cluster: it waits for all that a thread has under way, and took 0.7 us a k-block.
+// Arrive on a barrier of this CTA, behind reads and what this thread wrote to its shared memory.
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_light(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// arrive without any order over memory: for a buffer in TMEM, behind tcgen05.wait::ld, when what was read is in registers
+// Arrive on a barrier of any CTA of the cluster (address from mapa) without an order over memory: for a buffer in TMEM, between
+// tcgen05.wait::ld, when what was read is in registers, with tcgen05.fence::before_thread_sync, and the other side's fence::after.  No
+// thread tells another CTA that it wrote to shared memory: that would take a release over the cluster, which waits for all that a
+// thread has under way (0.7 us a k-block).
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -37,17 +36,25 @@ __device__ __forceinline__ bool elect() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one)::"memory");
   return one != 0;
 }
-// Nor an acquire over it, which takes some 200 cycles even where the phase is long over: what is waited for comes by TMA, bulk
-// copies and tcgen05.
+// What a wait orders.  kCta: the barrier's arrivals and copies are this CTA's.  kCluster: copies or products of another CTA of the cluster
+// arrive too, and what they read or wrote in shared memory is next.  kTmem: the same where only TMEM is next: the tcgen05 fences on
+// both sides are the order, the barrier needs none.
+enum Order { kCta, kCluster, kTmem };
+template <Order O = kCta>
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+#define MOE_TRY(ORDER)                                                                \
+  asm volatile(                                                                       \
+      "{\n\t.reg .pred p;\n\t"                                                       \
+      "mbarrier.try_wait.parity." ORDER ".shared::cta.b64 p, [%1], %2;\n\t"           \
+      "selp.u32 %0, 1, 0, p;\n\t}"                                                   \
+      : "=r"(ok)                                                                      \
+      : "r"(smem_u32(bar)), "r"(parity)                                               \
+      : "memory")
+  if constexpr (O == kCta) MOE_TRY("acquire.cta");
+  if constexpr (O == kCluster) MOE_TRY("acquire.cluster");
+  if constexpr (O == kTmem) MOE_TRY("relaxed.cluster");
+#undef MOE_TRY
   return ok != 0;
 }
 __device__ __forceinline__ unsigned long long now_ns() {
