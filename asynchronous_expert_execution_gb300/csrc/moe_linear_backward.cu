@@ -245,6 +245,15 @@ __device__ __forceinline__ void act_and_slope(int act, float z, float& y, float&
   }
 }
 
+// a b slope, the larger factor first: a b may lie outside fp32 where the result, of a slope of 0 say, does not.  The sign goes with the
+// larger one; NaN stays.
+__device__ __forceinline__ float triple(float a, float b, float slope) {
+  float large, small;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(large) : "f"(a), "f"(b));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(small) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return large * slope * small;
+}
+
 template <typename T> struct ActParams {
   Rows<const T> grad, z, mul;
   Rows<T> grad_z, grad_mul;
@@ -282,7 +291,7 @@ __global__ void __launch_bounds__(256) act_mul_backward_kernel(const ActParams<T
     for (int i = 0; i < V; ++i) {
       float y, slope;
       act_and_slope<T>(p.act, zv[i], y, slope);
-      oz[i] = (MUL ? gv[i] * mv[i] : gv[i]) * slope;
+      oz[i] = MUL ? triple(gv[i], mv[i], slope) : gv[i] * slope;
       om[i] = gv[i] * y;
     }
     RV::store(p.grad_z.at(row) + c, RV::pack(oz));

@@ -576,7 +576,8 @@ int64_t moe_async_linear_backward_workspace(const moe_async_linear_backward_args
 moe_status moe_async_linear_backward(const moe_async_linear_backward_args* args, void* stream);
 
 /* Gradients of y = act(z) * mul (of y = act(z): d_mul and d_grad_mul NULL) from grad = dL/dy:
- *   grad_z = grad * mul * act'(z), grad_mul = grad * act(z), each [T, H] in dtype (MOE_F32 or MOE_BF16), rounded once
+ *   grad_z = grad * mul * act'(z), grad_mul = grad * act(z), each [T, H] in dtype (MOE_F32 or MOE_BF16), rounded once (finite where
+ *   the result is: grad * mul alone may lie outside fp32)
  * relu's slope is 0 at 0.  An output may be any of the inputs, in the same layout.  fp32 slopes of silu and gelu are within
  * 24 * 2^-24 of the sum of their terms' absolute values (s + |z| s (1 - s), and Phi + |z| phi); for bf16 results within 2^-14.
  * Asynchronous. */

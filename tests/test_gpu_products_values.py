@@ -1,4 +1,6 @@
 """Values of the products' companions where rounding or the ends of the range decide them."""
+import math
+
 import pytest
 import torch
 
@@ -89,3 +91,45 @@ def test_quantisers_divide_beside_every_tie(moe):
         x[:, 1:127] = (near.view(torch.int32) + step).view(torch.float32)
         x[:, 0] = largest
         same(moe, x, 1)
+
+
+# ------------------------------------------------------------------ the epilogue's gradient
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+def test_products_beyond_the_range_on_the_way(moe, dtype, act):
+    """grad * mul may lie outside the type where grad * mul * act'(z) does not: a slope of 0 gives 0, and small slopes or factors a finite
+    result.  The slope's terms' absolute values are at most 2.1 times the slope here (silu at -3), and it is within 24 u of them, u = 2^-24, or
+    2^-14 in bf16; two products and the last rounding more: 55 u < 2^-18, or 2^-8 + 2^-12 < 2^-7 of the value."""
+    z = torch.tensor([[-3.0, -8.0, -60.0, 5.0, -3.0, -12.0, 2.0, -2000.0]], device="cuda")
+    grad = torch.tensor([[1e30, 1e25, 1e30, 1e-30, 1e-30, 1e22, 3e38, 1e30]], device="cuda")
+    mul = torch.tensor([[1e9, 1e14, 1e30, 1e-14, 1e-9, 1e18, 0.5, 1e30]], device="cuda")
+    t = lambda v: v.to(dtype)   # noqa: E731
+    for a, b in ((grad, mul), (mul, grad)):
+        gz, gm = moe.act_mul_backward(t(a), t(z), t(b), act)
+        zd, ab = t(z).double(), t(a).double() * t(b).double()
+        if act == "silu":
+            slope, big = torch.sigmoid(zd) * (1 + zd * torch.sigmoid(-zd)), zd.abs()
+        elif act == "gelu":
+            slope = 0.5 * torch.erfc(-zd * math.sqrt(0.5)) + zd * torch.exp(-0.5 * zd * zd) / math.sqrt(2 * math.pi)
+        else:
+            slope = (zd > 0).double()
+        want = ab * slope
+        inside = want.abs() < 3.3e38
+        assert int(inside.sum()) >= 5 and not bool(gz.isnan().any())
+        assert bool(gz[~inside].isinf().all()) and bool((gz[inside].sign() == want[inside].sign()).logical_or(want[inside].abs() < 1e-37).all())
+        off = (gz[inside].double() - want[inside]).abs()
+        assert bool((off <= (2.0 ** -7 if dtype == BF16 else 2.0 ** -18) * want[inside].abs() + 1e-37).all()), (gz.tolist(), want.tolist())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_nan_and_infinity_in_either_factor(moe, dtype):
+    """As the product of the three says: NaN from NaN, and from an infinity times 0, in either order."""
+    nan, inf = float("nan"), float("inf")
+    a = torch.tensor([[nan, 1.0, inf, inf, -inf, inf, -2.0, 0.0, -0.5]], device="cuda").to(dtype)
+    b = torch.tensor([[1.0, nan, 0.0, -2.0, -inf, 3.0, 4.0, -3.0, -4.0]], device="cuda").to(dtype)
+    z = torch.tensor([[1.0, 1.0, 1.0, 1.0, 1.0, -1.0, 1.0, 1.0, 1.0]], device="cuda").to(dtype)
+    for x, y in ((a, b), (b, a)):
+        gz, _ = moe.act_mul_backward(x, z, y, "relu")
+        assert gz.isnan().tolist()[0] == [True, True, True, False, False, True, False, False, False]
+        assert gz[0, 3:5].tolist() == [-inf, inf] and gz[0, 6:].tolist() == [-8.0, 0.0, 2.0]
