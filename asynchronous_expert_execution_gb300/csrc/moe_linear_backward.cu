@@ -368,6 +368,12 @@ extern "C" moe_status moe_async_linear_backward(const moe_async_linear_backward_
     if (!a->d_workspace || !aligned16(a->d_workspace)) return MOE_ERR_INVALID;
     if (a->workspace_bytes < need) return MOE_ERR_CAPACITY;
   }
+  // the three run beside each other: what one writes, the others must not read
+  const void* const in[] = {a->d_grad, gw ? a->d_x : nullptr, gx ? a->d_w : nullptr, a->d_workspace};
+  for (const void* i : in)
+    if (i && (i == a->d_grad_x || i == a->d_grad_w || i == a->d_grad_bias)) return MOE_ERR_INVALID;
+  if ((gw && (a->d_grad_w == a->d_grad_x || a->d_grad_w == a->d_residual)) || (gb && (a->d_grad_bias == a->d_grad_x || a->d_grad_bias == a->d_grad_w)))
+    return MOE_ERR_INVALID;
   const int sms = sm_count();
   if (sms < 2) return MOE_ERR_CUDA;
   const void* grad = a->d_grad;
@@ -397,7 +403,8 @@ extern "C" moe_status moe_async_act_mul_backward(int32_t dtype, int32_t act, con
       (d_mul != nullptr) != (d_grad_mul != nullptr))
     return MOE_ERR_INVALID;
   if (T == 0) return MOE_OK;
-  if (!d_grad || !d_z || !d_grad_z || grad_stride < H || z_stride < H || grad_z_stride < H || (d_mul && (mul_stride < H || grad_mul_stride < H)))
+  if (!d_grad || !d_z || !d_grad_z || grad_stride < H || z_stride < H || grad_z_stride < H || (d_mul && (mul_stride < H || grad_mul_stride < H)) ||
+      d_grad_z == d_grad_mul)
     return MOE_ERR_INVALID;
   return dtype == MOE_F32 ? act_backward<float>(act, d_grad, grad_stride, d_z, z_stride, d_mul, mul_stride, T, H, d_grad_z, grad_z_stride, d_grad_mul,
                                                 grad_mul_stride, stream)

@@ -165,7 +165,7 @@ def linear_backward(grad, x=None, weight=None, offsets=None, bias=False, residua
     grad_x = grad @ weight + residual [T, F], if weight is given; grad_weight = grad.T @ x [N, F], if x is given; grad_bias fp32
     [N], if `bias`.  Sums in fp32, rounded once to out_x's type (or out_dtype, or bf16; the residual's too) and to out_weight's
     (or weight_dtype, or bf16).  accumulate=True adds grad_weight and grad_bias to what out_weight and out_bias hold.
-    `out_x` may be `residual`.  With offsets (int32 [G + 1]) as in linear: weight and grad_weight [G, N, F], grad_bias [G, N];
+    `out_x` may be `residual`; else the outputs lie apart from each other and from grad, x and weight.  With offsets (int32 [G + 1]) as in linear: weight and grad_weight [G, N, F], grad_bias [G, N];
     rows of no group count nowhere, and in out_x are left as they were (in a new matrix: not set).
     An epilogue's gradient comes first: act_mul_backward."""
     return (_bound or _bind()).linear_backward(grad, x, weight, offsets, bias, residual, out_dtype, weight_dtype, out_x, out_weight, out_bias,
@@ -175,7 +175,7 @@ def linear_backward(grad, x=None, weight=None, offsets=None, bias=False, residua
 def act_mul_backward(grad, z, mul=None, act="silu", out_z=None, out_mul=None, stream=None):
     """Gradients of act(z) * mul (or act(z)): (grad_z, grad_mul) = (grad * mul * act'(z), grad * act(z)), the second None
     without mul.  grad, z, mul [T, H] fp32 or bf16; act as in linear; relu's slope at 0 is 0.  `out_z` and `out_mul` may be
-    any of the three."""
+    any of the three, each another."""
     return (_bound or _bind()).act_mul_backward(grad, z, mul, _act(act), out_z, out_mul, stream)
 
 

@@ -547,8 +547,8 @@ moe_status moe_async_quantize_blocks(int32_t dtype, const void* d_x, int64_t x_s
  *   grad_w[n, k]    = sum_t grad[t, n] x[t, k]
  *   grad_bias[n]    = sum_t grad[t, n]
  * (an epilogue's gradient comes first: moe_async_act_mul_backward).  Operands are bf16, sums fp32, results rounded
- * once.  Each of the three is computed if its pointer is given; accumulate != 0 adds grad_w and grad_bias to what
- * they hold.
+ * once.  Each of the three is computed if its pointer is given, and lies apart from the others and from the operands (where one
+ * is another, MOE_ERR_INVALID); accumulate != 0 adds grad_w and grad_bias to what they hold.
  *   d_grad : [rows, fan_out]     d_x : [rows, fan_in], for grad_w     d_w : [fan_out, fan_in], for grad_x
  *   d_grad_x : [rows, fan_in] in x_dtype, d_residual in the same or NULL; it may be grad_x itself
  *   d_grad_w : [fan_out, fan_in] in w_dtype           d_grad_bias : [fan_out] fp32
@@ -578,7 +578,7 @@ moe_status moe_async_linear_backward(const moe_async_linear_backward_args* args,
 /* Gradients of y = act(z) * mul (of y = act(z): d_mul and d_grad_mul NULL) from grad = dL/dy:
  *   grad_z = grad * mul * act'(z), grad_mul = grad * act(z), each [T, H] in dtype (MOE_F32 or MOE_BF16), rounded once (finite where
  *   the result is: grad * mul alone may lie outside fp32)
- * relu's slope is 0 at 0.  An output may be any of the inputs, in the same layout.  fp32 slopes of silu and gelu are within
+ * relu's slope is 0 at 0.  An output may be any of the inputs, in the same layout, but not the other output.  fp32 slopes of silu and gelu are within
  * 24 * 2^-24 of the sum of their terms' absolute values (s + |z| s (1 - s), and Phi + |z| phi); for bf16 results within 2^-14.
  * Asynchronous. */
 moe_status moe_async_act_mul_backward(int32_t dtype, int32_t act, const void* d_grad, int64_t grad_stride, const void* d_z, int64_t z_stride,

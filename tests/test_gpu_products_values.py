@@ -133,3 +133,33 @@ def test_nan_and_infinity_in_either_factor(moe, dtype):
         gz, _ = moe.act_mul_backward(x, z, y, "relu")
         assert gz.isnan().tolist()[0] == [True, True, True, False, False, True, False, False, False]
         assert gz[0, 3:5].tolist() == [-inf, inf] and gz[0, 6:].tolist() == [-8.0, 0.0, 2.0]
+
+
+def test_one_tensor_for_both_outputs_is_refused(moe):
+    g = gen(3)
+    grad, z, mul = (randn((40, 64), g, BF16) for _ in range(3))
+    for t in (z, torch.empty_like(z)):
+        with pytest.raises(moe.MoEError):
+            moe.act_mul_backward(grad, z, mul, out_z=t, out_mul=t)
+    both = torch.empty((40, 128), dtype=BF16, device="cuda")                 # two halves of one matrix are two outputs
+    a, b = moe.act_mul_backward(grad, z, mul, out_z=both[:, :64], out_mul=both[:, 64:])
+    c, d = moe.act_mul_backward(grad, z, mul)
+    assert torch.equal(a, c) and torch.equal(b, d)
+
+
+def test_gradients_over_operands_are_refused(moe):
+    """The three gradients of a call run beside each other: none is written over what another reads."""
+    g = gen(6)
+    grad, x, w = randn((64, 64), g, BF16), randn((64, 64), g, BF16), randn((64, 64), g, BF16)
+    kept = grad.clone(), x.clone(), w.clone()
+    for kw in (dict(out_x=x), dict(out_x=grad), dict(out_x=w), dict(residual=x, out_x=x), dict(out_weight=x), dict(out_weight=grad), dict(out_weight=w),
+               dict(residual=x.clone(), out_weight=w, accumulate=True)):
+        with pytest.raises(moe.MoEError):
+            moe.linear_backward(grad, x, w, **kw)
+    same_place = torch.empty_like(x)
+    with pytest.raises(moe.MoEError):
+        moe.linear_backward(grad, x, w, out_x=same_place, out_weight=same_place)
+    assert all(torch.equal(p, q) for p, q in zip(kept, (grad, x, w)))
+    a = moe.linear_backward(grad, x, w, residual=x)                          # read by two is fine
+    b = moe.linear_backward(x, x, w, residual=x)
+    assert torch.equal(a[0], moe.linear_backward(grad, None, w, residual=x, out_x=x.clone())[0]) and torch.equal(b[1], moe.linear_backward(x, x.clone())[1])
