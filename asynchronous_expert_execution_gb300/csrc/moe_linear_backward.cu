@@ -121,6 +121,11 @@ moe_status weight_grad(const Args* a, const void* grad, int64_t grad_stride, boo
 
 constexpr int kBiasThreads = 256;
 constexpr int kBiasCols = 64;                        // columns of a block: 8 a lane, four rows a warp
+constexpr int kBiasAhead = 8, kBiasRanks = 8;        // rows of a lane in flight; CTAs that share a group's rows, at most
+// Rows are counted in 32 bits, and the walk over them ends up to this far behind the last one.
+constexpr int kBiasStep = kBiasRanks * (kBiasThreads / 32) * 4 * kBiasAhead;
+constexpr int kMaxRows = INT32_MAX - 4096;
+static_assert((int64_t)kMaxRows + 2 * kBiasStep <= INT32_MAX && (int64_t)kMaxRows + 1024 <= INT32_MAX, "the bias's rows, and the products' tiles");
 
 // Column sums of a group's rows, bound by their one read.  A cluster takes 64 columns of a group (128 bytes a row; 256 columns left 2048 x
 // 256 to eight CTAs, 6.2 us): every quarter of its warps each so-many-th row, eight loads in flight.  Quarters meet by shuffles, warps in
@@ -138,7 +143,7 @@ __global__ void __launch_bounds__(kBiasThreads)
   float v[8] = {};
   const int step = ranks * warps * 4, first = (rank * warps + warp) * 4 + lane / 8;
   if (c + 8 <= l.T) {
-    constexpr int kAt = 8;
+    constexpr int kAt = kBiasAhead;
     for (int r = first; r < sp.n; r += kAt * step) {
       uint4 u[kAt];
 #pragma unroll
@@ -195,7 +200,7 @@ moe_status bias_grad(const Args* a, const void* grad, int64_t grad_stride, bool 
   const int64_t blocks = (int64_t)((l.T + kBiasCols - 1) / kBiasCols) * l.G;
   // a CTA for some 64 rows of an average group, as long as there are few
   int ranks = 1;
-  while (ranks < 8 && (int64_t)a->rows / l.G > 64 * ranks && blocks * ranks < 4 * sms) ranks *= 2;
+  while (ranks < kBiasRanks && (int64_t)a->rows / l.G > 64 * ranks && blocks * ranks < 4 * sms) ranks *= 2;
   return launch_op(grad_bias_kernel, dim3((unsigned)(blocks * ranks)), kBiasThreads, 0, ranks, s, static_cast<const __nv_bfloat16*>(grad), grad_stride, l,
                    a->d_grad_bias, a->accumulate);
 }
@@ -340,7 +345,7 @@ extern "C" int64_t moe_async_linear_backward_workspace(const moe_async_linear_ba
 extern "C" moe_status moe_async_linear_backward(const moe_async_linear_backward_args* a, void* stream) {
   using namespace moe;
   if (!a) return MOE_ERR_INVALID;
-  if (a->rows < 0 || a->rows > INT32_MAX - 1024 || a->fan_in < 1 || a->fan_in > INT32_MAX - 1024 || a->fan_out < 1 ||
+  if (a->rows < 0 || a->rows > kMaxRows || a->fan_in < 1 || a->fan_in > INT32_MAX - 1024 || a->fan_out < 1 ||
       a->fan_out > INT32_MAX - 1024 || a->groups < 0 || a->groups > kMaxExperts || (a->groups > 0) != (a->d_offsets != nullptr) ||
       (a->x_dtype != MOE_F32 && a->x_dtype != MOE_BF16) || (a->w_dtype != MOE_F32 && a->w_dtype != MOE_BF16))
     return MOE_ERR_INVALID;

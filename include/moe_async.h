@@ -555,7 +555,7 @@ moe_status moe_async_quantize_blocks(int32_t dtype, const void* d_x, int64_t x_s
  *   groups = G > 0: as in moe_async_linear; d_w and d_grad_w are [G, fan_out, fan_in] (matrices of fan_out * stride elements
  *   one behind another), d_grad_bias [G, fan_out]; rows of no group count nowhere, whatever they hold, and their grad_x is
  *   left as it was; a group without rows has a gradient of zeros.  Added to in fp32, values below 2^-126 are taken as 0.
- * fan_in is a multiple of 8, the bases and strides of x and w of 16 bytes, else MOE_ERR_UNSUPPORTED; fan_out and the other strides
+ * rows are at most 2^31 - 4097.  fan_in is a multiple of 8, the bases and strides of x and w of 16 bytes, else MOE_ERR_UNSUPPORTED; fan_out and the other strides
  * are free, but rows of grad that do not start on 16-byte boundaries are copied first, into a workspace (16-byte aligned) of
  * moe_async_linear_backward_workspace(args) bytes (0 if they do), the caller's until the call has run; calls that may run at
  * once need one each.  Smaller: MOE_ERR_CAPACITY.  0 rows: grad_w and grad_bias are set to zeros, or left.  Asynchronous. */

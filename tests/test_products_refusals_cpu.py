@@ -1,5 +1,5 @@
-"""Calls of the product's gradients that are refused before any CUDA call: places that two results, or a result and an operand, share
-(no GPU here)."""
+"""Calls of the product's gradients that are refused before any CUDA call: places that two results, or a result and an operand, share,
+and row counts whose walk would pass 32 bits (no GPU here)."""
 import ctypes
 
 import pytest
@@ -35,3 +35,19 @@ def test_one_place_for_both_outputs_is_refused(nat):
     N, lib = nat
     P, Q = 256, 512
     assert lib.moe_async_act_mul_backward(N.MOE_BF16, 1, P, 8, P, 8, P, 8, 4, 8, Q, 8, Q, 8, None) == N.MOE_ERR_INVALID
+
+
+def test_rows_whose_walk_would_pass_32_bits_are_refused(nat):
+    """The bias's gradient walks rows in 32 bits: eight CTAs of eight warps with four rows each, eight of them in flight a lane, 2048 a turn.
+    Its last turn looks up to two turns behind the last row; beyond 2^31 - 1 that would be a row before the matrix."""
+    N, lib = nat
+    turn = 8 * 8 * 4 * 8
+    most = 2 ** 31 - 1 - 2 * turn
+    for rows in (2 ** 31 - 1024 - 1, 2 ** 31 - 1 - turn, most + 1):
+        a = args(N, rows=rows, fan_in=8, fan_out=8, grad_stride=8, x_stride=8, w_stride=8, grad_x_stride=8, grad_w_stride=8, d_x=None, d_grad_x=None, d_grad_w=None)
+        assert lib.moe_async_linear_backward(a, None) == N.MOE_ERR_INVALID, rows
+    # what is accepted: no index of the walk passes 2^31 - 1
+    for n in (most, most - 1, most - turn):
+        for first in (0, turn // 8 - 1):
+            last = first + (n - 1 - first) // turn * turn                    # the last turn's first row
+            assert last < n and last + turn <= 2 ** 31 - 1 and last + 7 * (turn // 8) <= 2 ** 31 - 1
