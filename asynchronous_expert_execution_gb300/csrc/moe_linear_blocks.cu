@@ -849,6 +849,11 @@ constexpr int block_split_stages(bool own_sm) {
   return n < BlockSplitTail<BN>::kMaxStages ? n : BlockSplitTail<BN>::kMaxStages;
 }
 
+int blocks_split_capacity(int s, int sms) {
+  static Capacities known;
+  return s == 1 ? sms : capacity_of(linear_blocks_split_kernel<__nv_bfloat16, 64>, known, s, sms);
+}
+
 template <typename TO, int BN>
 moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, const Scales& sc, int sms, int splits, int64_t tiles, void* s) {
   // the ring holds the CTA's partials and its share of up to 8 ranks' (which may round up by a token each)
@@ -860,7 +865,8 @@ moe_status launch_split(const moe_async_linear_args* a, const LinearParams& l, c
   p.bn = BN;
   p.splits = splits;
   p.nft = (l.N + kBM - 1) / kBM;
-  p.stages = block_split_stages<BN>(tiles * splits <= sms && l.nk > block_split_stages<BN>(false) * splits);
+  // where clusters of whole-SM CTAs do not all find a place, two share an SM (148 CTAs in clusters of 4, 64 x 7168 x 4736: 14.9 us, alone 22.6)
+  p.stages = block_split_stages<BN>(tiles * splits <= blocks_split_capacity(splits, sms) && l.nk > block_split_stages<BN>(false) * splits);
   const int smem = p.stages * (kABlock + BN * kBKBytes) + (int)sizeof(BlockSplitTail<BN>) + 1024;
   if (!encode(&p.w, a->d_w, 1, l.F, l.N, a->w_stride, l.G, kBM) || !encode(&p.x, a->d_x, 1, l.F, l.T, a->x_stride, 0, BN)) return MOE_ERR_CUDA;
   if (cudaFuncSetAttribute(linear_blocks_split_kernel<TO, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmem) != cudaSuccess) return MOE_ERR_CUDA;
@@ -874,11 +880,6 @@ moe_status launch_few(const moe_async_linear_args* a, const LinearParams& l, con
   // half the warps where these take K in one pass all the same
   const int threads = l.nk <= few_blocks(TS, FS) * (kFewThreads / 64) ? kFewThreads / 2 : kFewThreads;
   return launch_op(linear_blocks_few_kernel<TO, TS, FS>, grid, threads, 0, 1, s, p, sc);
-}
-
-int blocks_split_capacity(int s, int sms) {
-  static Capacities known;
-  return s == 1 ? sms : capacity_of(linear_blocks_split_kernel<__nv_bfloat16, 64>, known, s, sms);
 }
 
 // Kernel, tile and split with the least expected time, in ns, from 25 shapes of 17 to 4096 tokens on 256 to 7168 features, dense and in 32

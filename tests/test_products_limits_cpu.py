@@ -52,3 +52,9 @@ def test_another_limit_in_the_shared_header_is_seen():
         except AssertionError:
             continue
         raise RuntimeError(f"{f}: two limits of one kernel went unseen")
+
+
+def test_launches_ask_the_same_question_as_the_plans():
+    """A split CTA takes a whole SM's ring only where the launch's clusters all find an SM a CTA: what the plan's cost took for granted."""
+    for f, ask in (("moe_linear.cu", "split_capacity<kForward>"), ("moe_linear_backward.cu", "split_capacity<MODE>"), ("moe_linear_blocks.cu", "blocks_split_capacity")):
+        assert f"tiles * splits <= {ask}(splits, sms)" in read(f), f
