@@ -29,7 +29,7 @@ EXPORTS = ("moe_async_create", "moe_async_route", "moe_async_enqueue", "moe_asyn
            "moe_async_add_rms_norm_backward_workspace", "moe_async_linear", "moe_async_linear_backward",
            "moe_async_linear_backward_workspace", "moe_async_act_mul_backward", "moe_async_linear_blocks",
            "moe_async_quantize_blocks", "moe_async_ops_status",
-           "moe_async_debug_latch_ops_error")
+           "moe_async_debug_latch_ops_error", "moe_async_debug_latch_ops_word")
 
 KERNEL_KINDS = ("enqueue", "schedule", "ffn1", "ffn2", "collect", "tick")
 
@@ -148,6 +148,7 @@ def load():
         "moe_async_quantize_blocks": [I32, P, I64, I32, I32, I32, I32, P, I64, F32P, I64, I64, P],
         "moe_async_ops_status": [P],
         "moe_async_debug_latch_ops_error": [P],
+        "moe_async_debug_latch_ops_word": [I32, P],
     }
     restype = {"moe_async_status_string": ctypes.c_char_p, "moe_async_add_rms_norm_backward_workspace": I64,
                "moe_async_linear_backward_workspace": I64}

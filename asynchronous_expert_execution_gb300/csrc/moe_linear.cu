@@ -230,16 +230,27 @@ unsigned int* ops_error_backward();
 unsigned int* ops_error_blocks();
 }
 
-extern "C" moe_status moe_async_ops_status(void* stream) {
-  using namespace moe;
+namespace {
+constexpr int kWords = 3;
+
+// The words of the current device; false: one is not to be had.
+bool error_words(unsigned int* (&words)[kWords]) {
   void* mine = nullptr;
-  if (cudaGetSymbolAddress(&mine, g_ops_error) != cudaSuccess) return MOE_ERR_CUDA;
-  unsigned int* const words[] = {static_cast<unsigned int*>(mine), ops_error_backward(), ops_error_blocks()};
-  constexpr int kWords = sizeof(words) / sizeof(words[0]);
+  if (cudaGetSymbolAddress(&mine, moe::g_ops_error) != cudaSuccess) return false;
+  words[0] = static_cast<unsigned int*>(mine);
+  words[1] = moe::ops_error_backward();
+  words[2] = moe::ops_error_blocks();
+  return words[1] && words[2];
+}
+}  // namespace
+
+extern "C" moe_status moe_async_ops_status(void* stream) {
+  unsigned int* words[kWords];
+  if (!error_words(words)) return MOE_ERR_CUDA;
   unsigned int e[kWords] = {};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int i = 0; i < kWords; ++i)
-    if (!words[i] || cudaMemcpyAsync(&e[i], words[i], sizeof(e[i]), cudaMemcpyDeviceToHost, s) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaMemcpyAsync(&e[i], words[i], sizeof(e[i]), cudaMemcpyDeviceToHost, s) != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
   unsigned int found = 0;
   for (int i = 0; i < kWords; ++i) {
@@ -251,17 +262,19 @@ extern "C" moe_status moe_async_ops_status(void* stream) {
   return static_cast<moe_status>(found);
 }
 
-extern "C" moe_status moe_async_debug_latch_ops_error(void* stream) {
+extern "C" moe_status moe_async_debug_latch_ops_word(int32_t word, void* stream) {
 #ifdef MOE_DEBUG_BOUNDS
-  using namespace moe;
+  unsigned int* words[kWords];
+  if (word < 0 || word >= kWords) return MOE_ERR_INVALID;
+  if (!error_words(words)) return MOE_ERR_CUDA;
   const unsigned int e = MOE_ERR_TIMEOUT;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cudaMemcpyToSymbolAsync(g_ops_error, &e, sizeof(e), 0, cudaMemcpyHostToDevice, s) == cudaSuccess &&
-                 cudaStreamSynchronize(s) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  return cudaMemcpyAsync(words[word], &e, sizeof(e), cudaMemcpyHostToDevice, s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 #else
+  (void)word;
   (void)stream;
   return MOE_ERR_UNSUPPORTED;
 #endif
 }
+
+extern "C" moe_status moe_async_debug_latch_ops_error(void* stream) { return moe_async_debug_latch_ops_word(0, stream); }

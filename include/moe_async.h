@@ -603,6 +603,10 @@ moe_status moe_async_debug_append_record(moe_async_t h, int32_t layer, int32_t b
  * it reported without a wait that runs out.  Release builds return MOE_ERR_UNSUPPORTED. */
 moe_status moe_async_debug_latch_ops_error(void* stream);
 
+/* The same for one of the words behind it: 0 the product's (the call above), 1 its gradients', 2 the block-scaled product's; another
+ * word is MOE_ERR_INVALID. */
+moe_status moe_async_debug_latch_ops_word(int32_t word, void* stream);
+
 /* 1 if the kernels can write `n` bytes at host address `p` directly (pinned host memory
  * mapped into the device's address space at the same address), else 0.  A caller may then
  * pass such a buffer as a collect output (d_y_out, d_slot_out, ...), so each merged row goes

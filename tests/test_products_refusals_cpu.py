@@ -51,3 +51,10 @@ def test_rows_whose_walk_would_pass_32_bits_are_refused(nat):
         for first in (0, turn // 8 - 1):
             last = first + (n - 1 - first) // turn * turn                    # the last turn's first row
             assert last < n and last + turn <= 2 ** 31 - 1 and last + 7 * (turn // 8) <= 2 ** 31 - 1
+
+
+def test_release_build_refuses_to_latch_a_word(nat):
+    N, lib = nat
+    if N.DEBUG_BOUNDS:
+        pytest.skip("the bounds-checked build is loaded")
+    assert lib.moe_async_debug_latch_ops_word(1, None) == N.MOE_ERR_UNSUPPORTED
