@@ -130,29 +130,17 @@ __device__ __forceinline__ void load_across(uint32_t dst, const CUtensorMap* m, 
   for (int i = 0; i < cols; i += 64) tma_2d<CG>(dst + i * kBKBytes, m, bar, c + i, row0 + kb * kBoxRows);
 }
 
-// kWeightGrad over two CTAs, a group's last k-block: `cols` columns from c of the group's last `live` rows, from `row` on, behind 64 - live
-// rows of zeros.  Behind the group's end lie rows of the next group or of none, with any content, so the copy itself has to know the end:
-// the map's rows are a window of 64 over all rows (encode_window), entered at a negative place, which brings zeros.  All of a pair's operands
-// come by copies that its leader waits for.  (The block as it lies there, and a warp of either CTA that clears the rows behind the end
-// and tells the leader, wants a release over the cluster, which waits for all that the thread has under way: 32 experts 8192 x 2880 x
-// 2880 took 287 us in fp32; boxes of 1, 2, 4 .. rows and of zeros 307.)
-__device__ __forceinline__ void load_end(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c, int cols, int row, int live) {
-  for (int i = 0; i < cols; i += 64) tma_3d<2>(dst + i * kBKBytes, m, bar, c + i, live - kBoxRows, row);
-}
-
 template <int MODE>
 __device__ __forceinline__ uint64_t a_desc(uint32_t saddr) { return MODE == kForward ? operand_desc(saddr) : across_desc(saddr, kBox); }
 template <int MODE>
 __device__ __forceinline__ uint64_t b_desc(uint32_t saddr) { return MODE == kWeightGrad ? across_desc(saddr, kBox) : operand_desc(saddr); }
 
-// The products of one k-block; `live`: rows of K that it holds (kWeightGrad: 16 a product, the others are left out), its first ones in
-// one CTA, its last ones in a pair.
+// The products of one k-block; `live`: rows of K that it holds (kWeightGrad: 16 a product, those behind are left out).
 template <int CG, int MODE, bool E4M3>
 __device__ __forceinline__ void product_block(uint32_t d, uint32_t smem, uint32_t idesc, bool accumulate, int live) {
   const uint64_t a = a_desc<MODE>(smem), b = b_desc<MODE>(smem + kABlock);
   if (MODE == kWeightGrad && live <= kBoxRows - 16) {
-    const int n = (live + 15) / 16, first = CG == 2 ? kBoxRows / 16 - n : 0;
-    for (int i = first; i < first + n; ++i) mma<CG, E4M3>(d, a + 128 * i, b + 128 * i, idesc, accumulate || i > first);
+    for (int i = 0; 16 * i < live; ++i) mma<CG, E4M3>(d, a + 128 * i, b + 128 * i, idesc, accumulate || i > 0);
   } else {
     mma_block<CG, E4M3, MODE != kForward, MODE == kWeightGrad>(d, a, b, idesc, accumulate);
   }
@@ -654,7 +642,7 @@ struct Divide {
 };
 
 struct PairParams {
-  CUtensorMap w, x[4];              // x: boxes of 16, 32, 64 and tokens / 2 rows; kWeightGrad: whole k-blocks, w's and x's last ones (load_end)
+  CUtensorMap w, x[4];              // x: boxes of 16, 32, 64 and tokens / 2 rows; kWeightGrad: 64 rows of K
   LinearParams l;
   CUtensorMap y;                    // kWeightGrad, boxed: the result, boxes of half a tile's rows x 32 features
   bool boxed;
@@ -663,6 +651,47 @@ struct PairParams {
   int tokens;                       // of a tile, a multiple of 32
   int stages, stage_bytes;          // of the ring: a k-block of a full tile each
 };
+
+// kWeightGrad per expert: how a group's last k-block comes (load_end), of w and of x: windows of 64 rows, boxes of 16 rows and of one.
+struct AcrossParams : PairParams {
+  CUtensorMap window[2], slab[2], row[2];
+};
+template <int MODE> using PairArgs = std::conditional_t<MODE == kWeightGrad, AcrossParams, PairParams>;
+
+// kWeightGrad over two CTAs: the last `live` rows of a group, from `row` on, where `live` is no multiple of 16 and less than 64.  Behind them lie
+// rows of the next group or of none, with any content, of which products of 16 rows would still reach some; so copies have to bring zeros
+// there, and all of a pair's operands come by copies that its leader waits for.  (One box, and a warp of either CTA that clears the rows
+// behind the end and tells the leader, wants a release over the cluster, which waits for all that the thread has under way: 32 experts
+// 8192 x 2880 x 2880 took 287 us in fp32, here 243; in boxes of 1, 2, 4 .. rows and of zeros 307, for a copy takes 60 cycles.)
+// A window is 64 rows that end with the group's last one; the box begins 64 - live rows into it, and what lies behind it is zeros.  A
+// group that ends within the matrix's first 64 rows has none: boxes of 16 rows, then of one, and of one row of zeros, which lies beside the
+// matrix.  (No box begins before the matrix: a window entered ahead of its first row, with the zeros in front, once faulted.)
+__device__ __forceinline__ bool has_window(int row, int live) { return row + live >= kBoxRows; }
+__device__ __forceinline__ int end_bytes(int row, int live, int cols) {          // of both CTAs
+  return 2 * (has_window(row, live) ? kBoxRows : (live + 15) / 16 * 16) * kBKBytes * (2 + cols / 64);
+}
+__device__ __forceinline__ void load_window(uint32_t dst, const CUtensorMap* windows, uint32_t bar, int c, int cols, int row, int live) {
+#pragma unroll 2
+  for (int i = 0; i < cols; i += 64) tma_3d<2>(dst + i * kBKBytes, windows, bar, c + i, kBoxRows - live, row + live - kBoxRows);
+}
+__device__ __forceinline__ void load_rows(uint32_t dst, const AcrossParams& p, int operand, uint32_t bar, int c, int cols, int width, int row, int live) {
+  for (int i = 0; i < cols; i += 64) {
+    const uint32_t to = dst + i * kBKBytes;
+    int r = 0;
+    for (; r + 16 <= live; r += 16) tma_2d<2>(to + r * kBKBytes, &p.slab[operand], bar, c + i, row + r);
+    for (; r < live; ++r) tma_2d<2>(to + r * kBKBytes, &p.row[operand], bar, c + i, row + r);
+    for (; r % 16; ++r) tma_2d<2>(to + r * kBKBytes, &p.row[operand], bar, (width + 7) / 8 * 8, row);
+  }
+}
+__device__ __forceinline__ void load_end(uint32_t dst, const AcrossParams& p, uint32_t bar, int f, int c, int cols, int row, int live) {
+  if (has_window(row, live)) {
+    load_window(dst, &p.window[0], bar, f, kBM, row, live);
+    load_window(dst + kABlock, &p.window[1], bar, c, cols, row, live);
+  } else {
+    load_rows(dst, p, 0, bar, f, kBM, p.l.N, row, live);
+    load_rows(dst + kABlock, p, 1, bar, c, cols, p.l.T, row, live);
+  }
+}
 
 struct PairTail {
   static constexpr int kMaxStages = 10;
@@ -832,7 +861,7 @@ __device__ __forceinline__ bool pair_finish(const LinearParams& l, int g, Row fi
 
 template <bool E4M3, typename TO, int MODE = kForward>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    linear_pair_kernel(const __grid_constant__ PairParams p) {
+    linear_pair_kernel(const __grid_constant__ PairArgs<MODE> p) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   constexpr bool kAcross = MODE == kWeightGrad;
@@ -918,20 +947,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     while (__all_sync(0xffffffffu, ok) && next_tile()) {
       if (!elect()) continue;
       const int wrow = tl.fti * 2 * kBM + rank * kBM, xrow = tl.row0 + rank * (tl.nmma / 2);
-      const int nk = kAcross ? tl.nk : l.nk;
+      // a group's last rows come by load_end, unless they fill 16s (without groups, copies bring zeros behind the last row by themselves)
+      const int nk = kAcross ? tl.nk : l.nk, whole = kAcross && l.offsets && tl.sum % 16 ? nk - 1 : nk;
       for (int kb = 0; kb < nk; ++kb) {
         if (!(ok = wait<kCluster>(&s->empty[st], phase, abort_flag))) break;
         const uint32_t a = smem_u32(smem + st * p.stage_bytes), bar = mapa(smem_u32(&s->full[st]), 0);
-        if (rank == 0) mbar_expect(&s->full[st], 2 * (kABlock + tl.brows * kBKBytes));
-        if (kAcross && tl.sum - kb * kBoxRows < kBoxRows) {
-          load_end(a, &p.x[1], bar, wrow, kBM, tl.sum0 + kb * kBoxRows, tl.sum - kb * kBoxRows);
-          load_end(a + kABlock, &p.x[2], bar, xrow, tl.brows, tl.sum0 + kb * kBoxRows, tl.sum - kb * kBoxRows);
-        } else {
+        if (!kAcross || kb < whole) {
+          if (rank == 0) mbar_expect(&s->full[st], 2 * (kABlock + tl.brows * kBKBytes));
           load_a<2, MODE, E4M3>(a, &p.w, bar, kb, wrow, tl.g, kAcross ? tl.sum0 : 0);
           if constexpr (kAcross)
             load_across<2>(a + kABlock, &p.x[0], bar, kb, xrow, tl.brows, tl.sum0);
           else
             tma_2d<2>(a + kABlock, &p.x[tl.box], bar, kb * kElems, xrow);
+        } else if constexpr (kAcross) {
+          const int row = tl.sum0 + kb * kBoxRows, live = tl.sum - kb * kBoxRows;
+          if (rank == 0) mbar_expect(&s->full[st], end_bytes(row, live, tl.brows));
+          load_end(a, p, bar, wrow, xrow, tl.brows, row, live);
         }
         if (++st == p.stages) st = 0, phase ^= 1;
       }
@@ -1175,12 +1206,12 @@ bool encode(CUtensorMap* m, const void* base, int size, int width, int rows, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Every row of a [rows][width] bf16 matrix as the first of a window of 64 rows, boxes of 128 bytes x a window, 128-byte swizzle, zeros
-// outside the window: element (c, a, b) is column c of row a + b.  (Windows that reach behind the last row are entered before it only.)
-bool encode_window(CUtensorMap* m, const void* base, int width, int rows, int64_t ld) {
+// The windows of 64 rows of a [rows][width] bf16 matrix of 64 rows at least, boxes of 128 bytes x 64 rows, 128-byte swizzle, zeros
+// outside the window: element (c, a, b) is column c of row a + b.  All windows lie in the matrix.
+bool encode_windows(CUtensorMap* m, const void* base, int width, int rows, int64_t ld) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)width, kBoxRows, (cuuint64_t)rows}, strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2};
+  const cuuint64_t dims[3] = {(cuuint64_t)width, kBoxRows, (cuuint64_t)(rows - kBoxRows + 1)}, strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2};
   const cuuint32_t box[3] = {kBKBytes / 2, kBoxRows, 1}, step[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -14,7 +14,7 @@ namespace moe {
 namespace {
 
 template <typename TO, int MODE>
-moe_status launch_pair(PairParams& p, const LinearParams& l, int tokens, int sms, void* s) {
+moe_status launch_pair(PairArgs<MODE>& p, const LinearParams& l, int tokens, int sms, void* s) {
   constexpr int kSmem = kPairRing + kStaging + (int)sizeof(PairTail) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   p.l = l;
@@ -108,10 +108,17 @@ moe_status weight_grad(const Args* a, const void* grad, int64_t grad_stride, boo
       return MOE_ERR_CUDA;
     return launch_split<TO, kWeightGrad>(p, l, plan.tokens, plan.splits, tiles, sms, s);
   }
-  PairParams p;
+  AcrossParams p;
   if (!encode(&p.w, a->d_x, 2, a->fan_in, a->rows, a->x_stride, 0, kBoxRows) || !encode(&p.x[0], grad, 2, a->fan_out, a->rows, grad_stride, 0, kBoxRows))
     return MOE_ERR_CUDA;
-  if (!encode_window(&p.x[1], a->d_x, a->fan_in, a->rows, a->x_stride) || !encode_window(&p.x[2], grad, a->fan_out, a->rows, grad_stride)) return MOE_ERR_CUDA;
+  for (int i = 0; l.offsets && i < 2; ++i) {
+    const void* of = i == 0 ? a->d_x : grad;
+    const int width = i == 0 ? a->fan_in : a->fan_out;
+    const int64_t ld = i == 0 ? a->x_stride : grad_stride;
+    if (!encode(&p.slab[i], of, 2, width, a->rows, ld, 0, 16) || !encode(&p.row[i], of, 2, width, a->rows, ld, 0, 1) ||
+        (a->rows >= kBoxRows && !encode_windows(&p.window[i], of, width, a->rows, ld)))
+      return MOE_ERR_CUDA;
+  }
   p.boxed = wide;                                    // unless rows start off 16-byte boundaries
   if (p.boxed && !encode_result<TO>(&p.y, a->d_grad_w, a->fan_in, a->fan_out, a->grad_w_stride, l.G)) return MOE_ERR_CUDA;
   return launch_pair<TO, kWeightGrad>(p, l, plan.tokens, sms, s);

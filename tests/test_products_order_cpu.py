@@ -52,18 +52,65 @@ def test_a_pair_reads_what_copies_brought():
     assert "clear_rows" in split                     # there the products are the same CTA's, behind the fence
 
 
+def ends(rows, width, row, live, c, cols):
+    """load_end's copies of one operand as (row of the stage, [row of the matrix or None for zeros]), and each box's first element."""
+    out, at = [], []
+    for i in range(0, cols, 64):
+        if row + live >= 64:
+            b, a0 = row + live - 64, 64 - live
+            assert rows >= 64 and 0 <= b <= rows - 64 and 0 < a0 < 64        # the window lies in the matrix, and the box begins in it
+            out.append((i, 0, [b + a if a < 64 else None for a in range(a0, a0 + 64)]))
+            at.append((c + i, b + a0))
+            continue
+        r = 0
+        while r + 16 <= live:
+            out.append((i, r, list(range(row + r, row + r + 16))))
+            at.append((c + i, row + r))
+            r += 16
+        while r < live:
+            out.append((i, r, [row + r]))
+            at.append((c + i, row + r))
+            r += 1
+        while r % 16:
+            zero = (width + 7) // 8 * 8
+            assert zero >= width and zero % 8 == 0                           # no column of the matrix, on a 16-byte boundary
+            out.append((i, r, [None]))
+            at.append((zero, row))
+            r += 1
+    return out, at
+
+
 def test_the_end_of_a_group_is_copied_with_zeros():
-    """load_end enters a window of 64 rows, whose first is `row`, at live - 64: what the copy brings, by its definition, is 64 - live rows of
-    zeros and the group's `live` last, none of another's and none outside the matrix; the products take the rows from there on."""
+    """The group's last rows, then zeros as far as products of 16 rows reach, each row once; the bytes that are waited for; and no box that
+    begins before the matrix or below its last row."""
     src = source("moe_linear.cuh")
-    for piece in ("tma_3d<2>(dst + i * kBKBytes, m, bar, c + i, live - kBoxRows, row);", "dims[3] = {(cuuint64_t)width, kBoxRows, (cuuint64_t)rows}",
-                  "n = (live + 15) / 16, first = CG == 2 ? kBoxRows / 16 - n : 0;"):
+    for piece in ("return row + live >= kBoxRows;", "2 * (has_window(row, live) ? kBoxRows : (live + 15) / 16 * 16) * kBKBytes * (2 + cols / 64);",
+                  "tma_3d<2>(dst + i * kBKBytes, windows, bar, c + i, kBoxRows - live, row + live - kBoxRows);",
+                  "for (; r + 16 <= live; r += 16) tma_2d<2>(to + r * kBKBytes, &p.slab[operand], bar, c + i, row + r);",
+                  "for (; r < live; ++r) tma_2d<2>(to + r * kBKBytes, &p.row[operand], bar, c + i, row + r);",
+                  "for (; r % 16; ++r) tma_2d<2>(to + r * kBKBytes, &p.row[operand], bar, (width + 7) / 8 * 8, row);",
+                  "dims[3] = {(cuuint64_t)width, kBoxRows, (cuuint64_t)(rows - kBoxRows + 1)}", "whole = kAcross && l.offsets && tl.sum % 16 ? nk - 1 : nk;",
+                  "load_window(dst, &p.window[0], bar, f, kBM, row, live);",
+                  "load_window(dst + kABlock, &p.window[1], bar, c, cols, row, live);", "load_rows(dst, p, 0, bar, f, kBM, p.l.N, row, live);",
+                  "load_rows(dst + kABlock, p, 1, bar, c, cols, p.l.T, row, live);", "load_end(a, p, bar, wrow, xrow, tl.brows, row, live);"):
         assert piece in src, piece
-    for rows in (1, 5, 63, 64, 65, 200):
+    for rows in (1, 5, 15, 63, 64, 65, 200):
         for end in range(1, rows + 1):
             for live in range(1, min(64, end + 1)):
-                row = end - live
-                got = [row + a if 0 <= a < 64 and 0 <= row < rows else None for a in range(live - 64, live)]
-                assert got == [None] * (64 - live) + list(range(row, end)) and end <= rows
-                n = (live + 15) // 16
-                assert all(v is None for v in got[:64 - 16 * n]) and (n == 4 or live <= 48)
+                if live % 16 == 0:
+                    continue
+                row, bytes_ = end - live, 0
+                for cols in (128, 64):
+                    copies, at = ends(rows, 997, row, live, 0, cols)
+                    for i in range(0, cols, 64):
+                        stage = {}
+                        for j, r, got in copies:
+                            if j == i:
+                                for k, v in enumerate(got):
+                                    assert r + k not in stage and r + k < 64
+                                    stage[r + k] = v
+                        assert [stage[k] for k in range(live)] == list(range(row, end))
+                        assert all(stage[k] is None for k in range(live, (live + 15) // 16 * 16))
+                        assert all(0 <= first < rows for _, first in at)
+                    bytes_ += 128 * sum(len(got) for _, _, got in copies)
+                assert 2 * bytes_ == 2 * (64 if end >= 64 else (live + 15) // 16 * 16) * 128 * (2 + 64 // 64)
