@@ -511,11 +511,12 @@ __global__ void __launch_bounds__(kThreads, 2) linear_blocks_split_kernel(const 
 
 // As the forward product's kernel for up to 16 tokens: weights straight into the registers of warp-wide matrix instructions.  A warp
 // takes whole k-blocks, kBlocks of them in flight, so that their sums stand under one scale a token.  Block (b, i): 8 FS features of up
-// to 8 TS tokens, those of the i-th group that has rows.
-constexpr int few_blocks(int ts, int fs) { return ts + fs == 2 ? 4 : ts + fs == 3 ? 2 : 1; }
+// to 8 TS tokens, those of the i-th group that has rows; TS or FS is 1.
+constexpr int few_blocks(int ts, int fs) { return ts + fs == 2 ? 4 : 2; }
 template <typename TO, int TS, int FS>
 __global__ void __launch_bounds__(kFewThreads, 1) linear_blocks_few_kernel(const __grid_constant__ FewParams p, const __grid_constant__ Scales sc) {
-  constexpr int kBlocks = few_blocks(TS, FS), kFeatures = 8 * FS, kTiles = TS * FS == 4 ? 2 : 1;
+  constexpr int kBlocks = few_blocks(TS, FS), kFeatures = 8 * FS;
+  static_assert(TS * FS <= 2, "one tile of 16 x 8 sums");
   __shared__ float part[kFewThreads / 32][8 * TS * kFeatures];
   ops_begin();
   const LinearParams& l = p.l;
@@ -553,16 +554,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_blocks_few_kernel(const
     xu[i] = t < nt ? units : 0;
     x[i] = static_cast<const uint4*>(p.x) + (row0 + (t < nt ? t : 0)) * (size_t)(p.ldx / 16);
   }
-  // the tokens of this lane's sums: features on the instruction's rows (FS = 2), two adjacent columns a tile; else rows 8 apart
+  // the tokens of this lane's sums: features on the instruction's rows (FS = 2), two adjacent columns; else rows 8 apart
   const int t0 = FS == 2 ? lane % 4 * 2 : lane / 4;
-  const auto token = [](int i, int j) { return FS == 2 ? i * 8 + j : 8 * j; };       // from t0
+  constexpr int kNext = FS == 2 ? 1 : 8;             // from t0 to the second
   const float* sx = sc.x + (int64_t)(row0 + t0) * sc.row;
   const float* sw = sc.w + ((size_t)g * sc.nfb + blockIdx.x * kFeatures / kBM) * l.nk;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  float sum[kTiles][4] = {};
+  float sum[4] = {};
   for (int b0 = warp; b0 < l.nk; b0 += kBlocks * warps) {
     uint4 wv[FS][kBlocks][2], xv[TS][kBlocks][2];
-    float f[kTiles][kBlocks][2], fw[kBlocks];
+    float f[kBlocks][2], fw[kBlocks];
 #pragma unroll
     for (int u = 0; u < kBlocks; ++u)
 #pragma unroll
@@ -580,39 +581,31 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_blocks_few_kernel(const
         for (int i = 0; i < TS; ++i) xv[i][u][h] = b * 8 + h * 4 + lane % 4 < xu[i] ? __ldg(x[i] + b * 8 + h * 4 + lane % 4) : zero;
       fw[u] = b < l.nk ? __ldg(sw + b) : 0.f;
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) f[i][u][j] = b < l.nk && t0 + token(i, j) < nt ? __ldg(sx + token(i, j) * sc.row + b * sc.block) : 0.f;
+      for (int j = 0; j < 2; ++j) f[u][j] = b < l.nk && t0 + kNext * j < nt ? __ldg(sx + kNext * j * sc.row + b * sc.block) : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < kBlocks; ++u) {
-      float c[kTiles][4] = {};
+      float c[4] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if constexpr (FS == 2) {
-#pragma unroll
-          for (int i = 0; i < TS; ++i) warp_mma<true>(c[i], wv[0][u][h], wv[1][u][h], xv[i][u][h]);
-        } else {
-          warp_mma<true>(c[0], xv[0][u][h], TS == 2 ? xv[TS - 1][u][h] : zero, wv[0][u][h]);
-        }
+        if constexpr (FS == 2)
+          warp_mma<true>(c, wv[0][u][h], wv[1][u][h], xv[0][u][h]);
+        else
+          warp_mma<true>(c, xv[0][u][h], TS == 2 ? xv[TS - 1][u][h] : zero, wv[0][u][h]);
       }
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float s = f[i][u][FS == 2 ? j % 2 : j / 2] * fw[u];
-          if (b0 + u * warps < l.nk) sum[i][j] = fmaf(c[i][j], s, sum[i][j]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float s = f[u][FS == 2 ? j % 2 : j / 2] * fw[u];
+        if (b0 + u * warps < l.nk) sum[j] = fmaf(c[j], s, sum[j]);
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = lane / 4 + j / 2 * 8, q = i * 8 + lane % 4 * 2 + j % 2;
-      if (FS == 2) part[warp][q * kFeatures + r] = sum[i][j];
-      else if (TS == 2 || j < 2) part[warp][r * kFeatures + q] = sum[i][j];
-    }
+  for (int j = 0; j < 4; ++j) {
+    const int r = lane / 4 + j / 2 * 8, q = lane % 4 * 2 + j % 2;
+    if (FS == 2) part[warp][q * kFeatures + r] = sum[j];
+    else if (TS == 2 || j < 2) part[warp][r * kFeatures + q] = sum[j];
+  }
   __syncthreads();
   if (out) {
     float v[1] = {part[0][threadIdx.x]};
@@ -915,13 +908,15 @@ moe_status blocks_launch(const moe_async_linear_args* a, const LinearParams& l, 
   const int sms = sm_count();
   if (sms < 2) return MOE_ERR_CUDA;
   const int groups = l.offsets ? std::min(l.G, l.T) : 1;
-  // as in the forward product: few tokens on small weights
+  // Up to 8 tokens the few kernel is ahead on small weights, to the forward product's bounds (few / split us, 1 and 8 tokens: on 512 x 256
+  // 3.6 / 4.6, 2880 x 2880 5.6 / 6.6, 7168 x 2048 5.8 / 8.3, 2048 x 9728 6.6 / 8.4, 7168 x 4096 9.8 / 9.9 and 10.1 / 10.1; beyond them 7168 x
+  // 7168 14.5 / 13.1, 512 x 16384 7.0 / 4.9, 8 rows of 32 groups on 7168 x 2048 32 / 24).  For 16 it holds one k-block in flight where it takes
+  // 16 features a block: 2880 x 2880 7.7 / 6.9, 2048 x 9728 11.4 / 8.5, 7168 x 4096 14.0 / 10.1 (7168 x 2048 8.0 / 8.5); with 8 features 7168
+  // x 256 4.8 / 7.2, 7168 x 1024 5.6 / 8.0.
   const int64_t features = (int64_t)l.N * groups;
-  if (l.T <= kFewTokens && features <= 64 * sms && features * l.F <= 32'000'000) {
-    const bool wide_rows = features > 8 * sms;
-    return l.T > 8 ? wide_rows ? launch_few<TO, 2, 2>(a, l, sc, s) : launch_few<TO, 2, 1>(a, l, sc, s)
-                   : wide_rows ? launch_few<TO, 1, 2>(a, l, sc, s) : launch_few<TO, 1, 1>(a, l, sc, s);
-  }
+  const bool wide_rows = features > 8 * sms;         // 16 features a block
+  if (l.T <= kFewTokens && features <= 64 * sms && features * l.F <= 32'000'000 && !(l.T > 8 && wide_rows))
+    return l.T > 8 ? launch_few<TO, 2, 1>(a, l, sc, s) : wide_rows ? launch_few<TO, 1, 2>(a, l, sc, s) : launch_few<TO, 1, 1>(a, l, sc, s);
   const LinearPlan plan = blocks_plan(l, sms, ((float)features + l.T) * l.F);
   if (plan.pair) return launch_pair<TO>(a, l, sc, sms, s);
   const int64_t tiles = (int64_t)((l.N + kBM - 1) / kBM) * (l.offsets ? l.T / plan.tokens + groups : (l.T + plan.tokens - 1) / plan.tokens);
