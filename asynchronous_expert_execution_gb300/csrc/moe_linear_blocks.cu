@@ -14,7 +14,8 @@
 //   pair   persistent, 256 tokens x 256 features over two SMs, tokens on the MMA's rows; for many tokens
 //   split  128 features x up to 64 tokens, features on the MMA's rows as in the forward product, K split over a cluster of up to 8 CTAs
 //   few    up to 16 tokens on small weights, by warp-wide matrix instructions
-// 4096 x 7168 x 7168 in bf16 takes 175 us (2.4 PFLOP/s, 64% of twice the measured bf16 rate), 256 x 7168 x 2048 16, 4 x 7168 x 2048 5.3.
+// 4096 x 7168 x 7168 in bf16 takes 201 us with a residual (2.1 PFLOP/s, 56% of twice the measured bf16 rate), 175 without; 256 x 7168 x 2048
+// 16, 4 x 7168 x 2048 5.3.
 #include "moe_linear.cuh"
 
 namespace moe {
@@ -879,7 +880,7 @@ moe_status launch_few(const moe_async_linear_args* a, const LinearParams& l, con
 // to 128 groups.  A k-block costs a split CTA of 16, 32 or 64 tokens 200, 260 or 360 alone on its SM, 330, 400 or 560 beside another; a
 // pair 430 in its first tile, 480 in those after, with 3,300 for the finish between.  The exchange takes 350 to 720 a rank.  `bytes`: all
 // operands; of the smaller of stream and sums, part shows.  Groups count half a tile each for their ends.
-// The choice's time is 4% above the best one's on average, 50% at worst (64 tokens on 7168 x 256: 11.0 against 7.2).
+// The choice's time is 4% above the best one's on average, 45% at worst (64 tokens on 7168 x 256: 10.5 against 7.2).
 LinearPlan blocks_plan(const LinearParams& l, int sms, float bytes) {
   const float groups = l.offsets ? std::min(l.G, l.T) : 1, per = l.T / groups;
   const auto token_tiles = [&](int t) { return l.offsets ? std::max(groups, l.T / (float)t + 0.5f * groups) : (float)((l.T + t - 1) / t); };
