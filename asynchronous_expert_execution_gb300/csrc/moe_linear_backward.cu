@@ -273,8 +273,8 @@ template <typename T> struct ActParams {
   int chunks, act;
 };
 
-// Bound by memory: three reads and two writes (8192 x 2880 bf16 36.1 us, 96% of the copy rate).  A thread asks for all that its kU units need before it uses the first.  The
-// outputs may be the inputs: every element is read by the thread that writes it, before.
+// Bound by memory: three reads and two writes (8192 x 2880 bf16 36.1 us, 96% of the copy rate).  A thread asks for all that its kU
+// units need before it uses the first.  The outputs may be the inputs: every element is read by the thread that writes it, before.
 template <typename T, int V, bool MUL>
 __global__ void __launch_bounds__(256) act_mul_backward_kernel(const ActParams<T> p) {
   using RV = RowVec<T, V>;

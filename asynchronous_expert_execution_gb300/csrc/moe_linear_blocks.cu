@@ -623,7 +623,7 @@ constexpr int kQuantBlock = 128;
 // The scale of a block whose largest |value| has these bits (NaN above infinity), and quotients by it that round as a division's do
 // wherever e4m3 can tell (below 2^-11 all become zeros).  1 / scale = hi + lo to 2^-47: hi is the rounded one, lo the rest.  v (hi + lo), as
 // v hi + round(v lo) rounded once, is a neighbour of v / scale in fp32.
-// fp32: from there one exact remainder gives the rounded quotient (Markstein, IBM J. Res. Dev. 34 (1990) 111, theorem 8).
+// fp32: from there one exact remainder gives the rounded quotient (Markstein, IBM J. Res. Dev. 34 (1990) 111).
 // bf16: it is the rounded quotient itself, unless that lies within 2^-46 of the middle between two fp32 numbers, which e4m3 can tell only
 // next to a border C between two of its numbers (five bits).  There v would be C (1 + 2^-24) scale or so to 46 bits; but scale is a bf16 number's
 // 448th part, eight bits or a seventh's repeating ones, whose products with that end in no 20 zeros (tests try every pair of mantissas).
